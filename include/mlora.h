@@ -392,6 +392,45 @@ int mlora_set_deterministic(mlora_t* h, int32_t on);
 enum { MLORA_LM_RECOMPUTE = 0, MLORA_LM_KEEP_LOGITS = 1 };
 int mlora_set_lm_backward(mlora_t* h, int32_t mode);
 
+/* ------------------------------------------------------------------------
+ * Gradient norms and clipping over many tensors (Deep Dive - Tinker,
+ * "optim_step advances adapter state", stands between a step's gradients and
+ * its update; the pages name no clipping, this definition is the library's).
+ * The tensors form groups -- one per adapter, so that no tenant's gradient
+ * changes another's step:
+ *     n_g = sqrt(sum of x^2 over the group's tensors)
+ *     factor_g = max_norm / n_g if n_g > max_norm, else 1
+ *     out = x * factor_g
+ * A norm that is an infinity or NaN leaves its group as it is (factor 1): the
+ * caller sees it in norms_out and skips the step.  Squares are summed in fp32
+ * over 64 elements a thread and in fp64 above that, in a fixed order, so that
+ * results repeat bit for bit; magnitudes whose squares leave fp32's range are
+ * summed relative to their largest.
+ *   grads, out: HOST arrays of DEVICE pointers to contiguous tensors of
+ *     `dtype` (mlora_dtype), aligned to their elements; out NULL: in place.
+ *     Equal pointers or no overlap.  sizes: HOST, elements, >= 0.
+ *   groups: HOST, 0 .. n_groups-1 for each tensor, or NULL: all in group 0.
+ *   max_norm >= 0; infinity: norms only (and copies, if out is given).
+ *   norms_out: DEVICE fp32 [n_groups] (may be NULL); 0 for a group without
+ *     elements.
+ *   workspace: DEVICE, 8-byte aligned, at least mlora_clip_grads_workspace()
+ *     bytes; calls that may overlap need one each.
+ * Queued on `stream`; no allocation on the device and no synchronisation, so
+ * the call can be captured into a CUDA graph.  Errors: E_ARG, E_CUDA, E_NOMEM
+ * (host memory). */
+typedef struct {
+    const void* const* grads;
+    void* const* out;
+    const int64_t* sizes;
+    const int32_t* groups;
+    int32_t n_tensors;
+    int32_t n_groups;
+    int32_t dtype;
+} mlora_grad_set;
+int64_t mlora_clip_grads_workspace(const mlora_grad_set* g);
+int mlora_clip_grads(const mlora_grad_set* g, float max_norm, float* norms_out, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then return and clear the device status word:
  * MLORA_OK, MLORA_E_RANGE or MLORA_E_TIMEOUT. */
 int mlora_check_status(mlora_t* h, void* stream);

@@ -1,0 +1,207 @@
+"""Python binding of the 8-bit key/value cache of libmlora.so
+(include/mlora_kv.h).  Argument marshalling only: every step runs in the
+library's CUDA kernels; PyTorch provides device memory and streams.
+
+    cache = KvCache.empty(n_pages, n_kv_heads, head_dim)     # or KvCache(k, v, k_scale, v_scale)
+    ws = kv_workspace()
+    kv_append(cache, page_table, kv_len, k, v)                              # newest rows into the cache
+    out, lse = kv_attention(cache, page_table, kv_len, q, max_len, workspace=ws)
+    k, v = kv_read(cache, page_table, kv_len, n_rows)                       # back as fp32 or bf16
+    kv_check_status(cache)                                                  # 0, or -2 (E_RANGE)
+
+page_table int32 [n_seqs, max_pages], kv_len int32 [n_seqs] (the lengths with
+the call's rows counted) and row_off int32 [n_seqs + 1] (None: one row a
+sequence) are CUDA tensors; max_rows and max_len are upper bounds the caller
+knows on the host.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_void_p
+
+from . import _check, _stream, load_library
+
+__all__ = ["PAGE", "KvCache", "kv_workspace", "kv_append", "kv_read", "kv_attention", "kv_check_status"]
+
+PAGE = 64
+COUNTER_BYTES = 65536
+WORKSPACE_BYTES = 32 << 20
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("status", c_void_p), ("n_pages", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32)]
+
+
+class _KvSeqs(ctypes.Structure):
+    _fields_ = [("page_table", c_void_p), ("kv_len", c_void_p), ("row_off", c_void_p), ("n_rows", c_int64),
+                ("n_seqs", c_int32), ("max_pages", c_int32), ("max_rows", c_int32)]
+
+
+class _KvAttn(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("workspace", c_void_p),
+                ("q_stride", c_int64), ("out_stride", c_int64), ("workspace_bytes", c_int64), ("max_len", c_int64),
+                ("dtype", c_int32), ("n_heads", c_int32), ("scale", c_float)]
+
+
+_SIGNATURES = {
+    "mlora_kv_append": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), c_int32, c_void_p, c_int64, c_void_p,
+                                  c_int64, c_void_p]),
+    "mlora_kv_read": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), c_int32, c_void_p, c_void_p, c_void_p]),
+    "mlora_kv_attention": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), POINTER(_KvAttn), c_void_p]),
+}
+
+_kv_lib = None
+
+
+def _lib():
+    global _kv_lib
+    if _kv_lib is None:
+        lib = load_library()
+        for name, (res, args) in _SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _kv_lib = lib
+    return _kv_lib
+
+
+def _dtype(t) -> int:
+    import torch
+    if t == torch.bfloat16:
+        return 0
+    if t == torch.float32:
+        return 1
+    raise ValueError(f"dtype {t}: bfloat16 or float32 is needed")
+
+
+class KvCache:
+    """A pool of cache pages: uint8 k, v [n_pages, n_kv_heads, 64, head_dim]
+    (the byte order inside a tile is the library's) and float32 k_scale, v_scale
+    [n_pages, n_kv_heads], contiguous CUDA tensors that the cache keeps alive."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        n_pages, n_kv, page, hd = k.shape
+        if page != PAGE or tuple(v.shape) != tuple(k.shape):
+            raise ValueError(f"k and v must be [n_pages, n_kv_heads, {PAGE}, head_dim]")
+        for t, dt, shape in ((k, torch.uint8, k.shape), (v, torch.uint8, k.shape),
+                             (k_scale, torch.float32, (n_pages, n_kv)), (v_scale, torch.float32, (n_pages, n_kv))):
+            if t.dtype != dt or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != k.device:
+                raise ValueError("cache tensors must be contiguous, on one device, uint8 pages and float32 scales")
+        if not k.is_cuda:
+            raise ValueError("cache tensors must be CUDA tensors")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, hd, k.device
+        self._c = _KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                           self.status.data_ptr(), n_pages, n_kv, hd)
+        self._ref = byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> "KvCache":
+        import torch
+        shape = (n_pages, n_kv_heads, PAGE, head_dim)
+        return cls(*[torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)],
+                   *[torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)])
+
+
+def kv_workspace(device="cuda", nbytes: int = WORKSPACE_BYTES):
+    """A zeroed workspace of kv_attention; calls that may overlap need one each."""
+    import torch
+    return torch.zeros(max(int(nbytes), COUNTER_BYTES), dtype=torch.uint8, device=device)
+
+
+def _ids(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows) -> _KvSeqs:
+    import torch
+    n, width = page_table.shape
+    dev = cache.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, which is not the current device")
+    return _KvSeqs(_ids("page_table", page_table, (n, width), dev), _ids("kv_len", kv_len, (n,), dev),
+                   None if row_off is None else _ids("row_off", row_off, (n + 1,), dev), n_rows, n, width, max_rows)
+
+
+def _rows(name, x, heads, hd, device) -> int:
+    """Row distance in elements of [n, heads, hd] rows whose heads lie side by side."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != hd or x.device != device:
+        raise ValueError(f"{name} must be [rows, {heads}, {hd}] on {device}")
+    st = x.stride()
+    if (st[2] != 1 and hd != 1) or (st[1] != hd and heads != 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return st[0] if x.shape[0] > 1 else max(st[0], heads * hd)
+
+
+def kv_append(cache: KvCache, page_table, kv_len, k, v, row_off=None, max_rows: int = 1, stream=None):
+    """Write the rows k, v [n_rows, n_kv_heads, head_dim] (bf16 or float32; rows
+    may be any multiple of 16 bytes apart) as the newest tokens of their
+    sequences."""
+    q = _seqs(cache, page_table, kv_len, row_off, k.shape[0], max_rows)
+    ldk = _rows("k", k, cache.n_kv_heads, cache.head_dim, cache.device)
+    ldv = _rows("v", v, cache.n_kv_heads, cache.head_dim, cache.device)
+    if v.shape[0] != k.shape[0] or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same rows and dtype")
+    _check(_lib().mlora_kv_append(cache._ref, byref(q), _dtype(k.dtype), k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                  _stream(stream)))
+
+
+def kv_read(cache: KvCache, page_table, kv_len, n_rows: int, row_off=None, max_rows: int = 1, dtype=None, stream=None):
+    """(k, v) [n_rows, n_kv_heads, head_dim] of the newest tokens, as float32 (default) or bf16."""
+    import torch
+    dtype = torch.float32 if dtype is None else dtype
+    q = _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows)
+    shape = (n_rows, cache.n_kv_heads, cache.head_dim)
+    ko = torch.empty(shape, dtype=dtype, device=cache.device)
+    vo = torch.empty(shape, dtype=dtype, device=cache.device)
+    _check(_lib().mlora_kv_read(cache._ref, byref(q), _dtype(dtype), ko.data_ptr(), vo.data_ptr(), _stream(stream)))
+    return ko, vo
+
+
+def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=None, max_rows: int = 1, scale=None,
+                 out=None, lse=None, workspace=None, stream=None):
+    """Attention of the rows q [n_rows, n_heads, head_dim] over their sequences'
+    cached positions up to their own.  Returns (out like q, lse float32
+    [n_rows, n_heads]); scale defaults to 1 / sqrt(head_dim).  Without a
+    workspace one is allocated and zeroed for the call."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, heads, head_dim]")
+    n_rows, heads, hd = q.shape
+    s = _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows)
+    ldq = _rows("q", q, heads, cache.head_dim, cache.device)
+    if out is None:
+        out = torch.empty((n_rows, heads, hd), dtype=q.dtype, device=cache.device)
+    elif out.dtype != q.dtype or out.shape[0] != n_rows:
+        raise ValueError("out must have q's rows and dtype")
+    ldo = _rows("out", out, heads, cache.head_dim, cache.device)
+    if lse is None:
+        lse = torch.empty((n_rows, heads), dtype=torch.float32, device=cache.device)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (n_rows, heads) or not lse.is_contiguous() or \
+            lse.device != cache.device:
+        raise ValueError("lse must be a contiguous float32 [rows, heads] tensor on the cache's device")
+    if workspace is None:
+        workspace = kv_workspace(cache.device)
+    elif not workspace.is_contiguous() or workspace.device != cache.device:
+        raise ValueError("workspace must be contiguous and on the cache's device")
+    a = _KvAttn(q.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ldq, ldo,
+                workspace.numel() * workspace.element_size(), max_len, _dtype(q.dtype), heads,
+                1.0 / math.sqrt(hd) if scale is None else scale)
+    _check(_lib().mlora_kv_attention(cache._ref, byref(s), byref(a), _stream(stream)))
+    return out, lse
+
+
+def kv_check_status(cache: KvCache, stream=None) -> int:
+    """Synchronise, return and clear the cache's status: 0, or -2 (E_RANGE)."""
+    import torch
+    (stream or torch.cuda.current_stream()).synchronize()
+    bad = int(cache.status.item())
+    cache.status.zero_()
+    return -2 if bad else 0

@@ -1,0 +1,218 @@
+"""Gradient norms and clipping (mlora_clip_grads) against NumPy doubles.
+
+Tolerances, with u = 2^-24: a thread's fp32 sum of at most 64 squares has a
+relative error of at most 65 u (all terms are positive), fp64 above it adds
+nothing that shows; the norm halves it and rounds once to fp32: 33.5 u + u.
+The factor adds u, the product u and the rounding to bf16 2^-8:
+  norm: 35 u;  out: (36 u + u) |x f| for fp32, + 2^-8 |x f| for bf16.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+U = 2.0 ** -24
+
+
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    import rl_step_gb300.grads as gr
+    return gr, gr._lib()
+
+
+def _set(gr, ptrs=(4096, 8192), sizes=(10, 20), groups=(0, 1), n_groups=2, dtype=1, out=None):
+    n = len(ptrs)
+    keep = ((ctypes.c_void_p * n)(*ptrs), None if out is None else (ctypes.c_void_p * n)(*out),
+            (ctypes.c_int64 * n)(*sizes), None if groups is None else (ctypes.c_int32 * n)(*groups))
+    g = gr._GradSet(*keep, n, n_groups, dtype)
+    g._keep = keep
+    return g
+
+
+def test_clip_refuses_without_a_gpu():
+    gr, lib = _lib()
+    ws = ctypes.c_void_p(4096)
+
+    def rc(g, max_norm=1.0, w=ws, nbytes=1 << 20):
+        return lib.mlora_clip_grads(ctypes.byref(g) if g is not None else None, max_norm, None, w, nbytes, None)
+
+    assert rc(None) == -1
+    for kw in (dict(dtype=2), dict(n_groups=0), dict(groups=(0, 2)), dict(groups=(-1, 0)), dict(sizes=(-1, 5)),
+               dict(ptrs=(None, 8192)), dict(ptrs=(4098, 8192)), dict(dtype=0, ptrs=(4097, 8192)),
+               dict(out=(4096, None)), dict(sizes=(1 << 45, 5)), dict(sizes=(1 << 44, 1 << 44))):
+        g = _set(gr, **kw)
+        assert rc(g) == -1 and lib.mlora_last_error(), kw
+        assert lib.mlora_clip_grads_workspace(ctypes.byref(g)) == 0
+    g = _set(gr)
+    assert rc(g, max_norm=-1.0) == -1 and rc(g, max_norm=math.nan) == -1
+    assert rc(g, w=None) == -1 and rc(g, w=ctypes.c_void_p(4100)) == -1 and rc(g, nbytes=8) == -1
+    assert lib.mlora_clip_grads_workspace(ctypes.byref(g)) == 16
+    assert rc(_set(gr, ptrs=(None, None), sizes=(0, 0)), w=None, nbytes=0) == 0      # nothing to do
+
+
+def _torch():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    _lib()
+    return torch
+
+
+def _check(xs, groups, max_norm, norms, outs, dtype, n_groups):
+    ref = [x.double().cpu().numpy().reshape(-1) for x in xs]
+    for g in range(n_groups):
+        mine = [r for r, k in zip(ref, groups) if k == g]
+        n = math.sqrt(sum(float((m * m).sum()) for m in mine))
+        assert abs(norms[g] - n) <= 35 * U * n, (g, norms[g], n)
+    f = {}
+    for g in set(groups):
+        n = math.sqrt(sum(float((r * r).sum()) for r, k in zip(ref, groups) if k == g))
+        f[g] = max_norm / n if n > max_norm else 1.0
+    for x, r, o, g in zip(xs, ref, outs, groups):
+        got, want = o.double().cpu().numpy().reshape(-1), r * f[g]
+        tol = ((0 if dtype == "fp32" else 2.0 ** -8) + 37 * U) * np.abs(want) + (1e-45 if dtype == "fp32" else 1e-40)
+        if f[g] == 1.0:
+            tol = 0 * tol
+        assert (np.abs(got - want) <= tol).all(), g
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_clip_groups_of_ragged_tensors(dtype, in_place):
+    """sizes around the chunk, empty tensors, groups in any order, a group without tensors,
+    tensors at odd offsets (no vector access), clipped and unclipped groups"""
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    g = torch.Generator(device="cuda").manual_seed(1)
+    sizes = [1, 3, 4, 16383, 16384, 16385, 0, 50001, 7, 131072, 257]
+    groups = [2, 0, 2, 1, 0, 4, 0, 1, 4, 4, 5]
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    for shift in (0, 1, 4):
+        buf = torch.randn(sum(sizes) + 20 * len(sizes), generator=g, device="cuda").to(dt)
+        xs, at = [], 0
+        for i, n in enumerate(sizes):
+            at = -(-at // 8) * 8 + shift * (i % 3)
+            xs.append(buf[at:at + n])
+            at += n
+        before = [x.clone() for x in xs]
+        outs = xs if in_place else [torch.full_like(x, 9) for x in xs]
+        rest = buf.clone()
+        s = gr.GradSet(xs, groups, n_groups=7, out=None if in_place else outs)
+        norms = gr.clip_grads(s, 150.0)
+        assert norms[3] == 0 and norms[6] == 0
+        _check(before, groups, 150.0, norms.cpu().numpy(), outs, dtype, 7)
+        for x, b in zip(xs, before):
+            x.copy_(b)
+        if not in_place:
+            assert torch.equal(buf, rest)
+        again = gr.clip_grads(s, 150.0)
+        assert torch.equal(norms, again)                     # bit for bit
+        if in_place:
+            for x, b in zip(xs, before):
+                x.copy_(b)
+            assert torch.equal(buf, rest)                    # nothing between the tensors was touched
+
+
+@pytest.mark.gpu
+def test_norms_only_and_zero():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    x = torch.randn(70000, device="cuda")
+    b = x.clone()
+    s = gr.GradSet([x])
+    n = gr.clip_grads(s, math.inf)
+    assert torch.equal(x, b) and abs(float(n) - float(b.double().norm())) <= 35 * U * float(n)
+    gr.clip_grads(s, 0.0)
+    assert (x == 0).all()
+    assert float(gr.clip_grads(s, 1.0)) == 0 and (x == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-42, 1e-30, 1e-20, 1e18, 1e25, 1e37])
+def test_magnitudes_whose_squares_leave_fp32(scale, dtype):
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    a = (torch.randn(40000, device="cuda") * scale).to(dt)
+    a[:100] = 0
+    b = torch.randn(20000, device="cuda").to(dt) * 0
+    s = gr.GradSet([a, b], [0, 1], out=[torch.empty_like(a), torch.empty_like(b)])
+    n = float(a.double().norm())
+    if n > 3e38:
+        a *= 0.01
+        n = float(a.double().norm())
+    norms = gr.clip_grads(s, 0.5 * n)
+    _check([a, b], [0, 1], 0.5 * n, norms.cpu().numpy(), s.out, dtype, 2)
+
+
+@pytest.mark.gpu
+def test_not_finite_gradients_are_left_and_reported():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    xs = [torch.ones(20000, device="cuda") for _ in range(4)]
+    xs[0][5] = math.inf
+    xs[1][19999] = math.nan
+    xs[2][1], xs[2][2] = math.inf, math.nan
+    b = [x.clone() for x in xs]
+    n = gr.clip_grads(gr.GradSet(xs, [0, 1, 2, 3]), 1.0).cpu().numpy()
+    assert math.isinf(n[0]) and math.isnan(n[1]) and math.isnan(n[2])
+    for x, y in zip(xs[:3], b[:3]):
+        assert torch.equal(torch.nan_to_num(x, 7, 8), torch.nan_to_num(y, 7, 8))
+    assert abs(float(xs[3].double().norm()) - 1) < 1e-6
+
+
+@pytest.mark.gpu
+def test_more_tensors_than_one_launch_holds():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    rng = np.random.default_rng(3)
+    sizes = rng.integers(0, 40000, 1300)
+    flat = torch.randn(int(sizes.sum()), device="cuda")
+    xs = list(torch.split(flat, sizes.tolist()))
+    groups = rng.integers(0, 9, len(sizes)).tolist()
+    xs = [x if x.data_ptr() % 4 == 0 else x.clone() for x in xs]
+    outs = [torch.empty_like(x) for x in xs]
+    s = gr.GradSet(xs, groups, out=outs)
+    norms = gr.clip_grads(s, 500.0)
+    _check(xs, groups, 500.0, norms.cpu().numpy(), outs, "fp32", 9)
+
+
+@pytest.mark.gpu
+def test_clip_captured_and_replayed():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    xs = [torch.zeros(n, device="cuda") for n in (30000, 11, 5000)]
+    s = gr.GradSet(xs, [0, 0, 2], n_groups=3)
+    norms = torch.full((3,), 5.0, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        gr.clip_grads(s, 2.0, norms_out=norms)
+    for _ in range(3):
+        for x in xs:
+            x.normal_()
+        b = [x.clone() for x in xs]
+        g.replay()
+        torch.cuda.synchronize()
+        _check(b, [0, 0, 2], 2.0, norms.cpu().numpy(), xs, "fp32", 3)
+
+
+@pytest.mark.gpu
+def test_gradset_refuses():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    x = torch.zeros(8, 8, device="cuda")
+    for f in (lambda: gr.GradSet([]), lambda: gr.GradSet([x.half()]), lambda: gr.GradSet([x.t()[1:, :3]]),
+              lambda: gr.GradSet([x, x.bfloat16()]), lambda: gr.GradSet([x.cpu()]), lambda: gr.GradSet([x], [0, 1]),
+              lambda: gr.GradSet([x], out=[x[:4]]),
+              lambda: gr.clip_grads(gr.GradSet([x]), 1.0, norms_out=torch.zeros(2, device="cuda"))):
+        with pytest.raises(ValueError):
+            f()
+    import rl_step_gb300 as m
+    for f in (lambda: gr.GradSet([x], [3], n_groups=2), lambda: gr.clip_grads(gr.GradSet([x]), -1.0)):
+        with pytest.raises(m.MLoRAError):
+            f()

@@ -1,0 +1,608 @@
+"""The 8-bit key/value cache (include/mlora_kv.h) against tests/_kv_model.py.
+
+append and read move values between formats by rules without rounding choices,
+so their bytes, scales and values have to be equal.
+
+Tolerances of the attention, per element, with u = 2^-24 (fp32's half step),
+A = sum_i p_i |v_i| and S = max_i |scale| sum_d |q_d k_d| of the row (doubles):
+  scores: q and the bytes enter exactly (bf16) or as two fp16 parts (fp32,
+    relative 2^-22); hd products are added in fp32, then scaled: at most
+    d = (hd + 8) u S + 2^-22 S, and 2^-23 |s - m| log2(e) from the exponent's
+    own rounding, |s - m| <= 2 S: together D = (hd + 16) u S + 2^-22 S
+  each p_i then has a relative error of 2 D (itself and the sum), exp2 adds
+    2^-22, the fp16 rounding of p 2^-11 (bf16) or 2^-22 (fp32), and the sums
+    over n positions at most n u each
+  out: (4 D + P + 2 n u + 2^-20) A + half a step of the type, with P = 2^-11 or 2^-22
+  lse: 2 D + n u + 2^-22 + 2 u |lse|
+(the products' order inside a matrix instruction may truncate instead of
+round: that is a full step, 2 u, which the factor 2 on D covers).
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import _kv_model as M
+
+EPS = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+
+
+# ----------------------------------------------------------------------------
+# on the CPU: layout and refusals
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("hd", [64, 128])
+def test_page_layout_is_a_permutation(hd):
+    for m in M.maps(hd):
+        assert sorted(m.reshape(-1)) == list(range(64 * hd))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_fragment_reads_touch_distinct_banks(hd):
+    """The 16-byte reads of eight consecutive lanes (token g of a key tile, or
+    token quad t of a value tile) fall on 32 different 4-byte banks."""
+    for j in range(2):
+        for a in range(hd // 64):
+            for ph in range(4):
+                lanes = range(8 * ph, 8 * ph + 8)
+                k = [M.byte_k(4 * ((ln // 4) >> 1) + 2 * j + ((ln // 4) & 1), (ln % 4 + 4 * a) * 16, hd)
+                     for ln in lanes]
+                assert sorted((x // 16) % 8 for x in k) == list(range(8))
+    for m in range(hd // 32):
+        for ph in range(4):
+            v = [M.byte_v(4 * (ln % 4), 32 * m + 4 * (ln // 4), hd) for ln in range(8 * ph, 8 * ph + 8)]
+            assert sorted((x // 16) % 8 for x in v) == list(range(8))
+
+
+def test_model_rounds_like_torch():
+    torch = pytest.importorskip("torch")
+    x = np.concatenate([np.linspace(-448, 448, 20001), np.logspace(-6, 2.6, 5000)]).astype(np.float32)
+    x = x[np.abs(x) <= 448]
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(M.e4m3_byte(x), want)
+
+
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    import rl_step_gb300.kv as kv
+    return kv, kv._lib()
+
+
+def _valid():
+    kv, lib = _lib()
+    p = 4096                                           # never dereferenced: every call below is refused on the host
+    c = kv._KvCache(p, p, p, p, None, 4, 2, 128)
+    q = kv._KvSeqs(p, p, None, 3, 3, 2, 1)
+    a = kv._KvAttn(p, p, p, p, 512, 512, 65536, 128, 0, 4, 0.1)
+    return kv, lib, c, q, a
+
+
+_BAD = [("c", "n_pages", 0), ("c", "n_kv_heads", 0), ("c", "n_kv_heads", 1025), ("c", "head_dim", 96),
+        ("c", "k", None), ("c", "v_scale", None), ("c", "v", 4104), ("q", "n_seqs", -1), ("q", "n_rows", -1),
+        ("q", "n_rows", 2), ("q", "n_rows", 1 << 31), ("q", "max_pages", 0), ("q", "max_rows", -1),
+        ("q", "max_rows", 2), ("q", "page_table", None), ("q", "kv_len", None)]
+
+
+@pytest.mark.parametrize("where,field,value", _BAD + [
+    ("a", "n_heads", 3), ("a", "n_heads", 0), ("a", "scale", math.inf), ("a", "scale", math.nan), ("a", "max_len", -1),
+    ("a", "q", None), ("a", "out", None), ("a", "q", 4104), ("a", "q_stride", 511), ("a", "q_stride", 516),
+    ("a", "out_stride", 256), ("a", "workspace", None), ("a", "workspace", 4104), ("a", "workspace_bytes", 65535),
+    ("a", "dtype", 2)])
+def test_attention_refuses(where, field, value):
+    kv, lib, c, q, a = _valid()
+    setattr({"c": c, "q": q, "a": a}[where], field, value)
+    assert lib.mlora_kv_attention(ctypes.byref(c), ctypes.byref(q), ctypes.byref(a), None) == -1
+    assert lib.mlora_last_error()
+
+
+@pytest.mark.parametrize("where,field,value", _BAD)
+def test_append_and_read_refuse(where, field, value):
+    kv, lib, c, q, _ = _valid()
+    setattr({"c": c, "q": q}[where], field, value)
+    p = ctypes.c_void_p(4096)
+    assert lib.mlora_kv_append(ctypes.byref(c), ctypes.byref(q), 0, p, 256, p, 256, None) == -1
+    assert lib.mlora_kv_read(ctypes.byref(c), ctypes.byref(q), 0, p, p, None) == -1
+
+
+def test_append_refuses_rows():
+    kv, lib, c, q, _ = _valid()
+    p, odd = ctypes.c_void_p(4096), ctypes.c_void_p(4104)
+    for args in ((0, None, 256, p, 256), (0, p, 256, None, 256), (0, p, 255, p, 256), (0, p, 256, p, 260),
+                 (0, odd, 256, p, 256), (2, p, 256, p, 256), (1, p, 258, p, 256)):
+        assert lib.mlora_kv_append(ctypes.byref(c), ctypes.byref(q), *args, None) == -1
+    assert lib.mlora_kv_read(ctypes.byref(c), ctypes.byref(q), 0, odd, p, None) == -1
+    q.row_off, q.max_rows, q.n_seqs, q.n_rows = 4096, 1 << 30, 1 << 20, (1 << 31) - 1     # more blocks than a grid holds
+    assert lib.mlora_kv_append(ctypes.byref(c), ctypes.byref(q), 0, p, 256, p, 256, None) == -1
+    assert lib.mlora_kv_read(ctypes.byref(c), ctypes.byref(q), 0, p, p, None) == -1
+
+
+def test_nothing_to_do_is_no_error():
+    kv, lib, c, q, a = _valid()
+    q.n_seqs = 0
+    assert lib.mlora_kv_attention(ctypes.byref(c), ctypes.byref(q), ctypes.byref(a), None) == 0
+    q.n_seqs, q.row_off, q.max_rows = 3, 4096, 0
+    assert lib.mlora_kv_append(ctypes.byref(c), ctypes.byref(q), 0, None, 256, None, 256, None) == 0
+
+
+def test_kv_header_and_binding_agree(tmp_path):
+    import os
+    import re
+    import shutil
+    import subprocess
+    kv, _ = _lib()
+    import rl_step_gb300.grads as gr
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no host C compiler")
+    structs = [("mlora_kv_cache", kv._KvCache), ("mlora_kv_seqs", kv._KvSeqs), ("mlora_kv_attn", kv._KvAttn),
+               ("mlora_grad_set", gr._GradSet)]
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "mlora_kv.h"', "int main(void) {"]
+    for name, cls in structs:
+        lines.append(f'printf("%zu ", sizeof({name}));')
+        lines += [f'printf("%zu ", offsetof({name}, {f[0]}));' for f in cls._fields_]
+    lines.append('printf("%d %d\\n", MLORA_KV_PAGE, MLORA_KV_COUNTER_BYTES); return 0; }')
+    (tmp_path / "a.c").write_text("\n".join(lines))
+    subprocess.run([cc, "-std=c11", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(tmp_path / "a.c"),
+                    "-o", str(tmp_path / "a")], check=True, capture_output=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "a")], capture_output=True, text=True).stdout.split()]
+    want = []
+    for _, cls in structs:
+        want += [ctypes.sizeof(cls)] + [getattr(cls, f[0]).offset for f in cls._fields_]
+    assert got == want + [kv.PAGE, kv.COUNTER_BYTES]
+    src = re.sub(r"/\*.*?\*/", "", "".join(open(os.path.join(root, "include", h)).read()
+                                          for h in ("mlora_kv.h", "mlora.h")), flags=re.S)
+    for name, (_, args) in {**kv._SIGNATURES, **gr._SIGNATURES}.items():
+        m = re.search(r"\b%s\s*\(([^)]*)\)" % name, src)
+        assert m and len(m.group(1).split(",")) == len(args), name
+
+
+# ----------------------------------------------------------------------------
+# on the GPU
+# ----------------------------------------------------------------------------
+def _torch():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    _lib()
+    return torch
+
+
+class Setup:
+    """A cache on the GPU beside its model; sequences own pages in a shuffled order."""
+
+    def __init__(self, caps, n_kv, hd, seed=0, extra=3):
+        self.torch = torch = _torch()
+        import rl_step_gb300.kv as kv
+        self.kv, self.hd, self.n_kv = kv, hd, n_kv
+        self.rng = np.random.default_rng(seed)
+        used = [-(-c // 64) for c in caps]
+        total = sum(used) + extra
+        order = self.rng.permutation(total).astype(np.int32)
+        width = max(max(used), 1)
+        self.table = np.full((len(caps), width), -1, np.int32)
+        at = 0
+        for s, u in enumerate(used):
+            self.table[s, :u] = order[at:at + u]
+            at += u
+        self.model = M.Cache(total, n_kv, hd)
+        for x in "kv":                                   # stale bytes, NaN among them
+            self.model.b[x][:] = self.rng.integers(0, 256, self.model.b[x].shape)
+            self.model.e[x][:] = 30
+        self.cache = kv.KvCache(*[torch.from_numpy(self.model.pages(x)).cuda() for x in "kv"],
+                                *[torch.full((total, n_kv), 2.0 ** 30, device="cuda") for _ in range(2)])
+        self.len = [0] * len(caps)
+        self.dtable = torch.from_numpy(self.table).cuda()
+
+    def i32(self, x):
+        return self.torch.tensor(list(x), dtype=self.torch.int32, device="cuda")
+
+    def off(self, rows):
+        return self.i32(np.concatenate([[0], np.cumsum(rows)]))
+
+    def rows(self, n, dtype, spread=1.0):
+        x = self.rng.standard_normal((n, 2 * self.n_kv, self.hd)) * np.exp(spread * self.rng.standard_normal((n, 1, 1)))
+        t = self.torch.from_numpy(x.astype(np.float32)).cuda()
+        return t.bfloat16() if dtype == "bf16" else t
+
+    def append(self, rows, dtype="bf16", x=None, use_off=True):
+        """rows[s] new tokens of each sequence, on both sides."""
+        n = sum(rows)
+        x = self.rows(n, dtype) if x is None else x
+        k, v = x[:, :self.n_kv], x[:, self.n_kv:]         # strided views
+        self.len = [a + b for a, b in zip(self.len, rows)]
+        self.kv.kv_append(self.cache, self.dtable, self.i32(self.len), k, v,
+                          row_off=self.off(rows) if use_off else None, max_rows=max(rows) if use_off else 1)
+        kn, vn = k.float().cpu().numpy(), v.float().cpu().numpy()
+        at = 0
+        for s, r in enumerate(rows):
+            if r:
+                self.model.append(self.table[s], self.len[s] - r, {"k": kn[at:at + r], "v": vn[at:at + r]})
+            at += r
+
+    def check_state(self):
+        """bytes of every position a sequence holds, and the scales of its pages"""
+        for x, pages, scale in (("k", self.cache.k, self.cache.k_scale), ("v", self.cache.v, self.cache.v_scale)):
+            got, sc = pages.cpu().numpy(), scale.cpu().numpy()
+            want = self.model.pages(x)
+            m = M.maps(self.hd)[0 if x == "k" else 1]
+            for s, n in enumerate(self.len):
+                for p in range(-(-n // 64)):
+                    live = m[:min(n - 64 * p, 64)].reshape(-1)
+                    g = got[self.table[s, p]].reshape(self.n_kv, -1)[:, live]
+                    w = want[self.table[s, p]].reshape(self.n_kv, -1)[:, live]
+                    nan = ((g & 0x7f) == 0x7f) & ((w & 0x7f) == 0x7f)        # a NaN's sign says nothing
+                    assert np.array_equal(np.where(nan, 0, g), np.where(nan, 0, w)), (x, s, p)
+                    assert np.array_equal(sc[self.table[s, p]],
+                                          2.0 ** self.model.e[x][self.table[s, p]].astype(np.float64)), (x, s, p)
+        assert self.kv.kv_check_status(self.cache) == 0
+
+
+def _attend(st, rows, heads, dtype="bf16", q=None, scale=None, use_off=True, slack=0, **kw):
+    """kv_attention of each sequence's newest rows[s], checked against the model."""
+    torch = st.torch
+    n = sum(rows)
+    if q is None:
+        q = torch.from_numpy(st.rng.standard_normal((n, heads, st.hd)).astype(np.float32) * 2).cuda()
+        q = q.bfloat16() if dtype == "bf16" else q
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, max(max(st.len), 1) + slack, scale=scale,
+                                  row_off=st.off(rows) if use_off else None, max_rows=max(rows) if use_off else 1, **kw)
+    assert st.kv.kv_check_status(st.cache) == 0
+    _compare(st, rows, q, out, lse, dtype, scale)
+    return q, out, lse
+
+
+def _compare(st, rows, q, out, lse, dtype, scale=None):
+    sc = 1 / math.sqrt(st.hd) if scale is None else scale
+    qn, on, ln = q.double().cpu().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    u = 2.0 ** -24
+    at = 0
+    for s, r in enumerate(rows):
+        if not r:
+            continue
+        n = st.len[s]
+        k, v = (st.model.values(x, st.table[s], n) for x in "kv")
+        o, l, mass, big = M.attention(qn[at:at + r], k, v, max(n - r, -r), sc)
+        D = ((st.hd + 16) * u + 2.0 ** -22) * big
+        P = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22
+        tol = (4 * D + P + 2 * n * u + 2.0 ** -20)[..., None] * mass + EPS[dtype] * np.abs(o) + 1e-40
+        bad = np.abs(on[at:at + r] - o) > tol
+        assert not bad.any(), (s, float((np.abs(on[at:at + r] - o) / tol).max()))
+        fin = np.isfinite(l)
+        assert np.array_equal(fin, np.isfinite(ln[at:at + r]))
+        assert np.array_equal(ln[at:at + r][~fin], l[~fin])
+        d = np.abs(ln[at:at + r][fin] - l[fin])
+        assert (d <= 2 * D[fin] + n * u + 2.0 ** -22 + 2 * u * np.abs(l[fin])).all(), (s, float(d.max()))
+        at += r
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hd,n_kv,dtype", [(128, 2, "bf16"), (64, 3, "bf16"), (128, 1, "fp32"), (64, 5, "fp32")])
+def test_append_in_pieces_equals_the_model(hd, n_kv, dtype):
+    st = Setup([300, 1, 64, 129, 200, 70], n_kv, hd, seed=hd + n_kv)
+    for rows in ([1, 1, 1, 1, 1, 1], [0, 0, 3, 63, 5, 0], [62, 0, 60, 1, 130, 1], [1, 0, 0, 64, 1, 65], [200, 0, 0, 0, 2, 3]):
+        st.append(rows, dtype)
+        st.check_state()
+
+
+@pytest.mark.gpu
+def test_append_one_token_each_without_row_off():
+    st = Setup([90] * 5, 2, 128, seed=3)
+    for _ in range(70):
+        st.append([1] * 5, use_off=False)
+    st.check_state()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_append_extreme_values(dtype):
+    """zeros, infinities, NaN, the largest and the smallest magnitudes, and scales that jump"""
+    st = Setup([130], 1, 64, seed=9)
+    x = st.rows(130, dtype).float()
+    x[3] = 0
+    x[5, :, 7], x[6, :, 8], x[9, :, 1] = math.inf, -math.inf, math.nan
+    x[20:30] *= 1e30
+    x[30] = 3.3e38
+    x[31] = 1e-44
+    x[64:] *= 1e-38                                       # the second page: below the smallest scale
+    x = x.bfloat16() if dtype == "bf16" else x
+    for a, b in ((0, 1), (1, 4), (4, 5), (5, 6), (6, 25), (25, 30), (30, 31), (31, 66), (66, 130)):
+        st.append([b - a], dtype, x[a:b])
+        st.check_state()
+    st2 = Setup([70], 1, 64, seed=9)
+    st2.append([3], dtype, x[:3] * 0)                      # a page of zeros, then ordinary values
+    st2.append([60], dtype, x[64:124])
+    st2.check_state()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "fp32"), (128, "fp32"), (64, "bf16")])
+def test_read_returns_the_stored_values(hd, dtype):
+    torch = _torch()
+    st = Setup([150, 64, 1, 77], 3, hd, seed=5)
+    st.append([150, 64, 1, 77])
+    for rows in ([150, 64, 1, 77], [1, 1, 1, 1], [65, 0, 1, 14]):
+        k, v = st.kv.kv_read(st.cache, st.dtable, st.i32(st.len), sum(rows), row_off=st.off(rows), max_rows=max(rows),
+                             dtype=torch.float32 if dtype == "fp32" else torch.bfloat16)
+        for x, got in (("k", k), ("v", v)):
+            want = np.concatenate([st.model.values(x, st.table[s], st.len[s])[st.len[s] - r:] for s, r in enumerate(rows)])
+            assert np.array_equal(got.double().cpu().numpy(), want)
+    assert st.kv.kv_check_status(st.cache) == 0
+
+
+_SHAPES = [  # heads, kv heads, hd
+    (4, 2, 128), (8, 1, 64), (3, 3, 128), (24, 2, 64), (40, 2, 128), (7, 1, 128), (64, 1, 64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("heads,n_kv,hd", _SHAPES)
+def test_attention_single_rows(heads, n_kv, hd, dtype):
+    lens = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300, 1000]
+    st = Setup(lens, n_kv, hd, seed=heads)
+    st.append(lens)
+    _attend(st, [1] * len(lens), heads, dtype, use_off=False)
+    _attend(st, [1] * len(lens), heads, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("heads,n_kv,hd", _SHAPES)
+def test_attention_several_rows(heads, n_kv, hd, dtype):
+    """drafted tokens and short prompts: ragged rows, rows that see only themselves"""
+    lens = [1, 5, 33, 64, 66, 130, 257]
+    st = Setup(lens, n_kv, hd, seed=heads + 1)
+    st.append(lens)
+    _attend(st, [1, 5, 2, 0, 3, 9, 4], heads, dtype)
+    _attend(st, [1, 5, 33, 20, 66, 70, 40], heads, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_seqs,length", [(1, 20000), (2, 9001), (3, 4097)])
+def test_attention_split_over_a_long_cache(n_seqs, length):
+    """few long sequences: the work is cut along the positions and joined; a small
+    workspace gives fewer parts and the same values"""
+    torch = _torch()
+    lens = [length - 117 * i for i in range(n_seqs)]
+    st = Setup(lens, 2, 128, seed=n_seqs)
+    st.append(lens)
+    ws = st.kv.kv_workspace()
+    q, out, lse = _attend(st, [1] * n_seqs, 8, workspace=ws)
+    assert int(ws[:st.kv.COUNTER_BYTES].max()) == 0
+    _, o2, l2 = _attend(st, [1] * n_seqs, 8, q=q, workspace=ws)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)               # bit for bit
+    for nbytes in (65536, 65536 + 40000, 65536 + 300000):
+        _attend(st, [1] * n_seqs, 8, q=q, workspace=st.kv.kv_workspace(nbytes=nbytes))
+    _attend(st, [3] * n_seqs, 8)
+    _attend(st, [1] * n_seqs, 8, q=q, slack=100000)                    # a loose bound of the lengths
+
+
+@pytest.mark.gpu
+def test_attention_concentrated_and_wide_scores():
+    """scores of +-200, one position with all the weight, values of very different scales"""
+    st = Setup([700, 700, 65], 1, 128, seed=2)
+    x = st.rows(1465, "bf16", spread=0.1).float()
+    x[100:164, 1] *= 1e-12                                 # tiny values on one page ..
+    x[700 + 64:700 + 128, 1] *= 1e9                        # .. large ones on another
+    st.append([700, 700, 65], x=x.bfloat16())
+    torch = st.torch
+    k = st.model.values("k", st.table[0], 700)
+    q = torch.from_numpy(np.stack([k[120, 0] * 3, k[5, 0] * 2])[None].repeat(3, 0).astype(np.float32)).cuda().bfloat16()
+    _attend(st, [1, 1, 1], 2, q=q)
+    _attend(st, [1, 1, 1], 2, q=q * 0)
+    _attend(st, [1, 1, 1], 2, q=q, scale=-0.3)
+    _attend(st, [1, 1, 1], 2, q=q * 1e-20)
+    _attend(st, [1, 1, 1], 2, "fp32", q=q.float() * 1e20, scale=1e-21)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_nan_and_infinity(dtype):
+    """NaN in a cached key or value, and infinities in a query, reach exactly the
+    rows and dims of the formula; stale NaN behind the end reach nothing"""
+    torch = _torch()
+    st = Setup([100, 100, 100], 1, 64, seed=4)
+    x = st.rows(300, "bf16").float()
+    x[10, 0, 3] = math.nan                                 # sequence 0: a key
+    x[150, 1, 5] = math.inf                                # sequence 1: a value (stored as NaN)
+    st.append([100, 100, 100], x=x.bfloat16())
+    q = torch.ones(3, 2, 64, device="cuda")
+    q[2, 1, 9] = math.inf
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q if dtype == "fp32" else q.bfloat16(), 100)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    nan = torch.isnan(out[1])
+    assert nan[:, 5].all() and int(nan.sum()) == 2 and torch.isfinite(lse[1]).all()
+    assert torch.isfinite(out[2, 0]).all() and torch.isnan(out[2, 1]).all()
+
+
+@pytest.mark.gpu
+def test_empty_slots_and_rows_behind_the_end():
+    torch = _torch()
+    st = Setup([64, 0, 10, 0], 2, 128, seed=6)
+    st.append([64, 0, 10, 0])
+    q = torch.randn(6, 4, 128, device="cuda").bfloat16()
+    out = torch.full((6, 4, 128), 7.0, device="cuda").bfloat16()
+    lse = torch.full((6, 4), 7.0, device="cuda")
+    st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, 64, out=out, lse=lse)
+    assert (out[4:] == 7).all() and (lse[4:] == 7).all()
+    for s in (1, 3):
+        assert (out[s] == 0).all() and (lse[s] == -math.inf).all()
+    _compare(st, [1, 0, 1, 0], q[[0, 2]], out[[0, 2]], lse[[0, 2]], "bf16")
+    before = st.cache.k.clone(), st.cache.v.clone()
+    x = st.rows(4, "bf16")
+    st.kv.kv_append(st.cache, st.dtable, st.i32([0, 0, 0, 0]), x[:, :2], x[:, 2:])
+    assert torch.equal(before[0], st.cache.k) and torch.equal(before[1], st.cache.v)
+    k, v = st.kv.kv_read(st.cache, st.dtable, st.i32([0] * 4), 4)
+    assert st.kv.kv_check_status(st.cache) == 0
+
+
+@pytest.mark.gpu
+def test_bad_sequences_are_flagged_and_leave_the_others_alone():
+    """every range error that only the device sees: NaN rows or skipped writes, status, and the
+    neighbours as if it were not there"""
+    torch = _torch()
+    for bad in ("len<0", "len>cap", "len>max", "page", "rows>max", "off<0", "off>n", "rows>len"):
+        st = Setup([128, 100, 128], 2, 128, seed=7)
+        st.append([128, 100, 128])
+        good = _attend(st, [2, 3, 2], 4)
+        q = good[0]
+        lens, off, table, max_rows, max_len = list(st.len), [0, 2, 5, 7], st.table.copy(), 3, 128
+        if bad == "len<0":
+            lens[1] = -5
+        elif bad == "len>cap":
+            lens[1], max_len = 129, 1 << 40
+        elif bad == "len>max":
+            lens[1], max_len = 128, 127
+            lens[0] = lens[2] = 127
+        elif bad == "page":
+            table[1, 0] = st.cache.n_pages
+            table[1, 1] = -1
+        elif bad == "rows>max":
+            max_rows = 2
+        elif bad == "off<0":
+            off = [0, 2, -3, 7]
+        elif bad == "off>n":
+            off = [0, 2, 9, 7]
+        elif bad == "rows>len":
+            lens[1] = 2
+        kw = dict(row_off=st.i32(off), max_rows=max_rows)
+        tab = torch.from_numpy(table).cuda()
+        before = st.cache.k.clone(), st.cache.v.clone(), st.cache.k_scale.clone(), st.cache.v_scale.clone()
+        out, lse = st.kv.kv_attention(st.cache, tab, st.i32(lens), q, max_len, **kw)
+        assert st.kv.kv_check_status(st.cache) == -2 and st.kv.kv_check_status(st.cache) == 0, bad
+        if bad in ("len<0", "len>cap", "len>max", "page", "rows>max", "rows>len"):
+            assert torch.isnan(out[2:5]).all() and torch.isnan(lse[2:5]).all(), bad
+        if bad not in ("len>max", "off<0", "off>n"):
+            for i in (slice(0, 2), slice(5, 7)):
+                assert torch.equal(out[i], good[1][i]) and torch.equal(lse[i], good[2][i]), bad
+        # nothing of a bad sequence is written
+        st.kv.kv_append(st.cache, tab, st.i32(lens), *[torch.zeros(7, 2, 128, device="cuda")] * 2, **kw)
+        if bad in ("len<0", "len>cap", "page", "rows>max", "rows>len"):
+            assert st.kv.kv_check_status(st.cache) == -2, bad
+            own = torch.from_numpy(st.table[1]).cuda().long()
+            for a, b in zip(before, (st.cache.k, st.cache.v, st.cache.k_scale, st.cache.v_scale)):
+                assert torch.equal(a[own], b[own]), bad
+        st.kv.kv_read(st.cache, tab, st.i32(lens), 7, **kw)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_shared_prefix_pages():
+    """two sequences over the same first pages, each with a tail of its own"""
+    st = Setup([128, 20, 30], 2, 128, seed=8)
+    st.append([128, 0, 0])
+    x = st.rows(50, "bf16")
+    st.append([0, 20, 30], x=x)
+    table = np.concatenate([np.repeat(st.table[:1, :2], 2, 0), st.table[1:, :1]], 1)
+    q = st.torch.randn(2, 4, 128, device="cuda").bfloat16()
+    out, lse = st.kv.kv_attention(st.cache, st.torch.from_numpy(table).cuda(), st.i32([148, 158]), q, 158)
+    st.table, st.len = table, [148, 158]
+    _compare(st, [1, 1], q, out, lse, "bf16")
+
+
+@pytest.mark.gpu
+def test_rows_of_strided_buffers_and_outputs():
+    """q, k, v as column blocks of one buffer, out as a column block of another"""
+    torch = _torch()
+    st = Setup([70, 70], 2, 64, seed=10)
+    buf = torch.randn(140, 4 + 2 + 2 + 1, 64, device="cuda").bfloat16()
+    st.append([70, 70], x=buf[:, 4:8])
+    st.check_state()
+    big = torch.zeros(2, 6, 64, device="cuda").bfloat16()
+    q = buf[69::70, :4]
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, 70, out=big[:, 1:5])
+    _compare(st, [1, 1], q, out, lse, "bf16")
+    assert (big[:, 0] == 0).all() and (big[:, 5] == 0).all()
+
+
+@pytest.mark.gpu
+def test_captured_steps_replay_on_new_data_and_another_stream():
+    """append and attention in one graph: the lengths, tables and rows are read at replay"""
+    torch = _torch()
+    st = Setup([200, 200, 200], 2, 128, seed=11)
+    st.append([100, 63, 1])
+    k, v = torch.zeros(3, 2, 128, device="cuda").bfloat16(), torch.zeros(3, 2, 128, device="cuda").bfloat16()
+    q, lens = torch.zeros(3, 8, 128, device="cuda").bfloat16(), st.i32(st.len)
+    out, lse, ws = torch.zeros_like(q), torch.zeros(3, 8, device="cuda"), st.kv.kv_workspace()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            st.kv.kv_append(st.cache, st.dtable, lens, k, v)
+            st.kv.kv_attention(st.cache, st.dtable, lens, q, 200, out=out, lse=lse, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        x = st.rows(3, "bf16")
+        k.copy_(x[:, :2])
+        v.copy_(x[:, 2:])
+        q.normal_()
+        lens += 1
+        st.len = [n + 1 for n in st.len]
+        g.replay()
+        torch.cuda.synchronize()
+        for s in range(3):
+            st.model.append(st.table[s], st.len[s] - 1, {"k": x[s:s + 1, :2].float().cpu().numpy(),
+                                                         "v": x[s:s + 1, 2:].float().cpu().numpy()})
+        st.check_state()
+        _compare(st, [1, 1, 1], q, out, lse, "bf16")
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once_with_a_workspace_each():
+    torch = _torch()
+    st = Setup([6000, 5000], 2, 128, seed=12)
+    st.append([6000, 5000])
+    q = torch.randn(2, 8, 128, device="cuda").bfloat16()
+    want = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, 6000)
+    lens = st.i32(st.len)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [st.kv.kv_workspace() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for s, w in zip(streams, ws):
+            got.append(st.kv.kv_attention(st.cache, st.dtable, lens, q, 6000, workspace=w, stream=s))
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+@pytest.mark.gpu
+def test_a_row_does_not_depend_on_its_batch():
+    torch = _torch()
+    lens = [900, 3, 450, 64, 2000]
+    st = Setup(lens, 2, 128, seed=13)
+    st.append(lens)
+    q = torch.randn(5, 8, 128, device="cuda").bfloat16()
+    ws = st.kv.kv_workspace()
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(lens), q, 2000, workspace=ws)
+    other = [n if s == 2 else 1 for s, n in enumerate(lens)]
+    o2, l2 = st.kv.kv_attention(st.cache, st.dtable, st.i32(other), q, 2000, workspace=ws)
+    assert torch.equal(out[2], o2[2]) and torch.equal(lse[2], l2[2])
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    torch = _torch()
+    st = Setup([64], 2, 128)
+    kv, c, tab, lens = st.kv, st.cache, st.dtable, st.i32([3])
+    x = torch.zeros(1, 2, 128, device="cuda")
+    for f in (lambda: kv.kv_append(c, tab, lens, x.half(), x.half()), lambda: kv.kv_append(c, tab.long(), lens, x, x),
+              lambda: kv.kv_append(c, tab, lens, x, x.bfloat16()), lambda: kv.kv_append(c, tab, lens[:0], x, x),
+              lambda: kv.kv_append(c, tab, lens, x.cpu(), x), lambda: kv.kv_append(c, tab, lens.cpu(), x, x),
+              lambda: kv.kv_attention(c, tab, lens, x[:, :, ::2], 64), lambda: kv.kv_attention(c, tab, lens, x[0], 64),
+              lambda: kv.kv_attention(c, tab, lens, x, 64, lse=torch.zeros(1, 3, device="cuda")),
+              lambda: kv.kv_attention(c, tab, lens, x, 64, out=x.bfloat16()),
+              lambda: kv.KvCache(c.k, c.v[:1], c.k_scale, c.v_scale),
+              lambda: kv.KvCache(c.k.cpu(), c.v.cpu(), c.k_scale.cpu(), c.v_scale.cpu())):
+        with pytest.raises(ValueError):
+            f()
+    import rl_step_gb300 as m
+    with pytest.raises(m.MLoRAError):
+        kv.kv_attention(c, tab, lens, torch.zeros(1, 3, 128, device="cuda"), 64)       # 3 heads over 2
+    with pytest.raises(m.MLoRAError):
+        kv.kv_attention(c, tab, lens, x, 64, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(m.MLoRAError):
+        kv.kv_append(c, tab, lens, x, x, max_rows=2)                                   # row_off is missing
