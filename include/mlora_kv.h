@@ -39,7 +39,8 @@
  * < 0, > max_rows or > kv_len > 0, rows outside 0 .. n_rows-1, or a page id
  * outside 0 .. n_pages-1 raises bit 0 of *status; append and read skip it (a
  * bad page: that page), attention writes NaN to those of its rows that lie in
- * range.
+ * range.  A device wait that exceeds its bound raises bit 1 (the workspace must
+ * then be zeroed before its next use).
  */
 #ifndef MLORA_KV_H
 #define MLORA_KV_H
@@ -62,7 +63,7 @@ typedef struct {
     uint8_t* v;
     float* k_scale;
     float* v_scale;
-    int32_t* status;       /* DEVICE int32 (may be NULL): bit 0 is raised on a range error */
+    int32_t* status;       /* DEVICE int32 (may be NULL): bits raised by the kernels (above)  */
     int32_t n_pages;       /* >= 1                                    */
     int32_t n_kv_heads;    /* 1 .. 1024                               */
     int32_t head_dim;      /* 64 or 128                               */

@@ -2,7 +2,41 @@
 // (include/mlora_kv.h): for each row and query head, one pass over the cached
 // positions with a running maximum and sum,
 //     s_i = scale q . k_i,  out = sum_i exp(s_i - lse) v_i,  lse = log sum_i exp(s_i).
+//
+// What bounds it.  Few rows a sequence: every cached byte is read once and used
+// for rows x group products, far below the tensor cores' rate, so the cache's
+// bytes over the HBM rate are the floor.  The design streams pages and keeps
+// the arithmetic beside the stream cheap:
+//  * One block handles 16 RG of a sequence's (row, head of the group) pairs
+//    against one key/value head, over a run of pages.  A producer warp copies
+//    each (page, head) tile of K and V -- contiguous 8 KB at head_dim 128 --
+//    into a ring of stages with cp.async.bulk.
+//  * The pairs are the 16 rows of mma.sync m16n8k16 (fp16 operands, fp32 sums):
+//    an e4m3 byte is exactly an fp16 value, two bytes convert in one
+//    instruction, and M = 16 fits the few rows of a decode step, where a
+//    128-row tcgen05 tile would be at most an eighth full and would want the
+//    converted tile written back to shared memory first.  The page's byte
+//    order (mlora_kv.h) puts each thread's fragment bytes side by side.
+//  * q enters as fp16 relative to its row's largest magnitude (a power of two,
+//    folded into the scale): exact for bf16 down to 2^-17 of that magnitude,
+//    and as a high and a low part (2^-22) on fp32.
+//  * The page's value scale 2^ev goes into the exponent of the probability,
+//    p' = exp2(s log2 e + ev - m') with m' the running maximum of s log2 e + ev,
+//    so pages of any scale add into one accumulator, the largest p' v8 sets the
+//    precision, and l += p' 2^-ev is what the definition sums.  p' is held at
+//    2^12 times its value, so that its fp16 rounding stays relative (2^-11)
+//    down to 2^-26 of the row's largest; on fp32 it is split like q.
+//  * Warps of a block take different 16-token slices of a page (each with a
+//    running maximum and sum of its own, joined at the end), so nothing but
+//    the ring's barriers is shared in the loop.
+//  * Long sequences are cut into runs of pages (flash-style split); a block
+//    leaves its rows' unnormalised sums, maximum and sum in the workspace, and
+//    the last block of the sequence and head to arrive joins them in order of
+//    the runs, so the result does not depend on who was last.
+#include <atomic>
+
 #include "kv_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace mlk {
 
@@ -10,105 +44,616 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value
+// Runs of pages of a split (see attn_t).
+constexpr int KV_SPLIT_BLOCKS = 456;
+constexpr int KV_LONG_RUN = 16, KV_SHORT_RUN = 2;
 
-// One block per (sequence, row, query head); four warps take every fourth
-// position, a lane holds HD / 32 dims; the warps' results are merged at the end.
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) kv_attn_simple_kernel(const __grid_constant__ KvView c,
-                                                             const T* __restrict__ q, int64_t ldq,
-                                                             T* __restrict__ out, int64_t ldo,
-                                                             float* __restrict__ lse, int64_t max_len, int n_heads,
-                                                             float scale) {
-    constexpr int D = HD / 32;
-    __shared__ float sm[4], sl[4], so[4][HD];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t u = blockIdx.x;
-    const int head = (int)(u % n_heads);
-    u /= n_heads;
-    const int i = (int)(u % c.max_rows), s = (int)(u / c.max_rows);
+struct AttnCall {
+    const void* q;
+    void* out;
+    float* lse;
+    int* counters;
+    float* part;
+    int64_t ldq, ldo, max_len;
+    int n_heads, group;
+    int tiles;                              // blocks' row tiles of a (sequence, key/value head)
+    int splits, chunk;                      // runs of `chunk` pages
+    int prow;                               // rows of a partial result
+    int64_t slot;                           // its floats: the rows' sums, maxima and sums of p
+    float qk;                               // scale * log2 e
+};
+
+template <int HD, int RG>
+struct AttnShape {
+    static constexpr int TS = RG == 4 ? 2 : 4;              // warps over a page's tokens
+    static constexpr int NW = RG * TS;                      // consumer warps
+    static constexpr int THREADS = 32 * NW + 32;
+    static constexpr int TILE = KV_PAGE * HD;               // bytes of a K or V tile
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int STAGES = HD == 128 ? 4 : 6;
+    static constexpr int ROWS = 16 * RG;
+    // ring, then barriers (16 B each stage), exponents, per-warp statistics, flags
+    static constexpr int BAR = STAGES * STAGE;
+    static constexpr int EXPS = BAR + 16 * STAGES;
+    static constexpr int STAT = EXPS + 8 * STAGES;
+    static constexpr int FLAGS = STAT + 2 * 4 * TS * ROWS;
+    static constexpr int SMEM = FLAGS + 16;
+    static_assert(TS * ROWS * HD * 4 <= BAR, "the joined sums reuse the ring");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// expected bytes without an arrival
+__device__ __forceinline__ void mbar_expect_only(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// what rounding (a, b) to fp16 left
+__device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return half2_bits(a - f.x, b - f.y);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ int scale_exp(float s) {
+    const int e = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
+    return e < KV_MIN_EXP ? KV_MIN_EXP : (e > KV_MAX_EXP ? KV_MAX_EXP : e);
+}
+// 2^e with e clamped to the normal range
+__device__ __forceinline__ float pow2_clamped(int e) { return kv_pow2(e < -126 ? -126 : (e > 127 ? 127 : e)); }
+
+// 16 consecutive elements
+__device__ __forceinline__ void load16_f(const float* p, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 a = reinterpret_cast<const float4*>(p)[i];
+        v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
+    }
+}
+__device__ __forceinline__ void load16_f(const bf16* p, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 w = reinterpret_cast<const uint4*>(p)[i];
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
+            v[8 * i + 2 * e] = f.x;
+            v[8 * i + 2 * e + 1] = f.y;
+        }
+    }
+}
+
+template <typename T, int HD, int RG>
+__global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(const __grid_constant__ KvView c,
+                                                                             const __grid_constant__ AttnCall a) {
+    using S = AttnShape<HD, RG>;
+    constexpr bool TWO = sizeof(T) == 4;                    // q and p as two fp16 parts
+    constexpr int NP = TWO ? 2 : 1;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = tcx::smem_u32(smem);
+    int* exps = reinterpret_cast<int*>(smem + S::EXPS);     // per stage: K's and V's exponent
+    float* st_m = reinterpret_cast<float*>(smem + S::STAT);
+    float* st_l = st_m + S::TS * S::ROWS;
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + S::FLAGS);   // abort, bad page, last, never set
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto full = [&](int i) { return sbase + S::BAR + 16 * i; };
+    auto empty = [&](int i) { return sbase + S::BAR + 16 * i + 8; };
+
+    const int split = (int)(blockIdx.x % a.splits);
+    const int unit = (int)(blockIdx.x / a.splits);          // (sequence, key/value head, row tile)
+    const int tile = unit % a.tiles;
+    const int h = unit / a.tiles % c.n_kv;
+    const int s = unit / a.tiles / c.n_kv;
+    const int page0 = split * a.chunk;
+    // the producer's first page ids, asked for before the length is known
+    int id = -1;
+    if (warp == S::NW && lane < a.chunk && page0 + lane < c.max_pages)
+        id = c.table[(int64_t)s * c.max_pages + page0 + lane];
+
     SeqRows r;
-    bool ok = kv_seq(c, s, max_len, r);
-    const int64_t r0 = r.row0 < 0 ? 0 : r.row0;
-    if (!ok) {
-        // rows of a bad sequence that exist get NaN (from the block of its row 0)
-        if (i == 0)
-            for (int64_t x = r0; x < (int64_t)r.row0 + r.n && x < c.n_rows; ++x) {
+    const bool ok = kv_seq(c, s, a.max_len, r);
+    const T* q = static_cast<const T*>(a.q);
+    T* out = static_cast<T*>(a.out);
+    if (!ok || r.len == 0) {
+        // rows without positions: zero (or NaN: a bad sequence), from one block of each head
+        if (split == 0 && tile == 0) {
+            const float v = ok ? 0.f : NAN;
+            const int64_t r1 = (int64_t)r.row0 + r.n < c.n_rows ? (int64_t)r.row0 + r.n : c.n_rows;
+            for (int64_t x = r.row0 < 0 ? 0 : r.row0; x < r1; ++x) {
                 const int64_t y = kv_row(c, x);
-                for (int d = threadIdx.x; d < HD; d += 128) out[y * ldo + head * HD + d] = from_f<T>(NAN);
-                if (lse && threadIdx.x == 0) lse[y * n_heads + head] = NAN;
+                for (int d = threadIdx.x; d < a.group * HD; d += S::THREADS) out[y * a.ldo + h * a.group * HD + d] = from_f<T>(v);
+                for (int d = threadIdx.x; a.lse && d < a.group; d += S::THREADS)
+                    a.lse[y * a.n_heads + h * a.group + d] = ok ? -INFINITY : NAN;
+            }
+        }
+        return;
+    }
+    const int pair0 = tile * S::ROWS;                       // first (row, head) pair of the tile
+    const int pairs = r.n * a.group;
+    if (pair0 >= pairs) return;
+    const int before = r.len - r.n;                         // positions before the sequence's rows
+    const int pair1 = pair0 + S::ROWS < pairs ? pair0 + S::ROWS : pairs;
+    const int lim_lo = before + pair0 / a.group + 1;        // positions that the tile's first row sees
+    const int lim_hi = before + (pair1 - 1) / a.group + 1;  // .. and its last
+    const int pages = (lim_hi + KV_PAGE - 1) / KV_PAGE;
+    const int nsplit = (pages + a.chunk - 1) / a.chunk;
+    if (split >= nsplit) return;
+    const int np = pages - page0 < a.chunk ? pages - page0 : a.chunk;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            tcx::mbar_init(full(i), 1);
+            tcx::mbar_init(empty(i), S::NW);
+        }
+        flags[0] = flags[1] = flags[2] = flags[3] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+
+    float o[HD / 8][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const int g = lane >> 2, t = lane & 3;
+    const int rg = warp / S::TS, ts = warp % S::TS;         // consumers: row group, token slice
+    if (warp == S::NW) {
+        // ---- producer
+        bool go = true;
+        for (int i0 = 0; i0 < np && go; i0 += 32) {
+            const int mine = i0 + lane;
+            if (i0 > 0 && mine < np) id = c.table[(int64_t)s * c.max_pages + page0 + mine];
+            bool good = true;
+            if (mine < np && (id < 0 || id >= c.n_pages)) {
+                raise_status(c.status, ST_RANGE);
+                good = false;
+                id = 0;                                     // a page that exists stands in; the rows become NaN
+            }
+            if (__any_sync(0xffffffffu, !good) && lane == 0) flags[1] = 1;
+            const int64_t at = (int64_t)(mine < np ? id : 0) * c.n_kv + h;
+            int ek = 0, ev = 0;
+            const int n = np - i0 < 32 ? np - i0 : 32;
+            bool have = false;
+            for (int i = 0; i < n; ++i) {
+                const int it = i0 + i, stage = it % S::STAGES;
+                const int64_t tile_at = __shfl_sync(0xffffffffu, at, i);
+                const int left = lim_hi - (page0 + it) * KV_PAGE;               // tokens of the page that count
+                const int tok = left < KV_PAGE ? left : KV_PAGE;
+                if (it >= S::STAGES) {
+                    if (lane == 0) go = tcx::mbar_wait(empty(stage), (it / S::STAGES - 1) & 1, flags);
+                    go = __shfl_sync(0xffffffffu, (int)go, 0);
+                    if (!go) {
+                        if (lane == 0) {
+                            raise_status(c.status, ST_TIMEOUT);
+                            flags[0] = 1;
+                        }
+                        break;
+                    }
+                }
+                if (lane == 0) {
+                    const uint32_t kb = tok * HD, vb = (tok + 3) / 4 * 4 * HD;
+                    mbar_expect_only(full(stage), kb + vb);
+                    bulk_load(sbase + stage * S::STAGE, c.k + tile_at * S::TILE, kb, full(stage));
+                    bulk_load(sbase + stage * S::STAGE + S::TILE, c.v + tile_at * S::TILE, vb, full(stage));
+                }
+                if (!have && (i + 1 == S::STAGES || i + 1 == n)) {
+                    // the scales of these pages, read behind the first copies
+                    if (mine < np) {
+                        ek = scale_exp(c.ks[at]);
+                        ev = scale_exp(c.vs[at]);
+                    }
+                    have = true;
+                    for (int j = 0; j <= i; ++j) {
+                        const int k_ = __shfl_sync(0xffffffffu, ek, j), v_ = __shfl_sync(0xffffffffu, ev, j);
+                        if (lane == 0) {
+                            exps[2 * ((i0 + j) % S::STAGES)] = k_;
+                            exps[2 * ((i0 + j) % S::STAGES) + 1] = v_;
+                            tcx::mbar_arrive(full((i0 + j) % S::STAGES));
+                        }
+                    }
+                } else if (have) {
+                    const int k_ = __shfl_sync(0xffffffffu, ek, i), v_ = __shfl_sync(0xffffffffu, ev, i);
+                    if (lane == 0) {
+                        exps[2 * stage] = k_;
+                        exps[2 * stage + 1] = v_;
+                        tcx::mbar_arrive(full(stage));
+                    }
+                }
+            }
+        }
+    } else {
+        // ---- consumers: q fragments.  A thread's dims at K step (x, i) are
+        // 64 x + 16 t + 4 i + 0..3, the four bytes of a word of the key tile.
+        uint32_t qa[NP][HD / 16][4];
+        float qf[2];                                        // row factor: its power of two, or NaN
+        int qe[2];
+        int limit[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int pair = pair0 + rg * 16 + g + 8 * e;
+            const bool live = pair < pairs;
+            limit[e] = live ? before + pair / a.group + 1 : 0;
+            const T* src = live ? q + kv_row(c, (int64_t)r.row0 + pair / a.group) * a.ldq +
+                                      ((int64_t)h * a.group + pair % a.group) * HD
+                                : nullptr;
+            float x[HD / 64][16];
+            float big = 0.f;
+            bool fin = true;
+#pragma unroll
+            for (int y = 0; y < HD / 64; ++y) {
+                if (live) {
+                    load16_f(src + 64 * y + 16 * t, x[y]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[y][i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    big = fmaxf(big, fabsf(x[y][i]));
+                    fin &= fabsf(x[y][i]) <= FLT_MAX;
+                }
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const unsigned nf = __ballot_sync(0xffffffffu, !fin);
+            int ex = 0;
+            if (big > 0.f && big <= FLT_MAX) frexpf(big, &ex);
+            qe[e] = ex;
+            qf[e] = (nf >> (lane & 28)) & 15u ? NAN : 1.f;
+            // 2^-ex in two steps: it can lie outside fp32
+            const float f1 = kv_pow2(-ex / 2), f2 = kv_pow2(-ex - (-ex / 2));
+#pragma unroll
+            for (int y = 0; y < HD / 64; ++y)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const float u = x[y][4 * i + 2 * z] * f1 * f2, w = x[y][4 * i + 2 * z + 1] * f1 * f2;
+                        const uint32_t hi = half2_bits(u, w);
+                        qa[0][4 * y + i][2 * z + e] = hi;
+                        if (TWO) qa[NP - 1][4 * y + i][2 * z + e] = half2_rest(u, w, hi);
+                    }
+        }
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
+
+        for (int it = 0; it < np; ++it) {
+            const int stage = it % S::STAGES;
+            if (!tcx::mbar_wait(full(stage), (it / S::STAGES) & 1, flags)) {
+                if (lane == 0) {
+                    raise_status(c.status, ST_TIMEOUT);
+                    flags[0] = 1;
+                }
+                break;
+            }
+            const int ek = exps[2 * stage], ev = exps[2 * stage + 1];
+            const uint32_t kt = sbase + stage * S::STAGE, vt = kt + S::TILE;
+            const int pos0 = (page0 + it) * KV_PAGE;
+            const float fk[2] = {a.qk * qf[0] * pow2_clamped(qe[0] + ek), a.qk * qf[1] * pow2_clamped(qe[1] + ek)};
+            const float fev = (float)ev, inv_vs = kv_pow2(-ev);
+#pragma unroll
+            for (int sl = ts; sl < 4; sl += S::TS) {
+                const int p0 = pos0 + 16 * sl;              // the slice's first position
+                if (p0 >= lim_hi) break;
+                // S = q K^T over 16 tokens: column n of key tile j is token 4 (n / 2) + 2 j + n % 2
+                float z[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.f;
+                    const int tok = 16 * sl + 4 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+                    for (int y = 0; y < HD / 64; ++y) {
+                        const uint4 w = lds128(kt + kv_byte_k<HD>(tok, 64 * y + 16 * t));
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t b0 = e4m3x2_to_half2((uint16_t)ws[i]);
+                            const uint32_t b1 = e4m3x2_to_half2((uint16_t)(ws[i] >> 16));
+#pragma unroll
+                            for (int n = 0; n < NP; ++n) mma16816(z[j], qa[n][4 * y + i], b0, b1);
+                        }
+                    }
+                }
+                // in units of log2, with the value scale's exponent; masked past the row's own position
+                float mx[2] = {m[0], m[1]};
+                const bool edge = p0 + 16 > lim_lo;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int e = x >> 1;
+                        z[j][x] = fmaf(z[j][x], fk[e], fev);
+                        if (edge && p0 + 4 * t + 2 * j + (x & 1) >= limit[e]) z[j][x] = -INFINITY;
+                        mx[e] = fmaxf(mx[e], z[j][x]);
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                }
+                if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        f[e] = mx[e] == -INFINITY ? 1.f : ex2(m[e] - mx[e]);
+                        m[e] = mx[e];
+                        l[e] *= f[e];
+                    }
+#pragma unroll
+                    for (int j = 0; j < HD / 8; ++j) {
+                        o[j][0] *= f[0]; o[j][1] *= f[0];
+                        o[j][2] *= f[1]; o[j][3] *= f[1];
+                    }
+                }
+                const float base[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - P_SHIFT,
+                                       (m[1] == -INFINITY ? 0.f : m[1]) - P_SHIFT};
+                float add[2] = {0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        z[j][x] = ex2(z[j][x] - base[x >> 1]);
+                        add[x >> 1] += z[j][x];
+                    }
+                l[0] = fmaf(add[0], inv_vs, l[0]);
+                l[1] = fmaf(add[1], inv_vs, l[1]);
+                uint32_t p[NP][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t hi = half2_bits(z[j][2 * e], z[j][2 * e + 1]);
+                        p[0][2 * j + e] = hi;
+                        if (TWO) p[NP - 1][2 * j + e] = half2_rest(z[j][2 * e], z[j][2 * e + 1], hi);
+                    }
+                // bytes of tokens behind the end can be anything, NaN among them: 0 stands in
+                const int valid = lim_hi - (p0 + 4 * t);
+                // A NaN among the values of the newest tokens must not reach the
+                // rows before it through 0 * NaN: the product takes 0 for it, and
+                // the rows that do see it are found by a second product.
+                const bool ragged = edge && lim_lo < lim_hi;
+                const uint32_t keep = valid >= 4 ? 0xffffffffu : (valid <= 0 ? 0u : (1u << (8 * valid)) - 1u);
+                // O += P V: dim 32 x + 4 n + e is column n of tile 4 x + e
+#pragma unroll
+                for (int x = 0; x < HD / 32; ++x) {
+                    const uint4 w = lds128(vt + (4 * sl + t) * 4 * HD + (((8 * x + g) ^ (2 * t)) << 4));
+                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t b = edge ? ws[e] & keep : ws[e];
+                        if (ragged) {
+                            const uint32_t nan = __vcmpeq4(b & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            b &= ~nan;
+                            if (__any_sync(0xffffffffu, nan != 0)) {
+                                uint32_t see[4];
+#pragma unroll
+                                for (int q2 = 0; q2 < 4; ++q2) {    // 1.0 where row q2 % 2 sees tokens 2 (q2 / 2) + 0, 1
+                                    const int left = limit[q2 & 1] - (p0 + 4 * t + (q2 & 2));
+                                    see[q2] = (left > 0 ? 0x3c00u : 0u) | (left > 1 ? 0x3c000000u : 0u);
+                                }
+                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816(hit, see, e4m3x2_to_half2((uint16_t)(nan & 0x3838u)),   // 0x38 is 1.0
+                                         e4m3x2_to_half2((uint16_t)((nan >> 16) & 0x3838u)));
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    if (hit[y] > 0.f) o[4 * x + e][y] = NAN;
+                            }
+                        }
+                        const uint32_t b0 = e4m3x2_to_half2((uint16_t)b);
+                        const uint32_t b1 = e4m3x2_to_half2((uint16_t)(b >> 16));
+#pragma unroll
+                        for (int n = 0; n < NP; ++n) mma16816(o[4 * x + e], p[n], b0, b1);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tcx::mbar_arrive(empty(stage));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (t == 0) {
+                st_m[ts * S::ROWS + rg * 16 + g + 8 * e] = m[e];
+                st_l[ts * S::ROWS + rg * 16 + g + 8 * e] = l[e];
+            }
+        }
+    }
+    __syncthreads();                                        // every page is used: the ring's memory is free
+    if (flags[0]) {
+        // a wait gave up: let the copies that may still be in flight land
+        // before the block's memory goes to another (again bounded), write nothing
+        if (threadIdx.x == 0)
+            for (int i = 0; i < S::STAGES && i < np; ++i) {
+                const int last = (np - 1 - i) / S::STAGES * S::STAGES + i;
+                tcx::mbar_wait(full(i), (last / S::STAGES) & 1, flags + 3, 1000000);
             }
         return;
     }
-    if (i >= r.n) return;
-    const int64_t row = kv_row(c, (int64_t)r.row0 + i);
-    const int n = r.len ? r.len - r.n + i + 1 : 0;          // positions this row sees
-    const int h = head / (n_heads / c.n_kv);
-    float qv[D], o[D], m = -INFINITY, l = 0.f;
+    // ---- join the warps of a row group
+    float* so = reinterpret_cast<float*>(smem);             // [TS][ROWS][HD]
+    if (warp < S::NW) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-        qv[d] = to_f(q[row * ldq + head * HD + lane * D + d]) * (scale * LOG2E);
-        o[d] = 0.f;
-    }
-    for (int p = warp; p < n; p += 4) {
-        const int id = kv_page(c, s, p / KV_PAGE);
-        if (id < 0) { ok = false; continue; }
-        const int64_t t = (int64_t)id * c.n_kv + h;
-        const uint8_t* kt = c.k + t * (KV_PAGE * HD);
-        const uint8_t* vt = c.v + t * (KV_PAGE * HD);
-        const int j = p % KV_PAGE;
-        float z = 0.f;
+        for (int e = 0; e < 2; ++e) {
+            const int row = rg * 16 + g + 8 * e;
+            float mm = -INFINITY;
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            float f[4];
-            e4m3x4_to_float4(kt[kv_byte_k<HD>(j, lane * D + d)], f);
-            z += qv[d] * f[0];
+            for (int w = 0; w < S::TS; ++w) mm = fmaxf(mm, st_m[w * S::ROWS + row]);
+            const float f = m[e] == -INFINITY ? (mm == -INFINITY ? 1.f : 0.f) : ex2(m[e] - mm);
+            float* dst = so + (ts * S::ROWS + row) * HD + 8 * t;
+#pragma unroll
+            for (int x = 0; x < HD / 32; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    *reinterpret_cast<float4*>(dst + 32 * x + 4 * y) =
+                        make_float4(o[4 * x][2 * e + y] * f, o[4 * x + 1][2 * e + y] * f, o[4 * x + 2][2 * e + y] * f,
+                                    o[4 * x + 3][2 * e + y] * f);
         }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-        z *= c.ks[t];
-        const float mn = fmaxf(m, z);
-        const float a = mn == -INFINITY ? 0.f : mn;
-        const float f0 = exp2f(m - a), w = exp2f(z - a), wv = w * c.vs[t];
-        l = l * f0 + w;
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            float f[4];
-            e4m3x4_to_float4(vt[kv_byte_v<HD>(j, lane * D + d)], f);
-            o[d] = o[d] * f0 + wv * f[0];
-        }
-        m = mn;
     }
-    if (!ok) l = NAN;
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-#pragma unroll
-    for (int d = 0; d < D; ++d) so[warp][lane * D + d] = o[d];
     __syncthreads();
-    const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    const float A = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int w = 0; w < 4; ++w) L += sl[w] * exp2f(sm[w] - A);
-    for (int d = threadIdx.x; d < HD; d += 128) {
-        float x = 0.f;
-        for (int w = 0; w < 4; ++w) x += so[w][d] * exp2f(sm[w] - A);
-        out[row * ldo + head * HD + d] = from_f<T>(n ? x / L : 0.f);
+    const int rows = pair1 - pair0;
+    float* part = a.part + (int64_t)blockIdx.x * a.slot;
+    const bool bad = flags[1] != 0;
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += S::THREADS) {
+        const int row = i / (HD / 4), d = i % (HD / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int w = 0; w < S::TS; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(so + (w * S::ROWS + row) * HD + d);
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+            mm = fmaxf(mm, st_m[w * S::ROWS + row]);
+        }
+#pragma unroll
+        for (int w = 0; w < S::TS; ++w) {
+            const float mw = st_m[w * S::ROWS + row];
+            ll += st_l[w * S::ROWS + row] * (mw == -INFINITY ? 1.f : ex2(mw - mm));
+        }
+        if (bad) ll = NAN;
+        if (nsplit > 1) {
+            *reinterpret_cast<float4*>(part + row * HD + d) = v;
+            if (d == 0) {
+                part[a.prow * HD + row] = mm;
+                part[a.prow * (HD + 1) + row] = ll;
+            }
+        } else {
+            const int pair = pair0 + row;
+            const int64_t y = kv_row(c, (int64_t)r.row0 + pair / a.group);
+            const int head = h * a.group + pair % a.group;
+            const float inv = 1.f / ll;
+            const float w[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+            store4_f(out + y * a.ldo + (int64_t)head * HD + d, w);
+            if (d == 0 && a.lse) a.lse[y * a.n_heads + head] = ((mm == -INFINITY ? 0.f : mm) - P_SHIFT + log2f(ll)) * LN2;
+        }
     }
-    if (lse && threadIdx.x == 0) lse[row * n_heads + head] = n ? (A + log2f(L)) * LN2 : -INFINITY;
+    if (nsplit == 1) return;
+    // ---- the last block of the unit to arrive joins its runs
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        const int arrived = atomicAdd(a.counters + unit, 1);
+        flags[2] = arrived == nsplit - 1;
+        if (arrived == nsplit - 1) a.counters[unit] = 0;    // as the next call finds it
+        __threadfence();
+    }
+    __syncthreads();
+    if (!flags[2]) return;
+    const float* p0 = a.part + (int64_t)unit * a.splits * a.slot;
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += S::THREADS) {
+        const int row = i / (HD / 4), d = i % (HD / 4) * 4;
+        float mm = -INFINITY;
+        for (int x = 0; x < nsplit; ++x) mm = fmaxf(mm, __ldcg(p0 + x * a.slot + a.prow * HD + row));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float ll = 0.f;
+#pragma unroll 8
+        for (int x = 0; x < nsplit; ++x) {
+            const float* px = p0 + x * a.slot;
+            const float mw = __ldcg(px + a.prow * HD + row);
+            const float f = mw == -INFINITY ? 1.f : ex2(mw - mm);   // 1: nothing but 0 or NaN stands there
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(px + row * HD + d));
+            ll = fmaf(__ldcg(px + a.prow * (HD + 1) + row), f, ll);
+            v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
+        }
+        const int pair = pair0 + row;
+        const int64_t y = kv_row(c, (int64_t)r.row0 + pair / a.group);
+        const int head = h * a.group + pair % a.group;
+        const float inv = 1.f / ll;
+        const float w[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+        store4_f(out + y * a.ldo + (int64_t)head * HD + d, w);
+        if (d == 0 && a.lse) a.lse[y * a.n_heads + head] = ((mm == -INFINITY ? 0.f : mm) - P_SHIFT + log2f(ll)) * LN2;
+    }
 }
 
+constexpr int MAX_UNITS_SPLIT = MLORA_KV_COUNTER_BYTES / 4;   // a counter for each unit
+
+template <typename T, int HD, int RG>
+cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
+    using S = AttnShape<HD, RG>;
+    AttnCall k;
+    k.q = a.q; k.out = a.out; k.lse = a.lse; k.ldq = a.ldq; k.ldo = a.ldo; k.max_len = a.max_len;
+    k.counters = static_cast<int*>(a.workspace);
+    k.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + MLORA_KV_COUNTER_BYTES);
+    k.n_heads = a.n_heads; k.group = a.n_heads / c.n_kv;
+    k.qk = a.scale * LOG2E;
+    const int64_t pairs = (int64_t)c.max_rows * k.group;
+    const int64_t tiles = (pairs + S::ROWS - 1) / S::ROWS;
+    k.prow = (int)(pairs < S::ROWS ? pairs : S::ROWS);
+    k.slot = ((int64_t)k.prow * (HD + 2) + 3) / 4 * 4;      // 16-byte aligned
+    const int64_t units = tiles * c.n_kv * c.n_seqs;
+    const int64_t cap = (int64_t)c.max_pages * KV_PAGE;
+    const int64_t longest = a.max_len < cap ? a.max_len : cap;
+    const int64_t pages = longest > 0 ? (longest + KV_PAGE - 1) / KV_PAGE : 1;
+    // Runs of pages: short enough that the blocks fill the GPU (about BLOCKS_SM
+    // on each SM) and that a long sequence is no tail of the launch, long
+    // enough that a block's start and the join stay small beside it.
+    int64_t chunk = pages;
+    if (units <= MAX_UNITS_SPLIT) {
+        const int64_t want = (int64_t)KV_SPLIT_BLOCKS;
+        const int64_t per_unit = (want + units - 1) / units;
+        chunk = (pages + per_unit - 1) / per_unit;
+        if (chunk > KV_LONG_RUN) chunk = KV_LONG_RUN;
+        if (chunk < KV_SHORT_RUN) chunk = KV_SHORT_RUN;
+        const int64_t slots = (a.workspace_bytes - MLORA_KV_COUNTER_BYTES) / (k.slot * 4);
+        const int64_t most = slots / units;                 // runs of a unit that the workspace holds
+        if (most < 2) chunk = pages;
+        else if ((pages + chunk - 1) / chunk > most) chunk = (pages + most - 1) / most;
+    }
+    k.tiles = (int)tiles;
+    k.chunk = (int)(chunk < pages ? chunk : pages);
+    k.splits = (int)((pages + k.chunk - 1) / k.chunk);
+    const int64_t blocks = units * k.splits;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    // once a device: the attribute stays with the function
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kv_attn_kernel<T, HD, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
+    kv_attn_kernel<T, HD, RG><<<(unsigned)blocks, S::THREADS, S::SMEM, s>>>(c, k);
+    return cudaGetLastError();
+}
+
+// 16 pairs a block where one row's group fits; more row groups share each page
+// tile (its reads and its place in shared memory) where a sequence has more.
 template <typename T, int HD>
-void attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
-    const int64_t blocks = (int64_t)c.n_seqs * c.max_rows * a.n_heads;
-    kv_attn_simple_kernel<T, HD><<<(unsigned)blocks, 128, 0, s>>>(c, static_cast<const T*>(a.q), a.ldq,
-                                                                  static_cast<T*>(a.out), a.ldo, a.lse, a.max_len,
-                                                                  a.n_heads, a.scale);
+cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
+    const int64_t pairs = (int64_t)c.max_rows * (a.n_heads / c.n_kv);
+    if (pairs <= 16) return attn_t<T, HD, 1>(c, a, s);
+    if (pairs <= 32) return attn_t<T, HD, 2>(c, a, s);
+    return attn_t<T, HD, 4>(c, a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s) {
-    if (dtype == MLORA_BF16) (head_dim == 64 ? attn_t<bf16, 64> : attn_t<bf16, 128>)(c, a, s);
-    else (head_dim == 64 ? attn_t<float, 64> : attn_t<float, 128>)(c, a, s);
-    return cudaGetLastError();
+    if (dtype == MLORA_BF16) return head_dim == 64 ? attn_rows<bf16, 64>(c, a, s) : attn_rows<bf16, 128>(c, a, s);
+    return head_dim == 64 ? attn_rows<float, 64>(c, a, s) : attn_rows<float, 128>(c, a, s);
 }
 
 }  // namespace mlk

@@ -199,9 +199,11 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
 
 
 def kv_check_status(cache: KvCache, stream=None) -> int:
-    """Synchronise, return and clear the cache's status: 0, or -2 (E_RANGE)."""
+    """Synchronise, return and clear the cache's status: 0, -2 (E_RANGE), or -5
+    (E_TIMEOUT: a bounded device wait gave up; zero the workspace before its
+    next use)."""
     import torch
     (stream or torch.cuda.current_stream()).synchronize()
     bad = int(cache.status.item())
     cache.status.zero_()
-    return -2 if bad else 0
+    return -5 if bad & 2 else -2 if bad & 1 else 0

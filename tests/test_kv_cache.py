@@ -417,6 +417,26 @@ def test_attention_nan_and_infinity(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [9, 70])
+def test_nan_of_a_later_row_does_not_reach_the_rows_before_it(n, dtype):
+    """a key and a value that are NaN at the same call's later rows: masked for the earlier ones"""
+    torch = _torch()
+    st = Setup([30 + n, 30 + n], 1, 128, seed=n)
+    x = st.rows(60 + 2 * n, "bf16").float()
+    x[30 + n - 3, 1, [0, 77]] = math.nan                   # sequence 0: values of its third newest row
+    x[60 + 2 * n - 2, 0, 5] = math.nan                     # sequence 1: a key of its second newest row
+    st.append([30 + n, 30 + n], x=x.bfloat16())
+    q = torch.randn(2 * n, 3, 128, device="cuda")
+    q = q if dtype == "fp32" else q.bfloat16()
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, 30 + n, row_off=st.off([n, n]), max_rows=n)
+    a = torch.isnan(out[:n])
+    assert not a[:n - 3].any() and a[n - 3:][:, :, [0, 77]].all() and int(a.sum()) == 3 * 3 * 2
+    assert torch.isfinite(lse[:n]).all()
+    assert torch.isfinite(out[n:-2]).all() and torch.isnan(out[-2:]).all() and torch.isnan(lse[-2:]).all()
+
+
+@pytest.mark.gpu
 def test_empty_slots_and_rows_behind_the_end():
     torch = _torch()
     st = Setup([64, 0, 10, 0], 2, 128, seed=6)
