@@ -116,7 +116,8 @@ int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype
  * Sums and softmax statistics are fp32; scores are formed from q's own values
  * and the stored bytes, the probabilities enter the second product as fp16
  * (relative rounding 2^-11, below bf16's own 2^-8), and on fp32 as two fp16
- * parts (2^-22), as q does.  The result of a row does not depend on the other
+ * parts (2^-22), as q does; a probability below 2^-26 of its row's largest has
+ * an absolute error of up to 2^-37 of that largest instead.  The result of a row does not depend on the other
  * sequences' contents, and repeats bit for bit.
  * workspace: DEVICE, 16-byte aligned, at least MLORA_KV_COUNTER_BYTES, whose
  * first MLORA_KV_COUNTER_BYTES were zeroed before its first use (every call

@@ -23,17 +23,21 @@
 //  * The page's value scale 2^ev goes into the exponent of the probability,
 //    p' = exp2(s log2 e + ev - m') with m' the running maximum of s log2 e + ev,
 //    so pages of any scale add into one accumulator, the largest p' v8 sets the
-//    precision, and l += p' 2^-ev is what the definition sums.  p' is held at
-//    2^12 times its value, so that its fp16 rounding stays relative (2^-11)
-//    down to 2^-26 of the row's largest; on fp32 it is split like q.
-//  * Warps of a block take different 16-token slices of a page (each with a
-//    running maximum and sum of its own, joined at the end), so nothing but
-//    the ring's barriers is shared in the loop.
+//    precision, and l += p' 2^-ev is what the definition sums.  m' follows the
+//    scores only when one passes it by 2^3 (the sums are then rescaled); p' is
+//    held at 2^12 times its value, so that it stays within fp16 and its rounding
+//    relative (2^-11) down to 2^-26 of the reference (absolute 2^-37 of it
+//    below that); on fp32 it is split like q.
+//  * Warps of a block take different halves of a page and, with one or two row
+//    groups, every other page, 32 tokens at a step (four independent chains of
+//    products); each has a running maximum and sum of its own, joined at the
+//    end, so nothing but the ring's barriers is shared in the loop.
 //  * Long sequences are cut into runs of pages (flash-style split); a block
 //    leaves its rows' unnormalised sums, maximum and sum in the workspace, and
 //    the last block of the sequence and head to arrive joins them in order of
 //    the runs, so the result does not depend on who was last.
 #include <atomic>
+#include <type_traits>
 
 #include "kv_common.cuh"
 #include "tc_ptx.cuh"
@@ -44,7 +48,8 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value
+constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
+constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
 // Runs of pages of a split (see attn_t).
 constexpr int KV_SPLIT_BLOCKS = 456;
 constexpr int KV_LONG_RUN = 16, KV_SHORT_RUN = 2;
@@ -64,22 +69,27 @@ struct AttnCall {
     float qk;                               // scale * log2 e
 };
 
-template <int HD, int RG>
+template <typename T, int HD, int RG>
 struct AttnShape {
-    static constexpr int TS = RG == 4 ? 2 : 4;              // warps over a page's tokens
-    static constexpr int NW = RG * TS;                      // consumer warps
+    static constexpr int NP = sizeof(T) == 4 ? 2 : 1;       // fp16 parts of q and of p
+    static constexpr int PG = RG == 4 ? 1 : 2;              // pages in work at once
+    static constexpr int WG = 2 * PG;                       // warps of a row group: page parity x half of the page
+    static constexpr int NW = RG * WG;                      // consumer warps
     static constexpr int THREADS = 32 * NW + 32;
     static constexpr int TILE = KV_PAGE * HD;               // bytes of a K or V tile
     static constexpr int STAGE = 2 * TILE;
     static constexpr int STAGES = HD == 128 ? 4 : 6;
     static constexpr int ROWS = 16 * RG;
-    // ring, then barriers (16 B each stage), exponents, per-warp statistics, flags
-    static constexpr int BAR = STAGES * STAGE;
+    static constexpr int BLOCKS_SM = RG == 1 ? 3 : 1;
+    // ring, then q's fragments, barriers (16 B each stage), exponents, per-warp statistics, flags
+    static constexpr int QFRAG = STAGES * STAGE;
+    static constexpr int BAR = QFRAG + RG * NP * (HD / 16) * 32 * 16;
     static constexpr int EXPS = BAR + 16 * STAGES;
     static constexpr int STAT = EXPS + 8 * STAGES;
-    static constexpr int FLAGS = STAT + 2 * 4 * TS * ROWS;
+    static constexpr int FLAGS = STAT + 2 * 4 * WG * ROWS;
     static constexpr int SMEM = FLAGS + 16;
-    static_assert(TS * ROWS * HD * 4 <= BAR, "the joined sums reuse the ring");
+    static_assert(WG * ROWS * HD * 4 <= QFRAG, "the joined sums reuse the ring");
+    static_assert(STAGES % PG == 0, "a stage keeps its page parity");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -147,16 +157,15 @@ __device__ __forceinline__ void load16_f(const bf16* p, float (&v)[16]) {
 }
 
 template <typename T, int HD, int RG>
-__global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(const __grid_constant__ KvView c,
-                                                                             const __grid_constant__ AttnCall a) {
-    using S = AttnShape<HD, RG>;
-    constexpr bool TWO = sizeof(T) == 4;                    // q and p as two fp16 parts
-    constexpr int NP = TWO ? 2 : 1;
+__global__ void __launch_bounds__(AttnShape<T, HD, RG>::THREADS, AttnShape<T, HD, RG>::BLOCKS_SM)
+    kv_attn_kernel(const __grid_constant__ KvView c, const __grid_constant__ AttnCall a) {
+    using S = AttnShape<T, HD, RG>;
+    constexpr int NP = S::NP;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = tcx::smem_u32(smem);
     int* exps = reinterpret_cast<int*>(smem + S::EXPS);     // per stage: K's and V's exponent
     float* st_m = reinterpret_cast<float*>(smem + S::STAT);
-    float* st_l = st_m + S::TS * S::ROWS;
+    float* st_l = st_m + S::WG * S::ROWS;
     volatile int* flags = reinterpret_cast<volatile int*>(smem + S::FLAGS);   // abort, bad page, last, never set
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto full = [&](int i) { return sbase + S::BAR + 16 * i; };
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(con
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             tcx::mbar_init(full(i), 1);
-            tcx::mbar_init(empty(i), S::NW);
+            tcx::mbar_init(empty(i), S::NW / S::PG);
         }
         flags[0] = flags[1] = flags[2] = flags[3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -216,7 +225,8 @@ __global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(con
     float o[HD / 8][4];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     const int g = lane >> 2, t = lane & 3;
-    const int rg = warp / S::TS, ts = warp % S::TS;         // consumers: row group, token slice
+    const int rg = warp / S::WG, wg = warp % S::WG;         // consumers: row group, place in it
+    const int half = wg & 1, pg = wg >> 1;                  // half of a page, page parity
     if (warp == S::NW) {
         // ---- producer
         bool go = true;
@@ -282,64 +292,77 @@ __global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(con
             }
         }
     } else {
-        // ---- consumers: q fragments.  A thread's dims at K step (x, i) are
-        // 64 x + 16 t + 4 i + 0..3, the four bytes of a word of the key tile.
-        uint32_t qa[NP][HD / 16][4];
-        float qf[2];                                        // row factor: its power of two, or NaN
-        int qe[2];
-        int limit[2];
+        // ---- consumers: q fragments, written by the group's first warps and read
+        // from shared memory at each step (the registers go to the sums).  A
+        // thread's dims at K step (y, i) are 64 y + 16 t + 4 i + 0..3, the four
+        // bytes of a word of the key tile.
+        uint4* qs = reinterpret_cast<uint4*>(smem + S::QFRAG) + rg * NP * (HD / 16) * 32 + lane;
+        float qf[2];                                        // scale * log2 e, or NaN where q is not finite
+        int qe[2];                                          // exponent of the row's largest magnitude
+        int limit[2];                                       // positions the row sees
+        {
+            uint32_t qa[NP][HD / 16][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int pair = pair0 + rg * 16 + g + 8 * e;
-            const bool live = pair < pairs;
-            limit[e] = live ? before + pair / a.group + 1 : 0;
-            const T* src = live ? q + kv_row(c, (int64_t)r.row0 + pair / a.group) * a.ldq +
-                                      ((int64_t)h * a.group + pair % a.group) * HD
-                                : nullptr;
-            float x[HD / 64][16];
-            float big = 0.f;
-            bool fin = true;
+            for (int e = 0; e < 2; ++e) {
+                const int pair = pair0 + rg * 16 + g + 8 * e;
+                const bool live = pair < pairs;
+                limit[e] = live ? before + pair / a.group + 1 : 0;
+                const T* src = live ? q + kv_row(c, (int64_t)r.row0 + pair / a.group) * a.ldq +
+                                          ((int64_t)h * a.group + pair % a.group) * HD
+                                    : nullptr;
+                float x[HD / 64][16];
+                float big = 0.f;
+                bool fin = true;
 #pragma unroll
-            for (int y = 0; y < HD / 64; ++y) {
-                if (live) {
-                    load16_f(src + 64 * y + 16 * t, x[y]);
-                } else {
+                for (int y = 0; y < HD / 64; ++y) {
+                    if (live) {
+                        load16_f(src + 64 * y + 16 * t, x[y]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[y][i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    big = fmaxf(big, fabsf(x[y][i]));
-                    fin &= fabsf(x[y][i]) <= FLT_MAX;
-                }
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            const unsigned nf = __ballot_sync(0xffffffffu, !fin);
-            int ex = 0;
-            if (big > 0.f && big <= FLT_MAX) frexpf(big, &ex);
-            qe[e] = ex;
-            qf[e] = (nf >> (lane & 28)) & 15u ? NAN : 1.f;
-            // 2^-ex in two steps: it can lie outside fp32
-            const float f1 = kv_pow2(-ex / 2), f2 = kv_pow2(-ex - (-ex / 2));
-#pragma unroll
-            for (int y = 0; y < HD / 64; ++y)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const float u = x[y][4 * i + 2 * z] * f1 * f2, w = x[y][4 * i + 2 * z + 1] * f1 * f2;
-                        const uint32_t hi = half2_bits(u, w);
-                        qa[0][4 * y + i][2 * z + e] = hi;
-                        if (TWO) qa[NP - 1][4 * y + i][2 * z + e] = half2_rest(u, w, hi);
+                        for (int i = 0; i < 16; ++i) x[y][i] = 0.f;
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        big = fmaxf(big, fabsf(x[y][i]));
+                        fin &= fabsf(x[y][i]) <= FLT_MAX;
+                    }
+                }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                const unsigned nf = __ballot_sync(0xffffffffu, !fin);
+                int ex = 0;
+                if (big > 0.f && big <= FLT_MAX) frexpf(big, &ex);
+                qe[e] = ex;
+                qf[e] = (nf >> (lane & 28)) & 15u ? NAN : a.qk;
+                // 2^-ex in two steps: it can lie outside fp32
+                const float f1 = kv_pow2(-ex / 2), f2 = kv_pow2(-ex - (-ex / 2));
+#pragma unroll
+                for (int y = 0; y < HD / 64; ++y)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const float u = x[y][4 * i + 2 * z] * f1 * f2, w = x[y][4 * i + 2 * z + 1] * f1 * f2;
+                            const uint32_t hi = half2_bits(u, w);
+                            qa[0][4 * y + i][2 * z + e] = hi;
+                            if (NP == 2) qa[NP - 1][4 * y + i][2 * z + e] = half2_rest(u, w, hi);
+                        }
+            }
+            if (wg == 0) {
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k)
+                        qs[(n * (HD / 16) + k) * 32] = make_uint4(qa[n][k][0], qa[n][k][1], qa[n][k][2], qa[n][k][3]);
+            }
         }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * S::NW) : "memory");   // the consumers
 #pragma unroll
         for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
 
-        for (int it = 0; it < np; ++it) {
+        for (int it = pg; it < np; it += S::PG) {
             const int stage = it % S::STAGES;
             if (!tcx::mbar_wait(full(stage), (it / S::STAGES) & 1, flags)) {
                 if (lane == 0) {
@@ -350,124 +373,146 @@ __global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(con
             }
             const int ek = exps[2 * stage], ev = exps[2 * stage + 1];
             const uint32_t kt = sbase + stage * S::STAGE, vt = kt + S::TILE;
-            const int pos0 = (page0 + it) * KV_PAGE;
-            const float fk[2] = {a.qk * qf[0] * pow2_clamped(qe[0] + ek), a.qk * qf[1] * pow2_clamped(qe[1] + ek)};
+            const int p0 = (page0 + it) * KV_PAGE + 32 * half;      // the first of this warp's 32 positions
+            const float fk[2] = {qf[0] * pow2_clamped(qe[0] + ek), qf[1] * pow2_clamped(qe[1] + ek)};
             const float fev = (float)ev, inv_vs = kv_pow2(-ev);
+            // EDGE: some row does not see all 32 positions
+            auto step = [&](auto edge) {
+                constexpr bool EDGE = decltype(edge)::value;
+                // S = q K^T, 16 tokens a slice u: column n of key tile j is token 4 (n / 2) + 2 j + n % 2
+                float z[2][2][4];
 #pragma unroll
-            for (int sl = ts; sl < 4; sl += S::TS) {
-                const int p0 = pos0 + 16 * sl;              // the slice's first position
-                if (p0 >= lim_hi) break;
-                // S = q K^T over 16 tokens: column n of key tile j is token 4 (n / 2) + 2 j + n % 2
-                float z[2][4];
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.f;
-                    const int tok = 16 * sl + 4 * (g >> 1) + 2 * j + (g & 1);
+                    for (int j = 0; j < 2; ++j) z[u][j][0] = z[u][j][1] = z[u][j][2] = z[u][j][3] = 0.f;
 #pragma unroll
-                    for (int y = 0; y < HD / 64; ++y) {
-                        const uint4 w = lds128(kt + kv_byte_k<HD>(tok, 64 * y + 16 * t));
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                for (int y = 0; y < HD / 64; ++y) {
+                    uint4 w[2][2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t b0 = e4m3x2_to_half2((uint16_t)ws[i]);
-                            const uint32_t b1 = e4m3x2_to_half2((uint16_t)(ws[i] >> 16));
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
-                            for (int n = 0; n < NP; ++n) mma16816(z[j], qa[n][4 * y + i], b0, b1);
+                        for (int j = 0; j < 2; ++j)
+                            w[u][j] = lds128(kt + kv_byte_k<HD>(32 * half + 16 * u + 4 * (g >> 1) + 2 * j + (g & 1),
+                                                                64 * y + 16 * t));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t qa[NP][4];
+#pragma unroll
+                        for (int n = 0; n < NP; ++n) {
+                            const uint4 v = qs[(n * (HD / 16) + 4 * y + i) * 32];
+                            qa[n][0] = v.x; qa[n][1] = v.y; qa[n][2] = v.z; qa[n][3] = v.w;
+                        }
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t b = i == 0 ? w[u][j].x : i == 1 ? w[u][j].y : i == 2 ? w[u][j].z : w[u][j].w;
+                                const uint32_t b0 = e4m3x2_to_half2((uint16_t)b);
+                                const uint32_t b1 = e4m3x2_to_half2((uint16_t)(b >> 16));
+#pragma unroll
+                                for (int n = 0; n < NP; ++n) mma16816(z[u][j], qa[n], b0, b1);
+                            }
+                    }
+                }
+                // scores in units of log2, with the value scale's exponent; this lane's largest
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float s2 = fmaf(z[u][j][x], fk[x >> 1], fev);
+                            if (EDGE && p0 + 16 * u + 4 * t + 2 * j + (x & 1) >= limit[x >> 1]) s2 = -INFINITY;
+                            mx[x >> 1] = fmaxf(mx[x >> 1], s2);
+                        }
+                // the reference moves only when a score passes it by 2^M_SLACK: then p' stays below fp16's range
+                if (__any_sync(0xffffffffu, mx[0] > m[0] + M_SLACK || mx[1] > m[1] + M_SLACK)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                        mx[e] = fmaxf(mx[e], m[e]);
+                        const float f = mx[e] == -INFINITY ? 1.f : ex2(m[e] - mx[e]);
+                        m[e] = mx[e];
+                        l[e] *= f;
+#pragma unroll
+                        for (int j = 0; j < HD / 8; ++j) {
+                            o[j][2 * e] *= f;
+                            o[j][2 * e + 1] *= f;
                         }
                     }
                 }
-                // in units of log2, with the value scale's exponent; masked past the row's own position
-                float mx[2] = {m[0], m[1]};
-                const bool edge = p0 + 16 > lim_lo;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int e = x >> 1;
-                        z[j][x] = fmaf(z[j][x], fk[e], fev);
-                        if (edge && p0 + 4 * t + 2 * j + (x & 1) >= limit[e]) z[j][x] = -INFINITY;
-                        mx[e] = fmaxf(mx[e], z[j][x]);
-                    }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                }
-                if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-                    float f[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        f[e] = mx[e] == -INFINITY ? 1.f : ex2(m[e] - mx[e]);
-                        m[e] = mx[e];
-                        l[e] *= f[e];
-                    }
-#pragma unroll
-                    for (int j = 0; j < HD / 8; ++j) {
-                        o[j][0] *= f[0]; o[j][1] *= f[0];
-                        o[j][2] *= f[1]; o[j][3] *= f[1];
-                    }
-                }
-                const float base[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - P_SHIFT,
-                                       (m[1] == -INFINITY ? 0.f : m[1]) - P_SHIFT};
+                const float off[2] = {fev + P_SHIFT - (m[0] == -INFINITY ? 0.f : m[0]),
+                                      fev + P_SHIFT - (m[1] == -INFINITY ? 0.f : m[1])};
                 float add[2] = {0.f, 0.f};
+                uint32_t p[2][NP][4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        z[j][x] = ex2(z[j][x] - base[x >> 1]);
-                        add[x >> 1] += z[j][x];
+                    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float e2 = fmaf(z[u][j][x], fk[x >> 1], off[x >> 1]);
+                            if (EDGE && p0 + 16 * u + 4 * t + 2 * j + (x & 1) >= limit[x >> 1]) e2 = -INFINITY;
+                            z[u][j][x] = ex2(e2);
+                            add[x >> 1] += z[u][j][x];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t hi = half2_bits(z[u][j][2 * e], z[u][j][2 * e + 1]);
+                            p[u][0][2 * j + e] = hi;
+                            if (NP == 2) p[u][NP - 1][2 * j + e] = half2_rest(z[u][j][2 * e], z[u][j][2 * e + 1], hi);
+                        }
                     }
                 l[0] = fmaf(add[0], inv_vs, l[0]);
                 l[1] = fmaf(add[1], inv_vs, l[1]);
-                uint32_t p[NP][4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t hi = half2_bits(z[j][2 * e], z[j][2 * e + 1]);
-                        p[0][2 * j + e] = hi;
-                        if (TWO) p[NP - 1][2 * j + e] = half2_rest(z[j][2 * e], z[j][2 * e + 1], hi);
-                    }
-                // bytes of tokens behind the end can be anything, NaN among them: 0 stands in
-                const int valid = lim_hi - (p0 + 4 * t);
-                // A NaN among the values of the newest tokens must not reach the
-                // rows before it through 0 * NaN: the product takes 0 for it, and
-                // the rows that do see it are found by a second product.
-                const bool ragged = edge && lim_lo < lim_hi;
-                const uint32_t keep = valid >= 4 ? 0xffffffffu : (valid <= 0 ? 0u : (1u << (8 * valid)) - 1u);
                 // O += P V: dim 32 x + 4 n + e is column n of tile 4 x + e
 #pragma unroll
-                for (int x = 0; x < HD / 32; ++x) {
-                    const uint4 w = lds128(vt + (4 * sl + t) * 4 * HD + (((8 * x + g) ^ (2 * t)) << 4));
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                for (int u = 0; u < 2; ++u) {
+                    // bytes of tokens behind the end can be anything, NaN among them: 0 stands in.  A NaN
+                    // among the newest tokens' values must not reach the rows before it through 0 * NaN
+                    // either: the product takes 0 for it, and the rows that do see it are found by a
+                    // second product.
+                    const int first = p0 + 16 * u + 4 * t;  // of this lane's four tokens
+                    const int valid = lim_hi - first;
+                    const uint32_t keep = valid >= 4 ? 0xffffffffu : (valid <= 0 ? 0u : (1u << (8 * valid)) - 1u);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t b = edge ? ws[e] & keep : ws[e];
-                        if (ragged) {
-                            const uint32_t nan = __vcmpeq4(b & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                            b &= ~nan;
-                            if (__any_sync(0xffffffffu, nan != 0)) {
-                                uint32_t see[4];
+                    for (int x = 0; x < HD / 32; ++x) {
+                        const uint4 w = lds128(vt + (8 * half + 4 * u + t) * 4 * HD + (((8 * x + g) ^ (2 * t)) << 4));
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                                for (int q2 = 0; q2 < 4; ++q2) {    // 1.0 where row q2 % 2 sees tokens 2 (q2 / 2) + 0, 1
-                                    const int left = limit[q2 & 1] - (p0 + 4 * t + (q2 & 2));
-                                    see[q2] = (left > 0 ? 0x3c00u : 0u) | (left > 1 ? 0x3c000000u : 0u);
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t b = ws[e];
+                            if (EDGE) {
+                                b &= keep;
+                                const uint32_t nan = __vcmpeq4(b & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                if (__any_sync(0xffffffffu, nan != 0)) {
+                                    b &= ~nan;
+                                    uint32_t see[4];
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {   // 1.0 where row k % 2 sees tokens 2 (k / 2) + 0, 1
+                                        const int left = limit[k & 1] - (first + (k & 2));
+                                        see[k] = (left > 0 ? 0x3c00u : 0u) | (left > 1 ? 0x3c000000u : 0u);
+                                    }
+                                    float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma16816(hit, see, e4m3x2_to_half2((uint16_t)(nan & 0x3838u)),   // 0x38 is 1.0
+                                             e4m3x2_to_half2((uint16_t)((nan >> 16) & 0x3838u)));
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        if (hit[k] > 0.f) o[4 * x + e][k] = NAN;
                                 }
-                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma16816(hit, see, e4m3x2_to_half2((uint16_t)(nan & 0x3838u)),   // 0x38 is 1.0
-                                         e4m3x2_to_half2((uint16_t)((nan >> 16) & 0x3838u)));
-#pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    if (hit[y] > 0.f) o[4 * x + e][y] = NAN;
                             }
-                        }
-                        const uint32_t b0 = e4m3x2_to_half2((uint16_t)b);
-                        const uint32_t b1 = e4m3x2_to_half2((uint16_t)(b >> 16));
+                            const uint32_t b0 = e4m3x2_to_half2((uint16_t)b);
+                            const uint32_t b1 = e4m3x2_to_half2((uint16_t)(b >> 16));
 #pragma unroll
-                        for (int n = 0; n < NP; ++n) mma16816(o[4 * x + e], p[n], b0, b1);
+                            for (int n = 0; n < NP; ++n) mma16816(o[4 * x + e], p[u][n], b0, b1);
+                        }
                     }
                 }
-            }
+            };
+            if (p0 + 32 <= lim_lo) step(std::false_type{});
+            else if (p0 < lim_hi) step(std::true_type{});
             __syncwarp();
             if (lane == 0) tcx::mbar_arrive(empty(stage));
         }
@@ -476,8 +521,8 @@ __global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(con
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
             if (t == 0) {
-                st_m[ts * S::ROWS + rg * 16 + g + 8 * e] = m[e];
-                st_l[ts * S::ROWS + rg * 16 + g + 8 * e] = l[e];
+                st_m[wg * S::ROWS + rg * 16 + g + 8 * e] = m[e];
+                st_l[wg * S::ROWS + rg * 16 + g + 8 * e] = l[e];
             }
         }
     }
@@ -493,16 +538,16 @@ __global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(con
         return;
     }
     // ---- join the warps of a row group
-    float* so = reinterpret_cast<float*>(smem);             // [TS][ROWS][HD]
+    float* so = reinterpret_cast<float*>(smem);             // [WG][ROWS][HD]
     if (warp < S::NW) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = rg * 16 + g + 8 * e;
             float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < S::TS; ++w) mm = fmaxf(mm, st_m[w * S::ROWS + row]);
+            for (int w = 0; w < S::WG; ++w) mm = fmaxf(mm, st_m[w * S::ROWS + row]);
             const float f = m[e] == -INFINITY ? (mm == -INFINITY ? 1.f : 0.f) : ex2(m[e] - mm);
-            float* dst = so + (ts * S::ROWS + row) * HD + 8 * t;
+            float* dst = so + (wg * S::ROWS + row) * HD + 8 * t;
 #pragma unroll
             for (int x = 0; x < HD / 32; ++x)
 #pragma unroll
@@ -521,13 +566,13 @@ __global__ void __launch_bounds__(AttnShape<HD, RG>::THREADS) kv_attn_kernel(con
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-        for (int w = 0; w < S::TS; ++w) {
+        for (int w = 0; w < S::WG; ++w) {
             const float4 x = *reinterpret_cast<const float4*>(so + (w * S::ROWS + row) * HD + d);
             v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
             mm = fmaxf(mm, st_m[w * S::ROWS + row]);
         }
 #pragma unroll
-        for (int w = 0; w < S::TS; ++w) {
+        for (int w = 0; w < S::WG; ++w) {
             const float mw = st_m[w * S::ROWS + row];
             ll += st_l[w * S::ROWS + row] * (mw == -INFINITY ? 1.f : ex2(mw - mm));
         }
@@ -590,7 +635,7 @@ constexpr int MAX_UNITS_SPLIT = MLORA_KV_COUNTER_BYTES / 4;   // a counter for e
 
 template <typename T, int HD, int RG>
 cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
-    using S = AttnShape<HD, RG>;
+    using S = AttnShape<T, HD, RG>;
     AttnCall k;
     k.q = a.q; k.out = a.out; k.lse = a.lse; k.ldq = a.ldq; k.ldo = a.ldo; k.max_len = a.max_len;
     k.counters = static_cast<int*>(a.workspace);

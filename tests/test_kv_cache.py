@@ -12,7 +12,13 @@ A = sum_i p_i |v_i| and S = max_i |scale| sum_d |q_d k_d| of the row (doubles):
   each p_i then has a relative error of 2 D (itself and the sum), exp2 adds
     2^-22, the fp16 rounding of p 2^-11 (bf16) or 2^-22 (fp32), and the sums
     over n positions at most n u each
-  out: (4 D + P + 2 n u + 2^-20) A + half a step of the type, with P = 2^-11 or 2^-22
+  below 2^-14 fp16's rounding is absolute, 2^-25: p_i is held as p'_i = 2^12
+    2^(s_i log2(e) + ev_i - m') with ev_i the exponent of its page's value scale
+    and m' reached by some position r, p'_r >= 2^12, so that the result's
+    divisor sum_i p'_i 2^-ev_i is at least 2^(12 - ev_r).  n errors of 2^-25 on
+    bytes of at most 448 < 2^9 make at most n 2^-25 2^9 2^(ev_r - 12) =
+    n 2^-28 2^ev_r <= F = n 2^-28 max_page 2^ev
+  out: (4 D + P + 2 n u + 2^-20) A + F + half a step of the type, with P = 2^-11 or 2^-22
   lse: 2 D + n u + 2^-22 + 2 u |lse|
 (the products' order inside a matrix instruction may truncate instead of
 round: that is a full step, 2 u, which the factor 2 on D covers).
@@ -266,7 +272,10 @@ def _compare(st, rows, q, out, lse, dtype, scale=None):
         o, l, mass, big = M.attention(qn[at:at + r], k, v, max(n - r, -r), sc)
         D = ((st.hd + 16) * u + 2.0 ** -22) * big
         P = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -22
-        tol = (4 * D + P + 2 * n * u + 2.0 ** -20)[..., None] * mass + EPS[dtype] * np.abs(o) + 1e-40
+        kv = np.arange(q.shape[1]) // (q.shape[1] // st.n_kv)
+        top = 2.0 ** st.model.e["v"][st.table[s, :-(-n // 64)]].astype(np.float64).max(0, initial=-200.0)
+        tol = (4 * D + P + 2 * n * u + 2.0 ** -20)[..., None] * mass + EPS[dtype] * np.abs(o) + \
+            (n * 2.0 ** -28 * top)[kv][:, None] + 1e-40
         bad = np.abs(on[at:at + r] - o) > tol
         assert not bad.any(), (s, float((np.abs(on[at:at + r] - o) / tol).max()))
         fin = np.isfinite(l)
