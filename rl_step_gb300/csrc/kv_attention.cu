@@ -57,7 +57,7 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
 constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
 // Runs of pages of a split (see attn_t).
-constexpr int KV_LONG_RUN = 64, KV_SHORT_RUN = 2;
+constexpr int KV_LONG_RUN = 64, KV_SHORT_RUN = 2, KV_ITEMS_BLOCK = 1;
 // The workspace's counters: the next item, finished blocks, then one for each unit.
 constexpr int CTR_NEXT = 0, CTR_DONE = 1, CTR_UNITS = 16;
 
@@ -93,15 +93,15 @@ struct AttnShape {
     static constexpr bool FOLD = sizeof(T) == 4;            // a pair takes two columns: its high and its low part
     static constexpr int PR = (FOLD ? 4 : 8) * NT;          // pairs of a row group
     static constexpr int ROWS = PR * RG;
-    static constexpr int PG = RG == 4 ? 1 : 2;              // pages in work at once
+    static constexpr int PG = RG == 1 ? 2 : 1;              // pages in work at once
     static constexpr int WG = 2 * PG;                       // warps of a row group: page parity x half of the page
     static constexpr int NW = RG * WG;                      // consumer warps
     static constexpr int THREADS = 32 * NW + 32;
     static constexpr int TILE = KV_PAGE * HD;               // bytes of a K or V tile
     static constexpr int STAGE = 2 * TILE;
     static constexpr int STAGES = (NT == 1 ? 4 : 6) * (128 / HD);
-    static constexpr int BLOCKS_SM = RG > 1 ? 1 : (NT == 1 ? 3 : 2);
-    static constexpr int JOIN_WG = 4096;                    // joining space of a row group, bytes
+    static constexpr int BLOCKS_SM = NW > 4 ? 1 : (NT == 1 ? 3 : 2);
+    static constexpr int JOIN_WG = 2048 * PG;               // joining space of a row group, bytes
     // ring, raw queries, joining space, per-warp statistics, barriers,
     // exponents, items, flags
     static constexpr int QRAW = STAGES * STAGE;
@@ -121,10 +121,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
                  : "memory");
-}
-// expected bytes without an arrival
-__device__ __forceinline__ void mbar_expect_only(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -244,12 +240,32 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        Item x;                                             // the same in every lane
-        int id = -1;                                        // lane i: page id of the run's page i
+        Item x = {};                                        // the same in every lane
+        // lane i: the next 32 pages' tiles and exponents, asked for a batch ahead
+        int64_t at = 0;
+        int ek = 0, ev = 0;
+        // (no branch: the vote and the loads are every lane's)
+        auto load_batch = [&](int i0) {
+            const int mine = i0 + lane;
+            const int64_t entry = (int64_t)x.s * c.max_pages + x.page0 + (mine < x.np ? mine : 0);
+            const int id = c.table[entry];
+            const bool good = id >= 0 && id < c.n_pages;
+            const unsigned bad = __ballot_sync(0xffffffffu, !good);
+            at = (int64_t)(good ? id : 0) * c.n_kv + x.h;   // a page that exists stands in; the rows become NaN
+            ek = scale_exp(c.ks[at]);
+            ev = bad != 0 ? EV_BAD : scale_exp(c.vs[at]);
+            if (bad != 0 && lane == 0) raise_status(c.status, ST_RANGE);
+            __syncwarp();
+        };
+        int after = 0;                                      // lane 0: the counter's answer for the item after the next
+        auto ask = [&]() {
+            if (lane == 0) after = atomicAdd(a.counters + CTR_NEXT, 1);
+            __syncwarp();
+        };
         // From item `index` on, the first one with work; empty and bad sequences' rows are written on the way.
         auto find = [&](int index) {
             for (;; ) {
-                if (index >= a.items) {
+                if ((unsigned)index >= (unsigned)a.items) { // (whatever stands in the workspace)
                     x.index = -1;
                     return;
                 }
@@ -260,7 +276,6 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                 x.h = x.unit / a.tiles % c.n_kv;
                 x.s = x.unit / a.tiles / c.n_kv;
                 x.page0 = split * a.chunk;
-                id = lane < a.chunk && x.page0 + lane < c.max_pages ? c.table[(int64_t)x.s * c.max_pages + x.page0 + lane] : -1;
                 SeqRows r;
                 const bool ok = kv_seq(c, x.s, a.max_len, r);
                 if (!ok || r.len == 0) {
@@ -291,12 +306,13 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                         if (x.np > 0) return;
                     }
                 }
-                int nx = 0;
-                if (lane == 0) nx = atomicAdd(a.counters + CTR_NEXT, 1);
-                index = gridDim.x + __shfl_sync(0xffffffffu, nx, 0);
+                index = gridDim.x + __shfl_sync(0xffffffffu, after, 0);
+                ask();
             }
         };
+        ask();
         find(blockIdx.x);
+        if (x.index >= 0) load_batch(0);
         int cnt = 0, n_item = 0;                            // pages and items so far
         bool go = true;
         while (go) {
@@ -309,7 +325,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             if (x.index < 0) break;
             // the queries: the pairs of a token are contiguous
             if (n_item >= 1 && !wait(q_empty, (n_item - 1) & 1)) break;
-            if (lane == 0) mbar_expect_only(q_full, x.pairs * HD * (int)sizeof(T));
+            if (lane == 0) tcx::mbar_expect_tx(q_full, x.pairs * HD * (int)sizeof(T));
             __syncwarp();
             for (int tok = x.pair0 / a.group + lane; tok * a.group < x.pair0 + x.pairs; tok += 32) {
                 const int p0 = tok * a.group > x.pair0 ? tok * a.group : x.pair0;
@@ -318,31 +334,17 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                           q + kv_row(c, (int64_t)x.row0 + tok) * a.ldq + ((int64_t)x.h * a.group + p0 - tok * a.group) * HD,
                           (p1 - p0) * HD * (int)sizeof(T), q_full);
             }
-            __syncwarp();
-            if (lane == 0) tcx::mbar_arrive(q_full);
             const int lim = x.before + (x.pair0 + x.pairs - 1) / a.group + 1;
-            const int np = x.np, page0 = x.page0, s = x.s, h = x.h;
-            Item nxt = x;
-            int nxt_id = -1;
+            const int np = x.np, page0 = x.page0;
             for (int i0 = 0; i0 < np && go; i0 += 32) {
-                const int mine = i0 + lane;
-                if (i0 > 0 && mine < np) id = c.table[(int64_t)s * c.max_pages + page0 + mine];
-                bool good = true;
-                if (mine < np && (id < 0 || id >= c.n_pages)) {
-                    raise_status(c.status, ST_RANGE);
-                    good = false;
-                    id = 0;                                 // a page that exists stands in; the rows become NaN
-                }
-                const bool bad = __any_sync(0xffffffffu, !good);
-                const int64_t at = (int64_t)(mine < np ? id : 0) * c.n_kv + h;
-                int ek = 0, ev = 0;
+                const int64_t at_now = at;
+                const int ek_now = ek, ev_now = ev;
                 const int n = np - i0 < 32 ? np - i0 : 32;
-                // copies of the first pages go out before their scales are here
-                const int ahead = n < S::STAGES ? n : S::STAGES;
                 for (int i = 0; i < n; ++i) {
-                    const int stage = (cnt + i) % S::STAGES;
-                    const int64_t tile_at = __shfl_sync(0xffffffffu, at, i);
-                    if (cnt + i >= S::STAGES && !wait(empty(stage), ((cnt + i) / S::STAGES - 1) & 1)) {
+                    const int stage = cnt % S::STAGES;
+                    const int64_t tile_at = __shfl_sync(0xffffffffu, at_now, i);
+                    const int k_ = __shfl_sync(0xffffffffu, ek_now, i), v_ = __shfl_sync(0xffffffffu, ev_now, i);
+                    if (cnt >= S::STAGES && !wait(empty(stage), (cnt / S::STAGES - 1) & 1)) {
                         go = false;
                         break;
                     }
@@ -350,42 +352,31 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                         const int left = lim - (page0 + i0 + i) * KV_PAGE;      // tokens of the page that count
                         const int tok = left < KV_PAGE ? left : KV_PAGE;
                         const uint32_t kb = tok * HD, vb = (tok + 3) / 4 * 4 * HD;
-                        mbar_expect_only(full(stage), kb + vb);
+                        exps[2 * stage] = k_;
+                        exps[2 * stage + 1] = v_;
+                        tcx::mbar_expect_tx(full(stage), kb + vb);
                         bulk_load(sbase + stage * S::STAGE, c.k + tile_at * S::TILE, kb, full(stage));
                         bulk_load(sbase + stage * S::STAGE + S::TILE, c.v + tile_at * S::TILE, vb, full(stage));
                     }
-                    if (i + 1 == ahead && mine < np) {
-                        ek = scale_exp(c.ks[at]);
-                        // a bad page: no exponent, the consumers make their rows NaN
-                        ev = bad ? EV_BAD : scale_exp(c.vs[at]);
-                    }
-                    for (int j = i + 1 < ahead ? i + 1 : (i + 1 == ahead ? 0 : i); j <= i; ++j) {
-                        const int k_ = __shfl_sync(0xffffffffu, ek, j), v_ = __shfl_sync(0xffffffffu, ev, j);
-                        if (lane == 0) {
-                            exps[2 * ((cnt + j) % S::STAGES)] = k_;
-                            exps[2 * ((cnt + j) % S::STAGES) + 1] = v_;
-                            tcx::mbar_arrive(full((cnt + j) % S::STAGES));
+                    ++cnt;
+                    // the ring is full, or the batch's pages are on their way: look for what comes next
+                    if (i + 1 == (n < S::STAGES ? n : S::STAGES)) {
+                        if (i0 + 32 < np) {
+                            load_batch(i0 + 32);
+                        } else {
+                            const int next = gridDim.x + __shfl_sync(0xffffffffu, after, 0);
+                            ask();
+                            find(next);
+                            if (x.index >= 0) load_batch(0);
                         }
                     }
-                    if (i0 == 0 && i + 1 == ahead) {
-                        // the ring is full (or the item's pages are on their way): look for the next item
-                        const int keep = id;
-                        int nx = 0;
-                        if (lane == 0) nx = atomicAdd(a.counters + CTR_NEXT, 1);
-                        const Item cur = x;
-                        find(gridDim.x + __shfl_sync(0xffffffffu, nx, 0));
-                        nxt = x;
-                        nxt_id = id;
-                        x = cur;
-                        id = keep;
-                    }
                 }
-                if (go) cnt += n;
             }
-            x = nxt;
-            id = nxt_id;
             ++n_item;
         }
+        // the counter's last answer is here before the block counts as finished
+        asm volatile("" ::"r"(after));
+        __threadfence();
     } else {
         const int g = lane >> 2, t = lane & 3;
         const int rg = warp / S::WG, wg = warp % S::WG;     // row group, place in it
@@ -860,6 +851,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
     }
     // the last block to finish leaves the item counter as it found it
     if (threadIdx.x == 0) {
+        __threadfence();
         if (atomicAdd(a.counters + CTR_DONE, 1) == (int)gridDim.x - 1) {
             a.counters[CTR_NEXT] = 0;
             a.counters[CTR_DONE] = 0;
@@ -904,7 +896,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     const int64_t blocks = (int64_t)n_sms * S::BLOCKS_SM;
     int64_t chunk = pages;
     if (units <= MAX_UNITS_SPLIT) {
-        const int64_t per_unit = (blocks + units - 1) / units;
+        const int64_t per_unit = (KV_ITEMS_BLOCK * blocks + units - 1) / units;
         chunk = (pages + per_unit - 1) / per_unit;
         if (chunk > KV_LONG_RUN) chunk = KV_LONG_RUN;
         if (chunk < KV_SHORT_RUN) chunk = KV_SHORT_RUN;
@@ -931,7 +923,7 @@ cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     constexpr int PR = AttnShape<T, HD, 1, 1>::PR;
     const int64_t pairs = (int64_t)c.max_rows * (a.n_heads / c.n_kv);
     if (pairs <= PR) return attn_t<T, HD, 1, 1>(c, a, s);
-    if (pairs <= 2 * PR) return attn_t<T, HD, 2, 1>(c, a, s);
+    if (pairs <= 2 * PR) return attn_t<T, HD, 1, 2>(c, a, s);
     if (pairs <= 4 * PR) return attn_t<T, HD, 2, 2>(c, a, s);
     return attn_t<T, HD, 2, 4>(c, a, s);
 }
