@@ -39,8 +39,7 @@
  * < 0, > max_rows or > kv_len > 0, rows outside 0 .. n_rows-1, or a page id
  * outside 0 .. n_pages-1 raises bit 0 of *status; append and read skip it (a
  * bad page: that page), attention writes NaN to those of its rows that lie in
- * range.  A device wait that exceeds its bound raises bit 1 (the workspace must
- * then be zeroed before its next use).
+ * range.  A device wait that exceeds its bound raises bit 1.
  */
 #ifndef MLORA_KV_H
 #define MLORA_KV_H
@@ -53,8 +52,8 @@ extern "C" {
 
 #define MLORA_KV_PAGE 64
 #define MLORA_KV_MIN_EXP (-100)
-/* Leading bytes of an attention workspace that hold its counters. */
-#define MLORA_KV_COUNTER_BYTES 65536
+/* An attention workspace that serves every shape. */
+#define MLORA_KV_WORKSPACE_BYTES (16 << 20)
 
 /* A pool of pages (DEVICE buffers).  k, v: n_pages * n_kv_heads * 64 *
  * head_dim bytes, 16-byte aligned; scales: n_pages * n_kv_heads. */
@@ -117,13 +116,15 @@ int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype
  * and the stored bytes, the probabilities enter the second product as fp16
  * (relative rounding 2^-11, below bf16's own 2^-8), and on fp32 as two fp16
  * parts (2^-22), as q does; a probability below 2^-26 of its row's largest has
- * an absolute error of up to 2^-37 of that largest instead.  The result of a row does not depend on the other
- * sequences' contents, and repeats bit for bit.
- * workspace: DEVICE, 16-byte aligned, at least MLORA_KV_COUNTER_BYTES, whose
- * first MLORA_KV_COUNTER_BYTES were zeroed before its first use (every call
- * leaves them zero); calls that may overlap need a workspace each.  A long
- * sequence is split over as many blocks as the workspace has room for partial
- * results: 32 MB serve every shape at full speed.  Errors: E_ARG, E_CUDA. */
+ * an absolute error of up to 2^-37 of that largest instead.  A call repeats
+ * bit for bit.
+ * workspace: DEVICE, 16-byte aligned, of any content (may be NULL); calls that
+ * may overlap need one each.  With MLORA_KV_WORKSPACE_BYTES the work is shared
+ * evenly whatever the lengths: long sequences are cut where a block's share
+ * ends and their parts joined, so the order of a row's sums depends on the
+ * lengths of the batch.  With less than the shape needs (0, say) no sequence is
+ * cut, and a row's result is bit for bit the same in every batch.
+ * Errors: E_ARG, E_CUDA. */
 typedef struct {
     const void* q;
     void* out;

@@ -8,11 +8,12 @@
 // bytes over the HBM rate are the floor.  The design streams pages and keeps
 // the arithmetic beside the stream cheap:
 //  * A work item is up to 8 NT RG (row, head of the group) pairs of a sequence
-//    against one key/value head, over a run of pages.  Blocks are persistent and
-//    take items from a counter; a producer warp copies each (page, head) tile of
-//    K and V -- contiguous 8 KB at head_dim 128 -- into a ring of stages with
-//    cp.async.bulk and runs ahead into the next item (its length, table, queries
-//    and first pages) while the consumer warps finish the current one.
+//    against one key/value head, over a run of pages.  Blocks are persistent:
+//    the pages of all items are one line that is cut into equal shares, one a
+//    block, whatever the sequences' lengths.  A producer warp copies each (page,
+//    head) tile of K and V -- contiguous 8 KB at head_dim 128 -- into a ring of
+//    stages with cp.async.bulk and runs ahead into the next item (its table,
+//    scales, queries and first pages) while the consumer warps finish this one.
 //  * The products are mma.sync m16n8k16 (fp16 operands, fp32 sums) with the
 //    cache's bytes as the 16-row operand and the pairs as the 8 columns:
 //    S^T = K q^T (16 tokens x 8 pairs), O^T += V^T P^T (16 dims x 8 pairs).  An
@@ -38,10 +39,12 @@
 //  * Warps of a row group take different halves of a page and, with one or two
 //    row groups, every other page, 32 tokens at a step; each has a running maximum and sum of its own, joined at the
 //    item's end, so nothing but the ring's barriers is shared in the loop.
-//  * Long sequences are cut into runs of pages (flash-style split); an item
-//    leaves its rows' unnormalised sums, maximum and sum in the workspace, and
-//    the last item of the sequence and head to arrive joins them in order of
-//    the runs, so the result does not depend on who was last.
+//  * A share's ends cut sequences: such an item leaves its rows' unnormalised
+//    sums, maximum and sum in the workspace, and a second small kernel joins the
+//    parts in order.  (Runs of a fixed length, taken from a counter, either left
+//    a tail -- items of 16 pages: 94 us where equal shares take @@ -- or ended too
+//    often; joined by the last item to arrive, a run's end cost its block about
+//    6 us of fences and atomics.)
 #include <atomic>
 #include <type_traits>
 
@@ -56,22 +59,23 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
 constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
-// Runs of pages of a split (see attn_t).
-constexpr int KV_LONG_RUN = 64, KV_SHORT_RUN = 2, KV_ITEMS_BLOCK = 1;
-// The workspace's counters: the next item, finished blocks, then one for each unit.
-constexpr int CTR_NEXT = 0, CTR_DONE = 1, CTR_UNITS = 16;
+constexpr int KV_SHORT_RUN = 2;             // pages: no block gets fewer
+constexpr int KV_WHOLE = 4;                 // pages: sequences up to this are not cut
+
+// A cut unit, left in the workspace by the block that begins it.
+struct Cut {
+    int blocks;                             // blocks that share it, from this one on (0: this block begins none)
+    int row0, pair0, pairs, h;
+};
 
 struct AttnCall {
     const void* q;
     void* out;
     float* lse;
-    int* counters;
-    float* part;
+    Cut* cuts;                              // one a block; null: sequences are not cut
+    float* part;                            // two partial results a block
     int64_t ldq, ldo, max_len;
     int n_heads, group;
-    int items;                              // units * splits
-    int tiles;                              // row tiles of a (sequence, key/value head)
-    int splits, chunk;                      // runs of `chunk` pages
     int prow;                               // rows of a partial result
     int64_t slot;                           // its floats: the rows' sums, maxima and sums of p
     float qk;                               // scale * log2 e
@@ -79,13 +83,12 @@ struct AttnCall {
 
 // What the producer tells the consumers about an item.
 struct Item {
-    int index;                              // -1: no more
-    int s, h;
+    int s, h;                               // s < 0: no more
     int row0;                               // the sequence's first row
     int pair0, pairs;                       // first pair of the tile, pairs in it
     int before;                             // positions before the sequence's rows
     int page0, np;                          // the run
-    int unit, nsplit;
+    int slot;                               // its partial result's place, or -1: the whole unit
 };
 
 template <typename T, int HD, int NT, int RG>
@@ -122,14 +125,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    // not volatile: a function of its operands, free to move between the loads and conversions
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -202,7 +200,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
     float* st_m = reinterpret_cast<float*>(smem + S::STAT); // [WG][ROWS]
     float* st_l = st_m + S::WG * S::ROWS;
     Item* items = reinterpret_cast<Item*>(smem + S::ITEMS);
-    volatile int* flags = reinterpret_cast<volatile int*>(smem + S::FLAGS);   // abort, -, last, -
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + S::FLAGS);   // [0]: a wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto full = [&](int i) { return sbase + S::BAR + 16 * i; };
     auto empty = [&](int i) { return sbase + S::BAR + 16 * i + 8; };
@@ -210,6 +208,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
     auto item_empty = [&](int i) { return sbase + S::BAR + 16 * S::STAGES + 16 + 8 * i; };
     const uint32_t q_full = sbase + S::BAR + 16 * S::STAGES + 32, q_empty = q_full + 8;
 
+    __shared__ int64_t warp_sum[S::NW + 1], s_rem;
+    __shared__ int s_first;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             tcx::mbar_init(full(i), 1);
@@ -221,8 +221,53 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
         }
         tcx::mbar_init(q_full, 1);
         tcx::mbar_init(q_empty, S::NW);
-        flags[0] = flags[1] = flags[2] = flags[3] = 0;
+        flags[0] = 0;
+        s_first = c.n_seqs;                                 // (no share, unless a sequence of it is found)
+        s_rem = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // ---- the block's share.  The pages of all units -- sequence by sequence, then
+    // key/value head, row tile, page -- are one line of `total` pages, cut into
+    // equal shares; every block adds the sequences up for itself.
+    auto weight = [&](const SeqRows& r) -> int64_t {
+        return (int64_t)((r.len + KV_PAGE - 1) / KV_PAGE) * ((r.n * a.group + S::ROWS - 1) / S::ROWS) * c.n_kv;
+    };
+    int64_t mine = 0, upto;
+    const int per = (c.n_seqs + S::THREADS - 1) / S::THREADS, s0 = threadIdx.x * per;
+    for (int s = s0; s < s0 + per && s < c.n_seqs; ++s) {
+        SeqRows r;
+        if (kv_seq(c, s, a.max_len, r)) mine += weight(r);
+    }
+    upto = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+        upto += lane >= x ? y : 0;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w <= S::NW; ++w) {
+        upto += w < warp ? warp_sum[w] : 0;
+        total += warp_sum[w];
+    }
+    int64_t shares = a.cuts ? (total + KV_SHORT_RUN - 1) / KV_SHORT_RUN : total;
+    if (shares > gridDim.x) shares = gridDim.x;
+    const bool busy = (int)blockIdx.x < shares;
+    const int64_t lo = busy ? (int64_t)blockIdx.x * total / shares : 0, hi = busy ? ((int64_t)blockIdx.x + 1) * total / shares : 0;
+    if (busy && upto - mine <= lo && lo < upto) {
+        int64_t rem = lo - (upto - mine);
+        for (int s = s0;; ++s) {
+            SeqRows r;
+            const int64_t w = s < c.n_seqs && kv_seq(c, s, a.max_len, r) ? weight(r) : 0;
+            if (rem < w || s >= c.n_seqs) {
+                s_first = s;
+                s_rem = rem;
+                break;
+            }
+            rem -= w;
+        }
     }
     __syncthreads();
 
@@ -240,15 +285,79 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        Item x = {};                                        // the same in every lane
-        // lane i: the next 32 pages' tiles and exponents, asked for a batch ahead
+        // The items of the share, in order.  A warp's lanes hold the lengths and rows of the next 32 sequences.
+        int64_t pos = lo, rem = busy ? s_rem : 0;           // place in the line; pages of the sequence before it
+        int s_now = busy ? s_first : 0, s_base = s_now;
+        int l_len = 0;
+        int64_t l_a = 0, l_b = 0;
+        auto lengths = [&]() {
+            const int s = s_base + lane < c.n_seqs ? s_base + lane : c.n_seqs - 1;
+            l_len = c.kv_len[s];
+            l_a = c.row_off ? c.row_off[s] : s;
+            l_b = c.row_off ? c.row_off[s + 1] : (int64_t)s + 1;
+        };
+        if (a.cuts && lane == 0) a.cuts[blockIdx.x].blocks = 0;
+        auto next = [&](Item& x) {
+            x.s = -1;
+            while (pos < hi && s_now < c.n_seqs) {
+                if (s_now - s_base >= 32) {
+                    s_base = s_now;
+                    lengths();
+                }
+                SeqRows r;
+                const int len = __shfl_sync(0xffffffffu, l_len, s_now - s_base);
+                const int64_t row_a = __shfl_sync(0xffffffffu, l_a, s_now - s_base);
+                const int64_t row_b = __shfl_sync(0xffffffffu, l_b, s_now - s_base);
+                const int64_t w = kv_seq_ok(c, len, row_a, row_b, a.max_len, r) ? weight(r) : 0;
+                if (rem >= w) {                             // the sequence is done, or has none
+                    rem = 0;
+                    ++s_now;
+                    continue;
+                }
+                const int pages = (len + KV_PAGE - 1) / KV_PAGE, tiles = (r.n * a.group + S::ROWS - 1) / S::ROWS;
+                const int unit = (int)(rem / pages), page0 = (int)(rem % pages);
+                int np = pages - page0;
+                if (a.cuts) {
+                    if (np > hi - pos) np = (int)(hi - pos);
+                } else if (page0 > 0) {                     // not cut: the unit is the block's where it begins
+                    pos += np;
+                    rem += np;
+                    continue;
+                }
+                const int tile = unit % tiles;
+                x.s = s_now;
+                x.h = unit / tiles;
+                x.row0 = r.row0;
+                x.pair0 = tile * S::ROWS;
+                x.pairs = r.n * a.group - x.pair0 < S::ROWS ? r.n * a.group - x.pair0 : S::ROWS;
+                x.before = r.len - r.n;
+                x.page0 = page0;
+                x.np = np;
+                x.slot = -1;
+                if (page0 > 0) {
+                    x.slot = 2 * blockIdx.x;
+                } else if (np < pages) {
+                    x.slot = 2 * blockIdx.x + 1;
+                    if (lane == 0) {
+                        const int64_t end = pos + pages;    // the block of page p is ((p + 1) shares - 1) / total
+                        a.cuts[blockIdx.x] = Cut{(int)((end * shares - 1) / total) - (int)blockIdx.x + 1, x.row0, x.pair0, x.pairs, x.h};
+                    }
+                    __syncwarp();
+                }
+                pos += np;
+                rem += np;
+                return;
+            }
+        };
+        // lane i: page id of x's page i0 + i
+        auto page_id = [&](const Item& x, int i0) -> int {
+            const int i = i0 + lane < x.np ? i0 + lane : i0;
+            return c.table[(int64_t)x.s * c.max_pages + x.page0 + i];
+        };
+        // lane i: tile and exponents of a page, from its id.  No branch: the vote and the loads are every lane's.
         int64_t at = 0;
         int ek = 0, ev = 0;
-        // (no branch: the vote and the loads are every lane's)
-        auto load_batch = [&](int i0) {
-            const int mine = i0 + lane;
-            const int64_t entry = (int64_t)x.s * c.max_pages + x.page0 + (mine < x.np ? mine : 0);
-            const int id = c.table[entry];
+        auto load_batch = [&](const Item& x, int id) {
             const bool good = id >= 0 && id < c.n_pages;
             const unsigned bad = __ballot_sync(0xffffffffu, !good);
             at = (int64_t)(good ? id : 0) * c.n_kv + x.h;   // a page that exists stands in; the rows become NaN
@@ -257,62 +366,16 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             if (bad != 0 && lane == 0) raise_status(c.status, ST_RANGE);
             __syncwarp();
         };
-        int after = 0;                                      // lane 0: the counter's answer for the item after the next
-        auto ask = [&]() {
-            if (lane == 0) after = atomicAdd(a.counters + CTR_NEXT, 1);
-            __syncwarp();
-        };
-        // From item `index` on, the first one with work; empty and bad sequences' rows are written on the way.
-        auto find = [&](int index) {
-            for (;; ) {
-                if ((unsigned)index >= (unsigned)a.items) { // (whatever stands in the workspace)
-                    x.index = -1;
-                    return;
-                }
-                const int split = index % a.splits;
-                x.index = index;
-                x.unit = index / a.splits;
-                const int tile = x.unit % a.tiles;
-                x.h = x.unit / a.tiles % c.n_kv;
-                x.s = x.unit / a.tiles / c.n_kv;
-                x.page0 = split * a.chunk;
-                SeqRows r;
-                const bool ok = kv_seq(c, x.s, a.max_len, r);
-                if (!ok || r.len == 0) {
-                    // rows without positions: zero (or NaN: a bad sequence), by one item of each head
-                    if (split == 0 && tile == 0) {
-                        const float v = ok ? 0.f : NAN;
-                        const int64_t r1 = (int64_t)r.row0 + r.n < c.n_rows ? (int64_t)r.row0 + r.n : c.n_rows;
-                        for (int64_t y = r.row0 < 0 ? 0 : r.row0; y < r1; ++y) {
-                            const int64_t z = kv_row(c, y);
-                            for (int d = lane; d < a.group * HD; d += 32)
-                                out[z * a.ldo + (int64_t)x.h * a.group * HD + d] = from_f<T>(v);
-                            for (int d = lane; a.lse && d < a.group; d += 32)
-                                a.lse[z * a.n_heads + x.h * a.group + d] = ok ? -INFINITY : NAN;
-                        }
-                    }
-                } else {
-                    x.pair0 = tile * S::ROWS;
-                    x.pairs = r.n * a.group - x.pair0;
-                    if (x.pairs > S::ROWS) x.pairs = S::ROWS;
-                    if (x.pairs > 0) {
-                        x.row0 = r.row0;
-                        x.before = r.len - r.n;
-                        // positions that the tile's last row sees
-                        const int lim = x.before + (x.pair0 + x.pairs - 1) / a.group + 1;
-                        const int pages = (lim + KV_PAGE - 1) / KV_PAGE;
-                        x.nsplit = (pages + a.chunk - 1) / a.chunk;
-                        x.np = pages - x.page0 < a.chunk ? pages - x.page0 : a.chunk;
-                        if (x.np > 0) return;
-                    }
-                }
-                index = gridDim.x + __shfl_sync(0xffffffffu, after, 0);
-                ask();
-            }
-        };
-        ask();
-        find(blockIdx.x);
-        if (x.index >= 0) load_batch(0);
+        lengths();
+        Item x = {}, y = {};                                // the same in every lane: the current item and the next
+        int y_id = 0;                                       // the next one's page ids, asked for an item ahead
+        next(x);
+        if (x.s >= 0) {
+            const int id = page_id(x, 0);
+            next(y);
+            if (y.s >= 0) y_id = page_id(y, 0);
+            load_batch(x, id);
+        }
         int cnt = 0, n_item = 0;                            // pages and items so far
         bool go = true;
         while (go) {
@@ -322,7 +385,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                 items[slot] = x;
                 tcx::mbar_arrive(item_full(slot));
             }
-            if (x.index < 0) break;
+            if (x.s < 0) break;
             // the queries: the pairs of a token are contiguous
             if (n_item >= 1 && !wait(q_empty, (n_item - 1) & 1)) break;
             if (lane == 0) tcx::mbar_expect_tx(q_full, x.pairs * HD * (int)sizeof(T));
@@ -350,33 +413,48 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                     }
                     if (lane == 0) {
                         const int left = lim - (page0 + i0 + i) * KV_PAGE;      // tokens of the page that count
-                        const int tok = left < KV_PAGE ? left : KV_PAGE;
+                        const int tok = left < KV_PAGE ? (left > 0 ? left : 0) : KV_PAGE;       // (a tile's last pages may lie behind its rows)
                         const uint32_t kb = tok * HD, vb = (tok + 3) / 4 * 4 * HD;
                         exps[2 * stage] = k_;
                         exps[2 * stage + 1] = v_;
                         tcx::mbar_expect_tx(full(stage), kb + vb);
-                        bulk_load(sbase + stage * S::STAGE, c.k + tile_at * S::TILE, kb, full(stage));
-                        bulk_load(sbase + stage * S::STAGE + S::TILE, c.v + tile_at * S::TILE, vb, full(stage));
+                        if (tok > 0) {
+                            bulk_load(sbase + stage * S::STAGE, c.k + tile_at * S::TILE, kb, full(stage));
+                            bulk_load(sbase + stage * S::STAGE + S::TILE, c.v + tile_at * S::TILE, vb, full(stage));
+                        }
                     }
                     ++cnt;
                     // the ring is full, or the batch's pages are on their way: look for what comes next
                     if (i + 1 == (n < S::STAGES ? n : S::STAGES)) {
                         if (i0 + 32 < np) {
-                            load_batch(i0 + 32);
+                            load_batch(x, page_id(x, i0 + 32));
                         } else {
-                            const int next = gridDim.x + __shfl_sync(0xffffffffu, after, 0);
-                            ask();
-                            find(next);
-                            if (x.index >= 0) load_batch(0);
+                            x = y;
+                            const int id = y_id;
+                            if (x.s >= 0) {
+                                next(y);
+                                if (y.s >= 0) y_id = page_id(y, 0);
+                                load_batch(x, id);
+                            }
                         }
                     }
                 }
             }
             ++n_item;
         }
-        // the counter's last answer is here before the block counts as finished
-        asm volatile("" ::"r"(after));
-        __threadfence();
+        // rows without positions, shared out over the blocks: zero (or NaN: a bad sequence)
+        for (int s = blockIdx.x; s < c.n_seqs; s += gridDim.x) {
+            SeqRows r;
+            const bool ok = kv_seq(c, s, a.max_len, r);
+            if (!ok) raise_status(c.status, ST_RANGE);
+            if (ok && r.len > 0) continue;
+            const int64_t r1 = (int64_t)r.row0 + r.n < c.n_rows ? (int64_t)r.row0 + r.n : c.n_rows;
+            for (int64_t i = r.row0 < 0 ? 0 : r.row0; i < r1; ++i) {
+                const int64_t z = kv_row(c, i);
+                for (int d = lane; d < a.n_heads * HD; d += 32) out[z * a.ldo + d] = from_f<T>(ok ? 0.f : NAN);
+                for (int d = lane; a.lse && d < a.n_heads; d += 32) a.lse[z * a.n_heads + d] = ok ? -INFINITY : NAN;
+            }
+        }
     } else {
         const int g = lane >> 2, t = lane & 3;
         const int rg = warp / S::WG, wg = warp % S::WG;     // row group, place in it
@@ -415,19 +493,22 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
         T* out = static_cast<T*>(a.out);
         int cnt = 0;                                        // pages so far
         for (int n_item = 0;; ++n_item) {
-            // a wait that gives up ends the loop in every consumer at the next any()
+            // a wait that gives up ends the loop in every consumer at the item's any()
             bool go = await(item_full(n_item & 1), (n_item / 2) & 1);
             if (!go) gave_up();
-            if (any(!go)) break;
             const Item& x = items[n_item & 1];
-            if (x.index < 0) break;
+            const bool end = go && x.s < 0;
+            if (!go || end) {
+                any(!go);
+                break;
+            }
             const int np = x.np, page0 = x.page0;
             const int lim_lo = x.before + x.pair0 / a.group + 1;                        // positions that the tile's first row sees
             const int lim_hi = x.before + (x.pair0 + x.pairs - 1) / a.group + 1;        // .. and its last
             // q's fragments: columns g of the tiles.  A thread's dims at K step
             // (y, i) are 64 y + 16 t + 4 i + 0..3, the four bytes of a word of the
             // key tile.
-            if (go) go = await(q_full, n_item & 1);
+            go = await(q_full, n_item & 1);
             if (!go) gave_up();
             uint32_t qb[NT][HD / 16][2];
             float o[HD / 16][NT][4];
@@ -493,7 +574,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
 #pragma unroll
                 for (int n = 0; n < NT; ++n) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
 
-            for (int it = S::PG == 2 ? (cnt ^ pg) & 1 : 0; it < np; it += S::PG) {
+            for (int it = S::PG == 2 ? (cnt ^ pg) & 1 : 0; go && it < np; it += S::PG) {
                 const int stage = (cnt + it) % S::STAGES;
                 if (!await(full(stage), ((cnt + it) / S::STAGES) & 1)) {
                     go = false;
@@ -503,7 +584,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                 const int ek = exps[2 * stage];
                 int ev = exps[2 * stage + 1];
                 if (ev == EV_BAD) { bad = true; ev = 0; }
-                const uint32_t kt = sbase + stage * S::STAGE;
+                const uint8_t* kt = smem + stage * S::STAGE;
                 const int p0 = (page0 + it) * KV_PAGE + 32 * half;      // the first of this warp's 32 positions
                 float fk[NT][E];
 #pragma unroll
@@ -527,7 +608,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const uint4 v = lds128(kt + k_at[y] + (16 * u + 2 * j) * HD);
+                                const uint4 v = *reinterpret_cast<const uint4*>(kt + k_at[y] + (16 * u + 2 * j) * HD);
                                 w[u][j][0] = v.x; w[u][j][1] = v.y; w[u][j][2] = v.z; w[u][j][3] = v.w;
                             }
 #pragma unroll
@@ -629,7 +710,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                         const uint32_t keep = valid >= 4 ? 0xffffffffu : (valid <= 0 ? 0u : (1u << (8 * valid)) - 1u);
 #pragma unroll
                         for (int y = 0; y < HD / 32; ++y) {
-                            const uint4 v = lds128(kt + v_at + 16 * u * HD + 128 * y);
+                            const uint4 v = *reinterpret_cast<const uint4*>(kt + v_at + 16 * u * HD + 128 * y);
                             uint32_t w[4] = {v.x, v.y, v.z, v.w};
                             if (EDGE) {
                                 uint32_t nan[4], some = 0;
@@ -710,15 +791,18 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const int row = rg * S::PR + (FOLD ? 4 * n + t : 8 * n + 2 * t + e);
+                    float mw[S::WG], lw[S::WG];
                     mm[n][e] = -INFINITY;
-                    ll[n][e] = 0.f;
-#pragma unroll
-                    for (int w = 0; w < S::WG; ++w) mm[n][e] = fmaxf(mm[n][e], st_m[w * S::ROWS + row]);
 #pragma unroll
                     for (int w = 0; w < S::WG; ++w) {
-                        const float mw = st_m[w * S::ROWS + row];       // 1: 0 or NaN stands there
-                        ll[n][e] += st_l[w * S::ROWS + row] * (mw == -INFINITY ? 1.f : ex2(mw - mm[n][e]));
+                        mw[w] = st_m[w * S::ROWS + row];
+                        lw[w] = st_l[w * S::ROWS + row];
+                        mm[n][e] = fmaxf(mm[n][e], mw[w]);
                     }
+#pragma unroll
+                    for (int w = 0; w < S::WG; ++w) lw[w] *= mw[w] == -INFINITY ? 1.f : ex2(mw[w] - mm[n][e]);   // 1: 0 or NaN
+                    // the same whichever page parity came first
+                    ll[n][e] = S::WG == 4 ? (lw[0] + lw[2 % S::WG]) + (lw[1] + lw[3 % S::WG]) : lw[0] + lw[1];
                     const float f = m[n][e] == -INFINITY ? 1.f : ex2(m[n][e] - mm[n][e]);
 #pragma unroll
                     for (int j = 0; j < HD / 16; ++j) {
@@ -767,8 +851,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             };
             if (S::PG == 2) join(std::integral_constant<int, 2>{}, pg == 1, pg == 0, half);
             join(std::integral_constant<int, 1>{}, wg == 1, wg == 0, 0);
-            const int nsplit = x.nsplit, unit = x.unit;
-            float* part = a.part + (int64_t)x.index * a.slot;
+            const int slot = x.slot;                        // >= 0: a part of a unit
+            float* part = a.part + (int64_t)slot * a.slot;
             if (wg == 0) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -776,7 +860,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                     for (int e = 0; e < E; ++e) {
                         const int row = rg * S::PR + (FOLD ? 4 * n + t : 8 * n + 2 * t + e);
                         if (row >= x.pairs) continue;
-                        const float inv = nsplit > 1 ? 1.f : 1.f / ll[n][e];
+                        const float inv = slot >= 0 ? 1.f : 1.f / ll[n][e];
                         const int pair = x.pair0 + row;
                         const int64_t yr = kv_row(c, (int64_t)x.row0 + pair / a.group);
                         const int head = x.h * a.group + pair % a.group;
@@ -784,56 +868,17 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                         for (int y = 0; y < HD / 32; ++y) {
                             const float w[4] = {o[2 * y][n][e] * inv, o[2 * y + 1][n][e] * inv, o[2 * y][n][2 + e] * inv,
                                                 o[2 * y + 1][n][2 + e] * inv};
-                            if (nsplit > 1) store4_f(part + row * HD + 32 * y + 4 * g, w);
+                            if (slot >= 0) store4_f(part + row * HD + 32 * y + 4 * g, w);
                             else store4_f(out + yr * a.ldo + (int64_t)head * HD + 32 * y + 4 * g, w);
                         }
                         if (g != 0) continue;
-                        if (nsplit > 1) {
+                        if (slot >= 0) {
                             part[a.prow * HD + row] = mm[n][e];
                             part[a.prow * (HD + 1) + row] = ll[n][e];
                         } else if (a.lse) {
                             a.lse[yr * a.n_heads + head] = ((mm[n][e] == -INFINITY ? 0.f : mm[n][e]) - P_SHIFT + log2f(ll[n][e])) * LN2;
                         }
                     }
-            }
-            if (nsplit > 1) {
-                // ---- the last item of the unit to arrive joins its runs
-                sync_all();
-                if (threadIdx.x == 0) {
-                    __threadfence();
-                    const int arrived = atomicAdd(a.counters + CTR_UNITS + unit, 1);
-                    flags[2] = arrived == nsplit - 1;
-                    if (arrived == nsplit - 1) a.counters[CTR_UNITS + unit] = 0;    // as the next call finds it
-                    __threadfence();
-                }
-                sync_all();
-                if (flags[2]) {
-                    const float* p0 = a.part + (int64_t)unit * a.splits * a.slot;
-                    for (int i = threadIdx.x; i < x.pairs * (HD / 4); i += 32 * S::NW) {
-                        const int row = i / (HD / 4), d = i % (HD / 4) * 4;
-                        float M = -INFINITY;
-                        for (int k = 0; k < nsplit; ++k) M = fmaxf(M, __ldcg(p0 + k * a.slot + a.prow * HD + row));
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        float L = 0.f;
-#pragma unroll 8
-                        for (int k = 0; k < nsplit; ++k) {
-                            const float* pk = p0 + k * a.slot;
-                            const float mw = __ldcg(pk + a.prow * HD + row);
-                            const float f = mw == -INFINITY ? 1.f : ex2(mw - M);    // 1: 0 or NaN stands there
-                            const float4 u = __ldcg(reinterpret_cast<const float4*>(pk + row * HD + d));
-                            L = fmaf(__ldcg(pk + a.prow * (HD + 1) + row), f, L);
-                            v.x = fmaf(u.x, f, v.x); v.y = fmaf(u.y, f, v.y); v.z = fmaf(u.z, f, v.z); v.w = fmaf(u.w, f, v.w);
-                        }
-                        const int pair = x.pair0 + row;
-                        const int64_t yr = kv_row(c, (int64_t)x.row0 + pair / a.group);
-                        const int head = x.h * a.group + pair % a.group;
-                        const float inv = 1.f / L;
-                        const float w[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-                        store4_f(out + yr * a.ldo + (int64_t)head * HD + d, w);
-                        if (d == 0 && a.lse)
-                            a.lse[yr * a.n_heads + head] = ((M == -INFINITY ? 0.f : M) - P_SHIFT + log2f(L)) * LN2;
-                    }
-                }
             }
             __syncwarp();
             if (lane == 0) tcx::mbar_arrive(item_empty(n_item & 1));
@@ -842,24 +887,68 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
     __syncthreads();
     if (flags[0]) {
         // a wait gave up: let copies that may still be in flight land before the
-        // block's memory goes to another (again bounded); nothing more is written
+        // block's memory goes to another (again bounded)
         if (threadIdx.x == 0) {
             const uint64_t t0 = tcx::globaltimer();
             while (tcx::globaltimer() - t0 < 2000000) {}
         }
-        return;
-    }
-    // the last block to finish leaves the item counter as it found it
-    if (threadIdx.x == 0) {
-        __threadfence();
-        if (atomicAdd(a.counters + CTR_DONE, 1) == (int)gridDim.x - 1) {
-            a.counters[CTR_NEXT] = 0;
-            a.counters[CTR_DONE] = 0;
-        }
     }
 }
 
-constexpr int MAX_UNITS_SPLIT = MLORA_KV_COUNTER_BYTES / 4 - CTR_UNITS;   // a counter for each unit
+// ----------------------------------------------------------------------------
+// Joins the parts of cut units, in order: the block that begins one left its
+// description.  W warps take a pair's parts in turn, lane i HD / 32 dims, and are
+// then added in order; a block holds 8 / W pairs.
+// ----------------------------------------------------------------------------
+template <typename T, int HD, int W>
+__global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ KvView c,
+                                                      const __grid_constant__ AttnCall a, int total) {
+    constexpr int D = HD / 32;
+    __shared__ float sl[8], so[8][HD];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int at = blockIdx.x * (8 / W) + warp / W;         // (block of the attention kernel, pair)
+    const int from = at / a.prow, row = at % a.prow;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the attention kernel's results are visible from here on
+    Cut u = {};
+    if (at < total) u = a.cuts[from];
+    const bool work = u.blocks > 0 && row < u.pairs;
+    auto part = [&](int k) { return a.part + (int64_t)(k == 0 ? 2 * from + 1 : 2 * (from + k)) * a.slot; };
+    float M = -INFINITY, l = 0.f, o[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) o[d] = 0.f;
+    if (work) {
+        for (int k = 0; k < u.blocks; ++k) M = fmaxf(M, part(k)[a.prow * HD + row]);
+#pragma unroll 4
+        for (int k = warp % W; k < u.blocks; k += W) {
+            const float* pk = part(k);
+            const float m = pk[a.prow * HD + row];
+            const float f = m == -INFINITY ? 1.f : ex2(m - M);      // 1: 0 or NaN stands there
+            l = fmaf(pk[a.prow * (HD + 1) + row], f, l);
+#pragma unroll
+            for (int d = 0; d < D; ++d) o[d] = fmaf(pk[row * HD + lane + 32 * d], f, o[d]);
+        }
+    }
+    if (W > 1) {
+        if (lane == 0) sl[warp] = l;
+#pragma unroll
+        for (int d = 0; d < D; ++d) so[warp][lane + 32 * d] = o[d];
+        __syncthreads();
+        if (warp % W != 0) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            l += sl[warp + w];
+#pragma unroll
+            for (int d = 0; d < D; ++d) o[d] += so[warp + w][lane + 32 * d];
+        }
+    }
+    if (!work) return;
+    const int pair = u.pair0 + row;
+    const int64_t y = kv_row(c, (int64_t)u.row0 + pair / a.group);
+    const int head = u.h * a.group + pair % a.group;
+#pragma unroll
+    for (int d = 0; d < D; ++d) static_cast<T*>(a.out)[y * a.ldo + (int64_t)head * HD + lane + 32 * d] = from_f<T>(o[d] / l);
+    if (lane == 0 && a.lse) a.lse[y * a.n_heads + head] = ((M == -INFINITY ? 0.f : M) - P_SHIFT + log2f(l)) * LN2;
+}
 
 template <typename T, int HD, int NT, int RG>
 cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
@@ -878,41 +967,41 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     }
     AttnCall k;
     k.q = a.q; k.out = a.out; k.lse = a.lse; k.ldq = a.ldq; k.ldo = a.ldo; k.max_len = a.max_len;
-    k.counters = static_cast<int*>(a.workspace);
-    k.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + MLORA_KV_COUNTER_BYTES);
     k.n_heads = a.n_heads; k.group = a.n_heads / c.n_kv;
     k.qk = a.scale * LOG2E;
     const int64_t pairs = (int64_t)c.max_rows * k.group;
-    const int64_t tiles = (pairs + S::ROWS - 1) / S::ROWS;
     k.prow = (int)(pairs < S::ROWS ? pairs : S::ROWS);
     k.slot = ((int64_t)k.prow * (HD + 2) + 3) / 4 * 4;      // 16-byte aligned
-    const int64_t units = tiles * c.n_kv * c.n_seqs;
+    const int64_t units = (pairs + S::ROWS - 1) / S::ROWS * c.n_kv * c.n_seqs;
     const int64_t cap = (int64_t)c.max_pages * KV_PAGE;
     const int64_t longest = a.max_len < cap ? a.max_len : cap;
     const int64_t pages = longest > 0 ? (longest + KV_PAGE - 1) / KV_PAGE : 1;
-    // Runs of pages: short enough that every resident block has one and that a
-    // long sequence is no tail of the launch, long enough that an item's start
-    // and the join stay small beside it.
-    const int64_t blocks = (int64_t)n_sms * S::BLOCKS_SM;
-    int64_t chunk = pages;
-    if (units <= MAX_UNITS_SPLIT) {
-        const int64_t per_unit = (KV_ITEMS_BLOCK * blocks + units - 1) / units;
-        chunk = (pages + per_unit - 1) / per_unit;
-        if (chunk > KV_LONG_RUN) chunk = KV_LONG_RUN;
-        if (chunk < KV_SHORT_RUN) chunk = KV_SHORT_RUN;
-        const int64_t slots = (a.workspace_bytes - MLORA_KV_COUNTER_BYTES) / (k.slot * 4);
-        const int64_t most = slots / units;                 // runs of a unit that the workspace holds
-        if (most < 2) chunk = pages;
-        else if ((pages + chunk - 1) / chunk > most) chunk = (pages + most - 1) / most;
-    }
-    k.tiles = (int)tiles;
-    k.chunk = (int)(chunk < pages ? chunk : pages);
-    k.splits = (int)((pages + k.chunk - 1) / k.chunk);
-    const int64_t items = units * k.splits;
-    if (items > (1 << 30)) return cudaErrorInvalidConfiguration;
-    k.items = (int)items;
-    kv_attn_kernel<T, HD, NT, RG><<<(unsigned)(items < blocks ? items : blocks), S::THREADS, S::SMEM, s>>>(c, k);
-    return cudaGetLastError();
+    // The blocks' equal shares cut sequences anywhere; a share's two ends leave
+    // partial results.  Short sequences and small workspaces: whole units only.
+    const int64_t most = (int64_t)n_sms * S::BLOCKS_SM;
+    int64_t blocks = (units * pages + KV_SHORT_RUN - 1) / KV_SHORT_RUN;
+    if (blocks > most) blocks = most;
+    const bool cut = pages > KV_WHOLE && a.workspace &&
+                     a.workspace_bytes >= blocks * (2 * k.slot * (int64_t)sizeof(float) + (int64_t)sizeof(Cut));
+    if (!cut) blocks = units < most ? units : most;
+    k.part = static_cast<float*>(a.workspace);
+    k.cuts = cut ? reinterpret_cast<Cut*>(k.part + blocks * 2 * k.slot) : nullptr;
+    kv_attn_kernel<T, HD, NT, RG><<<(unsigned)blocks, S::THREADS, S::SMEM, s>>>(c, k);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !cut) return e;
+    // the join waits on the device for the attention kernel's end: only its launch overlaps it
+    const int total = (int)(blocks * k.prow);
+    const bool many = blocks / units > 8;                   // parts of a unit: 8 warps a pair, or one
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(many ? total : (total + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, many ? kv_join_kernel<T, HD, 8> : kv_join_kernel<T, HD, 1>, c, k, total);
 }
 
 // One column tile (8 pairs; 4 on fp32) where a sequence's pairs fit it, then two;
@@ -958,10 +1047,8 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
         ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out)) & 15))
         return kv_fail(MLORA_E_ARG, "query and output rows must be 16-byte aligned and at least %lld elements apart",
                        (long long)row);
-    if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & 15) ||
-        a->workspace_bytes < MLORA_KV_COUNTER_BYTES)
-        return kv_fail(MLORA_E_ARG, "the workspace must be 16-byte aligned and hold at least %d bytes",
-                       MLORA_KV_COUNTER_BYTES);
+    if ((reinterpret_cast<uintptr_t>(a->workspace) & 15) || a->workspace_bytes < 0)
+        return kv_fail(MLORA_E_ARG, "the workspace must be 16-byte aligned");
     if ((int64_t)w.max_rows * a->n_heads > INT32_MAX / w.n_seqs)
         return kv_fail(MLORA_E_ARG, "too many sequences, rows and heads for one call");
     KvAttnArgs k;

@@ -28,7 +28,7 @@ int kv_check(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, KvV
     if (!c->k || !c->v || !c->k_scale || !c->v_scale) return kv_fail(MLORA_E_ARG, "NULL cache buffer");
     if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15)
         return kv_fail(MLORA_E_ARG, "cache buffers must be 16-byte aligned");
-    if (q->n_seqs < 0 || q->n_rows < 0 || q->n_rows > INT32_MAX || q->max_pages < 1 || q->max_rows < 0)
+    if (q->n_seqs < 0 || q->n_seqs > (1 << 24) || q->n_rows < 0 || q->n_rows > INT32_MAX || q->max_pages < 1 || q->max_rows < 0)
         return kv_fail(MLORA_E_ARG, "bad sequences (n_seqs %d, n_rows %lld, max_pages %d, max_rows %d)", q->n_seqs,
                        (long long)q->n_rows, q->max_pages, q->max_rows);
     if (!q->row_off && (q->max_rows != 1 || q->n_rows < q->n_seqs))
@@ -87,7 +87,11 @@ __global__ void __launch_bounds__(UT) kv_append_kernel(const __grid_constant__ K
     __shared__ float part[UT / 32];
     const KvUnit u = kv_unit(blockIdx.x, pages, c.n_kv);
     SeqRows r;
-    if (!kv_seq(c, u.s, INT64_MAX, r) || r.len == 0 || r.n == 0) return;
+    if (!kv_seq(c, u.s, INT64_MAX, r)) {
+        if (threadIdx.x == 0) raise_status(c.status, ST_RANGE);
+        return;
+    }
+    if (r.len == 0 || r.n == 0) return;
     const int start = r.len - r.n;
     const int page = start / KV_PAGE + u.p;
     if ((int64_t)page * KV_PAGE >= r.len) return;
@@ -197,7 +201,11 @@ __global__ void __launch_bounds__(128) kv_read_kernel(const __grid_constant__ Kv
     T* dst = u.is_v ? vo : ko;
     if (!dst) return;
     SeqRows r;
-    if (!kv_seq(c, u.s, INT64_MAX, r) || r.len == 0 || r.n == 0) return;
+    if (!kv_seq(c, u.s, INT64_MAX, r)) {
+        if (threadIdx.x == 0) raise_status(c.status, ST_RANGE);
+        return;
+    }
+    if (r.len == 0 || r.n == 0) return;
     const int start = r.len - r.n;
     const int page = start / KV_PAGE + u.p;
     if ((int64_t)page * KV_PAGE >= r.len) return;

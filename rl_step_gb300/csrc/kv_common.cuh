@@ -36,23 +36,21 @@ struct SeqRows {
     int row0;                          // the first of them
 };
 
-// Reads sequence s; false (and the status bit) if it is outside the ranges of
-// the header.  Everything in r is then unusable but row0 / n, which
-// kv_bad_rows() clips.
-__device__ __forceinline__ bool kv_seq(const KvView& c, int s, int64_t max_len, SeqRows& r) {
-    r.len = c.kv_len[s];
-    int64_t a = s, b = (int64_t)s + 1;
-    if (c.row_off) {
-        a = c.row_off[s];
-        b = c.row_off[s + 1];
-    }
+// A sequence's length and rows [a, b) against the ranges of the header; where
+// they are outside, only row0 and n of r can be used, clipped to the rows that
+// exist.
+__device__ __forceinline__ bool kv_seq_ok(const KvView& c, int len, int64_t a, int64_t b, int64_t max_len, SeqRows& r) {
+    r.len = len;
     r.row0 = (int)a;
     r.n = (int)(b - a < INT32_MAX ? b - a : INT32_MAX);
     const int64_t cap = (int64_t)c.max_pages * KV_PAGE;
-    const bool ok = r.len >= 0 && r.len <= cap && r.len <= max_len && a >= 0 && b >= a && b <= c.n_rows &&
-                    r.n <= c.max_rows && (r.n <= r.len || r.len == 0);
-    if (!ok) raise_status(c.status, ST_RANGE);
-    return ok;
+    return len >= 0 && len <= cap && len <= max_len && a >= 0 && b >= a && b <= c.n_rows && r.n <= c.max_rows &&
+           (r.n <= len || len == 0);
+}
+// Reads and checks sequence s (no status).
+__device__ __forceinline__ bool kv_seq(const KvView& c, int s, int64_t max_len, SeqRows& r) {
+    return kv_seq_ok(c, c.kv_len[s], c.row_off ? c.row_off[s] : s, c.row_off ? c.row_off[s + 1] : (int64_t)s + 1, max_len,
+                     r);
 }
 
 // Page id of a sequence's page p, or -1 (and the status bit) if it is no page.

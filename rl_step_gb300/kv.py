@@ -25,8 +25,7 @@ from . import _check, _stream, load_library
 __all__ = ["PAGE", "KvCache", "kv_workspace", "kv_append", "kv_read", "kv_attention", "kv_check_status"]
 
 PAGE = 64
-COUNTER_BYTES = 65536
-WORKSPACE_BYTES = 32 << 20
+WORKSPACE_BYTES = 16 << 20
 
 
 class _KvCache(ctypes.Structure):
@@ -108,9 +107,10 @@ class KvCache:
 
 
 def kv_workspace(device="cuda", nbytes: int = WORKSPACE_BYTES):
-    """A zeroed workspace of kv_attention; calls that may overlap need one each."""
+    """A workspace of kv_attention; calls that may overlap need one each.  With
+    nbytes = 0 no sequence is cut and results do not depend on the batch."""
     import torch
-    return torch.zeros(max(int(nbytes), COUNTER_BYTES), dtype=torch.uint8, device=device)
+    return torch.empty(int(nbytes), dtype=torch.uint8, device=device)
 
 
 def _ids(name, t, shape, device):
@@ -170,7 +170,7 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
     """Attention of the rows q [n_rows, n_heads, head_dim] over their sequences'
     cached positions up to their own.  Returns (out like q, lse float32
     [n_rows, n_heads]); scale defaults to 1 / sqrt(head_dim).  Without a
-    workspace one is allocated and zeroed for the call."""
+    workspace one is allocated for the call."""
     import torch
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
@@ -200,8 +200,7 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
 
 def kv_check_status(cache: KvCache, stream=None) -> int:
     """Synchronise, return and clear the cache's status: 0, -2 (E_RANGE), or -5
-    (E_TIMEOUT: a bounded device wait gave up; zero the workspace before its
-    next use)."""
+    (E_TIMEOUT: a bounded device wait gave up)."""
     import torch
     (stream or torch.cuda.current_stream()).synchronize()
     bad = int(cache.status.item())

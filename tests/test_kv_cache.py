@@ -93,7 +93,7 @@ _BAD = [("c", "n_pages", 0), ("c", "n_kv_heads", 0), ("c", "n_kv_heads", 1025), 
 @pytest.mark.parametrize("where,field,value", _BAD + [
     ("a", "n_heads", 3), ("a", "n_heads", 0), ("a", "scale", math.inf), ("a", "scale", math.nan), ("a", "max_len", -1),
     ("a", "q", None), ("a", "out", None), ("a", "q", 4104), ("a", "q_stride", 511), ("a", "q_stride", 516),
-    ("a", "out_stride", 256), ("a", "workspace", None), ("a", "workspace", 4104), ("a", "workspace_bytes", 65535),
+    ("a", "out_stride", 256), ("a", "workspace", 4104), ("a", "workspace_bytes", -1),
     ("a", "dtype", 2)])
 def test_attention_refuses(where, field, value):
     kv, lib, c, q, a = _valid()
@@ -148,7 +148,7 @@ def test_kv_header_and_binding_agree(tmp_path):
     for name, cls in structs:
         lines.append(f'printf("%zu ", sizeof({name}));')
         lines += [f'printf("%zu ", offsetof({name}, {f[0]}));' for f in cls._fields_]
-    lines.append('printf("%d %d\\n", MLORA_KV_PAGE, MLORA_KV_COUNTER_BYTES); return 0; }')
+    lines.append('printf("%d %d\\n", MLORA_KV_PAGE, MLORA_KV_WORKSPACE_BYTES); return 0; }')
     (tmp_path / "a.c").write_text("\n".join(lines))
     subprocess.run([cc, "-std=c11", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(tmp_path / "a.c"),
                     "-o", str(tmp_path / "a")], check=True, capture_output=True)
@@ -156,7 +156,7 @@ def test_kv_header_and_binding_agree(tmp_path):
     want = []
     for _, cls in structs:
         want += [ctypes.sizeof(cls)] + [getattr(cls, f[0]).offset for f in cls._fields_]
-    assert got == want + [kv.PAGE, kv.COUNTER_BYTES]
+    assert got == want + [kv.PAGE, kv.WORKSPACE_BYTES]
     src = re.sub(r"/\*.*?\*/", "", "".join(open(os.path.join(root, "include", h)).read()
                                           for h in ("mlora_kv.h", "mlora.h")), flags=re.S)
     for name, (_, args) in {**kv._SIGNATURES, **gr._SIGNATURES}.items():
@@ -378,10 +378,9 @@ def test_attention_split_over_a_long_cache(n_seqs, length):
     st.append(lens)
     ws = st.kv.kv_workspace()
     q, out, lse = _attend(st, [1] * n_seqs, 8, workspace=ws)
-    assert int(ws[:st.kv.COUNTER_BYTES].max()) == 0
     _, o2, l2 = _attend(st, [1] * n_seqs, 8, q=q, workspace=ws)
     assert torch.equal(out, o2) and torch.equal(lse, l2)               # bit for bit
-    for nbytes in (65536, 65536 + 40000, 65536 + 300000):
+    for nbytes in (0, 16, 40000, 300000, 4000000):
         _attend(st, [1] * n_seqs, 8, q=q, workspace=st.kv.kv_workspace(nbytes=nbytes))
     _attend(st, [3] * n_seqs, 8)
     _attend(st, [1] * n_seqs, 8, q=q, slack=100000)                    # a loose bound of the lengths
@@ -600,16 +599,19 @@ def test_two_calls_at_once_with_a_workspace_each():
 
 @pytest.mark.gpu
 def test_a_row_does_not_depend_on_its_batch():
+    """without a workspace no sequence is cut: bit for bit the same row in every batch"""
     torch = _torch()
     lens = [900, 3, 450, 64, 2000]
     st = Setup(lens, 2, 128, seed=13)
     st.append(lens)
     q = torch.randn(5, 8, 128, device="cuda").bfloat16()
-    ws = st.kv.kv_workspace()
+    ws = st.kv.kv_workspace(nbytes=0)
     out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(lens), q, 2000, workspace=ws)
     other = [n if s == 2 else 1 for s, n in enumerate(lens)]
     o2, l2 = st.kv.kv_attention(st.cache, st.dtable, st.i32(other), q, 2000, workspace=ws)
     assert torch.equal(out[2], o2[2]) and torch.equal(lse[2], l2[2])
+    o3, l3 = st.kv.kv_attention(st.cache, st.dtable[2:3].contiguous(), st.i32([450]), q[2:3], 450, workspace=ws)
+    assert torch.equal(out[2:3], o3) and torch.equal(lse[2:3], l3)
 
 
 @pytest.mark.gpu
@@ -632,6 +634,6 @@ def test_python_refusals():
     with pytest.raises(m.MLoRAError):
         kv.kv_attention(c, tab, lens, torch.zeros(1, 3, 128, device="cuda"), 64)       # 3 heads over 2
     with pytest.raises(m.MLoRAError):
-        kv.kv_attention(c, tab, lens, x, 64, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+        kv.kv_attention(c, tab, lens, x, 64, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")[4:])
     with pytest.raises(m.MLoRAError):
         kv.kv_append(c, tab, lens, x, x, max_rows=2)                                   # row_off is missing
