@@ -208,8 +208,6 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
     auto item_empty = [&](int i) { return sbase + S::BAR + 16 * S::STAGES + 16 + 8 * i; };
     const uint32_t q_full = sbase + S::BAR + 16 * S::STAGES + 32, q_empty = q_full + 8;
 
-    __shared__ int64_t warp_sum[S::NW + 1], s_rem;
-    __shared__ int s_first;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             tcx::mbar_init(full(i), 1);
@@ -222,59 +220,47 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
         tcx::mbar_init(q_full, 1);
         tcx::mbar_init(q_empty, S::NW);
         flags[0] = 0;
-        s_first = c.n_seqs;                                 // (no share, unless a sequence of it is found)
-        s_rem = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // ---- the block's share.  The pages of all units -- sequence by sequence, then
-    // key/value head, row tile, page -- are one line of `total` pages, cut into
-    // equal shares; every block adds the sequences up for itself.
-    auto weight = [&](const SeqRows& r) -> int64_t {
-        return (int64_t)((r.len + KV_PAGE - 1) / KV_PAGE) * ((r.n * a.group + S::ROWS - 1) / S::ROWS) * c.n_kv;
-    };
-    int64_t mine = 0, upto;
-    const int per = (c.n_seqs + S::THREADS - 1) / S::THREADS, s0 = threadIdx.x * per;
-    for (int s = s0; s < s0 + per && s < c.n_seqs; ++s) {
-        SeqRows r;
-        if (kv_seq(c, s, a.max_len, r)) mine += weight(r);
-    }
-    upto = mine;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
-        upto += lane >= x ? y : 0;
-    }
-    if (lane == 31) warp_sum[warp] = upto;
     __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w <= S::NW; ++w) {
-        upto += w < warp ? warp_sum[w] : 0;
-        total += warp_sum[w];
-    }
-    int64_t shares = a.cuts ? (total + KV_SHORT_RUN - 1) / KV_SHORT_RUN : total;
-    if (shares > gridDim.x) shares = gridDim.x;
-    const bool busy = (int)blockIdx.x < shares;
-    const int64_t lo = busy ? (int64_t)blockIdx.x * total / shares : 0, hi = busy ? ((int64_t)blockIdx.x + 1) * total / shares : 0;
-    if (busy && upto - mine <= lo && lo < upto) {
-        int64_t rem = lo - (upto - mine);
-        for (int s = s0;; ++s) {
-            SeqRows r;
-            const int64_t w = s < c.n_seqs && kv_seq(c, s, a.max_len, r) ? weight(r) : 0;
-            if (rem < w || s >= c.n_seqs) {
-                s_first = s;
-                s_rem = rem;
-                break;
-            }
-            rem -= w;
-        }
-    }
-    __syncthreads();
+    // the join's blocks may be set up while this kernel runs; they wait for its end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == S::NW) {
         // ---- producer
         const T* q = static_cast<const T*>(a.q);
         T* out = static_cast<T*>(a.out);
+        // The block's share.  The pages of all units -- sequence by sequence, then
+        // key/value head, row tile, page -- are one line of `total` pages, cut into
+        // equal shares; every block adds the sequences up for itself, a lane `per`
+        // of them.
+        auto weight = [&](const SeqRows& r) -> int64_t {
+            return (int64_t)((r.len + KV_PAGE - 1) / KV_PAGE) * ((r.n * a.group + S::ROWS - 1) / S::ROWS) * c.n_kv;
+        };
+        const int per = (c.n_seqs + 31) / 32, s0 = lane * per;
+        int64_t mine = 0;
+#pragma unroll 4
+        for (int i = 0; i < per; ++i) {
+            SeqRows r;
+            const int s = s0 + i < c.n_seqs ? s0 + i : c.n_seqs - 1;
+            const bool ok = kv_seq(c, s, a.max_len, r);
+            mine += ok && s0 + i < c.n_seqs ? weight(r) : 0;
+        }
+        int64_t upto = mine;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+            upto += lane >= x ? y : 0;
+        }
+        const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+        int64_t shares = a.cuts ? (total + KV_SHORT_RUN - 1) / KV_SHORT_RUN : total;
+        if (shares > gridDim.x) shares = gridDim.x;
+        const bool busy = (int)blockIdx.x < shares;
+        const int64_t lo = busy ? (int64_t)blockIdx.x * total / shares : 0, hi = busy ? ((int64_t)blockIdx.x + 1) * total / shares : 0;
+        // the lane whose sequences hold page lo; next() goes on from its first one
+        const unsigned holds = __ballot_sync(0xffffffffu, upto - mine <= lo && lo < upto);
+        const int from = holds ? __ffs(holds) - 1 : 0;
+        const int64_t before = __shfl_sync(0xffffffffu, upto - mine, from);
         // a bounded wait of lane 0 that the warp follows
         auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
             int ok = 1;
@@ -286,8 +272,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
         // The items of the share, in order.  A warp's lanes hold the lengths and rows of the next 32 sequences.
-        int64_t pos = lo, rem = busy ? s_rem : 0;           // place in the line; pages of the sequence before it
-        int s_now = busy ? s_first : 0, s_base = s_now;
+        int64_t pos = lo, rem = lo - before;                // place in the line; pages from the first of s_now's on
+        int s_now = from * per, s_base = s_now;
         int l_len = 0;
         int64_t l_a = 0, l_b = 0;
         auto lengths = [&]() {
@@ -309,8 +295,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                 const int64_t row_a = __shfl_sync(0xffffffffu, l_a, s_now - s_base);
                 const int64_t row_b = __shfl_sync(0xffffffffu, l_b, s_now - s_base);
                 const int64_t w = kv_seq_ok(c, len, row_a, row_b, a.max_len, r) ? weight(r) : 0;
-                if (rem >= w) {                             // the sequence is done, or has none
-                    rem = 0;
+                if (rem >= w) {                             // behind the sequence
+                    rem -= w;
                     ++s_now;
                     continue;
                 }
@@ -917,7 +903,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
     if (work) {
-        for (int k = 0; k < u.blocks; ++k) M = fmaxf(M, part(k)[a.prow * HD + row]);
+        for (int k = lane; k < u.blocks; k += 32) M = fmaxf(M, part(k)[a.prow * HD + row]);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
 #pragma unroll 4
         for (int k = warp % W; k < u.blocks; k += W) {
             const float* pk = part(k);
