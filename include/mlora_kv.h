@@ -53,7 +53,7 @@ extern "C" {
 #define MLORA_KV_PAGE 64
 #define MLORA_KV_MIN_EXP (-100)
 /* An attention workspace that serves every shape. */
-#define MLORA_KV_WORKSPACE_BYTES (16 << 20)
+#define MLORA_KV_WORKSPACE_BYTES (32 << 20)
 
 /* A pool of pages (DEVICE buffers).  k, v: n_pages * n_kv_heads * 64 *
  * head_dim bytes, 16-byte aligned; scales: n_pages * n_kv_heads. */

@@ -41,10 +41,12 @@
 //    item's end, so nothing but the ring's barriers is shared in the loop.
 //  * A share's ends cut sequences: such an item leaves its rows' unnormalised
 //    sums, maximum and sum in the workspace, and a second small kernel joins the
-//    parts in order.  (Runs of a fixed length, taken from a counter, either left
-//    a tail -- items of 16 pages: 94 us where equal shares take @@ -- or ended too
-//    often; joined by the last item to arrive, a run's end cost its block about
-//    6 us of fences and atomics.)
+//    parts in order.  (Runs of a fixed length taken from a counter left a tail or
+//    ended too often: 94 us at best for 32 sequences of 1023 to 8191 tokens, 4
+//    rows each, which equal shares serve in 65; joined by the last item to
+//    arrive, a run's end cost its block about 6 us of fences and atomics.  Warps
+//    that each stream a share of their own hide the ends of items better but
+//    end 84 to 125 us after the start where blocks' shares end together.)
 #include <atomic>
 #include <type_traits>
 
@@ -59,7 +61,11 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
 constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
-constexpr int KV_SHORT_RUN = 2;             // pages: no block gets fewer
+constexpr int KV_SHORT_RUN = 2;             // places: no block gets fewer
+// What a unit's start and end cost, in pages.  41 sequences of 0 to 3001 tokens,
+// 16 heads of 64, fp32: 58 us at 0, 45 at 2, 36 at 4, 37 at 6; 256 sequences of
+// 512 to 2048, 8 heads of 128: 130, 125, 123, 121 us.
+constexpr int KV_START = 5;
 constexpr int KV_WHOLE = 4;                 // pages: sequences up to this are not cut
 
 // A cut unit, left in the workspace by the block that begins it.
@@ -230,12 +236,12 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
         // ---- producer
         const T* q = static_cast<const T*>(a.q);
         T* out = static_cast<T*>(a.out);
-        // The block's share.  The pages of all units -- sequence by sequence, then
-        // key/value head, row tile, page -- are one line of `total` pages, cut into
-        // equal shares; every block adds the sequences up for itself, a lane `per`
-        // of them.
+        // The block's share.  All units -- sequence by sequence, then key/value head,
+        // row tile -- are one line of `total` places, KV_START for a unit's start and
+        // one for each page, cut into equal shares; every block adds the sequences
+        // up for itself, a lane `per` of them.
         auto weight = [&](const SeqRows& r) -> int64_t {
-            return (int64_t)((r.len + KV_PAGE - 1) / KV_PAGE) * ((r.n * a.group + S::ROWS - 1) / S::ROWS) * c.n_kv;
+            return r.len > 0 ? (int64_t)((r.len + KV_PAGE - 1) / KV_PAGE + KV_START) * ((r.n * a.group + S::ROWS - 1) / S::ROWS) * c.n_kv : 0;
         };
         const int per = (c.n_seqs + 31) / 32, s0 = lane * per;
         int64_t mine = 0;
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
         if (shares > gridDim.x) shares = gridDim.x;
         const bool busy = (int)blockIdx.x < shares;
         const int64_t lo = busy ? (int64_t)blockIdx.x * total / shares : 0, hi = busy ? ((int64_t)blockIdx.x + 1) * total / shares : 0;
-        // the lane whose sequences hold page lo; next() goes on from its first one
+        // the lane whose sequences hold place lo; next() goes on from its first one
         const unsigned holds = __ballot_sync(0xffffffffu, upto - mine <= lo && lo < upto);
         const int from = holds ? __ffs(holds) - 1 : 0;
         const int64_t before = __shfl_sync(0xffffffffu, upto - mine, from);
@@ -272,7 +278,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
         // The items of the share, in order.  A warp's lanes hold the lengths and rows of the next 32 sequences.
-        int64_t pos = lo, rem = lo - before;                // place in the line; pages from the first of s_now's on
+        int64_t pos = lo, rem = lo - before;                // place in the line, and from the first of s_now's on
         int s_now = from * per, s_base = s_now;
         int l_len = 0;
         int64_t l_a = 0, l_b = 0;
@@ -301,15 +307,17 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                     continue;
                 }
                 const int pages = (len + KV_PAGE - 1) / KV_PAGE, tiles = (r.n * a.group + S::ROWS - 1) / S::ROWS;
-                const int unit = (int)(rem / pages), page0 = (int)(rem % pages);
-                int np = pages - page0;
+                const int size = pages + KV_START;
+                const int unit = (int)(rem / size), off = (int)(rem % size);
+                int step = size - off;                      // places of the unit from here on
                 if (a.cuts) {
-                    if (np > hi - pos) np = (int)(hi - pos);
-                } else if (page0 > 0) {                     // not cut: the unit is the block's where it begins
-                    pos += np;
-                    rem += np;
-                    continue;
+                    if (step > hi - pos) step = (int)(hi - pos);
                 }
+                pos += step;
+                rem += step;
+                const int page0 = off > KV_START ? off - KV_START : 0, np = off + step - KV_START - page0;
+                // nothing but a start; or not cut: the unit is the block's where its line begins
+                if (np <= 0 || (!a.cuts && off > 0)) continue;
                 const int tile = unit % tiles;
                 x.s = s_now;
                 x.h = unit / tiles;
@@ -325,13 +333,11 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                 } else if (np < pages) {
                     x.slot = 2 * blockIdx.x + 1;
                     if (lane == 0) {
-                        const int64_t end = pos + pages;    // the block of page p is ((p + 1) shares - 1) / total
+                        const int64_t end = pos - step + size - off;    // the share of place p is ((p + 1) shares - 1) / total
                         a.cuts[blockIdx.x] = Cut{(int)((end * shares - 1) / total) - (int)blockIdx.x + 1, x.row0, x.pair0, x.pairs, x.h};
                     }
                     __syncwarp();
                 }
-                pos += np;
-                rem += np;
                 return;
             }
         };
@@ -949,6 +955,9 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     if (dev < 64) n_sms = sms[dev].load(std::memory_order_relaxed);
     if (n_sms == 0) {
         e = cudaFuncSetAttribute(kv_attn_kernel<T, HD, NT, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kv_attn_kernel<T, HD, NT, RG>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
         if (dev < 64) sms[dev].store(n_sms, std::memory_order_relaxed);

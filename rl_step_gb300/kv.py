@@ -25,7 +25,7 @@ from . import _check, _stream, load_library
 __all__ = ["PAGE", "KvCache", "kv_workspace", "kv_append", "kv_read", "kv_attention", "kv_check_status"]
 
 PAGE = 64
-WORKSPACE_BYTES = 16 << 20
+WORKSPACE_BYTES = 32 << 20
 
 
 class _KvCache(ctypes.Structure):
