@@ -66,7 +66,7 @@ constexpr int KV_SHORT_RUN = 2;             // places: no block gets fewer
 // 16 heads of 64, fp32: 58 us at 0, 45 at 2, 36 at 4, 37 at 6; 256 sequences of
 // 512 to 2048, 8 heads of 128: 130, 125, 123, 121 us.
 constexpr int KV_START = 5;
-constexpr int KV_WHOLE = 4;                 // pages: sequences up to this are not cut
+constexpr int KV_WHOLE = 8;                 // pages: sequences up to this are not cut
 
 // A cut unit, left in the workspace by the block that begins it.
 struct Cut {

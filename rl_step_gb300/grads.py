@@ -10,7 +10,10 @@ import ctypes
 from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_void_p
 from typing import Optional, Sequence
 
-from . import _check, _stream, load_library
+import torch
+
+from . import _check, load_library
+from .kv import _on
 
 __all__ = ["GradSet", "clip_grads"]
 
@@ -47,7 +50,6 @@ class GradSet:
 
     def __init__(self, grads: Sequence, groups: Optional[Sequence[int]] = None, n_groups: Optional[int] = None,
                  out: Optional[Sequence] = None):
-        import torch
         self.grads, self.out = list(grads), None if out is None else list(out)
         n = len(self.grads)
         if n == 0:
@@ -70,6 +72,7 @@ class GradSet:
         self._c = _GradSet(self._arrays[0], self._arrays[1], self._arrays[2], self._arrays[3], n, self.n_groups,
                            0 if dtype == torch.bfloat16 else 1)
         self._ref = byref(self._c)
+        self.index = self.grads[0].get_device()
         self._bytes = int(_lib().mlora_clip_grads_workspace(self._ref))
         if self._bytes == 0:                      # refused: raise its message
             _check(_lib().mlora_clip_grads(self._ref, 0.0, None, None, 0, None))
@@ -79,14 +82,12 @@ class GradSet:
 def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):
     """Clip each group of gs to max_norm; returns the norms before clipping
     (float32 [n_groups]).  Calls on one GradSet must be serialised."""
-    import torch
-    if gs.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {gs.device}, which is not the current device")
+    stream = _on(gs.index, stream)
     if norms_out is None:
         norms_out = torch.empty(gs.n_groups, dtype=torch.float32, device=gs.device)
-    elif norms_out.dtype != torch.float32 or norms_out.numel() != gs.n_groups or not norms_out.is_contiguous() or \
-            norms_out.device != gs.device:
+    elif norms_out.dtype is not torch.float32 or norms_out.numel() != gs.n_groups or \
+            not norms_out.is_contiguous() or norms_out.get_device() != gs.index:
         raise ValueError("norms_out must be a contiguous float32 tensor with a value for each group")
     _check(_lib().mlora_clip_grads(gs._ref, max_norm, norms_out.data_ptr(), gs.workspace.data_ptr(), gs._bytes,
-                                   _stream(stream)))
+                                   stream))
     return norms_out

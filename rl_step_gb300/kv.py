@@ -20,7 +20,9 @@ import ctypes
 import math
 from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_void_p
 
-from . import _check, _stream, load_library
+import torch
+
+from . import _check, load_library
 
 __all__ = ["PAGE", "KvCache", "kv_workspace", "kv_append", "kv_read", "kv_attention", "kv_check_status"]
 
@@ -66,13 +68,22 @@ def _lib():
     return _kv_lib
 
 
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_INT32, _FLOAT32 = torch.int32, torch.float32
+
+
 def _dtype(t) -> int:
-    import torch
-    if t == torch.bfloat16:
-        return 0
-    if t == torch.float32:
-        return 1
-    raise ValueError(f"dtype {t}: bfloat16 or float32 is needed")
+    d = _DTYPES.get(t)
+    if d is None:
+        raise ValueError(f"dtype {t}: bfloat16 or float32 is needed")
+    return d
+
+
+def _on(index: int, stream) -> int:
+    """The stream's handle (None: the current one of device `index`, which has to be the current device)."""
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 class KvCache:
@@ -81,7 +92,6 @@ class KvCache:
     [n_pages, n_kv_heads], contiguous CUDA tensors that the cache keeps alive."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
         n_pages, n_kv, page, hd = k.shape
         if page != PAGE or tuple(v.shape) != tuple(k.shape):
             raise ValueError(f"k and v must be [n_pages, n_kv_heads, {PAGE}, head_dim]")
@@ -94,13 +104,13 @@ class KvCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.n_pages, self.n_kv_heads, self.head_dim, self.device = n_pages, n_kv, hd, k.device
+        self.index = k.get_device()
         self._c = _KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                            self.status.data_ptr(), n_pages, n_kv, hd)
         self._ref = byref(self._c)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> "KvCache":
-        import torch
         shape = (n_pages, n_kv_heads, PAGE, head_dim)
         return cls(*[torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)],
                    *[torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)])
@@ -109,35 +119,34 @@ class KvCache:
 def kv_workspace(device="cuda", nbytes: int = WORKSPACE_BYTES):
     """A workspace of kv_attention; calls that may overlap need one each.  With
     nbytes = 0 no sequence is cut and results do not depend on the batch."""
-    import torch
     return torch.empty(int(nbytes), dtype=torch.uint8, device=device)
 
 
-def _ids(name, t, shape, device):
-    import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+def _ids(name, t, shape, index) -> int:
+    if t.dtype is not _INT32 or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the cache's device")
     return t.data_ptr()
 
 
 def _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows) -> _KvSeqs:
-    import torch
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seqs, max_pages]")
     n, width = page_table.shape
-    dev = cache.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, which is not the current device")
-    return _KvSeqs(_ids("page_table", page_table, (n, width), dev), _ids("kv_len", kv_len, (n,), dev),
-                   None if row_off is None else _ids("row_off", row_off, (n + 1,), dev), n_rows, n, width, max_rows)
+    index = cache.index
+    return _KvSeqs(_ids("page_table", page_table, (n, width), index), _ids("kv_len", kv_len, (n,), index),
+                   None if row_off is None else _ids("row_off", row_off, (n + 1,), index), n_rows, n, width, max_rows)
 
 
-def _rows(name, x, heads, hd, device) -> int:
+def _rows(name, x, heads, hd, index) -> int:
     """Row distance in elements of [n, heads, hd] rows whose heads lie side by side."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != hd or x.device != device:
-        raise ValueError(f"{name} must be [rows, {heads}, {hd}] on {device}")
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != hd or x.get_device() != index:
+        raise ValueError(f"{name} must be [rows, {heads}, {hd}] on the cache's device")
+    if x.is_contiguous():
+        return heads * hd
     st = x.stride()
-    if (st[2] != 1 and hd != 1) or (st[1] != hd and heads != 1):
+    if st[2] != 1 or (st[1] != hd and heads != 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return st[0] if x.shape[0] > 1 else max(st[0], heads * hd)
+    return st[0] if x.shape[0] > 1 else heads * hd
 
 
 def kv_append(cache: KvCache, page_table, kv_len, k, v, row_off=None, max_rows: int = 1, stream=None):
@@ -145,23 +154,22 @@ def kv_append(cache: KvCache, page_table, kv_len, k, v, row_off=None, max_rows: 
     may be any multiple of 16 bytes apart) as the newest tokens of their
     sequences."""
     q = _seqs(cache, page_table, kv_len, row_off, k.shape[0], max_rows)
-    ldk = _rows("k", k, cache.n_kv_heads, cache.head_dim, cache.device)
-    ldv = _rows("v", v, cache.n_kv_heads, cache.head_dim, cache.device)
+    ldk = _rows("k", k, cache.n_kv_heads, cache.head_dim, cache.index)
+    ldv = _rows("v", v, cache.n_kv_heads, cache.head_dim, cache.index)
     if v.shape[0] != k.shape[0] or v.dtype != k.dtype:
         raise ValueError("k and v must have the same rows and dtype")
     _check(_lib().mlora_kv_append(cache._ref, byref(q), _dtype(k.dtype), k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                  _stream(stream)))
+                                  _on(cache.index, stream)))
 
 
 def kv_read(cache: KvCache, page_table, kv_len, n_rows: int, row_off=None, max_rows: int = 1, dtype=None, stream=None):
     """(k, v) [n_rows, n_kv_heads, head_dim] of the newest tokens, as float32 (default) or bf16."""
-    import torch
     dtype = torch.float32 if dtype is None else dtype
     q = _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows)
     shape = (n_rows, cache.n_kv_heads, cache.head_dim)
     ko = torch.empty(shape, dtype=dtype, device=cache.device)
     vo = torch.empty(shape, dtype=dtype, device=cache.device)
-    _check(_lib().mlora_kv_read(cache._ref, byref(q), _dtype(dtype), ko.data_ptr(), vo.data_ptr(), _stream(stream)))
+    _check(_lib().mlora_kv_read(cache._ref, byref(q), _dtype(dtype), ko.data_ptr(), vo.data_ptr(), _on(cache.index, stream)))
     return ko, vo
 
 
@@ -171,37 +179,35 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
     cached positions up to their own.  Returns (out like q, lse float32
     [n_rows, n_heads]); scale defaults to 1 / sqrt(head_dim).  Without a
     workspace one is allocated for the call."""
-    import torch
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
     n_rows, heads, hd = q.shape
     s = _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows)
-    ldq = _rows("q", q, heads, cache.head_dim, cache.device)
+    ldq = _rows("q", q, heads, cache.head_dim, cache.index)
     if out is None:
-        out = torch.empty((n_rows, heads, hd), dtype=q.dtype, device=cache.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != q.dtype or out.shape[0] != n_rows:
         raise ValueError("out must have q's rows and dtype")
-    ldo = _rows("out", out, heads, cache.head_dim, cache.device)
+    ldo = _rows("out", out, heads, cache.head_dim, cache.index)
     if lse is None:
         lse = torch.empty((n_rows, heads), dtype=torch.float32, device=cache.device)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (n_rows, heads) or not lse.is_contiguous() or \
-            lse.device != cache.device:
+    elif lse.dtype is not _FLOAT32 or lse.shape != (n_rows, heads) or not lse.is_contiguous() or \
+            lse.get_device() != cache.index:
         raise ValueError("lse must be a contiguous float32 [rows, heads] tensor on the cache's device")
     if workspace is None:
         workspace = kv_workspace(cache.device)
-    elif not workspace.is_contiguous() or workspace.device != cache.device:
+    elif not workspace.is_contiguous() or workspace.get_device() != cache.index:
         raise ValueError("workspace must be contiguous and on the cache's device")
     a = _KvAttn(q.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ldq, ldo,
                 workspace.numel() * workspace.element_size(), max_len, _dtype(q.dtype), heads,
                 1.0 / math.sqrt(hd) if scale is None else scale)
-    _check(_lib().mlora_kv_attention(cache._ref, byref(s), byref(a), _stream(stream)))
+    _check(_lib().mlora_kv_attention(cache._ref, byref(s), byref(a), _on(cache.index, stream)))
     return out, lse
 
 
 def kv_check_status(cache: KvCache, stream=None) -> int:
     """Synchronise, return and clear the cache's status: 0, -2 (E_RANGE), or -5
     (E_TIMEOUT: a bounded device wait gave up)."""
-    import torch
     (stream or torch.cuda.current_stream()).synchronize()
     bad = int(cache.status.item())
     cache.status.zero_()
