@@ -402,10 +402,10 @@ int mlora_set_lm_backward(mlora_t* h, int32_t mode);
  *     factor_g = max_norm / n_g if n_g > max_norm, else 1
  *     out = x * factor_g
  * A norm that is an infinity or NaN leaves its group as it is (factor 1): the
- * caller sees it in norms_out and skips the step.  Squares are summed in fp32
- * over 64 elements a thread and in fp64 above that, in a fixed order, so that
- * results repeat bit for bit; magnitudes whose squares leave fp32's range are
- * summed relative to their largest.
+ * caller sees it in norms_out and skips the step.  Squares are added in fp32 (a
+ * norm is off by about 30 * 2^-24 of itself at most) in a fixed order: results
+ * repeat bit for bit; magnitudes whose squares leave fp32's range are added
+ * relative to their largest.
  *   grads, out: HOST arrays of DEVICE pointers to contiguous tensors of
  *     `dtype` (mlora_dtype), aligned to their elements; out NULL: in place.
  *     Equal pointers or no overlap.  sizes: HOST, elements, >= 0.
@@ -413,8 +413,8 @@ int mlora_set_lm_backward(mlora_t* h, int32_t mode);
  *   max_norm >= 0; infinity: norms only (and copies, if out is given).
  *   norms_out: DEVICE fp32 [n_groups] (may be NULL); 0 for a group without
  *     elements.
- *   workspace: DEVICE, 8-byte aligned, at least mlora_clip_grads_workspace()
- *     bytes; calls that may overlap need one each.
+ *   workspace: DEVICE, 8-byte aligned, of any content, at least
+ *     mlora_clip_grads_workspace() bytes; calls that may overlap need one each.
  * Queued on `stream`; no allocation on the device and no synchronisation, so
  * the call can be captured into a CUDA graph.  Errors: E_ARG, E_CUDA, E_NOMEM
  * (host memory). */

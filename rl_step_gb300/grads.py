@@ -76,7 +76,7 @@ class GradSet:
         self._bytes = int(_lib().mlora_clip_grads_workspace(self._ref))
         if self._bytes == 0:                      # refused: raise its message
             _check(_lib().mlora_clip_grads(self._ref, 0.0, None, None, 0, None))
-        self.workspace = torch.empty(self._bytes // 8, dtype=torch.float64, device=self.device)
+        self.workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
 
 
 def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):

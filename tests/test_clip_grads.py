@@ -1,9 +1,10 @@
 """Gradient norms and clipping (mlora_clip_grads) against NumPy doubles.
 
-Tolerances, with u = 2^-24: a thread's fp32 sum of at most 64 squares has a
-relative error of at most 65 u (all terms are positive), fp64 above it adds
-nothing that shows; the norm halves it and rounds once to fp32: 33.5 u + u.
-The factor adds u, the product u and the rounding to bf16 2^-8:
+Tolerances, with u = 2^-24: a thread's fp32 sum of at most 32 squares has a
+relative error of at most 33 u (all terms are positive), its chunks' compensated
+sum 2 u, the block's tree 8 u, the group's at most 8 compensated and 8 in a
+tree: 59 u on the square; the norm halves it and rounds twice: 31.5 u.  The
+factor adds u, the product u and the rounding to bf16 2^-8:
   norm: 35 u;  out: (36 u + u) |x f| for fp32, + 2^-8 |x f| for bf16.
 """
 import ctypes
@@ -47,8 +48,9 @@ def test_clip_refuses_without_a_gpu():
         assert lib.mlora_clip_grads_workspace(ctypes.byref(g)) == 0
     g = _set(gr)
     assert rc(g, max_norm=-1.0) == -1 and rc(g, max_norm=math.nan) == -1
-    assert rc(g, w=None) == -1 and rc(g, w=ctypes.c_void_p(4100)) == -1 and rc(g, nbytes=8) == -1
-    assert lib.mlora_clip_grads_workspace(ctypes.byref(g)) == 16
+    need = lib.mlora_clip_grads_workspace(ctypes.byref(g))
+    assert need > 0
+    assert rc(g, w=None) == -1 and rc(g, w=ctypes.c_void_p(4100)) == -1 and rc(g, nbytes=need - 1) == -1
     assert rc(_set(gr, ptrs=(None, None), sizes=(0, 0)), w=None, nbytes=0) == 0      # nothing to do
 
 
@@ -170,10 +172,11 @@ def test_more_tensors_than_one_launch_holds():
     torch = _torch()
     import rl_step_gb300.grads as gr
     rng = np.random.default_rng(3)
-    sizes = rng.integers(0, 40000, 1300)
+    sizes = rng.integers(0, 40000, 1900)
     flat = torch.randn(int(sizes.sum()), device="cuda")
     xs = list(torch.split(flat, sizes.tolist()))
-    groups = rng.integers(0, 9, len(sizes)).tolist()
+    # group 8 alone has more tensors than a launch's table
+    groups = np.where(np.arange(1900) < 900, 8, rng.integers(0, 8, 1900)).tolist()
     xs = [x if x.data_ptr() % 4 == 0 else x.clone() for x in xs]
     outs = [torch.empty_like(x) for x in xs]
     s = gr.GradSet(xs, groups, out=outs)
