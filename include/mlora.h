@@ -192,6 +192,16 @@ int mlora_forward_backward_custom(mlora_t* h, const mlora_batch* b,
 int mlora_optim_step(mlora_t* h, const mlora_adam* p, const int32_t* adapters,
                      int32_t n, int32_t* skipped_out, void* stream);
 
+/* The same step with each selected adapter's gradient clipped first: with n_a
+ * the norm over all of adapter a's accumulated gradients, they enter the update
+ * as G min(1, max_norm / n_a) (mlora_clip_grads below: definition, order of the
+ * sums, norms that are not finite).  One adapter's gradient does not change
+ * another's step.  max_norm >= 0; infinity: no clipping, norms only.
+ * norms_out: DEVICE fp32 [n_adapters] (may be NULL): the norms before
+ * clipping, 0 for adapters that are not selected. */
+int mlora_optim_step_clipped(mlora_t* h, const mlora_adam* p, float max_norm, const int32_t* adapters,
+                             int32_t n, float* norms_out, int32_t* skipped_out, void* stream);
+
 /* Write a checkpoint of every adapter (weights and Adam state) to `path`.
  * Synchronises `stream`.  Format, little-endian: 8-byte magic "MLORASTA",
  * u32 version = 1, u32 n_adapters, u32 n_layers, u32 d_model, u32 d_ffn,

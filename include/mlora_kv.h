@@ -139,6 +139,48 @@ typedef struct {
 } mlora_kv_attn;
 int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const mlora_kv_attn* a, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rollouts of the transformer-block model (OpenTinker, "Multi-LoRA rollout":
+ * rows of many adapters share the base projections).  The batch holds the new
+ * rows of seqs' sequences, each with its own adapter: whole prompts, parts of
+ * them, drafted tokens or one token a sequence.  Every layer rotates the rows'
+ * keys by their positions, appends keys and values to its own cache and
+ * attends over it; all else is mlora_tf_forward.  b->positions is not read
+ * (may be NULL): seqs says where the rows stand.  seqs.n_rows = b->n_tokens.
+ *
+ * Ranges, besides those above: positions must be below the handle's
+ * max_tokens (the bound of its rotary table).  A row outside them, with a bad
+ * token, target or adapter id, or of a sequence that is out of range gets NaN
+ * and raises MLORA_E_RANGE in mlora_tf_check_status; with a bad adapter id its
+ * keys and values in the cache are unspecified.  Rows of no sequence or of an
+ * empty slot get NaN and raise nothing, so a batch can be padded to a fixed
+ * size.  Gradients, weights and step counts are not changed.  No call
+ * allocates or synchronises, so a decode step can be captured into a graph
+ * (not while mlora_tf_profile_enable is on).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    const mlora_kv_cache* caches;  /* HOST [n_layers]: the layers' page pools, n_kv_heads of the model, head_dim 128 */
+    mlora_kv_seqs seqs;            /* the same pages of every pool                 */
+    void* workspace;               /* as in mlora_kv_attn                          */
+    int64_t workspace_bytes;
+    int64_t max_len;               /* upper bound of kv_len, 1 .. max_tokens       */
+} mlora_tf_context;
+
+/* Target-token logprobs of the rows; logprobs_out DEVICE fp32 [n_tokens], or
+ * NULL (a prompt that is only to be cached).  Errors: E_ARG, E_CUDA. */
+int mlora_tf_forward_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c, float* logprobs_out,
+                            void* stream);
+
+/* The same, and the next token of every sequence from its last row's
+ * distribution: the smallest id v with CDF(v) > uniforms[s] (as
+ * mlora_sampler_sample; the logits of the 256 ids around v are formed again
+ * in fp32).  b->targets is not read (may be NULL).  uniforms: DEVICE fp32
+ * [n_seqs] in [0, 1); next_out: DEVICE int32 [n_seqs], -1 for a sequence without
+ * a good last row; logprob_out: DEVICE fp32 [n_seqs], NaN there.  n_seqs <=
+ * max_tokens.  Errors: E_ARG, E_CUDA. */
+int mlora_tf_sample_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c, const float* uniforms,
+                           int32_t* next_out, float* logprob_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -129,6 +129,11 @@ int mlora_tf_forward_backward_custom(mlora_tf_t* h, const mlora_tf_batch* b, con
 int mlora_tf_optim_step(mlora_tf_t* h, const mlora_adam* p, const int32_t* adapters, int32_t n,
                         int32_t* skipped_out, void* stream);
 
+/* The same step with each selected adapter's gradient clipped to max_norm first,
+ * exactly as mlora_optim_step_clipped. */
+int mlora_tf_optim_step_clipped(mlora_tf_t* h, const mlora_adam* p, float max_norm, const int32_t* adapters,
+                                int32_t n, float* norms_out, int32_t* skipped_out, void* stream);
+
 /* Copy one fp32 adapter tensor into dst (DEVICE, caller-owned): projection
  * proj (MLORA_TF_*), factor 0 = A [r x in], 1 = B [out x r]; kind 0 = weight,
  * 1 = accumulated gradient, 2 = first moment, 3 = second moment.  Test and

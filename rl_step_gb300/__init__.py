@@ -29,7 +29,7 @@ from typing import Optional, Sequence
 __all__ = [
     "LIB_PATH", "load_library", "MLoRAError", "Handle",
     "mlora_create", "mlora_destroy", "mlora_forward", "mlora_forward_backward",
-    "mlora_forward_backward_custom", "mlora_optim_step", "mlora_save_state", "mlora_load_state", "mlora_export_merged",
+    "mlora_forward_backward_custom", "mlora_optim_step", "mlora_optim_step_clipped", "mlora_save_state", "mlora_load_state", "mlora_export_merged",
     "mlora_read_adapter", "mlora_write_adapter", "mlora_get_steps", "mlora_get_routing",
     "mlora_check_status", "mlora_routing_noalloc", "Sampler", "mlora_sampler_create",
     "mlora_sampler_publish", "mlora_sampler_logprobs", "mlora_sampler_sample",
@@ -96,6 +96,8 @@ _SIGNATURES = {
                                                 c_void_p, c_void_p]),
     "mlora_optim_step": (c_int32, [c_void_p, POINTER(_Adam), POINTER(c_int32), c_int32, c_void_p,
                                    c_void_p]),
+    "mlora_optim_step_clipped": (c_int32, [c_void_p, POINTER(_Adam), c_float, POINTER(c_int32), c_int32, c_void_p,
+                                           c_void_p, c_void_p]),
     "mlora_save_state": (c_int32, [c_void_p, c_char_p, c_void_p]),
     "mlora_load_state": (c_int32, [c_void_p, c_char_p, c_int32, c_void_p]),
     "mlora_export_merged": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p]),
@@ -289,6 +291,24 @@ def mlora_optim_step(h: Handle, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8, weigh
     _check(_lib.mlora_optim_step(h.ptr, ctypes.byref(p), arr, n, _ptr(skipped_out),
                                  _stream(stream)))
     return skipped_out
+
+
+def mlora_optim_step_clipped(h: Handle, max_norm: float, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8,
+                             weight_decay=0.0, adapters: Optional[Sequence[int]] = None, norms_out=None,
+                             skipped_out=None, stream=None):
+    """Adam step with each adapter's gradient clipped to max_norm; returns
+    (skipped flags int32, norms before clipping float32), [n_adapters] on the device."""
+    import torch
+    if skipped_out is None:
+        skipped_out = torch.empty(h.n_adapters, dtype=torch.int32, device="cuda")
+    if norms_out is None:
+        norms_out = torch.empty(h.n_adapters, dtype=torch.float32, device="cuda")
+    p = _Adam(lr, beta1, beta2, eps, weight_decay)
+    n = 0 if adapters is None else len(adapters)
+    arr = None if adapters is None else (c_int32 * max(1, n))(*adapters)
+    _check(_lib.mlora_optim_step_clipped(h.ptr, ctypes.byref(p), max_norm, arr, n, _ptr(norms_out),
+                                         _ptr(skipped_out), _stream(stream)))
+    return skipped_out, norms_out
 
 
 def mlora_save_state(h: Handle, path: str, stream=None):

@@ -22,7 +22,10 @@
 // (One resident kernel that counted arrivals a chunk instead took 981 us on the 32
 // adapters of the 8B widths, two whole passes 670 us, this 539 us; one
 // adapter, 39 MB: 37, 37 and 21 us.)
+#include <algorithm>
 #include <cfloat>
+#include <new>
+#include <vector>
 
 #include "clip.cuh"
 #include "kv_common.cuh"
@@ -365,15 +368,57 @@ cudaError_t launch_clip_norm(const ClipEntry* entries, int n, ClipSum* part, con
     return launch_tables<float>(nullptr, 0, entries, n, part, mask, 0.f, nullptr, first, s, launches);
 }
 
+namespace {
+
+constexpr int MAX_ADAPTERS = 1024;
+struct AdapterSums {
+    int g[MAX_ADAPTERS + 1];                 // adapter a's sums are [g[a], g[a+1])
+};
+
+__global__ void __launch_bounds__(CT) clip_finish_kernel(const __grid_constant__ AdapterSums t, const ClipSum* part,
+                                                         const int* __restrict__ mask, float max_norm, float* factor,
+                                                         float* norms) {
+    const int a = blockIdx.x;
+    const double norm = mask[a] ? group_norm(part, t.g[a], t.g[a + 1]) : 0.0;
+    if (threadIdx.x == 0) {
+        factor[a] = clip_factor(norm, max_norm);
+        if (norms) norms[a] = (float)norm;
+    }
+}
+
+std::vector<ClipEntry> adapter_entries(const float* G, const int64_t* off, int n_ad) {
+    std::vector<ClipEntry> e(n_ad);
+    for (int a = 0; a < n_ad; ++a) {
+        e[a].src = e[a].dst = const_cast<float*>(G) + off[a];
+        e[a].size = off[a + 1] - off[a];
+        e[a].group = a;
+    }
+    clip_number(e.data(), n_ad);
+    return e;
+}
+
+}  // namespace
+
+int64_t clip_adapter_sums(const int64_t* off, int n_ad) { return adapter_entries(nullptr, off, n_ad).back().g1; }
+
+cudaError_t launch_clip_adapters(const float* G, const int64_t* off, int n_ad, const int* mask, ClipSum* part,
+                                 float max_norm, float* factor, float* norms, cudaStream_t s, int64_t* launches) {
+    const std::vector<ClipEntry> e = adapter_entries(G, off, n_ad);
+    const cudaError_t err = launch_clip_norm(e.data(), n_ad, part, mask, s, launches);
+    if (err != cudaSuccess) return err;
+    AdapterSums t;
+    for (int a = 0; a < n_ad; ++a) t.g[a] = e[a].g0;
+    t.g[n_ad] = e[n_ad - 1].g1;
+    clip_finish_kernel<<<n_ad, CT, 0, s>>>(t, part, mask, max_norm, factor, norms);
+    if (launches) ++*launches;
+    return cudaGetLastError();
+}
+
 }  // namespace mlk
 
 // ----------------------------------------------------------------------------
 // C ABI
 // ----------------------------------------------------------------------------
-#include <algorithm>
-#include <new>
-#include <vector>
-
 using namespace mlk;
 
 namespace {

@@ -41,4 +41,12 @@ int clip_number(ClipEntry* e, int n);
 cudaError_t launch_clip_norm(const ClipEntry* entries, int n, ClipSum* part, const int* mask, cudaStream_t s,
                              int64_t* launches);
 
+// The handles' clipped optimizer steps: adapter a's gradient is the fp32 range
+// [off[a], off[a+1]) of G (off: host).  factor[a], norms[a] (may be null): the
+// factor that clips it and its norm, for the adapters with mask[a] != 0; 1 and 0
+// for the others.  part: clip_adapter_sums(off, n_ad) sums.
+int64_t clip_adapter_sums(const int64_t* off, int n_ad);
+cudaError_t launch_clip_adapters(const float* G, const int64_t* off, int n_ad, const int* mask, ClipSum* part,
+                                 float max_norm, float* factor, float* norms, cudaStream_t s, int64_t* launches);
+
 }  // namespace mlk

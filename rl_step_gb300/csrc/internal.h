@@ -160,9 +160,11 @@ void launch_loss_reduce(const double* val_row, const int* pad_off, int n_ad, dou
 struct AdamTab {
     int mode;      // 0 leave, 1 step, 2 skip (consume gradient only)
     float c1, c2;  // 1/(1-b1^t), 1/(1-b2^t)
+    float gs;      // factor of the gradient (clipping; 1: none)
 };
+// factor: null, or per adapter the factor its gradient is taken with
 void launch_adam_prep(int n_ad, const int* sel_mask, int* touched, int* nonfinite, int64_t* step,
-                      float beta1, float beta2, AdamTab* tab, int* skipped_out, cudaStream_t s);
+                      float beta1, float beta2, const float* factor, AdamTab* tab, int* skipped_out, cudaStream_t s);
 
 void launch_tf_adam(int n_ad, const int64_t* ad_off, const int* ranks, int64_t total, const AdamTab* tab, float* P,
                     float* G, float* M, float* Vm, float lr, float beta1, float beta2, float eps, float wd,

@@ -390,13 +390,14 @@ void launch_loss_reduce(const double* val_row, const int* pad_off, int n_ad, dou
 //                A2 -> A2s[l][(a*RP + j)*f + i],  B2 -> B2s[l][(a*d + i)*RP + j].
 // ----------------------------------------------------------------------------
 __global__ void adam_prep_kernel(int n_ad, const int* sel_mask, int* touched, int* nonfinite,
-                                 int64_t* step, float beta1, float beta2, AdamTab* tab,
+                                 int64_t* step, float beta1, float beta2, const float* factor, AdamTab* tab,
                                  int* skipped_out) {
     for (int a = threadIdx.x; a < n_ad; a += blockDim.x) {
         bool sel = sel_mask ? (sel_mask[a] != 0) : (touched[a] != 0);
         AdamTab e;
         e.mode = 0;
         e.c1 = e.c2 = 0.f;
+        e.gs = factor ? factor[a] : 1.f;
         int skipped = 0;
         if (sel) {
             if (nonfinite[a]) {
@@ -418,8 +419,8 @@ __global__ void adam_prep_kernel(int n_ad, const int* sel_mask, int* touched, in
 }
 
 void launch_adam_prep(int n_ad, const int* sel_mask, int* touched, int* nonfinite, int64_t* step,
-                      float beta1, float beta2, AdamTab* tab, int* skipped_out, cudaStream_t s) {
-    adam_prep_kernel<<<1, 1024, 0, s>>>(n_ad, sel_mask, touched, nonfinite, step, beta1, beta2, tab,
+                      float beta1, float beta2, const float* factor, AdamTab* tab, int* skipped_out, cudaStream_t s) {
+    adam_prep_kernel<<<1, 1024, 0, s>>>(n_ad, sel_mask, touched, nonfinite, step, beta1, beta2, factor, tab,
                                         skipped_out);
 }
 
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(256) adam_kernel(int n_ad, const int64_t* __re
             continue;
         }
         float4 g = G[i4], p = P[i4], m = M[i4], v = Vm[i4];
-        float gv[4] = {g.x, g.y, g.z, g.w};
+        float gv[4] = {g.x * e.gs, g.y * e.gs, g.z * e.gs, g.w * e.gs};
         float pv[4] = {p.x, p.y, p.z, p.w};
         float mv[4] = {m.x, m.y, m.z, m.w};
         float vv[4] = {v.x, v.y, v.z, v.w};

@@ -274,11 +274,12 @@ void read_t(const KvView& c, int head_dim, void* k, void* v, int pages, int64_t 
 
 }  // namespace
 
+bool kv_fits(const KvView& c) { return unit_blocks(c, touched_pages(c.max_rows)) >= 0; }
+
 cudaError_t launch_kv_append(const KvView& c, int head_dim, int dtype, const void* k, int64_t ldk, const void* v,
                              int64_t ldv, cudaStream_t s) {
     const int pages = touched_pages(c.max_rows);
     const int64_t blocks = unit_blocks(c, pages);
-    if (blocks < 0) return cudaErrorInvalidConfiguration;
     if (dtype == MLORA_BF16)
         (head_dim == 64 ? append_t<bf16, 64> : append_t<bf16, 128>)(c, k, ldk, v, ldv, pages, blocks, s);
     else
@@ -306,7 +307,7 @@ extern "C" int mlora_kv_append(const mlora_kv_cache* c, const mlora_kv_seqs* q, 
     if (k_stride < row || v_stride < row || k_stride % per16 || v_stride % per16 || !aligned16(k) || !aligned16(v))
         return kv_fail(MLORA_E_ARG, "key and value rows must be 16-byte aligned and at least %lld elements apart",
                        (long long)row);
-    if (unit_blocks(w, touched_pages(w.max_rows)) < 0)
+    if (!kv_fits(w))
         return kv_fail(MLORA_E_ARG, "too many sequences, heads and rows for one call");
     const cudaError_t e = launch_kv_append(w, c->head_dim, dtype, k, k_stride, v, v_stride,
                                            reinterpret_cast<cudaStream_t>(stream));
@@ -323,7 +324,7 @@ extern "C" int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, in
     if (!aligned16(k_out) || !aligned16(v_out)) return kv_fail(MLORA_E_ARG, "outputs must be 16-byte aligned");
     const int pages = touched_pages(w.max_rows);
     const int64_t blocks = unit_blocks(w, pages);
-    if (blocks < 0) return kv_fail(MLORA_E_ARG, "too many sequences, heads and rows for one call");
+    if (!kv_fits(w)) return kv_fail(MLORA_E_ARG, "too many sequences, heads and rows for one call");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == MLORA_BF16) read_t<bf16>(w, c->head_dim, k_out, v_out, pages, blocks, s);
     else read_t<float>(w, c->head_dim, k_out, v_out, pages, blocks, s);

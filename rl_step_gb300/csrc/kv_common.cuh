@@ -122,6 +122,9 @@ __device__ __forceinline__ void store4_f(bf16* p, const float (&v)[4]) {
 int kv_check(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, KvView* out);
 int kv_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 
+// Whether one launch can hold the calls' blocks (append, read).
+bool kv_fits(const KvView& c);
+
 // The operators on checked arguments; the transformer's rollouts call them with a row_map.
 cudaError_t launch_kv_append(const KvView& c, int head_dim, int dtype, const void* k, int64_t ldk, const void* v,
                              int64_t ldv, cudaStream_t s);

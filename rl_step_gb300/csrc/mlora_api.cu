@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "clip.cuh"
 #include "internal.h"
 
 using namespace mlk;
@@ -75,6 +76,8 @@ struct mlora {
     int64_t* step = nullptr;
     int *touched = nullptr, *nonfinite = nullptr, *sel_mask = nullptr;
     AdamTab* adam_tab = nullptr;
+    ClipSum* clip_sums = nullptr;       // partial sums of the gradient norms
+    float* clip_factor = nullptr;       // [n_ad]
     ShadowMap shadow;                   // padded-rank copies per layer (dtype)
     // routing
     RouteBufs rb;
@@ -348,6 +351,8 @@ extern "C" int mlora_create(const mlora_config* cfg, const mlora_init* init, mlo
         ALLOC(h->nonfinite, n_ad);
         ALLOC(h->sel_mask, n_ad);
         ALLOC(h->adam_tab, n_ad);
+        ALLOC(h->clip_sums, clip_adapter_sums(h->ad_off_h.data(), n_ad));
+        ALLOC(h->clip_factor, n_ad);
         memset(&h->shadow, 0, sizeof(h->shadow));
         for (int l = 0; l < L; ++l) {
             ALLOCB(h->shadow.A1[l], (size_t)n_ad * RP * d * es);
@@ -905,8 +910,9 @@ extern "C" int mlora_forward_backward_custom(mlora_t* h, const mlora_batch* b,
     return dispatch_step(h, b, la, logprobs_out, loss_out, true, stream);
 }
 
-extern "C" int mlora_optim_step(mlora_t* h, const mlora_adam* p, const int32_t* adapters, int32_t n,
-                                int32_t* skipped_out, void* stream) {
+// max_norm: null, or the norm each selected adapter's gradient is clipped to
+static int optim_step(mlora_t* h, const mlora_adam* p, const float* max_norm, const int32_t* adapters, int32_t n,
+                      float* norms_out, int32_t* skipped_out, void* stream) {
     if (!h || !p) return fail(MLORA_E_ARG, "NULL handle or adam params");
     if (!(p->lr >= 0.f) || !(p->beta1 >= 0.f && p->beta1 < 1.f) || !(p->beta2 >= 0.f && p->beta2 < 1.f) ||
         !(p->eps > 0.f) || !std::isfinite(p->weight_decay))
@@ -924,10 +930,15 @@ extern "C" int mlora_optim_step(mlora_t* h, const mlora_adam* p, const int32_t* 
         CUDA_TRY(cudaStreamSynchronize(s));   // the host vector goes out of scope
         sel = h->sel_mask;
     }
+    if (max_norm) {
+        ProfScope ps(h, s, MLORA_PROF_OTHER);
+        CUDA_TRY(launch_clip_adapters(h->G, h->ad_off_h.data(), h->n_ad, sel ? sel : h->touched, h->clip_sums, *max_norm,
+                                      h->clip_factor, norms_out, s, &h->launches));
+    }
     {
         ProfScope ps(h, s, MLORA_PROF_OTHER);
-        launch_adam_prep(h->n_ad, sel, h->touched, h->nonfinite, h->step, p->beta1, p->beta2, h->adam_tab,
-                         skipped_out, s);
+        launch_adam_prep(h->n_ad, sel, h->touched, h->nonfinite, h->step, p->beta1, p->beta2,
+                         max_norm ? h->clip_factor : nullptr, h->adam_tab, skipped_out, s);
         ++h->launches;
     }
     ProfScope ps_adam(h, s, MLORA_PROF_ADAM);
@@ -940,6 +951,19 @@ extern "C" int mlora_optim_step(mlora_t* h, const mlora_adam* p, const int32_t* 
     ++h->launches;
     CUDA_TRY(cudaGetLastError());
     return MLORA_OK;
+}
+
+extern "C" int mlora_optim_step(mlora_t* h, const mlora_adam* p, const int32_t* adapters, int32_t n,
+                                int32_t* skipped_out, void* stream) {
+    return optim_step(h, p, nullptr, adapters, n, nullptr, skipped_out, stream);
+}
+
+extern "C" int mlora_optim_step_clipped(mlora_t* h, const mlora_adam* p, float max_norm, const int32_t* adapters,
+                                        int32_t n, float* norms_out, int32_t* skipped_out, void* stream) try {
+    if (!(max_norm >= 0.f)) return fail(MLORA_E_ARG, "max_norm must be >= 0 (infinity: norms only)");
+    return optim_step(h, p, &max_norm, adapters, n, norms_out, skipped_out, stream);
+} catch (const std::bad_alloc&) {
+    return fail(MLORA_E_NOMEM, "no host memory for the adapter table");
 }
 
 // ----------------------------------------------------------------------------

@@ -33,6 +33,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "sampling.cuh"
 
 using namespace mlk;
 
@@ -120,75 +121,9 @@ __global__ void __launch_bounds__(256) sample_kernel(const float* __restrict__ p
         }
         const float lse = lse_row[p];
         const float* prow = part + (int64_t)p * part_ld;
-        // --- vocabulary tile
-        float run = 0.f;          // mass of the tiles before `base`
-        int T = -1, last_nz = -1;
-        float before_T = 0.f;
-        for (int base = 0; base < n_nt && T < 0; base += 32) {
-            const int j = base + lane;
-            const float m = j < n_nt ? __expf(prow[j] - lse) : 0.f;
-            float c = m;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float x = __shfl_up_sync(0xffffffffu, c, o);
-                if (lane >= o) c += x;
-            }
-            const unsigned nz = __ballot_sync(0xffffffffu, m > 0.f);
-            if (nz) last_nz = base + 31 - __clz(nz);
-            const unsigned pass = __ballot_sync(0xffffffffu, run + c > u);
-            if (pass) {
-                const int L = __ffs(pass) - 1;
-                T = base + L;
-                const float cprev = __shfl_sync(0xffffffffu, c - m, L);
-                before_T = run + cprev;
-            } else {
-                run += __shfl_sync(0xffffffffu, c, 31);
-            }
-        }
-        if (T < 0) {                 // rounding: u at or above the total mass
-            T = last_nz >= 0 ? last_nz : 0;
-            before_T = -INFINITY;    // take the tile's last non-zero column
-        }
-        // --- column inside tile T (bn = 256: 8 columns per lane; bn = 32: 1)
-        const int c0 = T * bn;
-        const int per = bn / 32;
-        float pv[8];
-        float ls = 0.f;
-        for (int e = 0; e < per; ++e) {
-            const int v = c0 + lane * per + e;
-            pv[e] = v < V ? __expf(z[(int64_t)p * ldz + v] - lse) : 0.f;
-            ls += pv[e];
-        }
-        float c = ls;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float x = __shfl_up_sync(0xffffffffu, c, o);
-            if (lane >= o) c += x;
-        }
-        int pick = -1;
-        const unsigned pass = __ballot_sync(0xffffffffu, before_T + c > u);
-        if (pass) {
-            const int L = __ffs(pass) - 1;
-            if (lane == L) {
-                float r = before_T + (c - ls);
-                for (int e = 0; e < per; ++e) {
-                    r += pv[e];
-                    if (r > u) { pick = c0 + lane * per + e; break; }
-                }
-                if (pick < 0) {          // rounding inside the lane's columns
-                    for (int e = per - 1; e >= 0; --e)
-                        if (pv[e] > 0.f) { pick = c0 + lane * per + e; break; }
-                }
-            }
-            pick = __shfl_sync(0xffffffffu, pick, L);
-        }
-        if (pick < 0) {                  // last non-zero column of the tile
-            int mine = -1;
-            for (int e = per - 1; e >= 0; --e)
-                if (pv[e] > 0.f) { mine = c0 + lane * per + e; break; }
-            const unsigned has = __ballot_sync(0xffffffffu, mine >= 0);
-            pick = has ? __shfl_sync(0xffffffffu, mine, 31 - __clz(has)) : c0;
-        }
+        float before;
+        const int c0 = sample_tile(prow, n_nt, lse, u, lane, before) * bn;
+        const int pick = sample_column(z + (int64_t)p * ldz + c0, c0, bn, V, lse, u, before, lane);
         if (lane == 0) {
             next_out[p] = pick;
             lp_out[p] = z[(int64_t)p * ldz + pick] - lse;

@@ -3,7 +3,8 @@
 // library's kernels on the caller's stream: routing and embedding
 // (routing.cu, kernels_misc.cu), RMSNorm / rotary / sequence metadata / Adam
 // (tf_kernels.cu), attention (attention_tc.cu), every projection on the
-// tcgen05 GEMM engine (gemm_tc.cu), and the LM head with its loss epilogue
+// tcgen05 GEMM engine (gemm_tc.cu), rollouts over the paged caches (kv_cache.cu,
+// kv_attention.cu), and the LM head with its loss epilogue
 // (gemm_tc.cu, kernels_misc.cu).  The host validates, builds descriptors and
 // queues work.
 #include <stdarg.h>
@@ -14,8 +15,10 @@
 #include <string>
 #include <vector>
 
-#include "../../include/mlora_tf.h"
+#include "../../include/mlora_kv.h"
+#include "clip.cuh"
 #include "internal.h"
+#include "rollout.cuh"
 
 using namespace mlk;
 
@@ -79,6 +82,8 @@ struct mlora_tf {
     int64_t* step = nullptr;
     int *touched = nullptr, *nonfinite = nullptr, *sel_mask = nullptr;
     AdamTab* adam_tab = nullptr;
+    ClipSum* clip_sums = nullptr;                  // partial sums of the gradient norms
+    float* clip_factor = nullptr;                  // [n_ad]
     bf16* As[NGROUPS] = {nullptr};                 // [L][n_ad * kx (+pad) x in_g]
     bf16* Bs[NGROUPS] = {nullptr};                 // [L][n_ad * N_g x kx]
     int64_t As_rows[NGROUPS] = {0}, As_layer[NGROUPS] = {0}, Bs_layer[NGROUPS] = {0};
@@ -86,6 +91,7 @@ struct mlora_tf {
     // routing and sequence metadata
     RouteBufs rb;
     int *pos_pad = nullptr, *seq_start = nullptr;
+    int *row_map = nullptr, *last_meta = nullptr;  // rollouts: padded row of each batch row; row tiles of the last rows
     float2* rope_cs = nullptr;                     // [max_tokens x 64] (cos, sin)
     // activations, per layer
     std::vector<bf16*> x1, vqkv, qkv, o, vo, x2, vgu, gu, act, vd;
@@ -362,6 +368,10 @@ extern "C" int mlora_tf_create(const mlora_tf_config* cfg, const mlora_tf_init* 
         TA(h->nonfinite, n_ad);
         TA(h->sel_mask, n_ad);
         TA(h->adam_tab, n_ad);
+        TA(h->clip_sums, clip_adapter_sums(h->ad_off_h.data(), n_ad));
+        TA(h->clip_factor, n_ad);
+        TA(h->row_map, (size_t)h->max_tokens);
+        TA(h->last_meta, 2);
         for (int g = 0; g < NGROUPS; ++g) {
             const int64_t kx = GROUP_KX[g];
             // at least 256 rows: the 256-wide single-CTA tile reads whole boxes
@@ -706,8 +716,71 @@ AttnArgs attn_args(mlora_tf_t* h, int l, int mp) {
     return a;
 }
 
+// A rollout call: the layers' caches as the kernels see them, and where the
+// next tokens go (sampling).
+struct TfCached {
+    std::vector<KvView> kv;          // [n_layers], row_map set
+    void* workspace;
+    int64_t workspace_bytes, max_len;
+    const float* uniforms;           // null: no sampling
+    int32_t* next_out;
+    float* logprob_out;
+};
+
+// Appends the rows' keys and values of layer l to its cache and attends over it.
+int cached_attention(mlora_tf_t* h, const TfCached& c, int l, cudaStream_t s) {
+    if (c.kv[l].n_seqs == 0 || c.kv[l].max_rows == 0) return MLORA_OK;
+    TfProf ps(h, s, MLORA_TF_PROF_ATTN_FWD);
+    const bf16* q = h->qkv[l];
+    TF_CUDA(launch_kv_append(c.kv[l], MLORA_TF_HEAD_DIM, MLORA_BF16, q + h->Q, h->Nqkv, q + h->Q + h->KV, h->Nqkv, s));
+    KvAttnArgs a;
+    a.q = q; a.ldq = h->Nqkv;
+    a.out = h->o[l]; a.ldo = h->Q;
+    a.lse = nullptr;
+    a.workspace = c.workspace; a.workspace_bytes = c.workspace_bytes;
+    a.max_len = c.max_len;
+    a.n_heads = h->nh;
+    a.scale = 1.f / sqrtf((float)MLORA_TF_HEAD_DIM);
+    TF_CUDA(launch_kv_attention(c.kv[l], MLORA_TF_HEAD_DIM, MLORA_BF16, a, s));
+    h->launches += 2;
+    return MLORA_OK;
+}
+
+// Next token of every sequence from its last row of h->xf: those rows side by
+// side, the LM head's tile partials over them, one sampling block a sequence.
+int cached_sample(mlora_tf_t* h, const TfCached& c, cudaStream_t s) {
+    const KvView& kv = c.kv[0];
+    const int n = kv.n_seqs, mt = (n + TILE_M - 1) / TILE_M;
+    if (n == 0) return MLORA_OK;
+    // free by now: the embedding's rows, the positions, and seq_start throughout
+    bf16* x = h->embed_bf;
+    int *perm = h->seq_start, *tgt = h->pos_pad;
+    launch_tf_last_rows(kv, c.max_len, h->rb.inv, h->tgt_pad, h->xf, h->d, x, perm, tgt, h->last_meta, s);
+    ++h->launches;
+    GemmParams p;
+    p.M = mt * TILE_M; p.N = h->V; p.K = h->d; p.Kx = 0;
+    p.group_m = tf_band_for_k(h->d);
+    p.mtiles_dev = h->last_meta;
+    p.mt_base = 0; p.mt_count = mt;
+    p.A = opnd(x, h->max_pad, h->d, h->d, 0);
+    p.B = opnd(h->Wout, h->V, h->d, h->d, 0);
+    p.ep.kind = EPI_LMFWD; p.ep.part = h->part; p.ep.zt = h->zt; p.ep.tgt = tgt;
+    p.ep.part_ld = h->part_ld; p.ep.V = h->V; p.ep.Vpad = h->Vpad;
+    p.ep.mt = h->mt; p.ep.lm_bn = 256;
+    int rc;
+    if ((rc = tf_gemm(h, p, s, MLORA_TF_PROF_LM_FWD))) return rc;
+    TfProf ps(h, s, MLORA_TF_PROF_LOSS);
+    const LossArgs la{-1, nullptr, nullptr, nullptr, 0.f, nullptr};
+    launch_combine_loss(la, h->part, h->n_nt, h->part_ld, h->zt, perm, tgt, h->last_meta, 0, mt, nullptr,
+                        h->lse, h->gvec, h->val_row, h->num_sms, s);
+    launch_tf_sample(h->part, h->n_nt, h->part_ld, h->lse, perm, x, h->Wout, h->d, h->V, c.uniforms, n,
+                     c.next_out, c.logprob_out, h->status, s);
+    h->launches += 2;
+    return MLORA_OK;
+}
+
 int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* logprobs_out, double* loss_out,
-            bool backward, cudaStream_t s) {
+            bool backward, cudaStream_t s, const TfCached* kc = nullptr) {
     const int64_t N = b->n_tokens;
     const int n_ad = h->n_ad, L = h->L, d = h->d, f = h->f, V = h->V;
     const int64_t MP = h->max_pad;
@@ -725,10 +798,12 @@ int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* l
         launch_routing(b->adapter_ids, N, n_ad, h->rb, backward ? h->touched : nullptr, h->status, s, &h->launches,
                        GRAD_CHUNK);
         // positions bound the sequence lengths the stored dS layout holds
-        launch_tf_rows(h->rb.perm_pad, h->rb.meta, h->rb.tile_ad, h->rb.pad_off, b->positions, b->adapter_ids,
-                       h->attn_ds ? h->attn_max_seq : (int)h->max_tokens, mp, h->pos_pad, h->seq_start, h->status,
-                       s);
-        ++h->launches;
+        if (!kc) {
+            launch_tf_rows(h->rb.perm_pad, h->rb.meta, h->rb.tile_ad, h->rb.pad_off, b->positions, b->adapter_ids,
+                           h->attn_ds ? h->attn_max_seq : (int)h->max_tokens, mp, h->pos_pad, h->seq_start, h->status,
+                           s);
+            ++h->launches;
+        }
     }
     // The fp32 residual stream.  With a backward to follow, every value that
     // feeds an RMSNorm is kept: the residual GEMMs read one version and write
@@ -742,8 +817,15 @@ int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* l
     };
     {
         TfProf ps(h, s, MLORA_TF_PROF_EMBED);
-        launch_embed<bf16>(h->rb.perm_pad, h->rb.meta, mp, b->tokens, b->targets, h->E, V, d, h->embed_bf, cur,
-                           h->tgt_pad, h->status, s);
+        // sampling: the tokens double as targets
+        launch_embed<bf16>(h->rb.perm_pad, h->rb.meta, mp, b->tokens, kc && kc->uniforms ? b->tokens : b->targets, h->E,
+                           V, d, h->embed_bf, cur, h->tgt_pad, h->status, s);
+        ++h->launches;
+    }
+    if (kc) {
+        TfProf ps(h, s, MLORA_TF_PROF_ROUTING);
+        launch_tf_cached_rows(kc->kv[0], kc->max_len, h->rb.perm_pad, h->rb.meta, h->rb.inv, (int)N, mp, h->pos_pad,
+                              h->tgt_pad, h->row_map, h->status, s);
         ++h->launches;
     }
     for (int l = 0; l < L; ++l) {
@@ -760,7 +842,9 @@ int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* l
             launch_rope(h->qkv[l], h->Nqkv, 0, h->nh + h->nkv, h->pos_pad, h->rope_cs, h->rb.meta, mp, 0, s);
             ++h->launches;
         }
-        {
+        if (kc) {
+            if ((rc = cached_attention(h, *kc, l, s))) return rc;
+        } else {
             TfProf ps(h, s, MLORA_TF_PROF_ATTN_FWD);
             const cudaError_t e = launch_attention_fwd(attn_args(h, l, mp), h->status, s);
             if (e != cudaSuccess) return tfail(MLORA_E_CUDA, "attention forward launch: %s", cudaGetErrorString(e));
@@ -787,7 +871,9 @@ int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* l
             if ((rc = tf_gemm(h, p, s, MLORA_TF_PROF_DOWN))) return rc;
         }
     }
+    if (kc && !kc->uniforms && !logprobs_out) return MLORA_OK;     // the caches are filled
     if ((rc = tf_norm_fwd(h, cur, h->gfinal, h->xf, h->rstdf, mp, s))) return rc;
+    if (kc && kc->uniforms) return cached_sample(h, *kc, s);
 
     // LM head (Tinker API Implementation on TPUs, section 10.3-10.4): per-tile
     // log-sum-exp partials and the target logit over all rows; the backward
@@ -985,6 +1071,80 @@ extern "C" int mlora_tf_forward(mlora_tf_t* h, const mlora_tf_batch* b, float* l
     return tf_dispatch(h, b, la, logprobs_out, nullptr, false, stream);
 }
 
+namespace {
+
+int tf_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c, TfCached& kc, float* logprobs_out,
+              void* stream) {
+    if (!h || !b || !c) return tfail(MLORA_E_ARG, "NULL handle, batch or context");
+    if (b->n_tokens < 0 || b->n_tokens > h->max_tokens)
+        return tfail(MLORA_E_ARG, "n_tokens %lld outside 0..max_tokens (%lld)", (long long)b->n_tokens,
+                     (long long)h->max_tokens);
+    if (b->n_tokens > 0 && (!b->tokens || !b->adapter_ids || (!kc.uniforms && logprobs_out && !b->targets)))
+        return tfail(MLORA_E_ARG, "NULL token array");
+    if (!c->caches) return tfail(MLORA_E_ARG, "NULL caches");
+    if (c->seqs.n_rows != b->n_tokens)
+        return tfail(MLORA_E_ARG, "%lld rows of sequences, %lld tokens", (long long)c->seqs.n_rows,
+                     (long long)b->n_tokens);
+    if (c->max_len < 1 || c->max_len > h->max_tokens)
+        return tfail(MLORA_E_ARG, "max_len %lld outside 1..max_tokens (%lld)", (long long)c->max_len,
+                     (long long)h->max_tokens);
+    if (c->workspace_bytes < 0 || reinterpret_cast<uintptr_t>(c->workspace) % 16)
+        return tfail(MLORA_E_ARG, "bad workspace");
+    kc.kv.resize(h->L);
+    for (int l = 0; l < h->L; ++l) {
+        const int rc = kv_check(&c->caches[l], &c->seqs, MLORA_BF16, &kc.kv[l]);
+        if (rc) return rc;
+        if (c->caches[l].n_kv_heads != h->nkv || c->caches[l].head_dim != MLORA_TF_HEAD_DIM)
+            return tfail(MLORA_E_ARG, "layer %d: a cache of %d heads of %d, the model has %d of %d", l,
+                         c->caches[l].n_kv_heads, c->caches[l].head_dim, h->nkv, MLORA_TF_HEAD_DIM);
+        kc.kv[l].row_map = h->row_map;
+    }
+    if (!kv_fits(kc.kv[0]) ||
+        (c->seqs.n_seqs > 0 && (int64_t)kc.kv[0].max_rows * h->nh > INT32_MAX / c->seqs.n_seqs))
+        return tfail(MLORA_E_ARG, "too many sequences, rows and heads for one call");
+    kc.workspace = c->workspace;
+    kc.workspace_bytes = c->workspace ? c->workspace_bytes : 0;
+    kc.max_len = c->max_len;
+    // 0xff: -1 and NaN, what stays where there is no row
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (kc.uniforms && c->seqs.n_seqs > 0) {
+        TF_CUDA(cudaMemsetAsync(kc.next_out, 0xff, sizeof(int32_t) * c->seqs.n_seqs, s));
+        TF_CUDA(cudaMemsetAsync(kc.logprob_out, 0xff, sizeof(float) * c->seqs.n_seqs, s));
+    }
+    mlora_tf_batch bb = *b;
+    if (!bb.targets) bb.targets = bb.tokens;     // logprobs that nobody reads
+    const LossArgs la{-1, nullptr, nullptr, nullptr, 0.f, nullptr};
+    const int rc = tf_step(h, &bb, la, logprobs_out, nullptr, false, s, &kc);
+    if (rc) return rc;
+    TF_CUDA(cudaGetLastError());
+    return MLORA_OK;
+}
+
+}  // namespace
+
+extern "C" int mlora_tf_forward_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c,
+                                       float* logprobs_out, void* stream) try {
+    TfCached kc{};
+    return tf_cached(h, b, c, kc, logprobs_out, stream);
+} catch (const std::bad_alloc&) {
+    return tfail(MLORA_E_NOMEM, "no host memory for the layers' caches");
+}
+
+extern "C" int mlora_tf_sample_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c,
+                                      const float* uniforms, int32_t* next_out, float* logprob_out, void* stream) try {
+    if (!h || !c) return tfail(MLORA_E_ARG, "NULL handle or context");
+    if (!uniforms || !next_out || !logprob_out) return tfail(MLORA_E_ARG, "NULL uniforms or outputs");
+    if (c->seqs.n_seqs > h->max_tokens)
+        return tfail(MLORA_E_ARG, "%d sequences, at most max_tokens (%lld)", c->seqs.n_seqs, (long long)h->max_tokens);
+    TfCached kc{};
+    kc.uniforms = uniforms;
+    kc.next_out = next_out;
+    kc.logprob_out = logprob_out;
+    return tf_cached(h, b, c, kc, nullptr, stream);
+} catch (const std::bad_alloc&) {
+    return tfail(MLORA_E_NOMEM, "no host memory for the layers' caches");
+}
+
 extern "C" int mlora_tf_forward_backward(mlora_tf_t* h, const mlora_tf_batch* b, int32_t loss_kind,
                                          const mlora_loss_inputs* li, float* logprobs_out, double* loss_out,
                                          void* stream) {
@@ -1016,8 +1176,9 @@ extern "C" int mlora_tf_forward_backward_custom(mlora_tf_t* h, const mlora_tf_ba
     return tf_dispatch(h, b, la, logprobs_out, loss_out, true, stream);
 }
 
-extern "C" int mlora_tf_optim_step(mlora_tf_t* h, const mlora_adam* p, const int32_t* adapters, int32_t n,
-                                   int32_t* skipped_out, void* stream) {
+// max_norm: null, or the norm each selected adapter's gradient is clipped to
+static int tf_optim(mlora_tf_t* h, const mlora_adam* p, const float* max_norm, const int32_t* adapters, int32_t n,
+                    float* norms_out, int32_t* skipped_out, void* stream) {
     if (!h || !p) return tfail(MLORA_E_ARG, "NULL handle or adam params");
     if (!(p->lr >= 0.f) || !(p->beta1 >= 0.f && p->beta1 < 1.f) || !(p->beta2 >= 0.f && p->beta2 < 1.f) ||
         !(p->eps > 0.f) || !std::isfinite(p->weight_decay))
@@ -1036,10 +1197,15 @@ extern "C" int mlora_tf_optim_step(mlora_tf_t* h, const mlora_adam* p, const int
         TF_CUDA(cudaStreamSynchronize(s));   // the host vector goes out of scope
         sel = h->sel_mask;
     }
+    if (max_norm) {
+        TfProf ps(h, s, MLORA_TF_PROF_OTHER);
+        TF_CUDA(launch_clip_adapters(h->G, h->ad_off_h.data(), h->n_ad, sel ? sel : h->touched, h->clip_sums, *max_norm,
+                                     h->clip_factor, norms_out, s, &h->launches));
+    }
     {
         TfProf ps(h, s, MLORA_TF_PROF_OTHER);
-        launch_adam_prep(h->n_ad, sel, h->touched, h->nonfinite, h->step, p->beta1, p->beta2, h->adam_tab,
-                         skipped_out, s);
+        launch_adam_prep(h->n_ad, sel, h->touched, h->nonfinite, h->step, p->beta1, p->beta2,
+                         max_norm ? h->clip_factor : nullptr, h->adam_tab, skipped_out, s);
         ++h->launches;
     }
     {
@@ -1050,6 +1216,19 @@ extern "C" int mlora_tf_optim_step(mlora_tf_t* h, const mlora_adam* p, const int
     }
     TF_CUDA(cudaGetLastError());
     return MLORA_OK;
+}
+
+extern "C" int mlora_tf_optim_step(mlora_tf_t* h, const mlora_adam* p, const int32_t* adapters, int32_t n,
+                                   int32_t* skipped_out, void* stream) {
+    return tf_optim(h, p, nullptr, adapters, n, nullptr, skipped_out, stream);
+}
+
+extern "C" int mlora_tf_optim_step_clipped(mlora_tf_t* h, const mlora_adam* p, float max_norm, const int32_t* adapters,
+                                           int32_t n, float* norms_out, int32_t* skipped_out, void* stream) try {
+    if (!(max_norm >= 0.f)) return tfail(MLORA_E_ARG, "max_norm must be >= 0 (infinity: norms only)");
+    return tf_optim(h, p, &max_norm, adapters, n, norms_out, skipped_out, stream);
+} catch (const std::bad_alloc&) {
+    return tfail(MLORA_E_NOMEM, "no host memory for the adapter table");
 }
 
 extern "C" int mlora_tf_read_adapter(mlora_tf_t* h, int32_t adapter, int32_t layer, int32_t proj, int32_t factor,

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(256) tf_adam_kernel(int n_ad, const int64_t* _
                 continue;
             }
             const float4 g = G[i4], p = P[i4], m = M[i4], v = Vm[i4];
-            const float gv[4] = {g.x, g.y, g.z, g.w};
+            const float gv[4] = {g.x * e.gs, g.y * e.gs, g.z * e.gs, g.w * e.gs};
             float pv[4] = {p.x, p.y, p.z, p.w};
             float mv[4] = {m.x, m.y, m.z, m.w};
             float vv[4] = {v.x, v.y, v.z, v.w};

@@ -9,6 +9,11 @@ library's CUDA kernels; PyTorch provides device memory and streams.
     k, v = kv_read(cache, page_table, kv_len, n_rows)                       # back as fp32 or bf16
     kv_check_status(cache)                                                  # 0, or -2 (E_RANGE)
 
+Rollouts of the transformer model over one cache per layer:
+
+    tf_forward_cached(h, caches, prompt, None, adapter_ids, page_table, kv_len, max_len, row_off, max_rows)
+    token, logprob = tf_sample_cached(h, caches, token, adapter_ids, uniforms, page_table, kv_len, max_len)
+
 page_table int32 [n_seqs, max_pages], kv_len int32 [n_seqs] (the lengths with
 the call's rows counted) and row_off int32 [n_seqs + 1] (None: one row a
 sequence) are CUDA tensors; max_rows and max_len are upper bounds the caller
@@ -23,8 +28,10 @@ from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_void_p
 import torch
 
 from . import _check, load_library
+from .transformer import _TfBatch
 
-__all__ = ["PAGE", "KvCache", "kv_workspace", "kv_append", "kv_read", "kv_attention", "kv_check_status"]
+__all__ = ["PAGE", "KvCache", "kv_workspace", "kv_append", "kv_read", "kv_attention", "kv_check_status",
+           "tf_forward_cached", "tf_sample_cached"]
 
 PAGE = 64
 WORKSPACE_BYTES = 32 << 20
@@ -46,11 +53,19 @@ class _KvAttn(ctypes.Structure):
                 ("dtype", c_int32), ("n_heads", c_int32), ("scale", c_float)]
 
 
+class _TfContext(ctypes.Structure):
+    _fields_ = [("caches", POINTER(_KvCache)), ("seqs", _KvSeqs), ("workspace", c_void_p),
+                ("workspace_bytes", c_int64), ("max_len", c_int64)]
+
+
 _SIGNATURES = {
     "mlora_kv_append": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), c_int32, c_void_p, c_int64, c_void_p,
                                   c_int64, c_void_p]),
     "mlora_kv_read": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), c_int32, c_void_p, c_void_p, c_void_p]),
     "mlora_kv_attention": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), POINTER(_KvAttn), c_void_p]),
+    "mlora_tf_forward_cached": (c_int32, [c_void_p, POINTER(_TfBatch), POINTER(_TfContext), c_void_p, c_void_p]),
+    "mlora_tf_sample_cached": (c_int32, [c_void_p, POINTER(_TfBatch), POINTER(_TfContext), c_void_p, c_void_p,
+                                         c_void_p, c_void_p]),
 }
 
 _kv_lib = None
@@ -125,6 +140,12 @@ def kv_workspace(device="cuda", nbytes: int = WORKSPACE_BYTES):
 def _ids(name, t, shape, index) -> int:
     if t.dtype is not _INT32 or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the cache's device")
+    return t.data_ptr()
+
+
+def _out(name, t, n, index) -> int:
+    if t.dtype is not _FLOAT32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous float32 tensor [{n}] on the cache's device")
     return t.data_ptr()
 
 
@@ -203,6 +224,60 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
                 1.0 / math.sqrt(hd) if scale is None else scale)
     _check(_lib().mlora_kv_attention(cache._ref, byref(s), byref(a), _on(cache.index, stream)))
     return out, lse
+
+
+def _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace):
+    if len(caches) != h.n_layers:
+        raise ValueError(f"{h.n_layers} caches are needed, one per layer")
+    c0 = caches[0]
+    if workspace is None:
+        workspace = kv_workspace(c0.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != c0.index:
+        raise ValueError("workspace must be contiguous and on the caches' device")
+    if any(c.index != c0.index for c in caches):
+        raise ValueError("the caches must be on one device")
+    arr = (_KvCache * len(caches))(*[c._c for c in caches])
+    ctx = _TfContext(arr, _seqs(c0, page_table, kv_len, row_off, tokens.numel(), max_rows), workspace.data_ptr(),
+                     workspace.numel() * workspace.element_size(), max_len)
+    ctx._keep = (arr, workspace)
+    return ctx
+
+
+def tf_forward_cached(h, caches, tokens, targets, adapter_ids, page_table, kv_len, max_len: int, row_off=None,
+                      max_rows: int = 1, workspace=None, logprobs_out=None, stream=None):
+    """Forward of the sequences' newest rows over one cache per layer, which gets
+    their keys and values; returns the targets' logprobs (targets None: only
+    the caches are filled).  Without a workspace one is allocated for the call."""
+    ctx = _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace)
+    c0 = caches[0]
+    n = tokens.numel()
+    if targets is not None and logprobs_out is None:
+        logprobs_out = torch.empty(n, dtype=torch.float32, device=c0.device)
+    b = _TfBatch(n, _ids("tokens", tokens, (n,), c0.index),
+                 None if targets is None else _ids("targets", targets, (n,), c0.index), None,
+                 _ids("adapter_ids", adapter_ids, (n,), c0.index))
+    _check(_lib().mlora_tf_forward_cached(h.ptr, byref(b), byref(ctx),
+                                          None if targets is None else _out("logprobs_out", logprobs_out, n, c0.index),
+                                          _on(c0.index, stream)))
+    return logprobs_out if targets is not None else None
+
+
+def tf_sample_cached(h, caches, tokens, adapter_ids, uniforms, page_table, kv_len, max_len: int, row_off=None,
+                     max_rows: int = 1, workspace=None, next_out=None, logprob_out=None, stream=None):
+    """The same, and the next token of every sequence from its last row:
+    returns (next int32 [n_seqs], its logprob float32 [n_seqs])."""
+    ctx = _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace)
+    c0 = caches[0]
+    n, m = tokens.numel(), page_table.shape[0]
+    if next_out is None:
+        next_out = torch.empty(m, dtype=torch.int32, device=c0.device)
+    if logprob_out is None:
+        logprob_out = torch.empty(m, dtype=torch.float32, device=c0.device)
+    b = _TfBatch(n, _ids("tokens", tokens, (n,), c0.index), None, None, _ids("adapter_ids", adapter_ids, (n,), c0.index))
+    _check(_lib().mlora_tf_sample_cached(h.ptr, byref(b), byref(ctx), _out("uniforms", uniforms, m, c0.index),
+                                         _ids("next_out", next_out, (m,), c0.index),
+                                         _out("logprob_out", logprob_out, m, c0.index), _on(c0.index, stream)))
+    return next_out, logprob_out
 
 
 def kv_check_status(cache: KvCache, stream=None) -> int:

@@ -17,7 +17,8 @@ from typing import Optional, Sequence
 from . import LOSS_KINDS, _Adam, _check, _LossInputs, _ptr, _stream, load_library
 
 __all__ = ["PROJ", "TF_PROF_CLASSES", "TfHandle", "tf_create", "tf_destroy", "tf_forward",
-           "tf_forward_backward", "tf_forward_backward_custom", "tf_optim_step", "tf_read_adapter",
+           "tf_forward_backward", "tf_forward_backward_custom", "tf_optim_step", "tf_optim_step_clipped",
+           "tf_read_adapter",
            "tf_get_steps", "tf_check_status", "tf_profile_enable", "tf_profile_read", "tf_set_lm_backward",
            "tf_set_attention_backward"]
 
@@ -59,6 +60,8 @@ _SIGNATURES = {
                                                    c_void_p, c_void_p]),
     "mlora_tf_optim_step": (c_int32, [c_void_p, POINTER(_Adam), POINTER(c_int32), c_int32, c_void_p,
                                       c_void_p]),
+    "mlora_tf_optim_step_clipped": (c_int32, [c_void_p, POINTER(_Adam), c_float, POINTER(c_int32), c_int32,
+                                              c_void_p, c_void_p, c_void_p]),
     "mlora_tf_read_adapter": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32,
                                         c_void_p, c_void_p]),
     "mlora_tf_get_steps": (c_int32, [c_void_p, POINTER(c_int64), c_void_p]),
@@ -228,6 +231,24 @@ def tf_optim_step(h: TfHandle, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8, weight
     _check(_lib().mlora_tf_optim_step(h.ptr, ctypes.byref(p), arr, n, _ptr(skipped_out),
                                       _stream(stream)))
     return skipped_out
+
+
+def tf_optim_step_clipped(h: TfHandle, max_norm: float, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8,
+                          weight_decay=0.0, adapters: Optional[Sequence[int]] = None, norms_out=None,
+                          skipped_out=None, stream=None):
+    """Adam step with each adapter's gradient clipped to max_norm; returns
+    (skipped flags int32, norms before clipping float32), [n_adapters] on the device."""
+    import torch
+    if skipped_out is None:
+        skipped_out = torch.empty(h.n_adapters, dtype=torch.int32, device="cuda")
+    if norms_out is None:
+        norms_out = torch.empty(h.n_adapters, dtype=torch.float32, device="cuda")
+    p = _Adam(lr, beta1, beta2, eps, weight_decay)
+    n = 0 if adapters is None else len(adapters)
+    arr = None if adapters is None else (c_int32 * max(1, n))(*adapters)
+    _check(_lib().mlora_tf_optim_step_clipped(h.ptr, ctypes.byref(p), max_norm, arr, n, _ptr(norms_out),
+                                              _ptr(skipped_out), _stream(stream)))
+    return skipped_out, norms_out
 
 
 def tf_read_adapter(h: TfHandle, adapter: int, layer: int, proj: str, factor: str, kind: str = "weight",

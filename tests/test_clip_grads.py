@@ -219,3 +219,80 @@ def test_gradset_refuses():
     for f in (lambda: gr.GradSet([x], [3], n_groups=2), lambda: gr.clip_grads(gr.GradSet([x]), -1.0)):
         with pytest.raises(m.MLoRAError):
             f()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("subset", [None, [2, 0]])
+def test_clipped_step_of_a_handle(subset):
+    """norms, moments and weights of the clipped step; an infinite bound is the plain step bit for bit"""
+    _torch()
+    import oracle
+    import rl_step_gb300 as m
+    import workloads as wl
+    from _gpu_util import create_handle, run_gpu_step
+    cfg = wl.get_config("tiny_fp32")
+    base, ad, b = wl.make_base_weights(cfg), wl.make_adapters(cfg), wl.make_batch(cfg, None)
+
+    def handle():
+        h = create_handle(cfg, base, ad, len(b["tokens"]))
+        run_gpu_step(h, b, "cross_entropy")
+        return h
+
+    def read(h, a, prefix):
+        return {(l, k): m.mlora_read_adapter(h, a, l, prefix + k).double().cpu().numpy()
+                for l in range(cfg.n_layers) for k in oracle.TENSORS}
+    h = handle()
+    grads = [read(h, a, "g") for a in range(3)]
+    weights = [read(h, a, "") for a in range(3)]
+    norms = [math.sqrt(sum(float((x * x).sum()) for x in g.values())) for g in grads]
+    chosen = [0, 1, 2] if subset is None else subset
+    max_norm = sorted(norms[a] for a in chosen)[-1] * 0.7
+    skipped, got = m.mlora_optim_step_clipped(h, max_norm, lr=1e-3, adapters=subset)
+    assert m.mlora_check_status(h) == 0 and m.mlora_get_steps(h) == [int(a in chosen) for a in range(3)]
+    b1, b2 = float(np.float32(0.9)), float(np.float32(0.999))
+    for a in range(3):
+        if a not in chosen:
+            assert float(got[a]) == 0
+            assert all((x == read(h, a, "")[k]).all() for k, x in weights[a].items())
+            continue
+        assert abs(float(got[a]) - norms[a]) <= 35 * U * norms[a]
+        f = min(1.0, max_norm / norms[a])
+        m1, m2, w = read(h, a, "m"), read(h, a, "v"), read(h, a, "")
+        for k, x in grads[a].items():
+            g = f * x
+            # the factor 36 u, its product u; moments: 1 - b and the product with it 2 u (v: twice the gradient's)
+            assert (np.abs(m1[k] - (1 - b1) * g) <= 40 * U * np.abs((1 - b1) * g) + 1e-40).all()
+            assert (np.abs(m2[k] - (1 - b2) * g * g) <= 78 * U * (1 - b2) * g * g + 1e-40).all()
+            want = oracle.adam_update(weights[a][k], g, 0.0, 0.0, 1, 1e-3, b1, b2, 1e-8, 0.0)[0]
+            # the update, at most lr: the moments' 40 u and 78 u / 2, a few u of its own arithmetic; the weight's rounding
+            assert (np.abs(w[k] - want) <= 1e-3 * 128 * U + 1.01 * U * np.abs(want)).all()
+    plain, free = handle(), handle()
+    m.mlora_optim_step(plain, lr=1e-3)
+    m.mlora_optim_step_clipped(free, math.inf, lr=1e-3)
+    for a in range(3):
+        for p in ("", "m", "v", "g"):
+            x, y = read(plain, a, p), read(free, a, p)
+            assert all(np.array_equal(x[k], y[k]) for k in x)
+    for bad in (-1.0, math.nan):
+        with pytest.raises(Exception):
+            m.mlora_optim_step_clipped(h, bad)
+    m.mlora_optim_step_clipped(h, 1.0, lr=1e-3)          # nothing accumulated for the chosen ones: no step
+    assert m.mlora_check_status(h) == 0
+
+
+@pytest.mark.gpu
+def test_clipped_step_skips_a_gradient_that_is_not_finite():
+    torch = _torch()
+    import rl_step_gb300 as m
+    import workloads as wl
+    from _gpu_util import create_handle, run_gpu_step
+    cfg = wl.get_config("tiny_fp32")
+    base, ad, b = wl.make_base_weights(cfg), wl.make_adapters(cfg), wl.make_batch(cfg, None)
+    h = create_handle(cfg, base, ad, len(b["tokens"]))
+    r = cfg.ranks[1]
+    m.mlora_write_adapter(h, 1, 0, "A1", torch.full((r, cfg.d_model), math.inf, device="cuda"))
+    run_gpu_step(h, b, "cross_entropy")
+    skipped, norms = m.mlora_optim_step_clipped(h, 1e-3, lr=1e-3)
+    assert skipped.tolist() == [0, 1, 0]
+    assert math.isfinite(float(norms[0])) and math.isfinite(float(norms[2])) and not math.isfinite(float(norms[1]))
+    assert m.mlora_get_steps(h) == [1, 0, 1]
