@@ -53,14 +53,6 @@ __device__ __forceinline__ bool kv_seq(const KvView& c, int s, int64_t max_len, 
                      r);
 }
 
-// Page id of a sequence's page p, or -1 (and the status bit) if it is no page.
-__device__ __forceinline__ int kv_page(const KvView& c, int s, int p) {
-    const int id = c.table[(int64_t)s * c.max_pages + p];
-    if (id >= 0 && id < c.n_pages) return id;
-    raise_status(c.status, ST_RANGE);
-    return -1;
-}
-
 __device__ __forceinline__ int64_t kv_row(const KvView& c, int64_t r) { return c.row_map ? c.row_map[r] : r; }
 
 // Byte of (token j, dim c) inside a (page, head) tile.
@@ -99,17 +91,7 @@ __device__ __forceinline__ void e4m3x4_to_float4(uint32_t w, float (&f)[4]) {
     f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
-// four consecutive elements (aligned to their size) as floats
-__device__ __forceinline__ void load4_f(const float* p, float (&v)[4]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-}
-__device__ __forceinline__ void load4_f(const bf16* p, float (&v)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-}
+// four consecutive elements (aligned to their size) from floats
 __device__ __forceinline__ void store4_f(float* p, const float (&v)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }

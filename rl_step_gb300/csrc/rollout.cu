@@ -97,8 +97,13 @@ __global__ void __launch_bounds__(256) tf_sample_kernel(const float* __restrict_
         for (int i = lane * 8; i < d; i += 256) {
             float xv[8];
             const uint4 xw = *reinterpret_cast<const uint4*>(xr + i);
-            load4_f(reinterpret_cast<const bf16*>(&xw), reinterpret_cast<float(&)[4]>(xv[0]));
-            load4_f(reinterpret_cast<const bf16*>(&xw) + 4, reinterpret_cast<float(&)[4]>(xv[4]));
+            const uint32_t xs[4] = {xw.x, xw.y, xw.z, xw.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xs[e]));
+                xv[2 * e] = f.x;
+                xv[2 * e + 1] = f.y;
+            }
             uint4 w[COLS];
 #pragma unroll
             for (int j = 0; j < COLS; ++j)
