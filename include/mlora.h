@@ -418,7 +418,8 @@ int mlora_set_lm_backward(mlora_t* h, int32_t mode);
  * relative to their largest.
  *   grads, out: HOST arrays of DEVICE pointers to contiguous tensors of
  *     `dtype` (mlora_dtype), aligned to their elements; out NULL: in place.
- *     Equal pointers or no overlap.  sizes: HOST, elements, >= 0.
+ *     A tensor and its output are equal or do not overlap, and no output
+ *     overlaps another tensor or output of the set.  sizes: HOST, elements, >= 0.
  *   groups: HOST, 0 .. n_groups-1 for each tensor, or NULL: all in group 0.
  *   max_norm >= 0; infinity: norms only (and copies, if out is given).
  *   norms_out: DEVICE fp32 [n_groups] (may be NULL); 0 for a group without

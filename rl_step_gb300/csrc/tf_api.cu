@@ -1133,10 +1133,11 @@ extern "C" int mlora_tf_forward_cached(mlora_tf_t* h, const mlora_tf_batch* b, c
 extern "C" int mlora_tf_sample_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c,
                                       const float* uniforms, int32_t* next_out, float* logprob_out, void* stream) try {
     if (!h || !c) return tfail(MLORA_E_ARG, "NULL handle or context");
+    TfCached kc{};
+    if (c->seqs.n_seqs == 0) return tf_cached(h, b, c, kc, nullptr, stream);     // checks, and nothing to sample
     if (!uniforms || !next_out || !logprob_out) return tfail(MLORA_E_ARG, "NULL uniforms or outputs");
     if (c->seqs.n_seqs > h->max_tokens)
         return tfail(MLORA_E_ARG, "%d sequences, at most max_tokens (%lld)", c->seqs.n_seqs, (long long)h->max_tokens);
-    TfCached kc{};
     kc.uniforms = uniforms;
     kc.next_out = next_out;
     kc.logprob_out = logprob_out;

@@ -62,6 +62,7 @@ class GradSet:
         for t in self.grads + (self.out or []):
             if t.dtype != dtype or t.device != self.device or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("tensors must be contiguous CUDA tensors of one dtype on one device")
+        self._no_overlap()
         if groups is not None and len(groups) != n:
             raise ValueError("groups must name a group for each tensor")
         self.n_groups = n_groups if n_groups is not None else (1 if groups is None else max(groups) + 1)
@@ -77,6 +78,21 @@ class GradSet:
         if self._bytes == 0:                      # refused: raise its message
             _check(_lib().mlora_clip_grads(self._ref, 0.0, None, None, 0, None))
         self.workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
+
+
+    def _no_overlap(self):
+        """What the call writes overlaps nothing else of the set (a tensor listed twice would be scaled twice)."""
+        span = lambda t, w: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w)
+        out = self.grads if self.out is None else self.out
+        spans = [span(t, True) for t in out]
+        spans += [span(g, False) for g, o in zip(self.grads, out) if g.data_ptr() != o.data_ptr()]
+        written = seen = 0                        # ends so far
+        for start, end, w in sorted(s for s in spans if s[1] > s[0]):
+            if start < (seen if w else written):
+                raise ValueError("an output overlaps another tensor of the set")
+            seen = max(seen, end)
+            if w:
+                written = max(written, end)
 
 
 def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):

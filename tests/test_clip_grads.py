@@ -296,3 +296,18 @@ def test_clipped_step_skips_a_gradient_that_is_not_finite():
     assert skipped.tolist() == [0, 1, 0]
     assert math.isfinite(float(norms[0])) and math.isfinite(float(norms[2])) and not math.isfinite(float(norms[1]))
     assert m.mlora_get_steps(h) == [1, 0, 1]
+
+
+@pytest.mark.gpu
+def test_gradset_refuses_overlapping_outputs():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    x, y = torch.ones(100, device="cuda"), torch.ones(300, device="cuda")
+    for grads, out in (([x, x], None), ([x[:60], x[50:]], None), ([x, x], [y[:100], y[99:199]]), ([x, y[:100]], [y[:100], y[100:200]]),
+                       ([y[:100], x], [y[50:150], y[200:]])):
+        with pytest.raises(ValueError):
+            gr.GradSet(grads, out=out)
+    s = gr.GradSet([x, x, y[:0], x[:0]], out=[y[:100], y[100:200], y[150:150], y[:0]])      # read twice, written apart
+    n = float(gr.clip_grads(s, 1.0))
+    assert abs(n - math.sqrt(200)) <= 35 * U * n and bool((y[:200] != 1).all()) and bool((y[200:] == 1).all())
+    gr.GradSet([x[:50], x[50:]], out=[x[:50], y[:50]])

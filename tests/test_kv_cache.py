@@ -637,3 +637,52 @@ def test_python_refusals():
         kv.kv_attention(c, tab, lens, x, 64, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")[4:])
     with pytest.raises(m.MLoRAError):
         kv.kv_append(c, tab, lens, x, x, max_rows=2)                                   # row_off is missing
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "bf16"), (128, "fp32"), (64, "fp32")])
+@pytest.mark.parametrize("most", [1, 2, 5, 6, 13, 14, 29, 30, 64, 65, 130])
+def test_append_any_rows_at_any_offset(hd, dtype, most):
+    """every size class of a call, new rows at every place of a group of four and of a page, scales that
+    grow and that do not, units with infinities and NaN, and with nothing finite"""
+    before = [0, 1, 2, 3, 5, 31, 62, 63, 64, 65, 127]
+    rows = [max(1, min(most, r)) for r in (most, most, 1, 2, most, 3, most, 4, most, most - 1, most)]
+    caps = [b + 2 * r for b, r in zip(before, rows)]
+    st = Setup(caps, 2, hd, seed=most)
+    st.append(before, dtype)
+    for gain, bad in ((1e-3, False), (300.0, True)):
+        n = sum(rows)
+        x = st.rows(n, "fp32") * gain
+        if bad:
+            x[::3, 0, 5] = math.inf
+            x[1::4, 3, hd - 1] = math.nan
+            x[rows[0]:rows[0] + rows[1]] = -math.inf       # a whole sequence's rows
+        st.append(rows, dtype, x=x.bfloat16() if dtype == "bf16" else x)
+        st.check_state()
+    n = sum(st.len)
+    k, v = st.kv.kv_read(st.cache, st.dtable, st.i32(st.len), n, row_off=st.off(st.len), max_rows=max(st.len))
+    at = 0
+    for s, ln in enumerate(st.len):
+        for name, got in (("k", k), ("v", v)):
+            want = st.model.values(name, st.table[s], ln)
+            g = got[at:at + ln].double().cpu().numpy()
+            assert np.array_equal(np.isnan(g), np.isnan(want)) and np.array_equal(g[~np.isnan(g)], want[~np.isnan(want)])
+        at += ln
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_wide_groups_and_odd_bounds(dtype):
+    """a hundred query heads on one key head, a bound of the lengths beyond 2^62, scale 0, the output over the queries"""
+    torch = _torch()
+    lens = [1, 63, 200, 641]
+    st = Setup(lens, 1, 64, seed=12)
+    st.append(lens)
+    ws = st.kv.kv_workspace()
+    q, out, lse = _attend(st, [1, 3, 2, 5], 100, dtype, workspace=ws)
+    _attend(st, [1, 3, 2, 5], 100, dtype, q=q, workspace=ws, slack=2 ** 62)
+    _attend(st, [1, 3, 2, 5], 100, dtype, q=q, workspace=ws, scale=0.0)
+    same = q.clone()
+    o2, l2 = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), same, 641, row_off=st.off([1, 3, 2, 5]), max_rows=5,
+                                out=same, workspace=ws)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)

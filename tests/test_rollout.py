@@ -345,6 +345,8 @@ def test_next_tokens_invert_the_distribution(small):
     b, lb = kv.tf_sample_cached(s.h, caches, last, one, u2, table, lens2, T, workspace=ws)
     assert t.tf_check_status(s.h) == -2
     assert sorted(np.nonzero(b.cpu().numpy() < 0)[0].tolist()) == [3, 7, 9]
+    none, _ = kv.tf_sample_cached(s.h, caches, last[:0], one[:0], u2[:0], table[:0], lens[:0], T, workspace=ws)
+    assert none.numel() == 0
     c, lc = kv.tf_sample_cached(s.h, caches, last[:0], one[:0], u2, table, lens2, T, workspace=ws,
                                 row_off=_int(torch, [0] * (n + 1)), max_rows=1)
     assert (c == -1).all() and torch.isnan(lc).all()
