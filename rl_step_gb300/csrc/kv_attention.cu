@@ -108,8 +108,11 @@ struct AttnShape {
     static constexpr int THREADS = 32 * NW + 32;
     static constexpr int TILE = KV_PAGE * HD;               // bytes of a K or V tile
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int STAGES = (NT == 1 ? 4 : 6) * (128 / HD);
-    static constexpr int BLOCKS_SM = NW > 4 ? 1 : (NT == 1 ? 3 : 2);
+    // small tiles leave room for a fourth block (41 sequences of 0 to 3001 tokens, 16 heads of 64, fp32: 37 us
+    // with three of 8 stages, 33 with four of 6, 36 with five of 4)
+    static constexpr bool FOUR = HD == 64 && NT == 1 && RG == 1;
+    static constexpr int STAGES = FOUR ? 6 : (NT == 1 ? 4 : 6) * (128 / HD);
+    static constexpr int BLOCKS_SM = FOUR ? 4 : (NW > 4 ? 1 : (NT == 1 ? 3 : 2));
     static constexpr int JOIN_WG = 2048 * PG;               // joining space of a row group, bytes
     // ring, raw queries, joining space, per-warp statistics, barriers,
     // exponents, items, flags
@@ -896,7 +899,7 @@ template <typename T, int HD, int W>
 __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ KvView c,
                                                       const __grid_constant__ AttnCall a, int total) {
     constexpr int D = HD / 32;
-    __shared__ float sl[8], so[8][HD];
+    __shared__ float sm[8], sl[8], so[8][HD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at = blockIdx.x * (8 / W) + warp / W;         // (block of the attention kernel, pair)
     const int from = at / a.prow, row = at % a.prow;
@@ -905,34 +908,49 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     if (at < total) u = a.cuts[from];
     const bool work = u.blocks > 0 && row < u.pairs;
     auto part = [&](int k) { return a.part + (int64_t)(k == 0 ? 2 * from + 1 : 2 * (from + k)) * a.slot; };
+    // the running maximum M, sum l and sums o of the warp's parts; JB parts' loads in flight
+    constexpr int JB = 4;
     float M = -INFINITY, l = 0.f, o[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
-    if (work) {
-        for (int k = lane; k < u.blocks; k += 32) M = fmaxf(M, part(k)[a.prow * HD + row]);
+    auto add = [&](float m, float lm, const float (&x)[D]) {
+        const float v = fmaxf(M, m);
+        const float fo = M == -INFINITY ? 1.f : ex2(M - v), fn = m == -INFINITY ? 1.f : ex2(m - v);   // 1: 0 or NaN stands there
+        l = l * fo + lm * fn;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-#pragma unroll 4
-        for (int k = warp % W; k < u.blocks; k += W) {
-            const float* pk = part(k);
-            const float m = pk[a.prow * HD + row];
-            const float f = m == -INFINITY ? 1.f : ex2(m - M);      // 1: 0 or NaN stands there
-            l = fmaf(pk[a.prow * (HD + 1) + row], f, l);
+        for (int d = 0; d < D; ++d) o[d] = o[d] * fo + x[d] * fn;
+        M = v;
+    };
+    if (work)
+        for (int k0 = warp % W; k0 < u.blocks; k0 += JB * W) {
+            float m[JB], lm[JB], x[JB][D];
 #pragma unroll
-            for (int d = 0; d < D; ++d) o[d] = fmaf(pk[row * HD + lane + 32 * d], f, o[d]);
+            for (int i = 0; i < JB; ++i) {
+                const float* pk = part(k0 + i * W < u.blocks ? k0 + i * W : k0);
+                m[i] = pk[a.prow * HD + row];
+                lm[i] = pk[a.prow * (HD + 1) + row];
+#pragma unroll
+                for (int d = 0; d < D; ++d) x[i][d] = pk[row * HD + lane + 32 * d];
+            }
+#pragma unroll
+            for (int i = 0; i < JB; ++i)
+                if (k0 + i * W < u.blocks) add(m[i], lm[i], x[i]);
         }
-    }
     if (W > 1) {
-        if (lane == 0) sl[warp] = l;
+        if (lane == 0) {
+            sm[warp] = M;
+            sl[warp] = l;
+        }
 #pragma unroll
         for (int d = 0; d < D; ++d) so[warp][lane + 32 * d] = o[d];
         __syncthreads();
         if (warp % W != 0) return;
 #pragma unroll
         for (int w = 1; w < W; ++w) {
-            l += sl[warp + w];
+            float x[D];
 #pragma unroll
-            for (int d = 0; d < D; ++d) o[d] += so[warp + w][lane + 32 * d];
+            for (int d = 0; d < D; ++d) x[d] = so[warp + w][lane + 32 * d];
+            add(sm[warp + w], sl[warp + w], x);
         }
     }
     if (!work) return;
