@@ -247,13 +247,30 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             return r.len > 0 ? (int64_t)((r.len + KV_PAGE - 1) / KV_PAGE + KV_START) * ((r.n * a.group + S::ROWS - 1) / S::ROWS) * c.n_kv : 0;
         };
         const int per = (c.n_seqs + 31) / 32, s0 = lane * per;
+        // a warp's lanes hold the lengths and rows of 32 sequences, from s_base on
+        int s_base = 0;
+        int l_len = 0;
+        int64_t l_a = 0, l_b = 0;
+        auto lengths = [&]() {
+            const int s = s_base + lane < c.n_seqs ? s_base + lane : c.n_seqs - 1;
+            l_len = c.kv_len[s];
+            l_a = c.row_off ? c.row_off[s] : s;
+            l_b = c.row_off ? c.row_off[s + 1] : (int64_t)s + 1;
+        };
+        lengths();
         int64_t mine = 0;
-#pragma unroll 4
-        for (int i = 0; i < per; ++i) {
+        if (per == 1) {
             SeqRows r;
-            const int s = s0 + i < c.n_seqs ? s0 + i : c.n_seqs - 1;
-            const bool ok = kv_seq(c, s, a.max_len, r);
-            mine += ok && s0 + i < c.n_seqs ? weight(r) : 0;
+            const bool ok = kv_seq_ok(c, l_len, l_a, l_b, a.max_len, r);
+            mine = ok && lane < c.n_seqs ? weight(r) : 0;
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < per; ++i) {
+                SeqRows r;
+                const int s = s0 + i < c.n_seqs ? s0 + i : c.n_seqs - 1;
+                const bool ok = kv_seq(c, s, a.max_len, r);
+                mine += ok && s0 + i < c.n_seqs ? weight(r) : 0;
+            }
         }
         int64_t upto = mine;
 #pragma unroll
@@ -280,17 +297,9 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        // The items of the share, in order.  A warp's lanes hold the lengths and rows of the next 32 sequences.
+        // the items of the share, in order
         int64_t pos = lo, rem = lo - before;                // place in the line, and from the first of s_now's on
-        int s_now = from * per, s_base = s_now;
-        int l_len = 0;
-        int64_t l_a = 0, l_b = 0;
-        auto lengths = [&]() {
-            const int s = s_base + lane < c.n_seqs ? s_base + lane : c.n_seqs - 1;
-            l_len = c.kv_len[s];
-            l_a = c.row_off ? c.row_off[s] : s;
-            l_b = c.row_off ? c.row_off[s + 1] : (int64_t)s + 1;
-        };
+        int s_now = from * per;
         if (a.cuts && lane == 0) a.cuts[blockIdx.x].blocks = 0;
         auto next = [&](Item& x) {
             x.s = -1;
@@ -349,27 +358,48 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
             const int i = i0 + lane < x.np ? i0 + lane : i0;
             return c.table[(int64_t)x.s * c.max_pages + x.page0 + i];
         };
-        // lane i: tile and exponents of a page, from its id.  No branch: the vote and the loads are every lane's.
+        // lane i: tile and scales of a page, from its id.  No branch: the vote and the loads are every lane's, and
+        // nothing waits for the loads here.
         int64_t at = 0;
-        int ek = 0, ev = 0;
+        float ks = 0.f, vs = 0.f;
+        unsigned bad = 0;
         auto load_batch = [&](const Item& x, int id) {
             const bool good = id >= 0 && id < c.n_pages;
-            const unsigned bad = __ballot_sync(0xffffffffu, !good);
+            bad = __ballot_sync(0xffffffffu, !good);
             at = (int64_t)(good ? id : 0) * c.n_kv + x.h;   // a page that exists stands in; the rows become NaN
-            ek = scale_exp(c.ks[at]);
-            ev = bad != 0 ? EV_BAD : scale_exp(c.vs[at]);
+            ks = c.ks[at];
+            vs = c.vs[at];
             if (bad != 0 && lane == 0) raise_status(c.status, ST_RANGE);
             __syncwarp();
         };
-        lengths();
+        // an item's queries: the pairs of a token are contiguous
+        auto queries = [&](const Item& x) {
+            if (lane == 0) tcx::mbar_expect_tx(q_full, x.pairs * HD * (int)sizeof(T));
+            __syncwarp();
+            for (int tok = x.pair0 / a.group + lane; tok * a.group < x.pair0 + x.pairs; tok += 32) {
+                const int p0 = tok * a.group > x.pair0 ? tok * a.group : x.pair0;
+                const int p1 = (tok + 1) * a.group < x.pair0 + x.pairs ? (tok + 1) * a.group : x.pair0 + x.pairs;
+                bulk_load(sbase + S::QRAW + (p0 - x.pair0) * HD * (int)sizeof(T),
+                          q + kv_row(c, (int64_t)x.row0 + tok) * a.ldq + ((int64_t)x.h * a.group + p0 - tok * a.group) * HD,
+                          (p1 - p0) * HD * (int)sizeof(T), q_full);
+            }
+            __syncwarp();
+        };
+        if (s_now >= 32) {
+            s_base = s_now;
+            lengths();
+        }
         Item x = {}, y = {};                                // the same in every lane: the current item and the next
         int y_id = 0;                                       // the next one's page ids, asked for an item ahead
         next(x);
         if (x.s >= 0) {
+            // (the pages come behind all of this: asked for here, they delayed the small loads, 29 us against 31 on 8
+            // sequences of 4096 to 8192 tokens)
             const int id = page_id(x, 0);
+            queries(x);
+            load_batch(x, id);
             next(y);
             if (y.s >= 0) y_id = page_id(y, 0);
-            load_batch(x, id);
         }
         int cnt = 0, n_item = 0;                            // pages and items so far
         bool go = true;
@@ -381,22 +411,15 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T
                 tcx::mbar_arrive(item_full(slot));
             }
             if (x.s < 0) break;
-            // the queries: the pairs of a token are contiguous
-            if (n_item >= 1 && !wait(q_empty, (n_item - 1) & 1)) break;
-            if (lane == 0) tcx::mbar_expect_tx(q_full, x.pairs * HD * (int)sizeof(T));
-            __syncwarp();
-            for (int tok = x.pair0 / a.group + lane; tok * a.group < x.pair0 + x.pairs; tok += 32) {
-                const int p0 = tok * a.group > x.pair0 ? tok * a.group : x.pair0;
-                const int p1 = (tok + 1) * a.group < x.pair0 + x.pairs ? (tok + 1) * a.group : x.pair0 + x.pairs;
-                bulk_load(sbase + S::QRAW + (p0 - x.pair0) * HD * (int)sizeof(T),
-                          q + kv_row(c, (int64_t)x.row0 + tok) * a.ldq + ((int64_t)x.h * a.group + p0 - tok * a.group) * HD,
-                          (p1 - p0) * HD * (int)sizeof(T), q_full);
+            if (n_item >= 1) {
+                if (!wait(q_empty, (n_item - 1) & 1)) break;
+                queries(x);
             }
             const int lim = x.before + (x.pair0 + x.pairs - 1) / a.group + 1;
             const int np = x.np, page0 = x.page0;
             for (int i0 = 0; i0 < np && go; i0 += 32) {
                 const int64_t at_now = at;
-                const int ek_now = ek, ev_now = ev;
+                const int ek_now = scale_exp(ks), ev_now = bad != 0 ? EV_BAD : scale_exp(vs);
                 const int n = np - i0 < 32 ? np - i0 : 32;
                 for (int i = 0; i < n; ++i) {
                     const int stage = cnt % S::STAGES;
