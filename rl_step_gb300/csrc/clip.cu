@@ -20,8 +20,11 @@
 //    of two of their own and are joined in fp64.  No atomics, a fixed order:
 //    results repeat bit for bit.
 // (One resident kernel that counted arrivals a chunk instead took 981 us on the 32
-// adapters of the 8B widths, two whole passes 670 us, this 539 us; one
-// adapter, 39 MB: 37, 37 and 21 us.)
+// adapters of the 8B widths, 39 MB each, two whole passes 670 us, this 474 us, 77 %
+// of the copy rate by the floor's bytes; one adapter 37, 37 and 19 us.  Of the 474,
+// about 100 are lines that left L2 before they were scaled: a launch read 76 MB
+// from HBM, 39 of them for the first time, until the scaling loads said that they
+// are the last ones and began with the newest lines; 61 MB since.)
 #include <algorithm>
 #include <cfloat>
 #include <new>
@@ -38,7 +41,7 @@ constexpr int CT = 256;                      // threads of a block
 
 // The tensors of one launch, passed by value: no table in device memory, so
 // nothing of the caller's is kept and a captured launch holds its own copy.  The
-// first blocks scale, the others add squares up.
+// first blocks add squares up, the others scale.
 template <int N>
 struct ClipTab {
     int n_scale, n_norm;                     // entries: those to scale, then those whose norm is wanted
@@ -122,13 +125,18 @@ struct Chunk {
     uint4 w[VECS<T>];
     const T* p;
     int n, nv;                               // elements, 16-byte pieces
+    // AGAIN: a later launch reads it once more, from L2; else this is that last time, and its lines may go first
+    template <bool AGAIN>
     __device__ __forceinline__ void load(const T* p_, int n_) {
         p = p_;
         n = n_;
         nv = aligned16(p) ? n / PER16<T> : 0;
 #pragma unroll
         for (int k = 0; k < VECS<T>; ++k)
-            if ((int)threadIdx.x + CT * k < nv) w[k] = __ldcg(reinterpret_cast<const uint4*>(p) + threadIdx.x + CT * k);
+            if ((int)threadIdx.x + CT * k < nv) {
+                const uint4* q = reinterpret_cast<const uint4*>(p) + threadIdx.x + CT * k;
+                w[k] = AGAIN ? __ldcg(q) : __ldcs(q);
+            }
     }
     // this thread's squares
     __device__ __forceinline__ float sum() const {
@@ -223,8 +231,11 @@ template <typename T, int N>
 __global__ void __launch_bounds__(CT, 4) clip_kernel(const __grid_constant__ ClipTab<N> t, ClipSum* part,
                                                      const int* __restrict__ mask, float max_norm, float* norms) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const bool scale = (int)blockIdx.x < t.scale_chunks;
-    const int chunk = scale ? t.scale0 + blockIdx.x : t.norm0 + blockIdx.x - t.scale_chunks;
+    // the blocks that add up come first: they read from HBM while those that scale wait for the launch before
+    const int adding = gridDim.x - t.scale_chunks;
+    const bool scale = (int)blockIdx.x >= adding;
+    // the last chunks that were read are scaled first: they are the likeliest to be in L2
+    const int chunk = scale ? t.scale0 + (int)(gridDim.x - 1 - blockIdx.x) : t.norm0 + blockIdx.x;
     const ClipEntry& e = scale ? clip_find(t.e, t.n_scale, chunk, &ClipEntry::chunk0)
                                : clip_find(t.e + t.n_scale, t.n_norm, chunk, &ClipEntry::sum0);
     const int64_t at = (int64_t)(scale ? chunk - e.chunk0 : (chunk - e.sum0) * e.per_sum) * CLIP_CHUNK;
@@ -232,10 +243,11 @@ __global__ void __launch_bounds__(CT, 4) clip_kernel(const __grid_constant__ Cli
     T* o = static_cast<T*>(e.dst) + at;
     const bool wanted = scale || !mask || mask[e.group];
     Chunk<T> x;
-    x.load(p, wanted ? chunk_len(e, at) : 0);
-    // every block waits, so that a launch's end means the end of all before it
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (scale) x.template load<false>(p, chunk_len(e, at));
+    else x.template load<true>(p, wanted ? chunk_len(e, at) : 0);
+    // every block waits before it writes, so that a launch's end means the end of all before it
     if (scale) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         __shared__ float s_f;
         const double norm = group_norm(part, e.g0, e.g1);
         if (threadIdx.x == 0) {
@@ -248,12 +260,13 @@ __global__ void __launch_bounds__(CT, 4) clip_kernel(const __grid_constant__ Cli
         float s = x.sum(), lost = 0.f;
         int64_t n = x.n;
         for (int k = 1; k < e.per_sum && wanted && at + (int64_t)k * CLIP_CHUNK < e.size; ++k) {
-            x.load(p + (int64_t)k * CLIP_CHUNK, chunk_len(e, at + (int64_t)k * CLIP_CHUNK));
+            x.template load<true>(p + (int64_t)k * CLIP_CHUNK, chunk_len(e, at + (int64_t)k * CLIP_CHUNK));
             n += x.n;
             add_to(s, lost, x.sum());
         }
         ClipSum sum{block_sum(s), 0};
         if (!(sum.v < 1e30f && sum.v > 1e-25f)) sum = sum_scaled(p, n);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         if (threadIdx.x == 0) part[chunk] = sum;
     }
 }
@@ -311,9 +324,10 @@ cudaError_t launch_tables(const ClipEntry* scale, int n_scale, const ClipEntry* 
     return cudaSuccess;
 }
 
-// Bytes of a batch: about a third of L2, since the next batch passes through it
-// while this one is scaled and written.
-constexpr int64_t CLIP_BATCH = 40 << 20;
+// Bytes of a batch (or one larger group): the next batch passes through L2 while
+// this one is scaled and written.  96 groups of 10 MB: 468 us with batches of 10
+// MB (too many launches), 404 with 20, 393 with 28, 415 with 40.
+constexpr int64_t CLIP_BATCH = 28 << 20;
 
 template <typename T>
 cudaError_t launch_clip(const ClipEntry* e, int n, ClipSum* part, float max_norm, float* norms, cudaStream_t s) {
