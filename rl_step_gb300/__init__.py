@@ -299,10 +299,11 @@ def mlora_optim_step_clipped(h: Handle, max_norm: float, lr=1e-4, beta1=0.9, bet
     """Adam step with each adapter's gradient clipped to max_norm; returns
     (skipped flags int32, norms before clipping float32), [n_adapters] on the device."""
     import torch
+    from .kv import _empty
     if skipped_out is None:
-        skipped_out = torch.empty(h.n_adapters, dtype=torch.int32, device="cuda")
+        skipped_out = _empty(h.n_adapters, torch.int32, "cuda", stream)
     if norms_out is None:
-        norms_out = torch.empty(h.n_adapters, dtype=torch.float32, device="cuda")
+        norms_out = _empty(h.n_adapters, torch.float32, "cuda", stream)
     p = _Adam(lr, beta1, beta2, eps, weight_decay)
     n = 0 if adapters is None else len(adapters)
     arr = None if adapters is None else (c_int32 * max(1, n))(*adapters)

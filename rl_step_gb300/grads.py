@@ -13,7 +13,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _check, load_library
-from .kv import _on
+from .kv import _empty, _on
 
 __all__ = ["GradSet", "clip_grads"]
 
@@ -46,7 +46,7 @@ def _lib():
 class GradSet:
     """The tensors of repeated clip_grads calls: contiguous CUDA tensors of one
     dtype (float32 or bf16), an optional group of each, optional outputs (None:
-    in place).  Keeps the tensors alive, and the calls' workspace."""
+    in place).  Keeps the tensors alive."""
 
     def __init__(self, grads: Sequence, groups: Optional[Sequence[int]] = None, n_groups: Optional[int] = None,
                  out: Optional[Sequence] = None):
@@ -77,7 +77,6 @@ class GradSet:
         self._bytes = int(_lib().mlora_clip_grads_workspace(self._ref))
         if self._bytes == 0:                      # refused: raise its message
             _check(_lib().mlora_clip_grads(self._ref, 0.0, None, None, 0, None))
-        self.workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
 
 
     def _no_overlap(self):
@@ -97,13 +96,14 @@ class GradSet:
 
 def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):
     """Clip each group of gs to max_norm; returns the norms before clipping
-    (float32 [n_groups]).  Calls on one GradSet must be serialised."""
-    stream = _on(gs.index, stream)
+    (float32 [n_groups])."""
+    handle = _on(gs.index, stream)
+    workspace = _empty(gs._bytes, torch.uint8, gs.device, stream)
     if norms_out is None:
-        norms_out = torch.empty(gs.n_groups, dtype=torch.float32, device=gs.device)
+        norms_out = _empty(gs.n_groups, torch.float32, gs.device, stream)
     elif norms_out.dtype is not torch.float32 or norms_out.numel() != gs.n_groups or \
             not norms_out.is_contiguous() or norms_out.get_device() != gs.index:
         raise ValueError("norms_out must be a contiguous float32 tensor with a value for each group")
-    _check(_lib().mlora_clip_grads(gs._ref, max_norm, norms_out.data_ptr(), gs.workspace.data_ptr(), gs._bytes,
-                                   stream))
+    _check(_lib().mlora_clip_grads(gs._ref, max_norm, norms_out.data_ptr(), workspace.data_ptr(), gs._bytes,
+                                   handle))
     return norms_out

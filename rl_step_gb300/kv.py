@@ -101,6 +101,15 @@ def _on(index: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor whose memory belongs to the stream that will use it: blocks of another
+    stream's pool can still be in use there, or be handed out again too early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class KvCache:
     """A pool of cache pages: uint8 k, v [n_pages, n_kv_heads, 64, head_dim]
     (the byte order inside a tile is the library's) and float32 k_scale, v_scale
@@ -188,8 +197,8 @@ def kv_read(cache: KvCache, page_table, kv_len, n_rows: int, row_off=None, max_r
     dtype = torch.float32 if dtype is None else dtype
     q = _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows)
     shape = (n_rows, cache.n_kv_heads, cache.head_dim)
-    ko = torch.empty(shape, dtype=dtype, device=cache.device)
-    vo = torch.empty(shape, dtype=dtype, device=cache.device)
+    ko = _empty(shape, dtype, cache.device, stream)
+    vo = _empty(shape, dtype, cache.device, stream)
     _check(_lib().mlora_kv_read(cache._ref, byref(q), _dtype(dtype), ko.data_ptr(), vo.data_ptr(), _on(cache.index, stream)))
     return ko, vo
 
@@ -206,17 +215,17 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
     s = _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows)
     ldq = _rows("q", q, heads, cache.head_dim, cache.index)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     elif out.dtype != q.dtype or out.shape[0] != n_rows:
         raise ValueError("out must have q's rows and dtype")
     ldo = _rows("out", out, heads, cache.head_dim, cache.index)
     if lse is None:
-        lse = torch.empty((n_rows, heads), dtype=torch.float32, device=cache.device)
+        lse = _empty((n_rows, heads), torch.float32, cache.device, stream)
     elif lse.dtype is not _FLOAT32 or lse.shape != (n_rows, heads) or not lse.is_contiguous() or \
             lse.get_device() != cache.index:
         raise ValueError("lse must be a contiguous float32 [rows, heads] tensor on the cache's device")
     if workspace is None:
-        workspace = kv_workspace(cache.device)
+        workspace = _empty(WORKSPACE_BYTES, torch.uint8, cache.device, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != cache.index:
         raise ValueError("workspace must be contiguous and on the cache's device")
     a = _KvAttn(q.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), ldq, ldo,
@@ -226,12 +235,12 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
     return out, lse
 
 
-def _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace):
+def _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace, stream):
     if len(caches) != h.n_layers:
         raise ValueError(f"{h.n_layers} caches are needed, one per layer")
     c0 = caches[0]
     if workspace is None:
-        workspace = kv_workspace(c0.device)
+        workspace = _empty(WORKSPACE_BYTES, torch.uint8, c0.device, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != c0.index:
         raise ValueError("workspace must be contiguous and on the caches' device")
     if any(c.index != c0.index for c in caches):
@@ -248,11 +257,11 @@ def tf_forward_cached(h, caches, tokens, targets, adapter_ids, page_table, kv_le
     """Forward of the sequences' newest rows over one cache per layer, which gets
     their keys and values; returns the targets' logprobs (targets None: only
     the caches are filled).  Without a workspace one is allocated for the call."""
-    ctx = _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace)
+    ctx = _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace, stream)
     c0 = caches[0]
     n = tokens.numel()
     if targets is not None and logprobs_out is None:
-        logprobs_out = torch.empty(n, dtype=torch.float32, device=c0.device)
+        logprobs_out = _empty(n, torch.float32, c0.device, stream)
     b = _TfBatch(n, _ids("tokens", tokens, (n,), c0.index),
                  None if targets is None else _ids("targets", targets, (n,), c0.index), None,
                  _ids("adapter_ids", adapter_ids, (n,), c0.index))
@@ -266,13 +275,13 @@ def tf_sample_cached(h, caches, tokens, adapter_ids, uniforms, page_table, kv_le
                      max_rows: int = 1, workspace=None, next_out=None, logprob_out=None, stream=None):
     """The same, and the next token of every sequence from its last row:
     returns (next int32 [n_seqs], its logprob float32 [n_seqs])."""
-    ctx = _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace)
+    ctx = _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace, stream)
     c0 = caches[0]
     n, m = tokens.numel(), page_table.shape[0]
     if next_out is None:
-        next_out = torch.empty(m, dtype=torch.int32, device=c0.device)
+        next_out = _empty(m, torch.int32, c0.device, stream)
     if logprob_out is None:
-        logprob_out = torch.empty(m, dtype=torch.float32, device=c0.device)
+        logprob_out = _empty(m, torch.float32, c0.device, stream)
     b = _TfBatch(n, _ids("tokens", tokens, (n,), c0.index), None, None, _ids("adapter_ids", adapter_ids, (n,), c0.index))
     _check(_lib().mlora_tf_sample_cached(h.ptr, byref(b), byref(ctx), _out("uniforms", uniforms, m, c0.index),
                                          _ids("next_out", next_out, (m,), c0.index),

@@ -686,3 +686,63 @@ def test_attention_wide_groups_and_odd_bounds(dtype):
     o2, l2 = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), same, 641, row_off=st.off([1, 3, 2, 5]), max_rows=5,
                                 out=same, workspace=ws)
     assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.gpu
+def test_outputs_on_another_stream_do_not_meet_the_current_ones_writes():
+    """memory that the current stream has still to write when it is handed out again: results asked for on
+    another stream must not lie there"""
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    st = Setup([500, 300], 2, 64, seed=21)
+    st.append([500, 300])
+    q = torch.randn(2, 8, 64, device="cuda")
+    lens = st.i32(st.len)
+    off = st.off([500, 300])
+    want = st.kv.kv_attention(st.cache, st.dtable, lens, q, 500)
+    wk, wv = st.kv.kv_read(st.cache, st.dtable, lens, 800, row_off=off, max_rows=500)
+    x = torch.randn(200001, device="cuda")
+    gs = gr.GradSet([x], out=[torch.empty_like(x)])
+    wn = gr.clip_grads(gs, math.inf)
+    big = torch.zeros(1 << 28, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for _ in range(40):                                    # some 10 ms of work before the fills
+        big.mul_(1.0)
+    old = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+           for n in (q.numel() * 4, 2 * 8 * 4, 800 * 2 * 64 * 4, 800 * 2 * 64 * 4, gs._bytes, 512, st.kv.WORKSPACE_BYTES)]
+    del old
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, lens, q, 500, stream=s)
+    k, v = st.kv.kv_read(st.cache, st.dtable, lens, 800, row_off=off, max_rows=500, stream=s)
+    norm = gr.clip_grads(gs, math.inf, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(k, wk) and torch.equal(v, wv) and torch.equal(norm, wn)
+
+
+@pytest.mark.gpu
+def test_pages_beyond_four_gigabytes():
+    """page ids whose bytes lie behind 2^32: the same results as from a small pool"""
+    torch = _torch()
+    import rl_step_gb300.kv as kv
+    n_pages, n_kv, hd = 70000, 8, 128                      # 4.6 GB each of keys and values
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    high = [69999, 65536, 65535, 32768, 69000, 1, 68001]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(410, 2 * n_kv, hd, generator=g, device="cuda").bfloat16()
+    q = torch.randn(5, 16, hd, generator=g, device="cuda").bfloat16()
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")
+    got = []
+    for pool, ids in ((n_pages, high), (7, list(range(7)))):
+        c = kv.KvCache.empty(pool, n_kv, hd)
+        table = i32([ids[:4] , ids[4:] + [-1]])
+        kv.kv_append(c, table, i32([250, 160]), x[:, :n_kv], x[:, n_kv:], row_off=i32([0, 250, 410]), max_rows=250)
+        out, lse = kv.kv_attention(c, table, i32([250, 160]), q, 250, row_off=i32([0, 2, 5]), max_rows=3)
+        k, v = kv.kv_read(c, table, i32([250, 160]), 410, row_off=i32([0, 250, 410]), max_rows=250)
+        assert kv.kv_check_status(c) == 0
+        got.append((out, lse, k, v))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
