@@ -123,7 +123,8 @@ int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype
  * evenly whatever the lengths: long sequences are cut where a block's share
  * ends and their parts joined, so the order of a row's sums depends on the
  * lengths of the batch.  With less than the shape needs (0, say) no sequence is
- * cut, and a row's result is bit for bit the same in every batch.
+ * cut, and a row's result is bit for bit the same whatever else a call with the
+ * same max_rows holds.
  * Errors: E_ARG, E_CUDA. */
 typedef struct {
     const void* q;

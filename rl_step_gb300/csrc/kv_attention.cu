@@ -97,12 +97,12 @@ struct Item {
     int slot;                               // its partial result's place, or -1: the whole unit
 };
 
-template <typename T, int HD, int NT, int RG>
+template <typename T, int HD, int NT, int RG, int PG_>
 struct AttnShape {
     static constexpr bool FOLD = sizeof(T) == 4;            // a pair takes two columns: its high and its low part
     static constexpr int PR = (FOLD ? 4 : 8) * NT;          // pairs of a row group
     static constexpr int ROWS = PR * RG;
-    static constexpr int PG = RG == 1 ? 2 : 1;              // pages in work at once
+    static constexpr int PG = PG_;                          // pages in work at once
     static constexpr int WG = 2 * PG;                       // warps of a row group: page parity x half of the page
     static constexpr int NW = RG * WG;                      // consumer warps
     static constexpr int THREADS = 32 * NW + 32;
@@ -111,8 +111,9 @@ struct AttnShape {
     // small tiles leave room for a fourth block (41 sequences of 0 to 3001 tokens, 16 heads of 64, fp32: 37 us
     // with three of 8 stages, 33 with four of 6, 36 with five of 4)
     static constexpr bool FOUR = HD == 64 && NT == 1 && RG == 1;
-    static constexpr int STAGES = FOUR ? 6 : (NT == 1 ? 4 : 6) * (128 / HD);
-    static constexpr int BLOCKS_SM = FOUR ? 4 : (NW > 4 ? 1 : (NT == 1 ? 3 : 2));
+    static constexpr bool SLIM = NW == 2;                   // two consumer warps: four blocks of three stages
+    static constexpr int STAGES = FOUR ? 6 : SLIM ? 3 : (NT == 1 ? 4 : 6) * (128 / HD);
+    static constexpr int BLOCKS_SM = FOUR || SLIM ? 4 : (NW > 4 ? 1 : (NT == 1 ? 3 : 2));
     static constexpr int JOIN_WG = 2048 * PG;               // joining space of a row group, bytes
     // ring, raw queries, joining space, per-warp statistics, barriers,
     // exponents, items, flags
@@ -197,10 +198,10 @@ __device__ __forceinline__ void load16_f(const bf16* p, float (&v)[16]) {
     }
 }
 
-template <typename T, int HD, int NT, int RG>
-__global__ void __launch_bounds__(AttnShape<T, HD, NT, RG>::THREADS, AttnShape<T, HD, NT, RG>::BLOCKS_SM)
+template <typename T, int HD, int NT, int RG, int PG_>
+__global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnShape<T, HD, NT, RG, PG_>::BLOCKS_SM)
     kv_attn_kernel(const __grid_constant__ KvView c, const __grid_constant__ AttnCall a) {
-    using S = AttnShape<T, HD, NT, RG>;
+    using S = AttnShape<T, HD, NT, RG, PG_>;
     constexpr bool FOLD = S::FOLD;
     constexpr int E = FOLD ? 1 : 2;                         // pairs of a thread in an 8-column tile
     extern __shared__ __align__(128) uint8_t smem[];
@@ -985,9 +986,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     if (lane == 0 && a.lse) a.lse[y * a.n_heads + head] = ((M == -INFINITY ? 0.f : M) - P_SHIFT + log2f(l)) * LN2;
 }
 
-template <typename T, int HD, int NT, int RG>
+template <typename T, int HD, int NT, int RG, int PG_>
 cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
-    using S = AttnShape<T, HD, NT, RG>;
+    using S = AttnShape<T, HD, NT, RG, PG_>;
     // once a device: its SMs, and the kernel's shared memory (the attribute stays with the function)
     static std::atomic<int> sms[64];
     int dev = 0, n_sms = 0;
@@ -995,9 +996,9 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) n_sms = sms[dev].load(std::memory_order_relaxed);
     if (n_sms == 0) {
-        e = cudaFuncSetAttribute(kv_attn_kernel<T, HD, NT, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        e = cudaFuncSetAttribute(kv_attn_kernel<T, HD, NT, RG, PG_>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kv_attn_kernel<T, HD, NT, RG>, cudaFuncAttributePreferredSharedMemoryCarveout,
+            e = cudaFuncSetAttribute(kv_attn_kernel<T, HD, NT, RG, PG_>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
@@ -1024,7 +1025,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     if (!cut) blocks = units < most ? units : most;
     k.part = static_cast<float*>(a.workspace);
     k.cuts = cut ? reinterpret_cast<Cut*>(k.part + blocks * 2 * k.slot) : nullptr;
-    kv_attn_kernel<T, HD, NT, RG><<<(unsigned)blocks, S::THREADS, S::SMEM, s>>>(c, k);
+    kv_attn_kernel<T, HD, NT, RG, PG_><<<(unsigned)blocks, S::THREADS, S::SMEM, s>>>(c, k);
     e = cudaGetLastError();
     if (e != cudaSuccess || !cut) return e;
     // the join waits on the device for the attention kernel's end: only its launch overlaps it
@@ -1044,15 +1045,27 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
 
 // One column tile (8 pairs; 4 on fp32) where a sequence's pairs fit it, then two;
 // more row groups share each page tile (its reads and its place in shared
-// memory) where a sequence has more.
+// memory) where a sequence has more.  A single row group has two pages in work; or,
+// heads of 128 and many units, one page and more blocks, which hide the ends of
+// units better (256 sequences of 512 to 2048 tokens, 2048 units: 118 us against 114;
+// one of 130,001, 8 units: 53.0 against 53.8; heads of 64, 656 units: 31.7 against
+// 40.6; where units are twice as long, 64 sequences of 1000 to 4001 and 16 heads, 108
+// against 110).  That choice looks at the whole batch, so it is made only where the
+// workspace lets results depend on it.
+constexpr int64_t KV_MANY = 600;
 template <typename T, int HD>
 cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
-    constexpr int PR = AttnShape<T, HD, 1, 1>::PR;
+    constexpr int PR = AttnShape<T, HD, 1, 1, 2>::PR;
     const int64_t pairs = (int64_t)c.max_rows * (a.n_heads / c.n_kv);
-    if (pairs <= PR) return attn_t<T, HD, 1, 1>(c, a, s);
-    if (pairs <= 2 * PR) return attn_t<T, HD, 1, 2>(c, a, s);
-    if (pairs <= 4 * PR) return attn_t<T, HD, 2, 2>(c, a, s);
-    return attn_t<T, HD, 2, 4>(c, a, s);
+    if (pairs <= PR) {
+        if constexpr (HD == 128)
+            if (a.workspace && a.workspace_bytes >= MLORA_KV_WORKSPACE_BYTES && (int64_t)c.n_seqs * c.n_kv >= KV_MANY)
+                return attn_t<T, HD, 1, 1, 1>(c, a, s);
+        return attn_t<T, HD, 1, 1, 2>(c, a, s);
+    }
+    if (pairs <= 2 * PR) return attn_t<T, HD, 1, 2, 1>(c, a, s);
+    if (pairs <= 4 * PR) return attn_t<T, HD, 2, 2, 1>(c, a, s);
+    return attn_t<T, HD, 2, 4, 1>(c, a, s);
 }
 
 }  // namespace

@@ -746,3 +746,19 @@ def test_pages_beyond_four_gigabytes():
         got.append((out, lse, k, v))
     for a, b in zip(*got):
         assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,dtype", [(8, "bf16"), (24, "bf16"), (16, "fp32")])
+def test_attention_many_units(heads, dtype):
+    """100 sequences of 8 key/value heads: short, long (cut) and empty ones, whole batch and without a workspace"""
+    rng = np.random.default_rng(31)
+    lens = [int(x) for x in rng.integers(0, 90, 92)] + [0, 1, 63, 64, 65, 600, 601, 777]
+    st = Setup(lens, 8, 128, seed=33)
+    st.append(lens)
+    live = [1 if n else 0 for n in lens]
+    q, out, lse = _attend(st, live, heads, dtype, workspace=st.kv.kv_workspace())
+    _, o2, l2 = _attend(st, live, heads, dtype, q=q, workspace=st.kv.kv_workspace())
+    assert st.torch.equal(out, o2) and st.torch.equal(lse, l2)
+    _attend(st, live, heads, dtype, q=q, workspace=st.kv.kv_workspace(nbytes=0))
+    _attend(st, live, heads, dtype, q=q, slack=5000)
