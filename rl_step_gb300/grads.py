@@ -46,7 +46,8 @@ def _lib():
 class GradSet:
     """The tensors of repeated clip_grads calls: contiguous CUDA tensors of one
     dtype (float32 or bf16), an optional group of each, optional outputs (None:
-    in place).  Keeps the tensors alive."""
+    in place).  Keeps the tensors alive, and a workspace for the calls on the
+    stream it was made on (other streams' and captured calls take one each)."""
 
     def __init__(self, grads: Sequence, groups: Optional[Sequence[int]] = None, n_groups: Optional[int] = None,
                  out: Optional[Sequence] = None):
@@ -77,6 +78,9 @@ class GradSet:
         self._bytes = int(_lib().mlora_clip_grads_workspace(self._ref))
         if self._bytes == 0:                      # refused: raise its message
             _check(_lib().mlora_clip_grads(self._ref, 0.0, None, None, 0, None))
+        with torch.cuda.device(self.index):
+            self._stream = torch.cuda.current_stream().cuda_stream
+            self._workspace = _empty(self._bytes, torch.uint8, self.device, None)
 
 
     def _no_overlap(self):
@@ -98,7 +102,10 @@ def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):
     """Clip each group of gs to max_norm; returns the norms before clipping
     (float32 [n_groups])."""
     handle = _on(gs.index, stream)
-    workspace = _empty(gs._bytes, torch.uint8, gs.device, stream)
+    if handle == gs._stream and not torch.cuda.is_current_stream_capturing():
+        workspace = gs._workspace
+    else:
+        workspace = _empty(gs._bytes, torch.uint8, gs.device, stream)
     if norms_out is None:
         norms_out = _empty(gs.n_groups, torch.float32, gs.device, stream)
     elif norms_out.dtype is not torch.float32 or norms_out.numel() != gs.n_groups or \

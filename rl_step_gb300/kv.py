@@ -215,7 +215,7 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
     s = _seqs(cache, page_table, kv_len, row_off, n_rows, max_rows)
     ldq = _rows("q", q, heads, cache.head_dim, cache.index)
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
+        out = _empty(q.shape, q.dtype, cache.device, stream)
     elif out.dtype != q.dtype or out.shape[0] != n_rows:
         raise ValueError("out must have q's rows and dtype")
     ldo = _rows("out", out, heads, cache.head_dim, cache.index)
