@@ -36,14 +36,15 @@
 //    held at 2^12 times its value, so that it stays within fp16 and its rounding
 //    relative (2^-11) down to 2^-26 of the reference (absolute 2^-37 of it
 //    below that); on fp32 it is split like q.
-//  * Warps of a row group take different halves of a page and, with one or two
-//    row groups, every other page, 32 tokens at a step; each has a running maximum and sum of its own, joined at the
-//    item's end, so nothing but the ring's barriers is shared in the loop.
+//  * Warps of a row group take different halves of a page and, where a single row
+//    group has two pages in work, every other page, 32 tokens at a step; each has
+//    a running maximum and sum of its own, joined at the item's end, so nothing
+//    but the ring's barriers is shared in the loop.
 //  * A share's ends cut sequences: such an item leaves its rows' unnormalised
 //    sums, maximum and sum in the workspace, and a second small kernel joins the
 //    parts in order.  (Runs of a fixed length taken from a counter left a tail or
 //    ended too often: 94 us at best for 32 sequences of 1023 to 8191 tokens, 4
-//    rows each, which equal shares serve in 65; joined by the last item to
+//    rows each, which equal shares serve in 62; joined by the last item to
 //    arrive, a run's end cost its block about 6 us of fences and atomics.  Warps
 //    that each stream a share of their own hide the ends of items better but
 //    end 84 to 125 us after the start where blocks' shares end together.)

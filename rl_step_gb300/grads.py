@@ -43,6 +43,21 @@ def _lib():
     return _grads_lib
 
 
+def _no_overlap(ptrs, outs, sizes, width):
+    """What a call writes must overlap nothing else of its set (a tensor listed twice would be scaled twice)."""
+    spans = [(o, o + n * width, True) for o, n in zip(outs, sizes) if n]
+    spans += [(p, p + n * width, False) for p, o, n in zip(ptrs, outs, sizes) if n and p != o]
+    spans.sort()
+    written = seen = 0                            # ends so far
+    for start, end, writes in spans:
+        if start < (seen if writes else written):
+            raise ValueError("an output overlaps another tensor of the set")
+        if end > seen:
+            seen = end
+        if writes and end > written:
+            written = end
+
+
 class GradSet:
     """The tensors of repeated clip_grads calls: contiguous CUDA tensors of one
     dtype (float32 or bf16), an optional group of each, optional outputs (None:
@@ -63,13 +78,14 @@ class GradSet:
         for t in self.grads + (self.out or []):
             if t.dtype != dtype or t.device != self.device or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("tensors must be contiguous CUDA tensors of one dtype on one device")
-        self._no_overlap()
+        ptrs = [t.data_ptr() for t in self.grads]
+        outs = None if self.out is None else [t.data_ptr() for t in self.out]
+        sizes = [t.numel() for t in self.grads]
+        _no_overlap(ptrs, outs or ptrs, sizes, self.grads[0].element_size())
         if groups is not None and len(groups) != n:
             raise ValueError("groups must name a group for each tensor")
         self.n_groups = n_groups if n_groups is not None else (1 if groups is None else max(groups) + 1)
-        ptrs = lambda ts: (c_void_p * n)(*[t.data_ptr() for t in ts])
-        self._arrays = (ptrs(self.grads), None if self.out is None else ptrs(self.out),
-                        (c_int64 * n)(*[t.numel() for t in self.grads]),
+        self._arrays = ((c_void_p * n)(*ptrs), None if outs is None else (c_void_p * n)(*outs), (c_int64 * n)(*sizes),
                         None if groups is None else (c_int32 * n)(*groups))
         self._c = _GradSet(self._arrays[0], self._arrays[1], self._arrays[2], self._arrays[3], n, self.n_groups,
                            0 if dtype == torch.bfloat16 else 1)
@@ -81,21 +97,6 @@ class GradSet:
         with torch.cuda.device(self.index):
             self._stream = torch.cuda.current_stream().cuda_stream
             self._workspace = _empty(self._bytes, torch.uint8, self.device, None)
-
-
-    def _no_overlap(self):
-        """What the call writes overlaps nothing else of the set (a tensor listed twice would be scaled twice)."""
-        span = lambda t, w: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w)
-        out = self.grads if self.out is None else self.out
-        spans = [span(t, True) for t in out]
-        spans += [span(g, False) for g, o in zip(self.grads, out) if g.data_ptr() != o.data_ptr()]
-        written = seen = 0                        # ends so far
-        for start, end, w in sorted(s for s in spans if s[1] > s[0]):
-            if start < (seen if w else written):
-                raise ValueError("an output overlaps another tensor of the set")
-            seen = max(seen, end)
-            if w:
-                written = max(written, end)
 
 
 def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):
