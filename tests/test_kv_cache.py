@@ -693,33 +693,37 @@ def test_outputs_on_another_stream_do_not_meet_the_current_ones_writes():
     """memory that the current stream has still to write when it is handed out again: results asked for on
     another stream must not lie there"""
     torch = _torch()
-    import rl_step_gb300.grads as gr
-    st = Setup([500, 300], 2, 64, seed=21)
-    st.append([500, 300])
-    q = torch.randn(2, 8, 64, device="cuda")
-    lens = st.i32(st.len)
-    off = st.off([500, 300])
-    want = st.kv.kv_attention(st.cache, st.dtable, lens, q, 500)
-    wk, wv = st.kv.kv_read(st.cache, st.dtable, lens, 800, row_off=off, max_rows=500)
-    x = torch.randn(200001, device="cuda")
-    gs = gr.GradSet([x], out=[torch.empty_like(x)])
-    wn = gr.clip_grads(gs, math.inf)
+    st = Setup([3500, 1300], 2, 64, seed=21)
+    st.append([3500, 1300])
+    q = torch.randn(4800, 8, 64, device="cuda")
+    lens, off = st.i32(st.len), st.off([3500, 1300])
+    ws = st.kv.kv_workspace()
+    args = (st.cache, st.dtable, lens)
+    want = st.kv.kv_attention(*args, q, 3500, row_off=off, max_rows=3500, workspace=ws)
+    wk, wv = st.kv.kv_read(*args, 4800, row_off=off, max_rows=3500)
     big = torch.zeros(1 << 28, device="cuda")
     s = torch.cuda.Stream()
-    torch.cuda.synchronize()
-    torch.cuda.empty_cache()
-    for _ in range(40):                                    # some 10 ms of work before the fills
-        big.mul_(1.0)
-    old = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
-           for n in (q.numel() * 4, 2 * 8 * 4, 800 * 2 * 64 * 4, 800 * 2 * 64 * 4, gs._bytes, 512, st.kv.WORKSPACE_BYTES)]
-    del old
-    out, lse = st.kv.kv_attention(st.cache, st.dtable, lens, q, 500, stream=s)
-    k, v = st.kv.kv_read(st.cache, st.dtable, lens, 800, row_off=off, max_rows=500, stream=s)
-    norm = gr.clip_grads(gs, math.inf, stream=s)
-    s.synchronize()
-    torch.cuda.synchronize()
+
+    def meet(nbytes, call):
+        """call(), while blocks of nbytes each wait to be filled with 255 by the current stream"""
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        old = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in nbytes]
+        torch.cuda.synchronize()
+        for _ in range(100):                               # some 30 ms of work before the fills
+            big.mul_(1.0)
+        for x in old:
+            x.fill_(255)
+        del old, x
+        got = call()
+        s.synchronize()
+        torch.cuda.synchronize()
+        return got
+    out, lse = meet([q.numel() * 4], lambda: st.kv.kv_attention(*args, q, 3500, row_off=off, max_rows=3500, workspace=ws,
+                                                                stream=s))
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
-    assert torch.equal(k, wk) and torch.equal(v, wv) and torch.equal(norm, wn)
+    k, v = meet([wk.numel() * 4] * 2, lambda: st.kv.kv_read(*args, 4800, row_off=off, max_rows=3500, stream=s))
+    assert torch.equal(k, wk) and torch.equal(v, wv)
 
 
 @pytest.mark.gpu
