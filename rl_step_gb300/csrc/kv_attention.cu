@@ -114,7 +114,7 @@ struct AttnShape {
     static constexpr bool FOUR = HD == 64 && NT == 1 && RG == 1;
     static constexpr bool SLIM = NW == 2;                   // two consumer warps: four blocks of three stages
     static constexpr int STAGES = FOUR ? 6 : SLIM ? 3 : (NT == 1 ? 4 : 6) * (128 / HD);
-    static constexpr int BLOCKS_SM = FOUR || SLIM ? 4 : (NW > 4 ? 1 : (NT == 1 ? 3 : 2));
+    static constexpr int BLOCKS_SM = FOUR || SLIM ? 4 : (NW > 4 ? 1 : 3);
     static constexpr int JOIN_WG = 2048 * PG;               // joining space of a row group, bytes
     // ring, raw queries, joining space, per-warp statistics, barriers,
     // exponents, items, flags
@@ -1044,9 +1044,12 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, many ? kv_join_kernel<T, HD, 8> : kv_join_kernel<T, HD, 1>, c, k, total);
 }
 
-// One column tile (8 pairs; 4 on fp32) where a sequence's pairs fit it, then two;
-// more row groups share each page tile (its reads and its place in shared
-// memory) where a sequence has more.  A single row group has two pages in work; or,
+// One column tile (8 pairs; 4 on fp32) where a sequence's pairs fit it.  More row
+// groups share each page tile (its reads and its place in shared memory) where a
+// sequence has more: two of a tile, or, where that pads little, four of two tiles,
+// which convert each byte for twice the columns (9 rows of 36 pairs: 89 us in
+// tiles of 64, 68 in tiles of 16; 64 pairs: 178 and 195; 72: 132 and 110; prompts
+// of 2000 rows: 2.01 and 2.12 ms).  A single row group has two pages in work; or,
 // heads of 128 and many units, one page and more blocks, which hide the ends of
 // units better (256 sequences of 512 to 2048 tokens, 2048 units: 118 us against 114;
 // one of 130,001, 8 units: 53.0 against 53.8; heads of 64, 656 units: 31.7 against
@@ -1064,9 +1067,9 @@ cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
                 return attn_t<T, HD, 1, 1, 1>(c, a, s);
         return attn_t<T, HD, 1, 1, 2>(c, a, s);
     }
-    if (pairs <= 2 * PR) return attn_t<T, HD, 1, 2, 1>(c, a, s);
-    if (pairs <= 4 * PR) return attn_t<T, HD, 2, 2, 1>(c, a, s);
-    return attn_t<T, HD, 2, 4, 1>(c, a, s);
+    // in columns, a padded one of the larger tile at 8 / 9 of the smaller one's cost
+    const int64_t small = (pairs + 2 * PR - 1) / (2 * PR) * 2 * PR, large = (pairs + 8 * PR - 1) / (8 * PR) * 8 * PR;
+    return 8 * large <= 9 * small ? attn_t<T, HD, 2, 4, 1>(c, a, s) : attn_t<T, HD, 1, 2, 1>(c, a, s);
 }
 
 }  // namespace
