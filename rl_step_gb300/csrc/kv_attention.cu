@@ -81,7 +81,7 @@ struct AttnCall {
     float* lse;
     Cut* cuts;                              // one a block; null: sequences are not cut
     float* part;                            // two partial results a block
-    int64_t ldq, ldo, max_len;
+    int64_t ldq, ldo;
     int n_heads, group;
     int prow;                               // rows of a partial result
     int64_t slot;                           // its floats: the rows' sums, maxima and sums of p
@@ -263,14 +263,14 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
         int64_t mine = 0;
         if (per == 1) {
             SeqRows r;
-            const bool ok = kv_seq_ok(c, l_len, l_a, l_b, a.max_len, r);
+            const bool ok = kv_seq_ok(c, l_len, l_a, l_b, r);
             mine = ok && lane < c.n_seqs ? weight(r) : 0;
         } else {
 #pragma unroll 4
             for (int i = 0; i < per; ++i) {
                 SeqRows r;
                 const int s = s0 + i < c.n_seqs ? s0 + i : c.n_seqs - 1;
-                const bool ok = kv_seq(c, s, a.max_len, r);
+                const bool ok = kv_seq(c, s, r);
                 mine += ok && s0 + i < c.n_seqs ? weight(r) : 0;
             }
         }
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                 const int len = __shfl_sync(0xffffffffu, l_len, s_now - s_base);
                 const int64_t row_a = __shfl_sync(0xffffffffu, l_a, s_now - s_base);
                 const int64_t row_b = __shfl_sync(0xffffffffu, l_b, s_now - s_base);
-                const int64_t w = kv_seq_ok(c, len, row_a, row_b, a.max_len, r) ? weight(r) : 0;
+                const int64_t w = kv_seq_ok(c, len, row_a, row_b, r) ? weight(r) : 0;
                 if (rem >= w) {                             // behind the sequence
                     rem -= w;
                     ++s_now;
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
         // rows without positions, shared out over the blocks: zero (or NaN: a bad sequence)
         for (int s = blockIdx.x; s < c.n_seqs; s += gridDim.x) {
             SeqRows r;
-            const bool ok = kv_seq(c, s, a.max_len, r);
+            const bool ok = kv_seq(c, s, r);
             if (!ok) raise_status(c.status, ST_RANGE);
             if (ok && r.len > 0) continue;
             const int64_t r1 = (int64_t)r.row0 + r.n < c.n_rows ? (int64_t)r.row0 + r.n : c.n_rows;
@@ -1006,7 +1006,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
         if (dev < 64) sms[dev].store(n_sms, std::memory_order_relaxed);
     }
     AttnCall k;
-    k.q = a.q; k.out = a.out; k.lse = a.lse; k.ldq = a.ldq; k.ldo = a.ldo; k.max_len = a.max_len;
+    k.q = a.q; k.out = a.out; k.lse = a.lse; k.ldq = a.ldq; k.ldo = a.ldo;
     k.n_heads = a.n_heads; k.group = a.n_heads / c.n_kv;
     k.qk = a.scale * LOG2E;
     const int64_t pairs = (int64_t)c.max_rows * k.group;
@@ -1014,7 +1014,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     k.slot = ((int64_t)k.prow * (HD + 2) + 3) / 4 * 4;      // 16-byte aligned
     const int64_t units = (pairs + S::ROWS - 1) / S::ROWS * c.n_kv * c.n_seqs;
     const int64_t cap = (int64_t)c.max_pages * KV_PAGE;
-    const int64_t longest = a.max_len < cap ? a.max_len : cap;
+    const int64_t longest = c.max_len < cap ? c.max_len : cap;
     const int64_t pages = longest > 0 ? (longest + KV_PAGE - 1) / KV_PAGE : 1;
     // The blocks' equal shares cut sequences anywhere; a share's two ends leave
     // partial results.  Short sequences and small workspaces: whole units only.
@@ -1087,7 +1087,7 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
                                   void* stream) {
     if (!a) return kv_fail(MLORA_E_ARG, "NULL attention arguments");
     KvView w;
-    const int rc = kv_check(c, q, a->dtype, &w);
+    const int rc = kv_check(c, q, a->dtype, a->max_len, &w);
     if (rc) return rc;
     if (a->n_heads < 1 || a->n_heads > 65536 || a->n_heads % c->n_kv_heads)
         return kv_fail(MLORA_E_ARG, "n_heads %d must be a positive multiple of n_kv_heads (%d)", a->n_heads,
@@ -1108,7 +1108,7 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
         return kv_fail(MLORA_E_ARG, "too many sequences, rows and heads for one call");
     KvAttnArgs k;
     k.q = a->q; k.out = a->out; k.lse = a->lse; k.workspace = a->workspace; k.ldq = a->q_stride; k.ldo = a->out_stride;
-    k.workspace_bytes = a->workspace_bytes; k.max_len = a->max_len; k.n_heads = a->n_heads; k.scale = a->scale;
+    k.workspace_bytes = a->workspace_bytes; k.n_heads = a->n_heads; k.scale = a->scale;
     const cudaError_t e = launch_kv_attention(w, c->head_dim, a->dtype, k, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return MLORA_OK;

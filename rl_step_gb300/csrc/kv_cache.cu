@@ -18,7 +18,7 @@ int kv_fail(int code, const char* fmt, ...) {
     return mlk_report_error(code, buf);
 }
 
-int kv_check(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, KvView* out) {
+int kv_check(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, int64_t max_len, KvView* out) {
     if (!c || !q) return kv_fail(MLORA_E_ARG, "NULL cache or sequences");
     if (dtype != MLORA_BF16 && dtype != MLORA_FP32) return kv_fail(MLORA_E_ARG, "unknown dtype %d", dtype);
     if (c->head_dim != 64 && c->head_dim != 128)
@@ -39,7 +39,7 @@ int kv_check(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, KvV
     v.k = c->k; v.v = c->v; v.ks = c->k_scale; v.vs = c->v_scale; v.status = c->status;
     v.table = q->page_table; v.kv_len = q->kv_len; v.row_off = q->row_off; v.row_map = nullptr;
     v.n_rows = q->n_rows; v.n_pages = c->n_pages; v.n_kv = c->n_kv_heads; v.n_seqs = q->n_seqs;
-    v.max_pages = q->max_pages;
+    v.max_pages = q->max_pages; v.max_len = max_len;
     // no sequence has more rows than there are
     v.max_rows = q->n_rows < q->max_rows ? (int)q->n_rows : q->max_rows;
     *out = v;
@@ -195,7 +195,7 @@ struct KvPart {
 };
 __device__ __forceinline__ bool kv_part(const KvView& c, const KvUnit& u, bool first_thread, KvPart& t) {
     SeqRows r;
-    if (!kv_seq(c, u.s, INT64_MAX, r)) {
+    if (!kv_seq(c, u.s, r)) {
         if (first_thread) raise_status(c.status, ST_RANGE);
         return false;
     }
@@ -460,7 +460,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 extern "C" int mlora_kv_append(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, const void* k,
                                int64_t k_stride, const void* v, int64_t v_stride, void* stream) {
     KvView w;
-    const int rc = kv_check(c, q, dtype, &w);
+    const int rc = kv_check(c, q, dtype, INT64_MAX, &w);
     if (rc) return rc;
     if (w.n_seqs == 0 || w.n_rows == 0 || w.max_rows == 0) return MLORA_OK;
     const int64_t row = (int64_t)c->n_kv_heads * c->head_dim;
@@ -480,7 +480,7 @@ extern "C" int mlora_kv_append(const mlora_kv_cache* c, const mlora_kv_seqs* q, 
 extern "C" int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, void* k_out,
                              void* v_out, void* stream) {
     KvView w;
-    const int rc = kv_check(c, q, dtype, &w);
+    const int rc = kv_check(c, q, dtype, INT64_MAX, &w);
     if (rc) return rc;
     if (w.n_seqs == 0 || w.n_rows == 0 || w.max_rows == 0 || (!k_out && !v_out)) return MLORA_OK;
     if (!aligned16(k_out) || !aligned16(v_out)) return kv_fail(MLORA_E_ARG, "outputs must be 16-byte aligned");

@@ -26,6 +26,7 @@ struct KvView {
     const int* row_off;                // null: one row a sequence
     const int* row_map;                // null, or where row r's data stands in the row arrays
     int64_t n_rows;
+    int64_t max_len;                   // a longer sequence is out of range, in every kernel of the call
     int n_pages, n_kv, n_seqs, max_pages, max_rows;
 };
 
@@ -39,18 +40,17 @@ struct SeqRows {
 // A sequence's length and rows [a, b) against the ranges of the header; where
 // they are outside, only row0 and n of r can be used, clipped to the rows that
 // exist.
-__device__ __forceinline__ bool kv_seq_ok(const KvView& c, int len, int64_t a, int64_t b, int64_t max_len, SeqRows& r) {
+__device__ __forceinline__ bool kv_seq_ok(const KvView& c, int len, int64_t a, int64_t b, SeqRows& r) {
     r.len = len;
     r.row0 = (int)a;
     r.n = (int)(b - a < INT32_MAX ? b - a : INT32_MAX);
     const int64_t cap = (int64_t)c.max_pages * KV_PAGE;
-    return len >= 0 && len <= cap && len <= max_len && a >= 0 && b >= a && b <= c.n_rows && r.n <= c.max_rows &&
+    return len >= 0 && len <= cap && len <= c.max_len && a >= 0 && b >= a && b <= c.n_rows && r.n <= c.max_rows &&
            (r.n <= len || len == 0);
 }
 // Reads and checks sequence s (no status).
-__device__ __forceinline__ bool kv_seq(const KvView& c, int s, int64_t max_len, SeqRows& r) {
-    return kv_seq_ok(c, c.kv_len[s], c.row_off ? c.row_off[s] : s, c.row_off ? c.row_off[s + 1] : (int64_t)s + 1, max_len,
-                     r);
+__device__ __forceinline__ bool kv_seq(const KvView& c, int s, SeqRows& r) {
+    return kv_seq_ok(c, c.kv_len[s], c.row_off ? c.row_off[s] : s, c.row_off ? c.row_off[s + 1] : (int64_t)s + 1, r);
 }
 
 __device__ __forceinline__ int64_t kv_row(const KvView& c, int64_t r) { return c.row_map ? c.row_map[r] : r; }
@@ -100,8 +100,9 @@ __device__ __forceinline__ void store4_f(bf16* p, const float (&v)[4]) {
 }
 
 // Checks the host can make of a cache and a call's sequences; *out is their
-// device view.  MLORA_OK or an error code with its message set.
-int kv_check(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, KvView* out);
+// device view, of sequences of at most max_len tokens.  MLORA_OK or an error code
+// with its message set.
+int kv_check(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype, int64_t max_len, KvView* out);
 int kv_fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 
 // Whether one launch can hold the calls' blocks (append, read).
@@ -115,7 +116,7 @@ struct KvAttnArgs {
     void* out;
     float* lse;
     void* workspace;
-    int64_t ldq, ldo, workspace_bytes, max_len;
+    int64_t ldq, ldo, workspace_bytes;
     int n_heads;
     float scale;
 };

@@ -8,7 +8,7 @@ namespace mlk {
 
 namespace {
 
-__global__ void __launch_bounds__(256) cached_rows_kernel(KvView c, int64_t max_len, const int* __restrict__ perm_pad,
+__global__ void __launch_bounds__(256) cached_rows_kernel(KvView c, const int* __restrict__ perm_pad,
                                                           const int* __restrict__ meta, const int* __restrict__ inv,
                                                           int n, int max_rows, int* pos_pad, int* tgt_pad, int* row_map,
                                                           int* status) {
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256) cached_rows_kernel(KvView c, int64_t max_
             }
             if (mine) {
                 SeqRows q;
-                if (!kv_seq(c, s, max_len, q)) {
+                if (!kv_seq(c, s, q)) {
                     raise_status(status, ST_RANGE);
                 } else if (q.len > 0) {
                     live = true;
@@ -46,13 +46,13 @@ __global__ void __launch_bounds__(256) cached_rows_kernel(KvView c, int64_t max_
     for (int t = first; t < n; t += step) row_map[t] = inv[t] >= 0 ? inv[t] : max_rows - 1;
 }
 
-__global__ void __launch_bounds__(128) last_rows_kernel(KvView c, int64_t max_len, const int* __restrict__ inv,
+__global__ void __launch_bounds__(128) last_rows_kernel(KvView c, const int* __restrict__ inv,
                                                         const int* __restrict__ tgt_pad, const bf16* __restrict__ xf,
                                                         int d, bf16* __restrict__ x, int* perm, int* tgt, int* meta) {
     const int s = blockIdx.x;
     int row = -1;
     SeqRows q;
-    if (s < c.n_seqs && kv_seq(c, s, max_len, q) && q.len > 0 && q.n > 0) {
+    if (s < c.n_seqs && kv_seq(c, s, q) && q.len > 0 && q.n > 0) {
         row = inv[q.row0 + q.n - 1];
         if (row >= 0 && tgt_pad[row] < 0) row = -1;
     }
@@ -137,18 +137,18 @@ __global__ void __launch_bounds__(256) tf_sample_kernel(const float* __restrict_
 
 }  // namespace
 
-void launch_tf_cached_rows(const KvView& c, int64_t max_len, const int* perm_pad, const int* meta, const int* inv, int n,
+void launch_tf_cached_rows(const KvView& c, const int* perm_pad, const int* meta, const int* inv, int n,
                            int max_rows, int* pos_pad, int* tgt_pad, int* row_map, int* status, cudaStream_t s) {
     int blocks = (max_rows + 255) / 256;
     if (blocks > 4096) blocks = 4096;
-    cached_rows_kernel<<<blocks, 256, 0, s>>>(c, max_len, perm_pad, meta, inv, n, max_rows, pos_pad, tgt_pad, row_map,
+    cached_rows_kernel<<<blocks, 256, 0, s>>>(c, perm_pad, meta, inv, n, max_rows, pos_pad, tgt_pad, row_map,
                                               status);
 }
 
-void launch_tf_last_rows(const KvView& c, int64_t max_len, const int* inv, const int* tgt_pad, const bf16* xf, int d,
+void launch_tf_last_rows(const KvView& c, const int* inv, const int* tgt_pad, const bf16* xf, int d,
                          bf16* x, int* perm, int* tgt, int* meta, cudaStream_t s) {
     const int rows = (c.n_seqs + TILE_M - 1) / TILE_M * TILE_M;
-    last_rows_kernel<<<rows, 128, 0, s>>>(c, max_len, inv, tgt_pad, xf, d, x, perm, tgt, meta);
+    last_rows_kernel<<<rows, 128, 0, s>>>(c, inv, tgt_pad, xf, d, x, perm, tgt, meta);
 }
 
 void launch_tf_sample(const float* part, int n_nt, int part_ld, const float* lse, const int* perm, const bf16* x,

@@ -721,7 +721,7 @@ AttnArgs attn_args(mlora_tf_t* h, int l, int mp) {
 struct TfCached {
     std::vector<KvView> kv;          // [n_layers], row_map set
     void* workspace;
-    int64_t workspace_bytes, max_len;
+    int64_t workspace_bytes;
     const float* uniforms;           // null: no sampling
     int32_t* next_out;
     float* logprob_out;
@@ -738,7 +738,6 @@ int cached_attention(mlora_tf_t* h, const TfCached& c, int l, cudaStream_t s) {
     a.out = h->o[l]; a.ldo = h->Q;
     a.lse = nullptr;
     a.workspace = c.workspace; a.workspace_bytes = c.workspace_bytes;
-    a.max_len = c.max_len;
     a.n_heads = h->nh;
     a.scale = 1.f / sqrtf((float)MLORA_TF_HEAD_DIM);
     TF_CUDA(launch_kv_attention(c.kv[l], MLORA_TF_HEAD_DIM, MLORA_BF16, a, s));
@@ -755,7 +754,7 @@ int cached_sample(mlora_tf_t* h, const TfCached& c, cudaStream_t s) {
     // free by now: the embedding's rows, the positions, and seq_start throughout
     bf16* x = h->embed_bf;
     int *perm = h->seq_start, *tgt = h->pos_pad;
-    launch_tf_last_rows(kv, c.max_len, h->rb.inv, h->tgt_pad, h->xf, h->d, x, perm, tgt, h->last_meta, s);
+    launch_tf_last_rows(kv, h->rb.inv, h->tgt_pad, h->xf, h->d, x, perm, tgt, h->last_meta, s);
     ++h->launches;
     GemmParams p;
     p.M = mt * TILE_M; p.N = h->V; p.K = h->d; p.Kx = 0;
@@ -824,7 +823,7 @@ int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* l
     }
     if (kc) {
         TfProf ps(h, s, MLORA_TF_PROF_ROUTING);
-        launch_tf_cached_rows(kc->kv[0], kc->max_len, h->rb.perm_pad, h->rb.meta, h->rb.inv, (int)N, mp, h->pos_pad,
+        launch_tf_cached_rows(kc->kv[0], h->rb.perm_pad, h->rb.meta, h->rb.inv, (int)N, mp, h->pos_pad,
                               h->tgt_pad, h->row_map, h->status, s);
         ++h->launches;
     }
@@ -1092,7 +1091,7 @@ int tf_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c,
         return tfail(MLORA_E_ARG, "bad workspace");
     kc.kv.resize(h->L);
     for (int l = 0; l < h->L; ++l) {
-        const int rc = kv_check(&c->caches[l], &c->seqs, MLORA_BF16, &kc.kv[l]);
+        const int rc = kv_check(&c->caches[l], &c->seqs, MLORA_BF16, c->max_len, &kc.kv[l]);
         if (rc) return rc;
         if (c->caches[l].n_kv_heads != h->nkv || c->caches[l].head_dim != MLORA_TF_HEAD_DIM)
             return tfail(MLORA_E_ARG, "layer %d: a cache of %d heads of %d, the model has %d of %d", l,
@@ -1104,7 +1103,6 @@ int tf_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c,
         return tfail(MLORA_E_ARG, "too many sequences, rows and heads for one call");
     kc.workspace = c->workspace;
     kc.workspace_bytes = c->workspace ? c->workspace_bytes : 0;
-    kc.max_len = c->max_len;
     // 0xff: -1 and NaN, what stays where there is no row
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (kc.uniforms && c->seqs.n_seqs > 0) {

@@ -478,3 +478,39 @@ def test_two_streams_and_one_handle_each():
     torch.cuda.synchronize()
     for a, b in zip(alone, lps):
         assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [-5, 72, 10 ** 6])
+def test_a_sequence_out_of_range_leaves_its_pages(small, length):
+    """a length below zero, beyond the call's max_len (but within the table) and beyond the table: nothing of the
+    sequence is appended, in any layer, by rows whose keys would make every page's scale grow"""
+    torch = _torch()
+    import rl_step_gb300.kv as kv
+    import rl_step_gb300.transformer as t
+    s = small
+    rng = np.random.default_rng(13)
+    table, n_pages = _tables(torch, [100] * 3)
+    caches = s.caches(n_pages)
+    ws = kv.kv_workspace()
+    prompt = _int(torch, rng.integers(0, s.cfg.vocab, 210))
+    kv.tf_forward_cached(s.h, caches, prompt, None, _int(torch, np.repeat([0, 1, 2], 70)), table, _int(torch, [70] * 3),
+                         70, row_off=_int(torch, [0, 70, 140, 210]), max_rows=70, workspace=ws)
+    for c in caches:                                   # stored scales below any that the next row needs
+        c.k_scale.mul_(2.0 ** -20)
+        c.v_scale.mul_(2.0 ** -20)
+    before = [[x.clone() for x in (c.k, c.v, c.k_scale, c.v_scale)] for c in caches]
+    own = table[1, :2].long()
+    tok, ad = _int(torch, [5, 6, 7]), _int(torch, [0, 1, 2])
+    for call in ("forward", "sample"):
+        if call == "forward":
+            lp = kv.tf_forward_cached(s.h, caches, tok, tok, ad, table, _int(torch, [71, length, 71]), 71, workspace=ws)
+        else:
+            nxt, lp = kv.tf_sample_cached(s.h, caches, tok, ad, torch.full((3,), 0.5, device="cuda"), table,
+                                          _int(torch, [71, length, 71]), 71, workspace=ws)
+            assert nxt[1] == -1 and (nxt[[0, 2]] >= 0).all()
+        assert torch.isnan(lp[1]) and torch.isfinite(lp[[0, 2]]).all()
+        assert t.tf_check_status(s.h) == -2 and [kv.kv_check_status(c) for c in caches] == [-2] * s.cfg.n_layers
+        for c, old in zip(caches, before):
+            for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), old):
+                assert torch.equal(x[own], y[own])
