@@ -17,8 +17,8 @@
 //    its threads' sums and every scaling block its group's sums in fp32 trees.
 //    All terms are positive: at most 33 + 2 + 8 + (sums of a group / 256 + 1) + 8
 //    roundings of 2^-24 on the square.  Sums outside 1e-25 .. 1e30 carry a power
-//    of two of their own and are joined in fp64.  No atomics, a fixed order:
-//    results repeat bit for bit.
+//    of two of their own and are joined in fp64, as those that are not finite are.
+//    No atomics, a fixed order: results repeat bit for bit.
 // (One resident kernel that counted arrivals a chunk instead took 981 us on the 32
 // adapters of the 8B widths, 39 MB each, two whole passes 670 us, this 474 us, 77 %
 // of the copy rate by the floor's bytes; one adapter 37, 37 and 19 us.  Of the 474,
@@ -211,7 +211,7 @@ __device__ __forceinline__ double group_norm(const ClipSum* part, int g0, int g1
     for (int i = g0 + threadIdx.x; i < g1; i += CT) {
         const ClipSum x = part[i];
         add_to(s, lost, x.v);
-        apart |= x.e != 0;
+        apart |= x.e != 0 || !(x.v <= FLT_MAX);     // (a compensated sum makes an infinity NaN)
     }
     if (!__syncthreads_or(apart)) return (double)sqrtf(block_sum(s));
     double v = 0.0;

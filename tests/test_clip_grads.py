@@ -311,3 +311,25 @@ def test_gradset_refuses_overlapping_outputs():
     n = float(gr.clip_grads(s, 1.0))
     assert abs(n - math.sqrt(200)) <= 35 * U * n and bool((y[:200] != 1).all()) and bool((y[200:] == 1).all())
     gr.GradSet([x[:50], x[50:]], out=[x[:50], y[:50]])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_an_infinity_in_a_large_group_is_reported_as_one(dtype):
+    """more sums than a block has threads, and the infinities before and behind the first 256 of them"""
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    n = 3_000_001
+    at = {0: [0], 1: [n - 1], 2: [5, 2_500_000], 3: [1_000_000, 1_000_001]}
+    xs = [torch.ones(n, device="cuda", dtype=dt) for _ in range(6)]
+    for g, where in at.items():
+        for i, w in enumerate(where):
+            xs[g][w] = math.inf if i == 0 else -math.inf
+    xs[4][0], xs[4][2_800_000] = math.inf, math.nan
+    b = [x.clone() for x in xs]
+    norms = gr.clip_grads(gr.GradSet(xs, list(range(6))), 1.0).cpu().numpy()
+    assert np.isposinf(norms[:4]).all() and np.isnan(norms[4]), norms
+    for x, y in zip(xs[:5], b[:5]):
+        assert torch.equal(torch.nan_to_num(x, 7, 8, 9), torch.nan_to_num(y, 7, 8, 9))
+    assert abs(norms[5] - math.sqrt(n)) <= 35 * U * math.sqrt(n) and bool((xs[5] < 1e-3).all())
