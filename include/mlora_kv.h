@@ -112,12 +112,14 @@ int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype
  * pointers and row distances are multiples of 16 bytes, out may be q.  lse: DEVICE fp32
  * [n_rows x n_heads], or NULL.  max_len: upper bound of kv_len (a longer
  * sequence is a range error); it sets how far the work is split.
- * Sums and softmax statistics are fp32; scores are formed from q's own values
- * and the stored bytes, the probabilities enter the second product as fp16
- * (relative rounding 2^-11, below bf16's own 2^-8), and on fp32 as two fp16
- * parts (2^-22), as q does; a probability below 2^-26 of its row's largest has
- * an absolute error of up to 2^-37 of that largest instead.  A call repeats
- * bit for bit.
+ * Sums and softmax statistics are fp32.  Scores are formed from the stored bytes
+ * and q as fp16 values relative to the power of two above the row's largest
+ * |q|: bf16 elements of at least 2^-17 of that are exact, smaller ones off by up
+ * to 2^-25 of it; fp32 elements enter as two fp16 parts, to 2^-22 of themselves or
+ * 2^-36 of it.  The probabilities enter the second product as fp16 (relative
+ * rounding 2^-11, below bf16's own 2^-8), and on fp32 as two fp16 parts (2^-22);
+ * a probability below 2^-26 of its row's largest has an absolute error of up to
+ * 2^-37 (fp32: 2^-48) of that largest instead.  A call repeats bit for bit.
  * workspace: DEVICE, 16-byte aligned, of any content (may be NULL); calls that
  * may overlap need one each.  With MLORA_KV_WORKSPACE_BYTES the work is shared
  * evenly whatever the lengths: long sequences are cut where a block's share

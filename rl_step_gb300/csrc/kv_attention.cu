@@ -27,7 +27,10 @@
 //  * q enters as fp16 relative to its row's largest magnitude (a power of two,
 //    folded into the scale): exact for bf16 down to 2^-17 of that magnitude.
 //    On fp32 the 8 columns are 4 pairs, each with its high and its low fp16
-//    part (2^-22): both products come out of one instruction, in one thread.
+//    part (2^-22, or 2^-36 of the row's largest magnitude): both products come
+//    out of one instruction, in one thread.  Low parts are held at 2^11 times
+//    their value: unscaled, fp16's smallest step cut them off at 2^-25 of the
+//    largest, 2^-15 of a value that is itself 2^-10 of it.
 //  * The page's value scale 2^ev goes into the exponent of the probability,
 //    p' = exp2(s log2 e + ev - m') with m' the running maximum of s log2 e + ev,
 //    so pages of any scale add into one accumulator, the largest p' v8 sets the
@@ -62,6 +65,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
 constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
+constexpr float LOW = 2048.f;               // low parts of fp32 values: rest of at most 2^-11 of a high part <= 2^15
 constexpr int KV_SHORT_RUN = 2;             // places: no block gets fewer
 // What a unit's start and end cost, in pages.  41 sequences of 0 to 3001 tokens,
 // 16 heads of 64, fp32: 58 us at 0, 45 at 2, 36 at 4, 37 at 6; 256 sequences of
@@ -147,10 +151,10 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// what rounding (a, b) to fp16 left
+// LOW times what rounding (a, b) to fp16 left
 __device__ __forceinline__ uint32_t half2_rest(float a, float b, uint32_t hi) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    return half2_bits(a - f.x, b - f.y);
+    return half2_bits((a - f.x) * LOW, (b - f.y) * LOW);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -167,10 +171,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// a value as its fp16 rounding (low half) and the fp16 rounding of the rest
+// a value as its fp16 rounding (low half) and the fp16 rounding of LOW times the rest
 __device__ __forceinline__ uint32_t high_low(float v) {
     const __half h = __float2half_rn(v);
-    const __half2 r = __halves2half2(h, __float2half_rn(v - __half2float(h)));
+    const __half2 r = __halves2half2(h, __float2half_rn((v - __half2float(h)) * LOW));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 constexpr int EV_BAD = 1 << 20;              // in place of an exponent: a bad page in the run
@@ -653,8 +657,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             if (FOLD) {
-                                z[u][n][0] += z[u][n][1];
-                                z[u][n][2] += z[u][n][3];
+                                z[u][n][0] = fmaf(z[u][n][1], 1.f / LOW, z[u][n][0]);
+                                z[u][n][2] = fmaf(z[u][n][3], 1.f / LOW, z[u][n][2]);
                             }
 #pragma unroll
                             for (int k = 0; k < 4; k += 3 - E) {
@@ -799,8 +803,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                 if (FOLD) {
 #pragma unroll
                     for (int j = 0; j < HD / 16; ++j) {
-                        o[j][n][0] += o[j][n][1];
-                        o[j][n][2] += o[j][n][3];
+                        o[j][n][0] = fmaf(o[j][n][1], 1.f / LOW, o[j][n][0]);
+                        o[j][n][2] = fmaf(o[j][n][3], 1.f / LOW, o[j][n][2]);
                     }
                 }
             }

@@ -766,3 +766,55 @@ def test_attention_many_units(heads, dtype):
     assert st.torch.equal(out, o2) and st.torch.equal(lse, l2)
     _attend(st, live, heads, dtype, q=q, workspace=st.kv.kv_workspace(nbytes=0))
     _attend(st, live, heads, dtype, q=q, slack=5000)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hd", [64, 128])
+def test_small_parts_of_fp32_queries_count(hd):
+    """queries of 2^-16 of their row's largest, whose key dim is zero: q is held to 2^-22 of itself and 2^-36 of
+    the power of two above the largest, 2 here"""
+    st = Setup([130, 40], 2, hd, seed=47)
+    x = st.rows(170, "fp32", spread=0.0)
+    x[:, :2, 0] = 0                                        # the large dim's keys
+    x[:, :2] *= 2.0 ** 16
+    st.append([130, 40], "fp32", x)
+    torch = st.torch
+    q = torch.from_numpy(st.rng.standard_normal((2, 4, hd)).astype(np.float32)).cuda() * 2.0 ** -16
+    q[:, :, 0] = 1.5
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, 130)
+    u, qn = 2.0 ** -24, q.double().cpu().numpy()
+    for s in range(2):
+        k, v = (st.model.values(x, st.table[s], st.len[s]) for x in "kv")
+        o, l, mass, big = M.attention(qn[s:s + 1], k, v, st.len[s] - 1, 1 / math.sqrt(hd))
+        most = np.abs(k).sum(2).max(0)[np.arange(4) // 2][None] * 2.0 ** -36 * 2 / math.sqrt(hd)
+        D = ((hd + 16) * u + 2.0 ** -22) * big + most
+        assert (np.abs(lse[s].double().cpu().numpy() - l) <= 2 * D + st.len[s] * u + 2.0 ** -22 + 2 * u * np.abs(l)).all()
+        assert (np.abs(out[s].double().cpu().numpy() - o) <= (4 * D + 2 * st.len[s] * u + 2.0 ** -20)[..., None] * mass + 2 * u * np.abs(o)).all()
+
+
+@pytest.mark.gpu
+def test_small_probabilities_of_fp32_rows_count():
+    """weights down to 2^-22 of the largest, each alone in its dim of the values: held to 2^-22 of themselves.
+
+    q and k are small integers and 7/16, so the products are exact; the score in units of log2 is rounded three
+    times (scale log2 e, its product, the difference): 3 u 23, times ln 2 in p; exp2 2^-22, the sum of 23 terms
+    and the division 25 u."""
+    n, hd = 23, 64
+    st = Setup([n], 1, hd, seed=48)
+    torch = st.torch
+    x = torch.zeros(n, 2, hd, device="cuda")
+    j = torch.arange(n, device="cuda").float()
+    x[:, 0, 0] = -torch.clamp(j, max=16)
+    x[:, 0, 1] = -torch.clamp(j - 16, min=0)
+    x[1:, 0, 2] = -0.4375
+    x[torch.arange(n), 1, torch.arange(n)] = 1.125
+    st.append([n], "fp32", x)
+    q = torch.zeros(1, 1, hd, device="cuda")
+    q[0, 0, :3] = 1.0
+    sc = float(np.float32(math.log(2)))
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32([n]), q, n, scale=sc)
+    k, v = (st.model.values(x, st.table[0], n) for x in "kv")
+    o, l, _, _ = M.attention(q.double().cpu().numpy(), k, v, n - 1, sc)
+    got, want = out.double().cpu().numpy()[0, 0, :n], o[0, 0, :n]
+    u = 2.0 ** -24
+    assert (np.abs(got / want - 1) <= 3 * u * 23 * math.log(2) + 2 * 2.0 ** -22 + 2.0 ** -22 + 25 * u).all()
