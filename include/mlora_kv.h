@@ -118,8 +118,11 @@ int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype
  * to 2^-25 of it; fp32 elements enter as two fp16 parts, to 2^-22 of themselves or
  * 2^-36 of it.  The probabilities enter the second product as fp16 (relative
  * rounding 2^-11, below bf16's own 2^-8), and on fp32 as two fp16 parts (2^-22);
- * a probability below 2^-26 of its row's largest has an absolute error of up to
- * 2^-37 (fp32: 2^-48) of that largest instead.  A call repeats bit for bit.
+ * a probability below 2^-22 of its row's largest has an absolute error of up to
+ * 2^-33 (fp32: 2^-44) of that largest instead.  The dims of a result do not
+ * touch one another, whatever the scales of the pages; a page whose value scale
+ * is below 2^-64 of the largest in the sequence may count as zero in out (never in
+ * lse).  A call repeats bit for bit.
  * workspace: DEVICE, 16-byte aligned, of any content (may be NULL); calls that
  * may overlap need one each.  With MLORA_KV_WORKSPACE_BYTES the work is shared
  * evenly whatever the lengths: long sequences are cut where a block's share

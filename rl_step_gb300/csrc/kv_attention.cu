@@ -31,14 +31,24 @@
 //    out of one instruction, in one thread.  Low parts are held at 2^11 times
 //    their value: unscaled, fp16's smallest step cut them off at 2^-25 of the
 //    largest, 2^-15 of a value that is itself 2^-10 of it.
-//  * The page's value scale 2^ev goes into the exponent of the probability,
-//    p' = exp2(s log2 e + ev - m') with m' the running maximum of s log2 e + ev,
-//    so pages of any scale add into one accumulator, the largest p' v8 sets the
-//    precision, and l += p' 2^-ev is what the definition sums.  m' follows the
-//    scores only when one passes it by 2^3 (the sums are then rescaled); p' is
-//    held at 2^12 times its value, so that it stays within fp16 and its rounding
-//    relative (2^-11) down to 2^-26 of the reference (absolute 2^-37 of it
-//    below that); on fp32 it is split like q.
+//  * p = exp2(s log2 e - m) with m a running maximum of s log2 e that follows the
+//    scores only when one passes it by 2^3 (the sums are then rescaled).  p is held
+//    at 2^12 times its value, so that it stays within fp16 and its rounding
+//    relative (2^-11) down to 2^-26 of the reference (absolute 2^-37 of it below
+//    that); on fp32 it is split like q.
+//  * The page's value scale 2^ev: a warp's accumulators are in units of 2^unit, and
+//    p' = p 2^(ev - unit) where that is within 2^-3 .. 1 (the factor goes into the
+//    exponent, l += p' 2^(unit - ev), and the bounds on p's rounding are 2^3
+//    higher).  At any other page the unit becomes 2^(ev + 1) and the accumulators,
+//    fp32 with room for it, are multiplied by the difference: so each dim keeps its
+//    precision beside pages whose scale another dim has made large, and l has every
+//    p whatever its page's scale.  (With the whole scale in p', p' left fp16's range
+//    for the sake of other pages, and the sums of values that are all zero, with
+//    ev = -100, left fp32's; it took 31.6 us where this takes 33.0 on 41 sequences
+//    of 0 to 3001 tokens, 16 heads of 64, fp32, and 115.5 where this takes 116.5 on
+//    256 of 512 to 2048, 8 heads of 128.  Units found by the producer for 32 pages
+//    at once: 33.0 and 117.3.)  A page below 2^-64 of the largest so far adds to l
+//    alone: below that the accumulators' range could end.
 //  * Warps of a row group take different halves of a page and, where a single row
 //    group has two pages in work, every other page, 32 tokens at a step; each has
 //    a running maximum and sum of its own, joined at the item's end, so nothing
@@ -66,6 +76,10 @@ constexpr float LN2 = 0.6931471805599453f;
 constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
 constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
 constexpr float LOW = 2048.f;               // low parts of fp32 values: rest of at most 2^-11 of a high part <= 2^15
+constexpr int V_FOLD = 3;                   // value scales of 2^-V_FOLD to 1 of the accumulators' unit go into p'
+constexpr int V_GAP = 64;                   // pages below 2^-V_GAP of the largest so far count as zero values: 2^31 terms
+                                            // p' v8 < 2^24 times 2^V_GAP stay within fp32
+constexpr int V_GONE = -60;                 // what such a page folds: p' <= 2^-45 is 0 in fp16, and so is its low part
 constexpr int KV_SHORT_RUN = 2;             // places: no block gets fewer
 // What a unit's start and end cost, in pages.  41 sequences of 0 to 3001 tokens,
 // 16 heads of 64, fp32: 58 us at 0, 45 at 2, 36 at 4, 37 at 6; 256 sequences of
@@ -88,7 +102,7 @@ struct AttnCall {
     int64_t ldq, ldo;
     int n_heads, group;
     int prow;                               // rows of a partial result
-    int64_t slot;                           // its floats: the rows' sums, maxima and sums of p
+    int64_t slot;                           // its floats: the rows' sums, maxima, sums of p and units
     float qk;                               // scale * log2 e
 };
 
@@ -120,12 +134,13 @@ struct AttnShape {
     static constexpr int STAGES = FOUR ? 6 : SLIM ? 3 : (NT == 1 ? 4 : 6) * (128 / HD);
     static constexpr int BLOCKS_SM = FOUR || SLIM ? 4 : (NW > 4 ? 1 : 3);
     static constexpr int JOIN_WG = 2048 * PG;               // joining space of a row group, bytes
-    // ring, raw queries, joining space, per-warp statistics, barriers,
-    // exponents, items, flags
+    // ring, raw queries, joining space, per-warp statistics and units,
+    // barriers, exponents, items, flags
     static constexpr int QRAW = STAGES * STAGE;
     static constexpr int JOIN = QRAW + ROWS * HD * (int)sizeof(T);
     static constexpr int STAT = JOIN + RG * JOIN_WG;
-    static constexpr int BAR = STAT + 8 * WG * ROWS;
+    static constexpr int UNIT = STAT + 8 * WG * ROWS;
+    static constexpr int BAR = UNIT + (4 * NW + 15) / 16 * 16;
     static constexpr int EXPS = BAR + 16 * STAGES + 64;
     static constexpr int ITEMS = EXPS + 8 * STAGES;
     static constexpr int FLAGS = ITEMS + 2 * 64;
@@ -177,9 +192,12 @@ __device__ __forceinline__ uint32_t high_low(float v) {
     const __half2 r = __halves2half2(h, __float2half_rn((v - __half2float(h)) * LOW));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+constexpr int UNIT_NONE = -(1 << 20);        // no page yet
 constexpr int EV_BAD = 1 << 20;              // in place of an exponent: a bad page in the run
 // 2^e with e clamped to the normal range
 __device__ __forceinline__ float pow2_clamped(int e) { return kv_pow2(e < -126 ? -126 : (e > 127 ? 127 : e)); }
+// 2^e for e <= 127, 0 where that is below the normal range
+__device__ __forceinline__ float pow2_or_0(int e) { return e < -126 ? 0.f : kv_pow2(e); }
 
 // 16 consecutive elements
 __device__ __forceinline__ void load16_f(const float* p, float (&v)[16]) {
@@ -214,6 +232,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
     int* exps = reinterpret_cast<int*>(smem + S::EXPS);     // per stage: K's and V's exponent
     float* st_m = reinterpret_cast<float*>(smem + S::STAT); // [WG][ROWS]
     float* st_l = st_m + S::WG * S::ROWS;
+    int* st_u = reinterpret_cast<int*>(smem + S::UNIT);     // [NW]
     Item* items = reinterpret_cast<Item*>(smem + S::ITEMS);
     volatile int* flags = reinterpret_cast<volatile int*>(smem + S::FLAGS);   // [0]: a wait gave up
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -538,6 +557,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
             float o[HD / 16][NT][4];
             float m[NT][E], l[NT][E], qf[NT][E];            // qf: scale * log2 e, or NaN where q is not finite
             int qe[NT][E], limit[NT][E];                    // exponent of the row's largest |q|; positions it sees
+            int unit = UNIT_NONE, top = UNIT_NONE;          // o is in units of 2^unit; largest value scale so far
             bool bad = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -615,7 +635,6 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < E; ++e) fk[n][e] = qf[n][e] * pow2_clamped(qe[n][e] + ek);
-                const float fev = (float)ev, inv_vs = kv_pow2(-ev);
                 // EDGE: some row does not see all 32 positions
                 auto step = [&](auto edge) {
                     constexpr bool EDGE = decltype(edge)::value;
@@ -646,7 +665,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                                 for (int n = 0; n < NT; ++n) mma16816(z[u][n], ka, qb[n][4 * y + i][0], qb[n][4 * y + i][1]);
                             }
                     }
-                    // scores in units of log2, with the value scale's exponent; this thread's largest
+                    // scores in units of log2; this thread's largest
                     const int pos = p0 + 4 * (g >> 1) + (g & 1);
                     float mx[NT][E];
                     bool up = false;
@@ -663,7 +682,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
 #pragma unroll
                             for (int k = 0; k < 4; k += 3 - E) {
                                 const int e = k & (E - 1);
-                                float s2 = fmaf(z[u][n][k], fk[n][e], fev);
+                                float s2 = z[u][n][k] * fk[n][e];
                                 if (EDGE && pos + 16 * u + (k & 2) >= limit[n][e]) s2 = -INFINITY;
                                 mx[n][e] = fmaxf(mx[n][e], s2);
                             }
@@ -671,8 +690,23 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
 #pragma unroll
                         for (int e = 0; e < E; ++e) up |= mx[n][e] > m[n][e] + M_SLACK;
                     }
-                    // the reference moves only when a score passes it by 2^M_SLACK: then p' stays below fp16's range
-                    if (__any_sync(0xffffffffu, up)) {
+                    // the reference moves only when a score passes it by 2^M_SLACK: then p' stays below fp16's range;
+                    // the unit only when the page's scale does not fold into p' (and not before the products, which
+                    // would wait for that scale)
+                    int fold = ev - unit;
+                    const bool off_unit = (unsigned)(fold + V_FOLD) > (unsigned)V_FOLD;
+                    if (__any_sync(0xffffffffu, up || off_unit)) {
+                        float fm = 1.f;
+                        if (off_unit) {
+                            if (ev >= top - V_GAP) {
+                                top = max(top, ev);
+                                fm = pow2_or_0(unit - ev - 1);
+                                unit = ev + 1;
+                                fold = -1;
+                            } else {
+                                fold = V_GONE;
+                            }
+                        }
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -685,24 +719,26 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                                 const float f = v == -INFINITY ? 1.f : ex2(m[n][e] - v);
                                 m[n][e] = v;
                                 l[n][e] *= f;
+                                const float fo = f * fm;
 #pragma unroll
                                 for (int j = 0; j < HD / 16; ++j) {
-                                    o[j][n][e] *= f;
-                                    o[j][n][2 + e] *= f;
+                                    o[j][n][e] *= fo;
+                                    o[j][n][2 + e] *= fo;
                                     if (FOLD) {
-                                        o[j][n][1] *= f;
-                                        o[j][n][3] *= f;
+                                        o[j][n][1] *= fo;
+                                        o[j][n][3] *= fo;
                                     }
                                 }
                             }
                     }
+                    const float shift = (float)(P_SHIFT + fold), unfold = kv_pow2(-fold);
                     uint32_t p[2][NT][2];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float off[E], add[E];
 #pragma unroll
                         for (int e = 0; e < E; ++e) {
-                            off[e] = fev + P_SHIFT - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
+                            off[e] = shift - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
                             add[e] = 0.f;
                         }
 #pragma unroll
@@ -720,7 +756,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                                 p[u][n][j] = transpose8x8(FOLD ? high_low(z[u][n][2 * j]) : half2_bits(z[u][n][2 * j], z[u][n][2 * j + 1]));
                         }
 #pragma unroll
-                        for (int e = 0; e < E; ++e) l[n][e] = fmaf(add[e], inv_vs, l[n][e]);
+                        for (int e = 0; e < E; ++e) l[n][e] = fmaf(add[e], unfold, l[n][e]);
                     }
                     // O^T += V^T P^T: rows g and g + 8 of tile 2 y + e are dims 32 y + 4 g + e and the one 2 behind it
 #pragma unroll
@@ -808,7 +844,12 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                     }
                 }
             }
+            if (lane == 0) st_u[warp] = unit;
             if (any(!go)) break;
+            int uu = KV_MIN_EXP;                            // the row group's unit: the largest
+#pragma unroll
+            for (int w = 0; w < S::WG; ++w) uu = max(uu, st_u[rg * S::WG + w]);
+            const float fu = pow2_or_0(unit - uu);
             float mm[NT][E], ll[NT][E];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -827,7 +868,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                     for (int w = 0; w < S::WG; ++w) lw[w] *= mw[w] == -INFINITY ? 1.f : ex2(mw[w] - mm[n][e]);   // 1: 0 or NaN
                     // the same whichever page parity came first
                     ll[n][e] = S::WG == 4 ? (lw[0] + lw[2 % S::WG]) + (lw[1] + lw[3 % S::WG]) : lw[0] + lw[1];
-                    const float f = m[n][e] == -INFINITY ? 1.f : ex2(m[n][e] - mm[n][e]);
+                    const float f = fu * (m[n][e] == -INFINITY ? 1.f : ex2(m[n][e] - mm[n][e]));
 #pragma unroll
                     for (int j = 0; j < HD / 16; ++j) {
                         o[j][n][e] *= f;
@@ -884,14 +925,14 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                     for (int e = 0; e < E; ++e) {
                         const int row = rg * S::PR + (FOLD ? 4 * n + t : 8 * n + 2 * t + e);
                         if (row >= x.pairs) continue;
-                        const float inv = slot >= 0 ? 1.f : 1.f / ll[n][e];
+                        const float inv = slot >= 0 ? 1.f : 1.f / ll[n][e], back = slot >= 0 ? 1.f : kv_pow2(uu);
                         const int pair = x.pair0 + row;
                         const int64_t yr = kv_row(c, (int64_t)x.row0 + pair / a.group);
                         const int head = x.h * a.group + pair % a.group;
 #pragma unroll
                         for (int y = 0; y < HD / 32; ++y) {
-                            const float w[4] = {o[2 * y][n][e] * inv, o[2 * y + 1][n][e] * inv, o[2 * y][n][2 + e] * inv,
-                                                o[2 * y + 1][n][2 + e] * inv};
+                            const float w[4] = {o[2 * y][n][e] * inv * back, o[2 * y + 1][n][e] * inv * back,
+                                                o[2 * y][n][2 + e] * inv * back, o[2 * y + 1][n][2 + e] * inv * back};
                             if (slot >= 0) store4_f(part + row * HD + 32 * y + 4 * g, w);
                             else store4_f(out + yr * a.ldo + (int64_t)head * HD + 32 * y + 4 * g, w);
                         }
@@ -899,6 +940,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                         if (slot >= 0) {
                             part[a.prow * HD + row] = mm[n][e];
                             part[a.prow * (HD + 1) + row] = ll[n][e];
+                            part[a.prow * (HD + 2) + row] = (float)uu;
                         } else if (a.lse) {
                             a.lse[yr * a.n_heads + head] = ((mm[n][e] == -INFINITY ? 0.f : mm[n][e]) - P_SHIFT + log2f(ll[n][e])) * LN2;
                         }
@@ -929,6 +971,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
                                                       const __grid_constant__ AttnCall a, int total) {
     constexpr int D = HD / 32;
     __shared__ float sm[8], sl[8], so[8][HD];
+    __shared__ int su[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int at = blockIdx.x * (8 / W) + warp / W;         // (block of the attention kernel, pair)
     const int from = at / a.prow, row = at % a.prow;
@@ -937,38 +980,44 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     if (at < total) u = a.cuts[from];
     const bool work = u.blocks > 0 && row < u.pairs;
     auto part = [&](int k) { return a.part + (int64_t)(k == 0 ? 2 * from + 1 : 2 * (from + k)) * a.slot; };
-    // the running maximum M, sum l and sums o of the warp's parts; JB parts' loads in flight
+    // the running maximum M, sum l and sums o (in units of 2^U) of the warp's parts; JB parts' loads in flight
     constexpr int JB = 4;
     float M = -INFINITY, l = 0.f, o[D];
+    int U = KV_MIN_EXP;
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
-    auto add = [&](float m, float lm, const float (&x)[D]) {
+    auto add = [&](float m, float lm, int unit, const float (&x)[D]) {
         const float v = fmaxf(M, m);
         const float fo = M == -INFINITY ? 1.f : ex2(M - v), fn = m == -INFINITY ? 1.f : ex2(m - v);   // 1: 0 or NaN stands there
+        const int w = max(U, unit);
+        const float po = fo * pow2_or_0(U - w), pn = fn * pow2_or_0(unit - w);
         l = l * fo + lm * fn;
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[d] = o[d] * fo + x[d] * fn;
+        for (int d = 0; d < D; ++d) o[d] = o[d] * po + x[d] * pn;
         M = v;
+        U = w;
     };
     if (work)
         for (int k0 = warp % W; k0 < u.blocks; k0 += JB * W) {
-            float m[JB], lm[JB], x[JB][D];
+            float m[JB], lm[JB], un[JB], x[JB][D];
 #pragma unroll
             for (int i = 0; i < JB; ++i) {
                 const float* pk = part(k0 + i * W < u.blocks ? k0 + i * W : k0);
                 m[i] = pk[a.prow * HD + row];
                 lm[i] = pk[a.prow * (HD + 1) + row];
+                un[i] = pk[a.prow * (HD + 2) + row];
 #pragma unroll
                 for (int d = 0; d < D; ++d) x[i][d] = pk[row * HD + lane + 32 * d];
             }
 #pragma unroll
             for (int i = 0; i < JB; ++i)
-                if (k0 + i * W < u.blocks) add(m[i], lm[i], x[i]);
+                if (k0 + i * W < u.blocks) add(m[i], lm[i], (int)un[i], x[i]);
         }
     if (W > 1) {
         if (lane == 0) {
             sm[warp] = M;
             sl[warp] = l;
+            su[warp] = U;
         }
 #pragma unroll
         for (int d = 0; d < D; ++d) so[warp][lane + 32 * d] = o[d];
@@ -979,7 +1028,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
             float x[D];
 #pragma unroll
             for (int d = 0; d < D; ++d) x[d] = so[warp + w][lane + 32 * d];
-            add(sm[warp + w], sl[warp + w], x);
+            add(sm[warp + w], sl[warp + w], su[warp + w], x);
         }
     }
     if (!work) return;
@@ -987,7 +1036,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     const int64_t y = kv_row(c, (int64_t)u.row0 + pair / a.group);
     const int head = u.h * a.group + pair % a.group;
 #pragma unroll
-    for (int d = 0; d < D; ++d) static_cast<T*>(a.out)[y * a.ldo + (int64_t)head * HD + lane + 32 * d] = from_f<T>(o[d] / l);
+    for (int d = 0; d < D; ++d) static_cast<T*>(a.out)[y * a.ldo + (int64_t)head * HD + lane + 32 * d] = from_f<T>(o[d] / l * kv_pow2(U));
     if (lane == 0 && a.lse) a.lse[y * a.n_heads + head] = ((M == -INFINITY ? 0.f : M) - P_SHIFT + log2f(l)) * LN2;
 }
 
@@ -1015,7 +1064,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     k.qk = a.scale * LOG2E;
     const int64_t pairs = (int64_t)c.max_rows * k.group;
     k.prow = (int)(pairs < S::ROWS ? pairs : S::ROWS);
-    k.slot = ((int64_t)k.prow * (HD + 2) + 3) / 4 * 4;      // 16-byte aligned
+    k.slot = ((int64_t)k.prow * (HD + 3) + 3) / 4 * 4;      // 16-byte aligned
     const int64_t units = (pairs + S::ROWS - 1) / S::ROWS * c.n_kv * c.n_seqs;
     const int64_t cap = (int64_t)c.max_pages * KV_PAGE;
     const int64_t longest = c.max_len < cap ? c.max_len : cap;

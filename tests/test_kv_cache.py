@@ -818,3 +818,132 @@ def test_small_probabilities_of_fp32_rows_count():
     got, want = out.double().cpu().numpy()[0, 0, :n], o[0, 0, :n]
     u = 2.0 ** -24
     assert (np.abs(got / want - 1) <= 3 * u * 23 * math.log(2) + 2 * 2.0 ** -22 + 2.0 ** -22 + 25 * u).all()
+
+
+# ----------------------------------------------------------------------------
+# Pages of very different value scales.  In the attention each dimension of a
+# result stands for itself: with p relative to its row's largest,
+#   |out_d - o_d| <= (4 D + P + 2 n u + 2^-20) A_d + half a step of the type + C sum_i |v_id|
+# where C = 2^-33 (bf16) or 2^-44 (fp32) is the absolute rounding of a p: fp16's
+# half step 2^-25 (and 2^-11 of it on fp32, whose low part is held 2^11 times as
+# large) at p' >= 2^(12 - 3) p, and on bf16 once more, before the factor 2^-3 .. 1.  Pages below 2^-64 of the largest scale of the row's
+# pages may count as zero in out, never in lse.
+# ----------------------------------------------------------------------------
+def _scaled_pages(pages, n_kv, hd, seed, outlier=False):
+    """a Setup whose sequence s has the pages pages[s], of values times 2^e each (None: zero); outlier: dim 5
+    alone is that large, and the others ordinary where that leaves them bits"""
+    st = Setup([64 * len(p) - 3 for p in pages], n_kv, hd, seed=seed)
+    lens = [64 * len(p) - 3 for p in pages]
+    x = st.rows(sum(lens), "fp32", spread=0.0)
+    at = 0
+    for p, n in zip(pages, lens):
+        for i, e in enumerate(p):
+            rows = x[at + 64 * i:min(at + 64 * i + 64, at + n), n_kv:]
+            if outlier:
+                rows[..., 5] *= 2.0 ** e
+            else:
+                rows *= 0.0 if e is None else 2.0 ** e
+        at += n
+    st.append(lens, "fp32", x)
+    st.check_state()
+    return st
+
+
+def _compare_dims(st, rows, q, out, lse, dtype, scale=None):
+    sc = 1 / math.sqrt(st.hd) if scale is None else scale
+    qn, on, ln = q.double().cpu().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    u = 2.0 ** -24
+    P, C = (2.0 ** -11, 2.0 ** -33) if dtype == "bf16" else (2.0 ** -22, 2.0 ** -44)
+    at = 0
+    for s, r in enumerate(rows):
+        n = st.len[s]
+        k, v = (st.model.values(x, st.table[s], n) for x in "kv")
+        e = np.repeat(st.model.e["v"][st.table[s, :-(-n // 64)]], 64, 0)[:n]             # [n, n_kv]
+        gone = e < e.max(0) - 64
+        o, l, mass, big = M.attention(qn[at:at + r], k, v, n - r, sc)
+        lost = M.attention(qn[at:at + r], k, v * gone[:, :, None], n - r, sc)[2]
+        kv = np.arange(q.shape[1]) // (q.shape[1] // st.n_kv)
+        D = ((st.hd + 16) * u + 2.0 ** -22) * big
+        tol = (4 * D + P + 2 * n * u + 2.0 ** -20)[..., None] * mass + EPS[dtype] * np.abs(o) + \
+            C * np.abs(v).sum(0)[kv] + lost + 1e-40
+        err = np.abs(on[at:at + r] - o)
+        assert (err <= tol).all(), (s, float((err / tol).max()))
+        d = np.abs(ln[at:at + r] - l)
+        assert (d <= 2 * D + n * u + 2.0 ** -22 + 2 * u * np.abs(l)).all(), (s, float(d.max()))
+        at += r
+
+
+def _scale_cases(kind, rng):
+    """pages, heads, n_kv, hd, rows of a sequence: one of each form of the kernel"""
+    gap = lambda n: [int(x) for x in rng.choice([0, 4, 5, 20, 38, 60], n)]
+    if kind == "single rows":
+        return [gap(3), [0, 60], [60, 0], [38, 0, 0], [4, 0, 5, 0, 9, 0]], 4, 2, 128, 1
+    if kind == "heads of 64":
+        return [gap(4), [0, 45], [45, 0]], 3, 3, 64, 1
+    if kind == "cut":
+        return [gap(70), gap(41)], 4, 2, 128, 1
+    if kind == "16 pairs":
+        return [gap(3), gap(12)], 12, 2, 128, 3
+    if kind == "64 pairs":
+        return [gap(3), gap(11)], 16, 1, 64, 9
+    return [gap(3) for _ in range(76)], 8, 8, 128, 1       # many units
+
+
+_KINDS = ["single rows", "heads of 64", "cut", "16 pairs", "64 pairs", "many units"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", _KINDS)
+def test_a_large_value_in_one_dim_leaves_the_others(kind, dtype):
+    """a page whose scale is 2^4 to 2^60 times its neighbours' for one dim's sake: the other dims are the neighbours'"""
+    pages, heads, n_kv, hd, r = _scale_cases(kind, np.random.default_rng(41))
+    st = _scaled_pages(pages, n_kv, hd, 43, outlier=True)
+    torch = st.torch
+    rows = [r] * len(pages)
+    for gain in (0.0, 1.0):
+        q = torch.from_numpy(st.rng.standard_normal((sum(rows), heads, hd)).astype(np.float32)).cuda() * gain
+        q = q.bfloat16() if dtype == "bf16" else q
+        out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, max(st.len), row_off=st.off(rows), max_rows=r)
+        _compare_dims(st, rows, q, out, lse, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", _KINDS)
+def test_every_page_counts_whatever_its_scale(kind, dtype):
+    """zeros beside values of up to 2^110 in every order: each position has its share of the sum"""
+    pages, heads, n_kv, hd, r = _scale_cases(kind, np.random.default_rng(42))
+    rng = np.random.default_rng(44)
+    pages = [[[None, -100, -30, 0, 45, 110][int(rng.integers(6))] for _ in p] for p in pages]
+    pages[0], pages[1] = ([None, 60, None] if len(pages[0]) < 9 else pages[0]), ([110, None] if len(pages[1]) < 9 else pages[1])
+    st = _scaled_pages(pages, n_kv, hd, 45)
+    torch = st.torch
+    rows = [r] * len(pages)
+    for gain in (0.0, 1.0):
+        q = torch.from_numpy(st.rng.standard_normal((sum(rows), heads, hd)).astype(np.float32)).cuda() * gain
+        q = q.bfloat16() if dtype == "bf16" else q
+        for nbytes in (st.kv.WORKSPACE_BYTES, 0):
+            out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32(st.len), q, max(st.len), row_off=st.off(rows),
+                                          max_rows=r, workspace=st.kv.kv_workspace(nbytes=nbytes))
+            _compare_dims(st, rows, q, out, lse, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("heads,rows,nbytes", [(1, 1, None), (1, 1, 0), (12, 1, None), (24, 3, None)])
+def test_the_sum_over_many_positions_of_zero_values(heads, rows, nbytes, dtype):
+    """70,000 equal scores over values that are all zero: lse = log n.  Every term is the same power of two, so
+    the sums are exact; the logarithm and its scaling are a few u."""
+    n, hd = 70000, 64
+    st = Setup([n], 1, hd, seed=46)
+    x = st.rows(n, "bf16")
+    x[:, 1] = 0
+    st.append([n], x=x)
+    torch = st.torch
+    q = torch.zeros(rows, heads, hd, device="cuda", dtype=torch.float32 if dtype == "fp32" else torch.bfloat16)
+    ws = st.kv.kv_workspace() if nbytes is None else st.kv.kv_workspace(nbytes=nbytes)
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32([n]), q, n, row_off=st.off([rows]), max_rows=rows, workspace=ws)
+    want = np.log(np.arange(n - rows + 1, n + 1))[:, None]
+    assert (np.abs(lse.double().cpu().numpy() - want) <= 8 * 2.0 ** -24 * want + 2.0 ** -22).all()
+    assert (out == 0).all()
