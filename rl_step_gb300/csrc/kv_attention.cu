@@ -71,7 +71,7 @@ namespace mlk {
 
 namespace {
 
-constexpr double LOG2E = 1.4426950408889634;
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
 constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
@@ -103,8 +103,7 @@ struct AttnCall {
     int n_heads, group;
     int prow;                               // rows of a partial result
     int64_t slot;                           // its floats: the rows' sums, maxima, sums of p and units
-    float qk;                               // scale * log2 e = qk 2^qk_exp, 1/2 <= |qk| < 1
-    int qk_exp;
+    float qk;                               // scale * log2 e
 };
 
 // What the producer tells the consumers about an item.
@@ -195,12 +194,8 @@ __device__ __forceinline__ uint32_t high_low(float v) {
 }
 constexpr int UNIT_NONE = -(1 << 20);        // no page yet
 constexpr int EV_BAD = 1 << 20;              // in place of an exponent: a bad page in the run
-// x 2^e for |x| < 1: q, the keys' scale and the caller's can lie on both sides of fp32's range and make up for
-// one another, so their exponents are added before one factor is formed (|e| beyond 252 is 0 or an infinity)
-__device__ __forceinline__ float times_pow2(float x, int e) {
-    e = e < -252 ? -252 : (e > 252 ? 252 : e);
-    return x * kv_pow2(e >> 1) * kv_pow2(e - (e >> 1));
-}
+// 2^e with e clamped to the normal range
+__device__ __forceinline__ float pow2_clamped(int e) { return kv_pow2(e < -126 ? -126 : (e > 127 ? 127 : e)); }
 // 2^e for e <= 127, 0 where that is below the normal range
 __device__ __forceinline__ float pow2_or_0(int e) { return e < -126 ? 0.f : kv_pow2(e); }
 
@@ -560,8 +555,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
             if (!go) gave_up();
             uint32_t qb[NT][HD / 16][2];
             float o[HD / 16][NT][4];
-            float m[NT][E], l[NT][E], qf[NT][E];            // qf: qk, NaN where q is not finite, 0 where it is 0
-            int qe[NT][E], limit[NT][E];                    // exponent of the row's largest |q| and of qk; positions it sees
+            float m[NT][E], l[NT][E], qf[NT][E];            // qf: scale * log2 e, or NaN where q is not finite
+            int qe[NT][E], limit[NT][E];                    // exponent of the row's largest |q|; positions it sees
             int unit = UNIT_NONE, top = UNIT_NONE;          // o is in units of 2^unit; largest value scale so far
             bool bad = false;
 #pragma unroll
@@ -591,7 +586,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                 const unsigned nf = __ballot_sync(0xffffffffu, !fin);
                 int ex = 0;
                 if (big > 0.f && big <= FLT_MAX) frexpf(big, &ex);
-                const float f = (nf >> (lane & 28)) & 15u ? NAN : (big > 0.f ? a.qk : 0.f);
+                const float f = (nf >> (lane & 28)) & 15u ? NAN : a.qk;
                 // 2^-ex in two steps: it can lie outside fp32
                 const float f1 = kv_pow2(-ex / 2), f2 = kv_pow2(-ex - (-ex / 2));
 #pragma unroll
@@ -609,7 +604,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                 for (int e = 0; e < E; ++e) {
                     const int from = 4 * (2 * t + e);
                     const int r2 = rg * S::PR + (FOLD ? 4 * n + t : 8 * n + 2 * t + e);
-                    qe[n][e] = __shfl_sync(0xffffffffu, ex, from) + a.qk_exp;
+                    qe[n][e] = __shfl_sync(0xffffffffu, ex, from);
                     qf[n][e] = __shfl_sync(0xffffffffu, f, from);
                     limit[n][e] = r2 < x.pairs ? x.before + (x.pair0 + r2) / a.group + 1 : 0;
                     m[n][e] = -INFINITY;
@@ -639,7 +634,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < E; ++e) fk[n][e] = times_pow2(qf[n][e], qe[n][e] + ek);
+                    for (int e = 0; e < E; ++e) fk[n][e] = qf[n][e] * pow2_clamped(qe[n][e] + ek);
                 // EDGE: some row does not see all 32 positions
                 auto step = [&](auto edge) {
                     constexpr bool EDGE = decltype(edge)::value;
@@ -1046,7 +1041,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
 }
 
 template <typename T, int HD, int NT, int RG, int PG_>
-cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t* launches) {
+cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     using S = AttnShape<T, HD, NT, RG, PG_>;
     // once a device: its SMs, and the kernel's shared memory (the attribute stays with the function)
     static std::atomic<int> sms[64];
@@ -1066,7 +1061,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t
     AttnCall k;
     k.q = a.q; k.out = a.out; k.lse = a.lse; k.ldq = a.ldq; k.ldo = a.ldo;
     k.n_heads = a.n_heads; k.group = a.n_heads / c.n_kv;
-    k.qk = (float)frexp((double)a.scale * LOG2E, &k.qk_exp);
+    k.qk = a.scale * LOG2E;
     const int64_t pairs = (int64_t)c.max_rows * k.group;
     k.prow = (int)(pairs < S::ROWS ? pairs : S::ROWS);
     k.slot = ((int64_t)k.prow * (HD + 3) + 3) / 4 * 4;      // 16-byte aligned
@@ -1086,7 +1081,6 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t
     k.cuts = cut ? reinterpret_cast<Cut*>(k.part + blocks * 2 * k.slot) : nullptr;
     kv_attn_kernel<T, HD, NT, RG, PG_><<<(unsigned)blocks, S::THREADS, S::SMEM, s>>>(c, k);
     e = cudaGetLastError();
-    if (launches) *launches += cut ? 2 : 1;
     if (e != cudaSuccess || !cut) return e;
     // the join waits on the device for the attention kernel's end: only its launch overlaps it
     const int total = (int)(blocks * k.prow);
@@ -1117,54 +1111,30 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t
 // workspace lets results depend on it.
 constexpr int64_t KV_MANY = 600;
 template <typename T, int HD>
-cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t* launches) {
+cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     constexpr int PR = AttnShape<T, HD, 1, 1, 2>::PR;
     const int64_t pairs = (int64_t)c.max_rows * (a.n_heads / c.n_kv);
     if (pairs <= PR) {
         if constexpr (HD == 128)
             if (a.workspace && a.workspace_bytes >= MLORA_KV_WORKSPACE_BYTES && (int64_t)c.n_seqs * c.n_kv >= KV_MANY)
-                return attn_t<T, HD, 1, 1, 1>(c, a, s, launches);
-        return attn_t<T, HD, 1, 1, 2>(c, a, s, launches);
+                return attn_t<T, HD, 1, 1, 1>(c, a, s);
+        return attn_t<T, HD, 1, 1, 2>(c, a, s);
     }
     // in columns, a padded one of the larger tile at 8 / 9 of the smaller one's cost
     const int64_t small = (pairs + 2 * PR - 1) / (2 * PR) * 2 * PR, large = (pairs + 8 * PR - 1) / (8 * PR) * 8 * PR;
-    return 8 * large <= 9 * small ? attn_t<T, HD, 2, 4, 1>(c, a, s, launches) : attn_t<T, HD, 1, 2, 1>(c, a, s, launches);
+    return 8 * large <= 9 * small ? attn_t<T, HD, 2, 4, 1>(c, a, s) : attn_t<T, HD, 1, 2, 1>(c, a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s,
-                                int64_t* launches) {
-    if (dtype == MLORA_BF16) return (head_dim == 64 ? attn_rows<bf16, 64> : attn_rows<bf16, 128>)(c, a, s, launches);
-    return (head_dim == 64 ? attn_rows<float, 64> : attn_rows<float, 128>)(c, a, s, launches);
+cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s) {
+    if (dtype == MLORA_BF16) return head_dim == 64 ? attn_rows<bf16, 64>(c, a, s) : attn_rows<bf16, 128>(c, a, s);
+    return head_dim == 64 ? attn_rows<float, 64>(c, a, s) : attn_rows<float, 128>(c, a, s);
 }
 
 }  // namespace mlk
 
 using namespace mlk;
-
-namespace {
-
-// Whether a row that the call writes holds a part of a row that it may still
-// read: n rows of `row` bytes, sq and so >= row bytes apart.  The queries
-// themselves as the output are no such case.
-bool rows_clash(uintptr_t q, int64_t sq, uintptr_t o, int64_t so, int64_t row, int64_t n) {
-    if (q == o && (sq == so || n == 1)) return false;
-    if (o >= q + (n - 1) * sq + row || q >= o + (n - 1) * so + row) return false;
-    if (sq == so) {                                         // columns of one buffer: side by side or not
-        const int64_t d = (int64_t)((o > q ? o - q : q - o) % (uintptr_t)so);
-        return d < row || so - d < row;
-    }
-    for (int64_t i = 0; i < n; ++i) {                       // the output rows that begin just before and behind row i
-        const int64_t at = (int64_t)(q - o) + i * sq;
-        const int64_t j = at >= 0 ? at / so : -1;
-        if (j >= 0 && j < n && at - j * so < row) return true;
-        if (j + 1 < n && (j + 1) * so - at < row) return true;
-    }
-    return false;
-}
-
-}  // namespace
 
 extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const mlora_kv_attn* a,
                                   void* stream) {
@@ -1185,10 +1155,6 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
         ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out)) & 15))
         return kv_fail(MLORA_E_ARG, "query and output rows must be 16-byte aligned and at least %lld elements apart",
                        (long long)row);
-    const int64_t es = 16 / per16;
-    if (rows_clash(reinterpret_cast<uintptr_t>(a->q), a->q_stride * es, reinterpret_cast<uintptr_t>(a->out),
-                   a->out_stride * es, row * es, w.n_rows))
-        return kv_fail(MLORA_E_ARG, "the output's rows overlap queries (out may be q, with its stride, or lie apart)");
     if ((reinterpret_cast<uintptr_t>(a->workspace) & 15) || a->workspace_bytes < 0)
         return kv_fail(MLORA_E_ARG, "the workspace must be 16-byte aligned");
     if ((int64_t)w.max_rows * a->n_heads > INT32_MAX / w.n_seqs)
@@ -1196,7 +1162,7 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
     KvAttnArgs k;
     k.q = a->q; k.out = a->out; k.lse = a->lse; k.workspace = a->workspace; k.ldq = a->q_stride; k.ldo = a->out_stride;
     k.workspace_bytes = a->workspace_bytes; k.n_heads = a->n_heads; k.scale = a->scale;
-    const cudaError_t e = launch_kv_attention(w, c->head_dim, a->dtype, k, reinterpret_cast<cudaStream_t>(stream), nullptr);
+    const cudaError_t e = launch_kv_attention(w, c->head_dim, a->dtype, k, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return MLORA_OK;
 }

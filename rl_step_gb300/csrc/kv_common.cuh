@@ -120,8 +120,6 @@ struct KvAttnArgs {
     int n_heads;
     float scale;
 };
-// launches (may be null) counts the kernels
-cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s,
-                                int64_t* launches);
+cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s);
 
 }  // namespace mlk
