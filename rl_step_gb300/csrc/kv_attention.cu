@@ -71,7 +71,7 @@ namespace mlk {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr double LOG2E = 1.4426950408889634;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr int P_SHIFT = 12;                 // p' is held at 2^12 times its value,
 constexpr float M_SLACK = 3.f;              // against a reference at most 2^3 below the largest: p' <= 2^15
@@ -103,7 +103,8 @@ struct AttnCall {
     int n_heads, group;
     int prow;                               // rows of a partial result
     int64_t slot;                           // its floats: the rows' sums, maxima, sums of p and units
-    float qk;                               // scale * log2 e
+    float qk;                               // scale * log2 e = qk 2^qk_exp, 1/2 <= |qk| < 1
+    int qk_exp;
 };
 
 // What the producer tells the consumers about an item.
@@ -194,8 +195,12 @@ __device__ __forceinline__ uint32_t high_low(float v) {
 }
 constexpr int UNIT_NONE = -(1 << 20);        // no page yet
 constexpr int EV_BAD = 1 << 20;              // in place of an exponent: a bad page in the run
-// 2^e with e clamped to the normal range
-__device__ __forceinline__ float pow2_clamped(int e) { return kv_pow2(e < -126 ? -126 : (e > 127 ? 127 : e)); }
+// x 2^e for |x| < 1: q, the keys' scale and the caller's can lie on both sides of fp32's range and make up for
+// one another, so their exponents are added before one factor is formed (|e| beyond 252 is 0 or an infinity)
+__device__ __forceinline__ float times_pow2(float x, int e) {
+    e = e < -252 ? -252 : (e > 252 ? 252 : e);
+    return x * kv_pow2(e >> 1) * kv_pow2(e - (e >> 1));
+}
 // 2^e for e <= 127, 0 where that is below the normal range
 __device__ __forceinline__ float pow2_or_0(int e) { return e < -126 ? 0.f : kv_pow2(e); }
 
@@ -555,8 +560,8 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
             if (!go) gave_up();
             uint32_t qb[NT][HD / 16][2];
             float o[HD / 16][NT][4];
-            float m[NT][E], l[NT][E], qf[NT][E];            // qf: scale * log2 e, or NaN where q is not finite
-            int qe[NT][E], limit[NT][E];                    // exponent of the row's largest |q|; positions it sees
+            float m[NT][E], l[NT][E], qf[NT][E];            // qf: qk, NaN where q is not finite, 0 where it is 0
+            int qe[NT][E], limit[NT][E];                    // exponent of the row's largest |q| and of qk; positions it sees
             int unit = UNIT_NONE, top = UNIT_NONE;          // o is in units of 2^unit; largest value scale so far
             bool bad = false;
 #pragma unroll
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                 const unsigned nf = __ballot_sync(0xffffffffu, !fin);
                 int ex = 0;
                 if (big > 0.f && big <= FLT_MAX) frexpf(big, &ex);
-                const float f = (nf >> (lane & 28)) & 15u ? NAN : a.qk;
+                const float f = (nf >> (lane & 28)) & 15u ? NAN : (big > 0.f ? a.qk : 0.f);
                 // 2^-ex in two steps: it can lie outside fp32
                 const float f1 = kv_pow2(-ex / 2), f2 = kv_pow2(-ex - (-ex / 2));
 #pragma unroll
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                 for (int e = 0; e < E; ++e) {
                     const int from = 4 * (2 * t + e);
                     const int r2 = rg * S::PR + (FOLD ? 4 * n + t : 8 * n + 2 * t + e);
-                    qe[n][e] = __shfl_sync(0xffffffffu, ex, from);
+                    qe[n][e] = __shfl_sync(0xffffffffu, ex, from) + a.qk_exp;
                     qf[n][e] = __shfl_sync(0xffffffffu, f, from);
                     limit[n][e] = r2 < x.pairs ? x.before + (x.pair0 + r2) / a.group + 1 : 0;
                     m[n][e] = -INFINITY;
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < E; ++e) fk[n][e] = qf[n][e] * pow2_clamped(qe[n][e] + ek);
+                    for (int e = 0; e < E; ++e) fk[n][e] = times_pow2(qf[n][e], qe[n][e] + ek);
                 // EDGE: some row does not see all 32 positions
                 auto step = [&](auto edge) {
                     constexpr bool EDGE = decltype(edge)::value;
@@ -1061,7 +1066,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     AttnCall k;
     k.q = a.q; k.out = a.out; k.lse = a.lse; k.ldq = a.ldq; k.ldo = a.ldo;
     k.n_heads = a.n_heads; k.group = a.n_heads / c.n_kv;
-    k.qk = a.scale * LOG2E;
+    k.qk = (float)frexp((double)a.scale * LOG2E, &k.qk_exp);
     const int64_t pairs = (int64_t)c.max_rows * k.group;
     k.prow = (int)(pairs < S::ROWS ? pairs : S::ROWS);
     k.slot = ((int64_t)k.prow * (HD + 3) + 3) / 4 * 4;      // 16-byte aligned

@@ -947,3 +947,19 @@ def test_the_sum_over_many_positions_of_zero_values(heads, rows, nbytes, dtype):
     want = np.log(np.arange(n - rows + 1, n + 1))[:, None]
     assert (np.abs(lse.double().cpu().numpy() - want) <= 8 * 2.0 ** -24 * want + 2.0 ** -22).all()
     assert (out == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scales_that_make_up_for_tiny_or_huge_factors(dtype):
+    """ordinary scores from queries, keys and a scale whose exponents are far from zero, and queries of zero"""
+    torch = _torch()
+    for kgain, qgain, sc in ((2.0 ** -70, 2.0 ** -60, 2.0 ** 126), (2.0 ** -60, 2.0 ** -68, float(np.float32(3.0e38))),
+                             (2.0 ** 100, 2.0 ** 10, 2.0 ** -113), (2.0 ** 60, 2.0 ** 66, 2.0 ** -129),
+                             (2.0 ** -60, 2.0 ** 100, 2.0 ** -43), (2.0 ** 110, 0.0, 2.0 ** 30)):
+        st = Setup([100, 65, 1], 2, 64, seed=49)
+        x = st.rows(166, "fp32", spread=0.1)
+        x[:, :2] *= kgain
+        st.append([100, 65, 1], "fp32", x)
+        q = torch.from_numpy(st.rng.standard_normal((3, 4, 64)).astype(np.float32)).cuda() * qgain
+        _attend(st, [1, 1, 1], 4, dtype, q=q.bfloat16() if dtype == "bf16" else q, scale=sc)
