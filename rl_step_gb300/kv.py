@@ -291,8 +291,12 @@ def tf_sample_cached(h, caches, tokens, adapter_ids, uniforms, page_table, kv_le
 
 def kv_check_status(cache: KvCache, stream=None) -> int:
     """Synchronise, return and clear the cache's status: 0, -2 (E_RANGE), or -5
-    (E_TIMEOUT: a bounded device wait gave up)."""
-    (stream or torch.cuda.current_stream()).synchronize()
-    bad = int(cache.status.item())
-    cache.status.zero_()
+    (E_TIMEOUT: a bounded device wait gave up).  The word is read and cleared in
+    the order of `stream` (None: the current one): a bit that later work there
+    raises is kept.  Calls of the cache on other streams should have ended."""
+    stream = stream or torch.cuda.current_stream(cache.index)
+    with torch.cuda.stream(stream):
+        bad = int(cache.status.item())
+        if bad:
+            cache.status.zero_()
     return -5 if bad & 2 else -2 if bad & 1 else 0

@@ -963,3 +963,27 @@ def test_scales_that_make_up_for_tiny_or_huge_factors(dtype):
         st.append([100, 65, 1], "fp32", x)
         q = torch.from_numpy(st.rng.standard_normal((3, 4, 64)).astype(np.float32)).cuda() * qgain
         _attend(st, [1, 1, 1], 4, dtype, q=q.bfloat16() if dtype == "bf16" else q, scale=sc)
+
+
+@pytest.mark.gpu
+def test_the_status_is_read_and_cleared_on_the_stream():
+    """kv_check_status(cache, stream): read and cleared in that stream's order, so that no later call's bit there is lost"""
+    torch = _torch()
+    st = Setup([64], 1, 64, seed=50)
+    s = torch.cuda.Stream()
+
+    class Word:
+        def __init__(self, value):
+            self.value, self.where = value, []
+
+        def item(self):
+            self.where.append(torch.cuda.current_stream())
+            return self.value
+
+        def zero_(self):
+            self.where.append(torch.cuda.current_stream())
+    st.cache.status = Word(1)
+    assert st.kv.kv_check_status(st.cache, stream=s) == -2
+    assert st.cache.status.where == [s, s]
+    st.cache.status = Word(3)
+    assert st.kv.kv_check_status(st.cache) == -5 and set(st.cache.status.where) == {torch.cuda.current_stream()}
