@@ -99,11 +99,19 @@ class GradSet:
             self._workspace = _empty(self._bytes, torch.uint8, self.device, None)
 
 
+def _capturing(stream) -> bool:
+    """Whether the stream of the call (None: the current one) is being captured."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):
     """Clip each group of gs to max_norm; returns the norms before clipping
     (float32 [n_groups])."""
     handle = _on(gs.index, stream)
-    if handle == gs._stream and not torch.cuda.is_current_stream_capturing():
+    if handle == gs._stream and not _capturing(stream):
         workspace = gs._workspace
     else:
         workspace = _empty(gs._bytes, torch.uint8, gs.device, stream)

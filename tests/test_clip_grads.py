@@ -333,3 +333,25 @@ def test_an_infinity_in_a_large_group_is_reported_as_one(dtype):
     for x, y in zip(xs[:5], b[:5]):
         assert torch.equal(torch.nan_to_num(x, 7, 8, 9), torch.nan_to_num(y, 7, 8, 9))
     assert abs(norms[5] - math.sqrt(n)) <= 35 * U * math.sqrt(n) and bool((xs[5] < 1e-3).all())
+
+
+@pytest.mark.gpu
+def test_a_capture_on_a_stream_that_is_not_current_takes_its_own_workspace():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    s = torch.cuda.Stream()
+    other = torch.cuda.Stream()
+    x = torch.ones(100000, device="cuda")
+    norms = torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        gs = gr.GradSet([x])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        with torch.cuda.stream(other):
+            gr.clip_grads(gs, math.inf, norms_out=norms, stream=s)
+    gs._workspace.fill_(0x5a)
+    g.replay()
+    torch.cuda.synchronize()
+    assert abs(float(norms) - math.sqrt(100000)) <= 35 * U * math.sqrt(100000)
+    assert bool((gs._workspace == 0x5a).all())             # a replay can run beside the set's own calls
