@@ -109,7 +109,8 @@ int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype
  *     out = sum_i exp(s_i - lse) v_i,   lse = log sum_i exp(s_i).
  * A row without positions gets out = 0 and lse = -infinity.  q, out: rows of
  * n_heads * head_dim elements of `dtype`, q_stride / out_stride elements apart;
- * pointers and row distances are multiples of 16 bytes, out may be q.  lse: DEVICE fp32
+ * pointers and row distances are multiples of 16 bytes; out may be q (with its
+ * stride), else no row of out overlaps one of q.  lse: DEVICE fp32
  * [n_rows x n_heads], or NULL.  max_len: upper bound of kv_len (a longer
  * sequence is a range error); it sets how far the work is split.
  * Sums and softmax statistics are fp32.  Scores are formed from the stored bytes

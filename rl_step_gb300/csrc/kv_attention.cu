@@ -1141,6 +1141,29 @@ cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const 
 
 using namespace mlk;
 
+namespace {
+
+// Whether a row that the call writes holds a part of a row that it may still
+// read: n rows of `row` bytes, sq and so >= row bytes apart.  The queries
+// themselves as the output are no such case.
+bool rows_clash(uintptr_t q, int64_t sq, uintptr_t o, int64_t so, int64_t row, int64_t n) {
+    if (q == o && (sq == so || n == 1)) return false;
+    if (o >= q + (n - 1) * sq + row || q >= o + (n - 1) * so + row) return false;
+    if (sq == so) {                                         // columns of one buffer: side by side or not
+        const int64_t d = (int64_t)((o > q ? o - q : q - o) % (uintptr_t)so);
+        return d < row || so - d < row;
+    }
+    for (int64_t i = 0; i < n; ++i) {                       // the output rows that begin just before and behind row i
+        const int64_t at = (int64_t)(q - o) + i * sq;
+        const int64_t j = at >= 0 ? at / so : -1;
+        if (j >= 0 && j < n && at - j * so < row) return true;
+        if (j + 1 < n && (j + 1) * so - at < row) return true;
+    }
+    return false;
+}
+
+}  // namespace
+
 extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const mlora_kv_attn* a,
                                   void* stream) {
     if (!a) return kv_fail(MLORA_E_ARG, "NULL attention arguments");
@@ -1160,6 +1183,10 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
         ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out)) & 15))
         return kv_fail(MLORA_E_ARG, "query and output rows must be 16-byte aligned and at least %lld elements apart",
                        (long long)row);
+    const int64_t es = 16 / per16;
+    if (rows_clash(reinterpret_cast<uintptr_t>(a->q), a->q_stride * es, reinterpret_cast<uintptr_t>(a->out),
+                   a->out_stride * es, row * es, w.n_rows))
+        return kv_fail(MLORA_E_ARG, "the output's rows overlap queries (out may be q, with its stride, or lie apart)");
     if ((reinterpret_cast<uintptr_t>(a->workspace) & 15) || a->workspace_bytes < 0)
         return kv_fail(MLORA_E_ARG, "the workspace must be 16-byte aligned");
     if ((int64_t)w.max_rows * a->n_heads > INT32_MAX / w.n_seqs)

@@ -102,6 +102,16 @@ def test_attention_refuses(where, field, value):
     assert lib.mlora_last_error()
 
 
+@pytest.mark.parametrize("out,out_stride", [(4096, 1024), (4096 + 16, 512), (4096 + 1024, 512), (4096 - 512, 512),
+                                            (4096 + 512, 1024), (4096 + 2048, 512), (4096 + 512, 768), (4096 - 2048, 1024)])
+def test_attention_refuses_an_output_that_overlaps_other_queries(out, out_stride):
+    """three rows of 512 elements (1 KB) at 4096 on: an output is the queries themselves, or apart from them"""
+    kv, lib, c, q, a = _valid()
+    a.out, a.out_stride = out, out_stride
+    assert lib.mlora_kv_attention(ctypes.byref(c), ctypes.byref(q), ctypes.byref(a), None) == -1
+    assert b"overlap" in lib.mlora_last_error()
+
+
 @pytest.mark.parametrize("where,field,value", _BAD)
 def test_append_and_read_refuse(where, field, value):
     kv, lib, c, q, _ = _valid()
@@ -987,3 +997,24 @@ def test_the_status_is_read_and_cleared_on_the_stream():
     assert st.cache.status.where == [s, s]
     st.cache.status = Word(3)
     assert st.kv.kv_check_status(st.cache) == -5 and set(st.cache.status.where) == {torch.cuda.current_stream()}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 2, 70])
+def test_outputs_beside_the_queries_are_taken(n):
+    """columns and rows of one buffer that do not touch the queries', in every order"""
+    torch = _torch()
+    st = Setup([70], 2, 64, seed=51)
+    st.append([70])
+    buf = torch.randn(4 * n, 9, 64, device="cuda").bfloat16()
+    off, lens = st.off([n]), st.i32([70])
+    want = None
+    x = torch.randn(n, 4, 64, device="cuda").bfloat16()
+    for q, out in ((buf[:n, :4], buf[:n, 4:8]), (buf[:n, 5:], buf[:n, 1:5]), (buf[:n, :4], buf[n:2 * n, 2:6]),
+                   (buf[::2][:n, :4], buf[1::2][:n, :4]), (buf[::2][:n, :4], buf[:n, 4:8]), (buf[:n, 4:8], buf[::4][:n, :4]),
+                   (buf[3 * n:, :4], buf[::3][:n, 4:8]), (buf[:n, :4], buf[:n, :4])):
+        q.copy_(x)
+        o, lse = st.kv.kv_attention(st.cache, st.dtable, lens, q, 70, row_off=off, max_rows=n, out=out)
+        if want is None:
+            want = o.clone(), lse
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
