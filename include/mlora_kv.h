@@ -166,7 +166,7 @@ int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const ml
  * (not while mlora_tf_profile_enable is on).
  * ------------------------------------------------------------------------ */
 typedef struct {
-    const mlora_kv_cache* caches;  /* HOST [n_layers]: the layers' page pools, n_kv_heads of the model, head_dim 128 */
+    const mlora_kv_cache* caches;  /* HOST [n_layers]: the layers' page pools, which do not overlap, n_kv_heads of the model, head_dim 128 */
     mlora_kv_seqs seqs;            /* the same pages of every pool                 */
     void* workspace;               /* as in mlora_kv_attn                          */
     int64_t workspace_bytes;

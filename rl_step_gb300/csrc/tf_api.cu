@@ -11,8 +11,10 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/mlora_kv.h"
@@ -1072,6 +1074,23 @@ extern "C" int mlora_tf_forward(mlora_tf_t* h, const mlora_tf_batch* b, float* l
 
 namespace {
 
+// Whether two layers' caches (or keys and values of one) share memory: each layer
+// would find the last one's bytes.
+bool caches_overlap(const mlora_kv_cache* c, int n) {
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    for (int l = 0; l < n; ++l) {
+        const int64_t tiles = (int64_t)c[l].n_pages * c[l].n_kv_heads;
+        for (const void* p : {(const void*)c[l].k, (const void*)c[l].v, (const void*)c[l].k_scale, (const void*)c[l].v_scale}) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            spans.emplace_back(at, at + tiles * (p == c[l].k || p == c[l].v ? MLORA_KV_PAGE * c[l].head_dim : sizeof(float)));
+        }
+    }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+        if (spans[i].first < spans[i - 1].second) return true;
+    return false;
+}
+
 int tf_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c, TfCached& kc, float* logprobs_out,
               void* stream) {
     if (!h || !b || !c) return tfail(MLORA_E_ARG, "NULL handle, batch or context");
@@ -1098,6 +1117,7 @@ int tf_cached(mlora_tf_t* h, const mlora_tf_batch* b, const mlora_tf_context* c,
                          c->caches[l].n_kv_heads, c->caches[l].head_dim, h->nkv, MLORA_TF_HEAD_DIM);
         kc.kv[l].row_map = h->row_map;
     }
+    if (caches_overlap(c->caches, h->L)) return tfail(MLORA_E_ARG, "the layers' caches overlap");
     if (!kv_fits(kc.kv[0]) ||
         (c->seqs.n_seqs > 0 && (int64_t)kc.kv[0].max_rows * h->nh > INT32_MAX / c->seqs.n_seqs))
         return tfail(MLORA_E_ARG, "too many sequences, rows and heads for one call");

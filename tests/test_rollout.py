@@ -514,3 +514,22 @@ def test_a_sequence_out_of_range_leaves_its_pages(small, length):
         for c, old in zip(caches, before):
             for x, y in zip((c.k, c.v, c.k_scale, c.v_scale), old):
                 assert torch.equal(x[own], y[own])
+
+
+@pytest.mark.gpu
+def test_layers_that_share_pages_are_refused(small):
+    """one pool for two layers would hold the last one's keys and values alone"""
+    torch = _torch()
+    import rl_step_gb300 as m
+    import rl_step_gb300.kv as kv
+    s = small
+    z, lens, table = _int(torch, [1, 2]), _int(torch, [1, 1]), _int(torch, [[0], [1]])
+    a, b = s.caches(4)[:2]
+    whole = kv.KvCache.empty(6, s.cfg.n_kv_heads, s.cfg.head_dim)
+    part = lambda i, j: kv.KvCache(whole.k[i:j], whole.v[i:j], whole.k_scale[i:j], whole.v_scale[i:j])
+    for pair in ([a, a], [a, kv.KvCache(b.k, a.v, b.k_scale, b.v_scale)], [part(0, 4), part(2, 6)],
+                 [a, kv.KvCache(b.k, b.v, a.k_scale, b.v_scale)], [a, kv.KvCache(a.v, b.v, b.k_scale, b.v_scale)]):
+        with pytest.raises(m.MLoRAError):
+            kv.tf_forward_cached(s.h, pair, z, z, z, table, lens, 1)
+    lp = kv.tf_forward_cached(s.h, [part(0, 3), part(3, 6)], z, z, z, table, lens, 1)      # side by side
+    assert torch.isfinite(lp).all()
