@@ -1046,7 +1046,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
 }
 
 template <typename T, int HD, int NT, int RG, int PG_>
-cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
+cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t* launches) {
     using S = AttnShape<T, HD, NT, RG, PG_>;
     // once a device: its SMs, and the kernel's shared memory (the attribute stays with the function)
     static std::atomic<int> sms[64];
@@ -1086,6 +1086,7 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
     k.cuts = cut ? reinterpret_cast<Cut*>(k.part + blocks * 2 * k.slot) : nullptr;
     kv_attn_kernel<T, HD, NT, RG, PG_><<<(unsigned)blocks, S::THREADS, S::SMEM, s>>>(c, k);
     e = cudaGetLastError();
+    if (launches) *launches += cut ? 2 : 1;
     if (e != cudaSuccess || !cut) return e;
     // the join waits on the device for the attention kernel's end: only its launch overlaps it
     const int total = (int)(blocks * k.prow);
@@ -1116,25 +1117,26 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
 // workspace lets results depend on it.
 constexpr int64_t KV_MANY = 600;
 template <typename T, int HD>
-cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s) {
+cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t* launches) {
     constexpr int PR = AttnShape<T, HD, 1, 1, 2>::PR;
     const int64_t pairs = (int64_t)c.max_rows * (a.n_heads / c.n_kv);
     if (pairs <= PR) {
         if constexpr (HD == 128)
             if (a.workspace && a.workspace_bytes >= MLORA_KV_WORKSPACE_BYTES && (int64_t)c.n_seqs * c.n_kv >= KV_MANY)
-                return attn_t<T, HD, 1, 1, 1>(c, a, s);
-        return attn_t<T, HD, 1, 1, 2>(c, a, s);
+                return attn_t<T, HD, 1, 1, 1>(c, a, s, launches);
+        return attn_t<T, HD, 1, 1, 2>(c, a, s, launches);
     }
     // in columns, a padded one of the larger tile at 8 / 9 of the smaller one's cost
     const int64_t small = (pairs + 2 * PR - 1) / (2 * PR) * 2 * PR, large = (pairs + 8 * PR - 1) / (8 * PR) * 8 * PR;
-    return 8 * large <= 9 * small ? attn_t<T, HD, 2, 4, 1>(c, a, s) : attn_t<T, HD, 1, 2, 1>(c, a, s);
+    return 8 * large <= 9 * small ? attn_t<T, HD, 2, 4, 1>(c, a, s, launches) : attn_t<T, HD, 1, 2, 1>(c, a, s, launches);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s) {
-    if (dtype == MLORA_BF16) return head_dim == 64 ? attn_rows<bf16, 64>(c, a, s) : attn_rows<bf16, 128>(c, a, s);
-    return head_dim == 64 ? attn_rows<float, 64>(c, a, s) : attn_rows<float, 128>(c, a, s);
+cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s,
+                                int64_t* launches) {
+    if (dtype == MLORA_BF16) return (head_dim == 64 ? attn_rows<bf16, 64> : attn_rows<bf16, 128>)(c, a, s, launches);
+    return (head_dim == 64 ? attn_rows<float, 64> : attn_rows<float, 128>)(c, a, s, launches);
 }
 
 }  // namespace mlk
@@ -1194,7 +1196,7 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
     KvAttnArgs k;
     k.q = a->q; k.out = a->out; k.lse = a->lse; k.workspace = a->workspace; k.ldq = a->q_stride; k.ldo = a->out_stride;
     k.workspace_bytes = a->workspace_bytes; k.n_heads = a->n_heads; k.scale = a->scale;
-    const cudaError_t e = launch_kv_attention(w, c->head_dim, a->dtype, k, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_kv_attention(w, c->head_dim, a->dtype, k, reinterpret_cast<cudaStream_t>(stream), nullptr);
     if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "attention launch: %s", cudaGetErrorString(e));
     return MLORA_OK;
 }

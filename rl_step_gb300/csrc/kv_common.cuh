@@ -120,6 +120,8 @@ struct KvAttnArgs {
     int n_heads;
     float scale;
 };
-cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s);
+// launches (may be null) counts the kernels
+cudaError_t launch_kv_attention(const KvView& c, int head_dim, int dtype, const KvAttnArgs& a, cudaStream_t s,
+                                int64_t* launches);
 
 }  // namespace mlk

@@ -742,8 +742,8 @@ int cached_attention(mlora_tf_t* h, const TfCached& c, int l, cudaStream_t s) {
     a.workspace = c.workspace; a.workspace_bytes = c.workspace_bytes;
     a.n_heads = h->nh;
     a.scale = 1.f / sqrtf((float)MLORA_TF_HEAD_DIM);
-    TF_CUDA(launch_kv_attention(c.kv[l], MLORA_TF_HEAD_DIM, MLORA_BF16, a, s));
-    h->launches += 2;
+    ++h->launches;
+    TF_CUDA(launch_kv_attention(c.kv[l], MLORA_TF_HEAD_DIM, MLORA_BF16, a, s, &h->launches));
     return MLORA_OK;
 }
 

@@ -533,3 +533,22 @@ def test_layers_that_share_pages_are_refused(small):
             kv.tf_forward_cached(s.h, pair, z, z, z, table, lens, 1)
     lp = kv.tf_forward_cached(s.h, [part(0, 3), part(3, 6)], z, z, z, table, lens, 1)      # side by side
     assert torch.isfinite(lp).all()
+
+
+@pytest.mark.gpu
+def test_joined_attention_counts_as_a_launch(small):
+    """where long sequences may be cut, each layer launches one kernel more"""
+    torch = _torch()
+    import rl_step_gb300.kv as kv
+    import rl_step_gb300.transformer as t
+    s = small
+    table = _int(torch, [np.arange(16)])
+    caches = s.caches(16)
+    z = _int(torch, [1])
+    n = []
+    for nbytes in (0, kv.WORKSPACE_BYTES):
+        ws = kv.kv_workspace(nbytes=nbytes)
+        at = t._lib().mlora_tf_kernel_launches(s.h.ptr)
+        kv.tf_forward_cached(s.h, caches, z, z, z, table, _int(torch, [1]), 1024, workspace=ws)
+        n.append(t._lib().mlora_tf_kernel_launches(s.h.ptr) - at)
+    assert n[1] == n[0] + s.cfg.n_layers
