@@ -39,7 +39,7 @@
 //  * The page's value scale 2^ev: a warp's accumulators are in units of 2^unit, and
 //    p' = p 2^(ev - unit) where that is within 2^-3 .. 1 (the factor goes into the
 //    exponent, l += p' 2^(unit - ev), and the bounds on p's rounding are 2^3
-//    higher).  At any other page the unit becomes 2^(ev + 1) and the accumulators,
+//    higher).  At any other page the unit becomes 2^ev and the accumulators,
 //    fp32 with room for it, are multiplied by the difference: so each dim keeps its
 //    precision beside pages whose scale another dim has made large, and l has every
 //    p whatever its page's scale.  (With the whole scale in p', p' left fp16's range
@@ -705,9 +705,9 @@ __global__ void __launch_bounds__(AttnShape<T, HD, NT, RG, PG_>::THREADS, AttnSh
                         if (off_unit) {
                             if (ev >= top - V_GAP) {
                                 top = max(top, ev);
-                                fm = pow2_or_0(unit - ev - 1);
-                                unit = ev + 1;
-                                fold = -1;
+                                fm = pow2_or_0(unit - ev);
+                                unit = ev;
+                                fold = 0;
                             } else {
                                 fold = V_GONE;
                             }

@@ -13,11 +13,11 @@ A = sum_i p_i |v_i| and S = max_i |scale| sum_d |q_d k_d| of the row (doubles):
     2^-22, the fp16 rounding of p 2^-11 (bf16) or 2^-22 (fp32), and the sums
     over n positions at most n u each
   below 2^-14 fp16's rounding is absolute, 2^-25: p_i is held as p'_i = 2^12
-    2^(s_i log2(e) + ev_i - m') with ev_i the exponent of its page's value scale
-    and m' reached by some position r, p'_r >= 2^12, so that the result's
-    divisor sum_i p'_i 2^-ev_i is at least 2^(12 - ev_r).  n errors of 2^-25 on
-    bytes of at most 448 < 2^9 make at most n 2^-25 2^9 2^(ev_r - 12) =
-    n 2^-28 2^ev_r <= F = n 2^-28 max_page 2^ev
+    2^(s_i log2(e) - m + ev_i - unit) with ev_i the exponent of its page's value
+    scale, unit at most the largest of them, and m reached by some position, so
+    that the result's divisor sum_i p'_i 2^(unit - ev_i) is at least 2^12.  n errors
+    of 2^-25 on bytes of at most 448 < 2^9, in units of 2^unit, make at most
+    n 2^-25 2^9 2^(unit - 12) = n 2^-28 2^unit <= F = n 2^-28 max_page 2^ev
   out: (4 D + P + 2 n u + 2^-20) A + F + half a step of the type, with P = 2^-11 or 2^-22
   lse: 2 D + n u + 2^-22 + 2 u |lse|
 (the products' order inside a matrix instruction may truncate instead of
