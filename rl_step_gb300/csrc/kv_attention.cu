@@ -80,12 +80,17 @@ constexpr int V_FOLD = 3;                   // value scales of 2^-V_FOLD to 1 of
 constexpr int V_GAP = 64;                   // pages below 2^-V_GAP of the largest so far count as zero values: 2^31 terms
                                             // p' v8 < 2^24 times 2^V_GAP stay within fp32
 constexpr int V_GONE = -60;                 // what such a page folds: p' <= 2^-45 is 0 in fp16, and so is its low part
-constexpr int KV_SHORT_RUN = 2;             // places: no block gets fewer
+// Places: no block gets fewer.  One sequence of 1000 tokens, 8 heads of 128: 9.8 us at 1, 10.8 at 2, 11.1 at 4; one
+// of 4000, 1 head: 10.2, 9.7, 9.9 (replayed graphs); long ones have more places than blocks.
+constexpr int KV_SHORT_RUN = 2;
 // What a unit's start and end cost, in pages.  41 sequences of 0 to 3001 tokens,
 // 16 heads of 64, fp32: 58 us at 0, 45 at 2, 36 at 4, 37 at 6; 256 sequences of
 // 512 to 2048, 8 heads of 128: 130, 125, 123, 121 us.
 constexpr int KV_START = 5;
-constexpr int KV_WHOLE = 8;                 // pages: sequences up to this are not cut
+// Pages: sequences up to this are not cut.  Uncut, and cut at 4 or less: 256 sequences of 64 to 512 tokens, 8 heads
+// of 128, 60.8 and 68.4 us, 64 of them 18.7 and 20.5, 3 of 21 to 299, 2 heads, 9.3 and 10.3; but 8 of 300 to 512, 8
+// heads, 15.9 and 11.2.  At 16, 8 sequences of 600 to 1000 take 20.7 us in place of 12.4 (replayed graphs).
+constexpr int KV_WHOLE = 8;
 
 // A cut unit, left in the workspace by the block that begins it.
 struct Cut {
