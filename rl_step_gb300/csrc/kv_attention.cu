@@ -1190,7 +1190,9 @@ extern "C" int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* 
         ((reinterpret_cast<uintptr_t>(a->q) | reinterpret_cast<uintptr_t>(a->out)) & 15))
         return kv_fail(MLORA_E_ARG, "query and output rows must be 16-byte aligned and at least %lld elements apart",
                        (long long)row);
-    const int64_t es = 16 / per16;
+    const int64_t es = 16 / per16, furthest = INT64_MAX / 16 / w.n_rows;
+    if (a->q_stride > furthest || a->out_stride > furthest)
+        return kv_fail(MLORA_E_ARG, "query or output rows are further apart than memory reaches");
     if (rows_clash(reinterpret_cast<uintptr_t>(a->q), a->q_stride * es, reinterpret_cast<uintptr_t>(a->out),
                    a->out_stride * es, row * es, w.n_rows))
         return kv_fail(MLORA_E_ARG, "the output's rows overlap queries (out may be q, with its stride, or lie apart)");

@@ -112,6 +112,19 @@ def test_attention_refuses_an_output_that_overlaps_other_queries(out, out_stride
     assert b"overlap" in lib.mlora_last_error()
 
 
+@pytest.mark.parametrize("q_stride,out_stride,out", [(1 << 62, 1 << 62, 4096), (1 << 62, 512, 4096 + 1024), (512, 1 << 60, 0),
+                                                     (1 << 62, 1 << 62, 4096 + 16)])
+@pytest.mark.parametrize("n", [1, 3])
+def test_attention_refuses_rows_beyond_memory(q_stride, out_stride, out, n):
+    """distances whose products with the rows or the element size leave 64 bits"""
+    kv, lib, c, q, a = _valid()
+    q.n_seqs = q.n_rows = n
+    a.q_stride, a.out_stride = q_stride, out_stride
+    a.out = out or a.out
+    assert lib.mlora_kv_attention(ctypes.byref(c), ctypes.byref(q), ctypes.byref(a), None) == -1
+    assert b"apart" in lib.mlora_last_error()
+
+
 @pytest.mark.parametrize("where,field,value", _BAD)
 def test_append_and_read_refuse(where, field, value):
     kv, lib, c, q, _ = _valid()
