@@ -412,10 +412,11 @@ int mlora_set_lm_backward(mlora_t* h, int32_t mode);
  *     factor_g = max_norm / n_g if n_g > max_norm, else 1
  *     out = x * factor_g
  * A norm that is an infinity or NaN leaves its group as it is (factor 1): the
- * caller sees it in norms_out and skips the step.  Squares are added in fp32 (a
- * norm is off by about 30 * 2^-24 of itself at most) in a fixed order: results
- * repeat bit for bit; magnitudes whose squares leave fp32's range are added
- * relative to their largest.
+ * caller sees it in norms_out and skips the step.  (A finite norm beyond fp32's
+ * largest value is infinity in norms_out, and clips all the same.)  Squares are
+ * added in fp32 (a norm is off by about 30 * 2^-24 of itself at most) in a fixed
+ * order: results repeat bit for bit; magnitudes whose squares leave fp32's range
+ * are added relative to their largest.
  *   grads, out: HOST arrays of DEVICE pointers to contiguous tensors of
  *     `dtype` (mlora_dtype), aligned to their elements; out NULL: in place.
  *     A tensor and its output are equal or do not overlap, and no output

@@ -76,7 +76,7 @@ typedef struct {
     int64_t n_rows;              /* rows of the row arrays                             */
     int32_t n_seqs;              /* >= 0                                               */
     int32_t max_pages;           /* >= 1                                               */
-    int32_t max_rows;            /* upper bound of n_s (1 where row_off is NULL)       */
+    int32_t max_rows;            /* upper bound of n_s (1 where row_off is NULL); 0: nothing to do */
 } mlora_kv_seqs;
 
 /* Write the rows' keys and values into the cache.  k, v: DEVICE rows of
@@ -129,8 +129,8 @@ int mlora_kv_read(const mlora_kv_cache* c, const mlora_kv_seqs* q, int32_t dtype
  * evenly whatever the lengths: long sequences are cut where a block's share
  * ends and their parts joined, so the order of a row's sums depends on the
  * lengths of the batch.  With less than the shape needs (0, say) no sequence is
- * cut, and a row's result is bit for bit the same whatever else a call with the
- * same max_rows holds.
+ * cut, and a row's result is bit for bit the same whatever other sequences a call
+ * with the same max_rows holds.
  * Errors: E_ARG, E_CUDA. */
 typedef struct {
     const void* q;
@@ -159,10 +159,12 @@ int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const ml
  * max_tokens (the bound of its rotary table).  A row outside them, with a bad
  * token, target or adapter id, or of a sequence that is out of range gets NaN
  * and raises MLORA_E_RANGE in mlora_tf_check_status; with a bad adapter id its
- * keys and values in the cache are unspecified.  Rows of no sequence or of an
- * empty slot get NaN and raise nothing, so a batch can be padded to a fixed
- * size.  Gradients, weights and step counts are not changed.  No call
- * allocates or synchronises, so a decode step can be captured into a graph
+ * keys and values in the cache are unspecified.  The caches' own status reports
+ * sequences out of range too, and alone a bad page id, whose sequence's rows get
+ * NaN.  Rows of no sequence or of an empty slot get NaN and raise nothing, so a
+ * batch can be padded to a fixed size.  Gradients, weights and step counts are not
+ * changed.  No call allocates or synchronises, so a decode step can be captured
+ * into a graph
  * (not while mlora_tf_profile_enable is on).
  * ------------------------------------------------------------------------ */
 typedef struct {

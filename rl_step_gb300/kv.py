@@ -208,7 +208,8 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
     """Attention of the rows q [n_rows, n_heads, head_dim] over their sequences'
     cached positions up to their own.  Returns (out like q, lse float32
     [n_rows, n_heads]); scale defaults to 1 / sqrt(head_dim).  Without a
-    workspace one is allocated for the call."""
+    workspace one is allocated for the call.  Nothing is recorded for autograd,
+    whatever q, out or lse require."""
     if q.dim() != 3:
         raise ValueError("q must be [rows, heads, head_dim]")
     n_rows, heads, hd = q.shape

@@ -355,3 +355,15 @@ def test_a_capture_on_a_stream_that_is_not_current_takes_its_own_workspace():
     torch.cuda.synchronize()
     assert abs(float(norms) - math.sqrt(100000)) <= 35 * U * math.sqrt(100000)
     assert bool((gs._workspace == 0x5a).all())             # a replay can run beside the set's own calls
+
+
+@pytest.mark.gpu
+def test_a_norm_beyond_fp32_clips_all_the_same():
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    x = torch.full((10000,), 3e38, device="cuda")
+    y = torch.empty_like(x)
+    assert math.isinf(float(gr.clip_grads(gr.GradSet([x], out=[y]), 1.0)))
+    want = 1 / math.sqrt(10000)
+    # norm 32 u, product u; the factor 1 / 3e40 is below fp32's normal range: off by at most 2^-150, times 3e38
+    assert bool(((y.double() - want).abs() <= 37 * U * want + 2.0 ** -150 * 3e38).all())
