@@ -21,7 +21,7 @@
 //    No atomics, a fixed order: results repeat bit for bit.
 // (One resident kernel that counted arrivals a chunk instead took 981 us on the 32
 // adapters of the 8B widths, 39 MB each, two whole passes 670 us, this 474 us, 77 %
-// of the copy rate by the floor's bytes; one adapter 37, 37 and 19 us.  Of the 474,
+// of the copy rate by the floor's bytes; one adapter 37, 37 and 20.6 us.  Of the 474,
 // about 100 are lines that left L2 before they were scaled: a launch read 76 MB
 // from HBM, 39 of them for the first time, until the scaling loads said that they
 // are the last ones and began with the newest lines; 61 MB since.)

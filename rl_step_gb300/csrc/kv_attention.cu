@@ -84,8 +84,9 @@ constexpr int V_GONE = -60;                 // what such a page folds: p' <= 2^-
 // of 4000, 1 head: 10.2, 9.7, 9.9 (replayed graphs); long ones have more places than blocks.
 constexpr int KV_SHORT_RUN = 2;
 // What a unit's start and end cost, in pages.  41 sequences of 0 to 3001 tokens,
-// 16 heads of 64, fp32: 58 us at 0, 45 at 2, 36 at 4, 37 at 6; 256 sequences of
-// 512 to 2048, 8 heads of 128: 130, 125, 123, 121 us.
+// 16 heads of 64, fp32: 62.4 us at 0, 37.4 at 2, 33.3 at 4 to 6, 34.3 at 8; 256
+// sequences of 512 to 2048, 8 heads of 128: 124.2, 120.0, 117.8 to 117.3, 117.0; 64 of
+// 4097 to 32767: 363 at 0, 357 to 359 from 2 on.
 constexpr int KV_START = 5;
 // Pages: sequences up to this are not cut.  Uncut, and cut at 4 or less: 256 sequences of 64 to 512 tokens, 8 heads
 // of 128, 60.8 and 68.4 us, 64 of them 18.7 and 20.5, 3 of 21 to 299, 2 heads, 9.3 and 10.3; but 8 of 300 to 512, 8
@@ -1111,15 +1112,19 @@ cudaError_t attn_t(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t
 // One column tile (8 pairs; 4 on fp32) where a sequence's pairs fit it.  More row
 // groups share each page tile (its reads and its place in shared memory) where a
 // sequence has more: two of a tile, or, where that pads little, four of two tiles,
-// which convert each byte for twice the columns (9 rows of 36 pairs: 89 us in
-// tiles of 64, 68 in tiles of 16; 64 pairs: 178 and 195; 72: 132 and 110; prompts
-// of 2000 rows: 2.01 and 2.12 ms).  A single row group has two pages in work; or,
-// heads of 128 and many units, one page and more blocks, which hide the ends of
-// units better (256 sequences of 512 to 2048 tokens, 2048 units: 118 us against 114;
-// one of 130,001, 8 units: 53.0 against 53.8; heads of 64, 656 units: 31.7 against
-// 40.6; where units are twice as long, 64 sequences of 1000 to 4001 and 16 heads, 108
-// against 110).  That choice looks at the whole batch, so it is made only where the
-// workspace lets results depend on it.
+// which convert each byte for twice the columns (32 sequences of 1023 to 8191
+// tokens, 8 heads of 128: 36 pairs 181 us in tiles of 64, 132 in tiles of 16; 64
+// pairs 184 and 202; 72 pairs 337 and 247; 8 prompts of 2000 rows 2.09 and 2.25 ms;
+// fp32, 32 and 8: 231 and 209, 304 and 359, 443 and 402, 3.58 and 4.09 ms).  A single
+// row group has two pages in work; or, heads of 128 and many units, one page and
+// more blocks, which hide the ends of units better (256 sequences of 512 to 2048
+// tokens, 2048 units: 122 us against 118; of 64 to 512: 75 against 64; one of 130,001,
+// 8 units: 54.0 against 55.8; heads of 64, 656 units: 31.7 against 40.6; where units
+// are twice as long, 64 sequences of 1000 to 4001 and 16 heads, 109 against 113).
+// That choice looks at the whole batch, so it is made only where the workspace lets
+// results depend on it.  The tile follows the call's largest row count: a prompt of
+// 2000 rows beside 255 single tokens takes 694 us, the two in calls of their own 300
+// and 117.
 constexpr int64_t KV_MANY = 600;
 template <typename T, int HD>
 cudaError_t attn_rows(const KvView& c, const KvAttnArgs& a, cudaStream_t s, int64_t* launches) {
