@@ -1031,3 +1031,42 @@ def test_outputs_beside_the_queries_are_taken(n):
         if want is None:
             want = o.clone(), lse
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_a_nan_among_zero_values_reaches_the_rows_that_see_it(rows, dtype):
+    """values that count as zero beside their neighbours', one of them NaN: its dim is NaN, the others are the formula's"""
+    st = Setup([256, 256], 1, 128, seed=52)
+    x = st.rows(512, "fp32", spread=0.0)
+    x[64:128, 1] = 0                                       # sequence 0: its second page, which every row sees whole
+    x[70, 1, 5] = math.nan
+    x[256 + 192:, 1] = 0                                   # sequence 1: its last page, which holds the newest rows
+    x[256 + 216, 1, 9] = math.inf
+    x[256:256 + 192, 1] *= 2.0 ** 40
+    st.append([256, 256], "fp32", x)
+    torch = st.torch
+    q = torch.from_numpy(st.rng.standard_normal((2 * rows, 4, 128)).astype(np.float32)).cuda()
+    q = q.bfloat16() if dtype == "bf16" else q
+    out, lse = st.kv.kv_attention(st.cache, st.dtable, st.i32([256, 256]), q, 256, row_off=st.off([rows, rows]), max_rows=rows)
+    assert torch.isfinite(lse).all()
+    nan = torch.isnan(out)
+    sees = torch.zeros_like(nan)
+    sees[:rows, :, 5] = True
+    sees[[rows + i for i in range(rows) if 256 - rows + i >= 216], :, 9] = True
+    assert torch.equal(nan, sees)
+    for y in "kv":
+        st.model.b[y] = np.where((st.model.b[y] & 0x7f) == 0x7f, 0, st.model.b[y])
+    _compare_dims(st, [rows, rows], q, torch.where(nan, torch.zeros_like(out), out) + _model_dims(st, rows, q, sees), lse, dtype)
+
+
+def _model_dims(st, rows, q, where):
+    """the model's results at `where`, 0 elsewhere"""
+    torch = st.torch
+    got = np.zeros(tuple(q.shape))
+    for s in range(len(st.len)):
+        k, v = (st.model.values(x, st.table[s], st.len[s]) for x in "kv")
+        got[s * rows:(s + 1) * rows] = M.attention(q[s * rows:(s + 1) * rows].double().cpu().numpy(), k, v, st.len[s] - rows,
+                                                   1 / math.sqrt(st.hd))[0]
+    return torch.where(where, torch.from_numpy(got).cuda(), torch.zeros(q.shape, device="cuda", dtype=torch.float64)).to(q.dtype)
