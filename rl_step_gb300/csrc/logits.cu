@@ -1,0 +1,807 @@
+// Log-probabilities of given tokens with entropy, log-sum-exp and alternatives,
+// and their gradient in the logits (include/mlora_logits.h).
+//
+// What bounds both: bytes.  The forward reads each logit once, the gradient
+// reads and writes each once.
+//
+// Forward.  A team of threads (a warp for small vocabularies, a block, or a cluster
+// of blocks where the rows are few) takes a row.  In base 2, with c = scale log2 e,
+// each thread keeps the maximum m of its x c and
+//     s = sum 2^(x c - m),   t = sum 2^(x c - m) (x c - m),
+// corrected when m rises, a group of 16 logits at a time; joined over the team
+//     lse = (m + log2 s) ln 2,   entropy = (log2 s - t / s) ln 2.
+// m is the maximum itself, so the largest term of t is 0 and the entropy of a sure
+// row does not come from a difference of large numbers.
+// Alternatives without a second pass: a thread leaves each group's largest value
+// in shared memory.  The `top` largest groups -- of equal ones the first -- hold all
+// alternatives, as a group is 16 ids in a row; they are found from 64-bit keys
+// (value, complement of the id), whose order is the order of the results, and only
+// their 32 or 64 bytes are read again.
+#include <cfloat>
+#include <cooperative_groups.h>
+
+#include "kv_common.cuh"
+#include "logits.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace mlk {
+
+namespace {
+
+constexpr int G = 16;                         // logits of a group
+constexpr int BT = 256;                       // threads of a block
+constexpr int MAX_TOP = MLORA_LOGITS_MAX_TOP;
+constexpr int LIST = 576;                     // entries of a team's list: MAX_TOP groups of 16 and at most 30 logits beside them
+constexpr float LOWEST = -1e30f;              // below it a logit counts as -infinity in the quick pass
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+typedef unsigned long long u64;
+
+// ---- elementary operations ---------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+// two fp32 operations at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<u64&>(d))
+        : "l"(reinterpret_cast<u64&>(a)), "l"(reinterpret_cast<u64&>(b)), "l"(reinterpret_cast<u64&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<u64&>(d))
+        : "l"(reinterpret_cast<u64&>(a)), "l"(reinterpret_cast<u64&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<u64&>(d))
+        : "l"(reinterpret_cast<u64&>(a)), "l"(reinterpret_cast<u64&>(b)));
+    return d;
+}
+// a number in the order of the values (-0 as 0); no value maps to 0
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ u64 key64(uint32_t key, uint32_t id) { return (u64)key << 32 | (uint32_t)~id; }
+__device__ __forceinline__ uint32_t id_of(u64 key) { return ~(uint32_t)key; }
+
+// 32 bytes, for the last time or not
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// A group's 16 logits as they are loaded.
+template <typename T> struct Group;
+template <> struct Group<bf16> {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const bf16* p) { load32(p, w); }
+    __device__ __forceinline__ float max() const {
+        uint32_t m = max_nan2(max_nan2(max_nan2(w[0], w[1]), max_nan2(w[2], w[3])),
+                              max_nan2(max_nan2(w[4], w[5]), max_nan2(w[6], w[7])));
+        const float2 f = bf16_pair(m);
+        return max_nan(f.x, f.y);
+    }
+    // pair i, not below LOWEST (its nearest bf16 value)
+    __device__ __forceinline__ float2 clamped(int i) const { return bf16_pair(max_nan2(w[i], 0xf149f149u)); }
+};
+template <> struct Group<float> {
+    uint32_t w[16];
+    __device__ __forceinline__ void load(const float* p) {
+        load32(p, reinterpret_cast<uint32_t (&)[8]>(w[0]));
+        load32(p + 8, reinterpret_cast<uint32_t (&)[8]>(w[8]));
+    }
+    __device__ __forceinline__ float max() const {
+        float m = max_nan(__uint_as_float(w[0]), __uint_as_float(w[1]));
+#pragma unroll
+        for (int i = 2; i < 16; ++i) m = max_nan(m, __uint_as_float(w[i]));
+        return m;
+    }
+    __device__ __forceinline__ float2 clamped(int i) const {
+        return make_float2(max_nan(__uint_as_float(w[2 * i]), LOWEST), max_nan(__uint_as_float(w[2 * i + 1]), LOWEST));
+    }
+};
+
+// m, s, t of some of a row's logits (above); m = -FLT_MAX where there are none
+struct Part {
+    float m, s, t;
+};
+__device__ __forceinline__ Part join(const Part& a, const Part& b) {
+    const float m = max_nan(a.m, b.m);
+    const float da = a.m - m, db = b.m - m, fa = ex2(da), fb = ex2(db);
+    // no terms, and a distance that need not be finite
+    const float ta = a.s == 0.f ? 0.f : fmaf(a.s, da, a.t) * fa, tb = b.s == 0.f ? 0.f : fmaf(b.s, db, b.t) * fb;
+    // (fa, fb are 0 beyond 2^-126 of the other, and their t with them)
+    return Part{m, fmaf(a.s, fa, b.s * fb), (fa == 0.f ? 0.f : ta) + (fb == 0.f ? 0.f : tb)};
+}
+
+// What a team shares.
+struct TeamShared {
+    u64 list[LIST];
+    u64 pick[MAX_TOP];
+    Part part[BT / 32];
+    Part all;
+    u64 tau;
+    int n;
+};
+
+template <int NT>
+__device__ __forceinline__ void team_sync() {
+    if (NT == 32) __syncwarp();
+    else __syncthreads();
+}
+
+// over the team; every thread returns it, in one fixed order
+template <int NT>
+__device__ __forceinline__ Part team_join(Part p, TeamShared& sh, int tid) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        Part q;
+        q.m = __shfl_xor_sync(0xffffffffu, p.m, o);
+        q.s = __shfl_xor_sync(0xffffffffu, p.s, o);
+        q.t = __shfl_xor_sync(0xffffffffu, p.t, o);
+        // the lower lane's part first on both sides, so that both form the same number
+        p = tid & o ? join(q, p) : join(p, q);
+    }
+    if (NT == 32) return p;
+    __syncthreads();
+    if ((tid & 31) == 0) sh.part[tid >> 5] = p;
+    __syncthreads();
+    p = sh.part[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) p = join(p, sh.part[w]);
+    return p;
+}
+
+// A block's share of a row: groups of 16 that begin at 32 bytes, and the logits
+// before and behind them, which the cluster's first block takes one by one.
+template <typename T>
+struct Share {
+    const T* row;
+    const T* first;                          // group 0 of the share
+    int id0;                                 // its first id
+    int groups;
+    int head, tail0, edges;                  // ids [0, head) and [tail0, V); edges = both
+    __device__ __forceinline__ int edge_id(int i) const { return i < head ? i : tail0 + i - head; }
+};
+template <typename T>
+__device__ __forceinline__ Share<T> share_of(const T* row, int V, int rank, int blocks) {
+    Share<T> s;
+    s.row = row;
+    const int off = (int)(reinterpret_cast<uintptr_t>(row) & 31) / (int)sizeof(T);
+    s.head = off ? 32 / (int)sizeof(T) - off : 0;
+    if (s.head > V) s.head = V;
+    const int all = (V - s.head) / G;
+    s.tail0 = s.head + all * G;
+    s.edges = rank == 0 ? s.head + V - s.tail0 : 0;
+    const int per = (all + blocks - 1) / blocks, a = min(rank * per, all), b = min(a + per, all);
+    s.groups = b - a;
+    s.id0 = s.head + a * G;
+    s.first = row + s.id0;
+    return s;
+}
+
+// The k largest of the n keys of list into out, in falling order (n may be below
+// k); the keys are distinct.
+template <int NT>
+__device__ __forceinline__ void rank_keys(const u64* list, int n, int k, u64* out, int tid) {
+    for (int i = tid; i < n; i += NT) {
+        const u64 mine = list[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += list[j] > mine;
+        if (rank < k) out[rank] = mine;
+    }
+}
+
+// The share's k largest logits in sh.pick as (value, id) keys in falling order, 0
+// where there are none.  gmax: the groups' keys; mine: the largest (key, group) of
+// this thread's.
+template <typename T, int NT>
+__device__ void top_of_share(const Share<T>& r, const uint32_t* gmax, u64 mine, int k, TeamShared& sh, int tid) {
+    constexpr int QUAD = NT == 32 ? 1 : NT / 64;       // threads of a first-round key: 32 or 64 keys, at least k
+    if (tid == 0) { sh.tau = 1; sh.n = 0; }
+    if (QUAD > 1) {
+#pragma unroll
+        for (int o = 1; o < QUAD; o <<= 1) {
+            const u64 q = __shfl_xor_sync(0xffffffffu, mine, o);
+            mine = q > mine ? q : mine;
+        }
+    }
+    if (tid % QUAD == 0) sh.list[tid / QUAD] = mine;
+    team_sync<NT>();
+    // the k-th largest of these keys: at least k groups are not below it
+    if (tid < NT / QUAD) {
+        const u64 key = sh.list[tid];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < NT / QUAD; ++j) rank += sh.list[j] > key;
+        if (rank == k - 1 && key) sh.tau = key;
+    }
+    team_sync<NT>();
+    u64 tau = sh.tau;
+    for (int g = tid; g < r.groups; g += NT) {
+        const u64 key = key64(gmax[g], g);
+        if (key >= tau) {
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < LIST) sh.list[at] = key;
+        }
+    }
+    team_sync<NT>();
+    if (sh.n > LIST) {
+        // few threads hold many of the largest groups: the k-th largest key bit by bit
+        tau = 0;
+        for (int bit = 63; bit >= 0; --bit) {
+            const u64 want = tau | (u64)1 << bit;
+            team_sync<NT>();
+            if (tid == 0) sh.n = 0;
+            team_sync<NT>();
+            int c = 0;
+            for (int g = tid; g < r.groups; g += NT) c += key64(gmax[g], g) >= want;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if ((tid & 31) == 0) atomicAdd(&sh.n, c);
+            team_sync<NT>();
+            if (sh.n >= k) tau = want;
+        }
+        team_sync<NT>();
+        if (tid == 0) sh.n = 0;
+        team_sync<NT>();
+        for (int g = tid; g < r.groups; g += NT) {
+            const u64 key = key64(gmax[g], g);
+            if (key >= tau) sh.list[atomicAdd(&sh.n, 1)] = key;
+        }
+        team_sync<NT>();
+    }
+    // the k largest groups
+    const int ng = sh.n, kg = ng < k ? ng : k;
+    rank_keys<NT>(sh.list, ng, k, sh.pick, tid);
+    team_sync<NT>();
+    const uint32_t low = kg == k ? (uint32_t)(sh.pick[k - 1] >> 32) : 0;
+    if (tid == 0) sh.n = 0;
+    team_sync<NT>();
+    // their logits that are not below the last one's largest, and the edges
+    for (int i = tid; i < kg * G + r.edges; i += NT) {
+        const int id = i < kg * G ? r.id0 + (int)id_of(sh.pick[i / G]) * G + i % G : r.edge_id(i - kg * G);
+        const float x = to_f(r.row[id]);
+        const uint32_t key = key_of(x);
+        if (x > -INFINITY && key >= low) {
+            sh.list[atomicAdd(&sh.n, 1)] = key64(key, id);
+        }
+    }
+    team_sync<NT>();
+    const int n = sh.n;
+    for (int i = tid; i < k; i += NT) sh.pick[i] = 0;
+    team_sync<NT>();
+    rank_keys<NT>(sh.list, n, k, sh.pick, tid);
+    team_sync<NT>();
+}
+
+// A row that the quick pass cannot take: NaN, an infinite maximum, or one so large
+// that a product with c is off by a power of two.  *kind: 1 NaN or +infinity, 2 no
+// finite logit; *top: the maximum.
+template <typename T, int NT, bool CLUSTER>
+__device__ __noinline__ Part careful(const Share<T>& r, float c, TeamShared& sh, int tid, int* kind, float* top) {
+    float m = -INFINITY;
+    auto each = [&](auto&& f) {
+        for (int i = tid; i < r.groups * G; i += NT) f(to_f(r.first[i]));
+        for (int i = tid; i < r.edges; i += NT) f(to_f(r.row[r.edge_id(i)]));
+    };
+    each([&](float x) { m = max_nan(m, x); });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    team_sync<NT>();
+    if ((tid & 31) == 0) sh.part[tid >> 5].m = m;
+    team_sync<NT>();
+    m = sh.part[0].m;
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) m = max_nan(m, sh.part[w].m);
+    team_sync<NT>();
+    if (CLUSTER) {
+        cg::cluster_group cl = cg::this_cluster();
+        if (tid == 0) sh.all.m = m;
+        cl.sync();
+        float all = -INFINITY;
+        for (unsigned b = 0; b < cl.num_blocks(); ++b) all = max_nan(all, cl.map_shared_rank(&sh, b)->all.m);
+        cl.sync();
+        m = all;
+    }
+    *kind = !(m <= FLT_MAX) ? 1 : m == -INFINITY ? 2 : 0;
+    *top = m;
+    Part p{0.f, 0.f, 0.f};                   // relative to the maximum, whose product with c may leave fp32
+    if (*kind) return p;
+    each([&](float x) {
+        // distances that leave fp32 or its exponents count as none
+        const float d = fmaxf((x - m) * c, -200.f), e = ex2(d);
+        p.s += e;
+        p.t = fmaf(e, d, p.t);
+    });
+    return team_join<NT>(p, sh, tid);
+}
+
+// Rows of at most this many logits go to a warp each.  1,000 logits: see launch.
+constexpr int WARP_V = 4096;
+
+template <typename T, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(BT, 4) token_logprobs_kernel(const __grid_constant__ LogitsView v,
+                                                               const __grid_constant__ mlora_token_stats out, int gcap) {
+    extern __shared__ uint32_t gmax_all[];
+    __shared__ TeamShared shared[BT / NT];
+    const int tid = threadIdx.x % NT, team = threadIdx.x / NT;
+    TeamShared& sh = shared[team];
+    uint32_t* gmax = gmax_all + team * gcap;
+    int rank = 0, blocks = 1;
+    if (CLUSTER) {
+        rank = (int)cg::this_cluster().block_rank();
+        blocks = (int)cg::this_cluster().num_blocks();
+    }
+    const int64_t row = CLUSTER ? blockIdx.x / blocks : (int64_t)blockIdx.x * (BT / NT) + team;
+    if (row >= v.n_rows) return;             // a whole team (a cluster's row exists)
+    int64_t o = row;
+    int y = v.targets ? v.targets[row] : -1;
+    if (v.out_row) {
+        if (row + v.row0 >= (int64_t)v.row_tiles[0] * TILE_M) return;
+        o = v.out_row[row];
+        if (o < 0 || y < 0) return;
+    } else if (y < -1 || y >= v.V) {
+        if (rank == 0 && tid == 0) raise_status(v.status, ST_RANGE);
+        y = -1;
+    }
+    const float c = v.scale * LOG2E;
+    const T* x = static_cast<const T*>(v.x) + row * v.ld;
+    const Share<T> r = share_of(x, v.V, rank, blocks);
+    const int k = v.top;
+
+    // the quick pass
+    constexpr int UN = sizeof(T) == 2 ? 4 : 2;      // groups in flight: 128 bytes a thread
+    Part p{-FLT_MAX, 0.f, 0.f};
+    float2 s2 = make_float2(0.f, 0.f), t2 = s2;
+    u64 best = 0;
+    const float2 cc = make_float2(c, c);
+    for (int g0 = tid; g0 < r.groups; g0 += UN * NT) {
+        Group<T> q[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (g0 + u * NT < r.groups) q[u].load(r.first + (int64_t)(g0 + u * NT) * G);
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int g = g0 + u * NT;
+            if (g >= r.groups) break;
+            const float gm = q[u].max();
+            if (k) {
+                const uint32_t key = key_of(gm);
+                gmax[g] = key;
+                const u64 key2 = key64(key, g);
+                best = key2 > best ? key2 : best;
+            }
+            const float m = max_nan(p.m, max_nan(gm, LOWEST) * c);
+            const float d = p.m - m, f = ex2(d);
+            p.m = m;
+            // the group's sums apart: 8 and V / (16 threads) additions in a row, not their product
+            const float2 mm = make_float2(-m, -m);
+            float2 sg = make_float2(0.f, 0.f), tg = sg;
+#pragma unroll
+            for (int i = 0; i < G / 2; ++i) {
+                const float2 a = fma2(q[u].clamped(i), cc, mm);
+                const float2 e = make_float2(ex2(a.x), ex2(a.y));
+                sg = add2(sg, e);
+                tg = fma2(e, a, tg);
+            }
+            // (before the first group d may be -infinity, and s and t are 0)
+            const float ds = fmaxf(d, -1e30f);
+            const float2 ff = make_float2(f, f);
+            t2 = fma2(fma2(s2, make_float2(ds, ds), t2), ff, tg);
+            s2 = fma2(s2, ff, sg);
+        }
+    }
+    p.s = s2.x + s2.y;
+    p.t = t2.x + t2.y;
+    for (int i = tid; i < r.edges; i += NT) {
+        const float xv = max_nan(to_f(x[r.edge_id(i)]), LOWEST);
+        // what the rounding of its product leaves: up to 2^-24 of it, as in every group
+        const float m = __fmul_rn(xv, c), left = fmaf(xv, c, -m), e = ex2(left);
+        p = join(p, Part{m, e, e * left});
+    }
+    p = team_join<NT>(p, sh, tid);
+    auto over_cluster = [&](Part q) {
+        if (!CLUSTER) return q;
+        cg::cluster_group cl = cg::this_cluster();
+        if (tid == 0) sh.all = q;
+        cl.sync();
+        q = cl.map_shared_rank(&sh, 0)->all;
+        for (int b = 1; b < blocks; ++b) q = join(q, cl.map_shared_rank(&sh, b)->all);
+        cl.sync();
+        return q;
+    };
+    p = over_cluster(p);
+    int kind = 0;
+    float top = 0.f;
+    const bool large = !(fabsf(p.m) < 1e6f && p.s <= FLT_MAX);
+    if (large) {
+        p = careful<T, NT, CLUSTER>(r, c, sh, tid, &kind, &top);
+        if (!kind) p = over_cluster(p);
+    }
+    const float ls = log2f(p.s);
+    auto logprob = [&](float xv) {
+        if (large) return fmaf(xv - top, v.scale, -ls * LN2);
+        if (xv < LOWEST) return xv * v.scale;            // (its product with c may leave fp32)
+        return (fmaf(xv, c, -p.m) - ls) * LN2;           // the product is taken from m before it is rounded, as in the sums
+    };
+    const float nan = __int_as_float(0x7fc00000);
+    if (k && !kind) {
+        top_of_share<T, NT>(r, gmax, best, k, sh, tid);
+        if (CLUSTER) {
+            cg::cluster_group cl = cg::this_cluster();
+            cl.sync();
+            if (rank == 0) {
+                for (int i = tid; i < blocks * k; i += NT) sh.list[i] = cl.map_shared_rank(&sh, i / k)->pick[i % k];
+            }
+            cl.sync();
+            if (rank == 0) {
+                // places without one are all 0 and hold no rank of their own
+                if (tid == 0) sh.n = 0;
+                u64 mine[(8 * MAX_TOP + NT - 1) / NT];
+                int n = 0;
+                for (int i = tid; i < blocks * k; i += NT) mine[n++] = sh.list[i];
+                __syncthreads();
+                for (int i = 0; i < n; ++i)
+                    if (mine[i]) sh.list[atomicAdd(&sh.n, 1)] = mine[i];
+                for (int i = tid; i < k; i += NT) sh.pick[i] = 0;
+                __syncthreads();
+                rank_keys<NT>(sh.list, sh.n, k, sh.pick, tid);
+                __syncthreads();
+            }
+        }
+    }
+    if (rank) return;
+    for (int i = tid; i < k; i += NT) {
+        const u64 key = kind ? 0 : sh.pick[i];
+        if (out.top_ids) out.top_ids[o * k + i] = key ? (int)id_of(key) : -1;
+        if (out.top_logprobs) {
+            out.top_logprobs[o * k + i] = kind == 1 ? nan : key ? logprob(of_key((uint32_t)(key >> 32))) : -INFINITY;
+        }
+    }
+    if (tid == 0) {
+        if (out.lse) out.lse[o] = kind == 1 ? nan : kind == 2 ? -INFINITY : large ? fmaf(top, v.scale, ls * LN2) : (p.m + ls) * LN2;
+        if (out.entropy) out.entropy[o] = kind == 1 ? nan : kind == 2 ? 0.f : fmaxf((ls - p.t / p.s) * LN2, 0.f);
+        if (out.logprobs)
+            out.logprobs[o] = y < 0 || kind == 1 ? nan : kind == 2 ? -INFINITY : logprob(to_f(x[y]));
+    }
+}
+
+// ----------------------------------------------------------------------------
+// gradient
+// ----------------------------------------------------------------------------
+struct GradView {
+    LogitsView v;
+    mlora_token_grads g;
+    void* out;
+    int64_t ldo;
+    int segment;                            // ids of a block
+};
+
+// dx = p (k0 + k1 a) + what the row's own ids add, a = log2 p.
+struct RowGrad {
+    float c, lse2, k0, k1;
+};
+__device__ __forceinline__ float grad_of(float x, const RowGrad& r) {
+    const float a = max_nan(fmaf(x, r.c, -r.lse2), -200.f);
+    return ex2(a) * fmaf(r.k1, a, r.k0);
+}
+
+// A block takes `segment` ids of one row; bound by reading and writing them.  The
+// ids that get more than the softmax's part (the target and the alternatives) are
+// read before the block writes anything, as dlogits may be the logits, and written
+// last, each by one thread with all that it gets.
+template <typename T>
+__global__ void __launch_bounds__(BT) token_grad_kernel(const __grid_constant__ GradView w) {
+    const LogitsView& v = w.v;
+    const int64_t row = blockIdx.x;
+    const int V = v.V, k = w.g.d_top ? v.top : 0, tid = threadIdx.x;
+    const int a = blockIdx.y * w.segment, b = min(V - a, w.segment) + a;
+    const T* x = static_cast<const T*>(v.x) + row * v.ld;
+    T* out = static_cast<T*>(w.out) + row * w.ldo;
+    __shared__ int s_id[MAX_TOP + 1];
+    __shared__ float s_d[MAX_TOP + 1];
+    __shared__ RowGrad s_r;
+    __shared__ int s_zero;
+    if (tid <= k) {
+        int id;
+        float d = 0.f;
+        if (tid == 0) {
+            id = v.targets && w.g.d_logprobs ? v.targets[row] : -1;
+        } else {
+            id = w.g.top_ids[row * v.top + tid - 1];
+        }
+        if (id < -1 || id >= V) {
+            if (blockIdx.y == 0) raise_status(v.status, ST_RANGE);
+            id = -1;
+        }
+        if (id >= 0) d = tid == 0 ? w.g.d_logprobs[row] : w.g.d_top[row * v.top + tid - 1];
+        s_id[tid] = id;
+        s_d[tid] = d;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const float de = w.g.d_entropy ? w.g.d_entropy[row] : 0.f, dl = w.g.d_lse ? w.g.d_lse[row] : 0.f;
+        const float lse = w.g.lse[row];
+        float sum = 0.f;
+        bool zero = de == 0.f && dl == 0.f;
+        for (int i = 0; i <= k; ++i) {
+            sum += s_d[i];
+            zero = zero && s_d[i] == 0.f;
+        }
+        RowGrad r;
+        r.c = v.scale * LOG2E;
+        r.lse2 = lse * LOG2E;
+        r.k0 = v.scale * (dl - sum);
+        r.k1 = 0.f;
+        if (de != 0.f) {
+            r.k0 = fmaf(-v.scale * de, w.g.entropy[row], r.k0);
+            r.k1 = -v.scale * de * LN2;
+        }
+        s_r = r;
+        s_zero = zero || lse == -INFINITY;
+    }
+    __syncthreads();
+    const RowGrad r = s_r;
+    const bool zero = s_zero;
+    // the ids with more, first
+    float own = 0.f;
+    int own_id = -1;
+    if (!zero && tid <= k && s_id[tid] >= a && s_id[tid] < b) {
+        const int id = s_id[tid];
+        bool first = true;
+        for (int i = 0; i < tid; ++i) first = first && s_id[i] != id;
+        if (first) {
+            float d = 0.f;
+            for (int i = tid; i <= k; ++i) d += s_id[i] == id ? s_d[i] : 0.f;
+            own_id = id;
+            own = fmaf(v.scale, d, grad_of(to_f(x[id]), r));
+        }
+    }
+    __syncthreads();
+    constexpr int PER = 32 / (int)sizeof(T);
+    const uintptr_t px = reinterpret_cast<uintptr_t>(x + a) & 31, po = reinterpret_cast<uintptr_t>(out + a) & 31;
+    int lead = b - a, vecs = 0;             // ids before the first whole 32 bytes, and 32 bytes
+    if (px == po) {
+        lead = min((int)((32 - px) % 32 / sizeof(T)), b - a);
+        vecs = (b - a - lead) / PER;
+    }
+    const T* xv = x + a + lead;
+    T* ov = out + a + lead;
+    const float2 cc = make_float2(r.c, r.c), ll = make_float2(-r.lse2, -r.lse2), k0 = make_float2(r.k0, r.k0),
+                 k1 = make_float2(r.k1, r.k1);
+    auto pair = [&](float2 q) {
+        float2 e = fma2(q, cc, ll);
+        e.x = max_nan(e.x, -200.f);
+        e.y = max_nan(e.y, -200.f);
+        return mul2(make_float2(ex2(e.x), ex2(e.y)), fma2(k1, e, k0));
+    };
+    constexpr int UN = 4;
+    for (int i0 = tid; i0 < vecs; i0 += UN * BT) {
+        uint32_t q[UN][8];
+        if (!zero) {
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
+                if (i0 + u * BT < vecs) load32(xv + (int64_t)(i0 + u * BT) * PER, q[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            if (i0 + u * BT >= vecs) break;
+            if (zero) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[u][j] = 0;
+            } else if (sizeof(T) == 2) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 d = pair(bf16_pair(q[u][j]));
+                    q[u][j] = pack_bf16x2(d.x, d.y);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 d = pair(make_float2(__uint_as_float(q[u][j]), __uint_as_float(q[u][j + 1])));
+                    q[u][j] = __float_as_uint(d.x);
+                    q[u][j + 1] = __float_as_uint(d.y);
+                }
+            }
+            store32(ov + (int64_t)(i0 + u * BT) * PER, q[u]);
+        }
+    }
+    const int done = lead + vecs * PER;
+    for (int i = tid; i < lead; i += BT) out[a + i] = zero ? from_f<T>(0.f) : from_f<T>(grad_of(to_f(x[a + i]), r));
+    for (int i = a + done + tid; i < b; i += BT) out[i] = zero ? from_f<T>(0.f) : from_f<T>(grad_of(to_f(x[i]), r));
+    __syncthreads();
+    if (own_id >= 0) out[own_id] = from_f<T>(own);
+}
+
+// ----------------------------------------------------------------------------
+// launches
+// ----------------------------------------------------------------------------
+constexpr int MAX_GROUPS = MLORA_LOGITS_MAX_VOCAB / G / 8;
+
+template <typename T, int NT, bool CLUSTER>
+cudaError_t launch_rows(const LogitsView& v, const mlora_token_stats& out, int blocks, cudaStream_t s) {
+    const int groups = v.V / G, gcap = v.top ? (groups + blocks - 1) / blocks : 0;
+    const size_t smem = sizeof(uint32_t) * gcap * (BT / NT);
+    auto* kern = token_logprobs_kernel<T, NT, CLUSTER>;
+    if (smem > 32 * 1024) {
+        // one size for all calls: threads that launch at once do not lower each other's
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_GROUPS * 4);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    const int64_t grid = CLUSTER ? v.n_rows * blocks : (v.n_rows + BT / NT - 1) / (BT / NT);
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(BT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = CLUSTER ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, v, out, gcap);
+}
+
+template <typename T>
+cudaError_t launch_t(const LogitsView& v, const mlora_token_stats& out, int num_sms, cudaStream_t s) {
+    if (v.V <= WARP_V) return launch_rows<T, 32, false>(v, out, 1, s);
+    // blocks of a cluster: four blocks an SM, shares of 4,096 logits at least, and groups that fit shared memory
+    int blocks = 1;
+    while (blocks < 8 && v.n_rows * blocks < 4 * (int64_t)num_sms && v.V / blocks >= 2 * WARP_V) blocks *= 2;
+    while (blocks < 8 && v.top && v.V / G / blocks > 12000) blocks *= 2;
+    return blocks == 1 ? launch_rows<T, BT, false>(v, out, 1, s) : launch_rows<T, BT, true>(v, out, blocks, s);
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogitsView& x, const mlora_token_stats& out, int num_sms, cudaStream_t s) {
+    return x.dtype == MLORA_BF16 ? launch_t<bf16>(x, out, num_sms, s) : launch_t<float>(x, out, num_sms, s);
+}
+
+int logits_check(float scale, int32_t top, int32_t vocab) {
+    if (vocab < 1 || vocab > MLORA_LOGITS_MAX_VOCAB)
+        return kv_fail(MLORA_E_ARG, "a vocabulary of %d, 1 .. %d are possible", vocab, MLORA_LOGITS_MAX_VOCAB);
+    if (top < 0 || top > MAX_TOP) return kv_fail(MLORA_E_ARG, "%d alternatives, at most %d", top, MAX_TOP);
+    if (!(scale >= 0x1p-20f && scale <= 0x1p20f)) return kv_fail(MLORA_E_ARG, "scale must lie in 2^-20 .. 2^20");
+    return MLORA_OK;
+}
+
+}  // namespace mlk
+
+// ----------------------------------------------------------------------------
+// C ABI
+// ----------------------------------------------------------------------------
+using namespace mlk;
+
+namespace {
+
+int view_check(const mlora_logits* x, LogitsView* v) {
+    if (!x) return kv_fail(MLORA_E_ARG, "NULL logits");
+    const int rc = logits_check(x->scale, x->top, x->vocab);
+    if (rc) return rc;
+    if (x->dtype != MLORA_BF16 && x->dtype != MLORA_FP32) return kv_fail(MLORA_E_ARG, "unknown dtype %d", x->dtype);
+    const int es = x->dtype == MLORA_BF16 ? 2 : 4;
+    // (a launch has a block or eight a row)
+    if (x->n_rows < 0 || x->n_rows > INT32_MAX / 8) return kv_fail(MLORA_E_ARG, "%lld rows", (long long)x->n_rows);
+    if (x->stride < x->vocab || x->stride > INT64_MAX / 4 / (x->n_rows + 1) / es)
+        return kv_fail(MLORA_E_ARG, "rows %lld elements apart", (long long)x->stride);
+    if (x->n_rows > 0 && !x->logits) return kv_fail(MLORA_E_ARG, "NULL logits");
+    if (reinterpret_cast<uintptr_t>(x->logits) % es) return kv_fail(MLORA_E_ARG, "logits are not aligned to their elements");
+    *v = LogitsView{};
+    v->x = x->logits;
+    v->ld = x->stride;
+    v->n_rows = x->n_rows;
+    v->targets = x->targets;
+    v->status = x->status;
+    v->scale = x->scale;
+    v->V = x->vocab;
+    v->dtype = x->dtype;
+    v->top = x->top;
+    return MLORA_OK;
+}
+
+int sm_count(int* n) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "device: %s", cudaGetErrorString(e));
+    return MLORA_OK;
+}
+
+// Whether rows of `width` bytes, lda and ldb bytes apart, share a byte.
+bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t n, int64_t width) {
+    const char *pa = static_cast<const char*>(a), *pb = static_cast<const char*>(b);
+    if (pa + (n - 1) * lda + width <= pb || pb + (n - 1) * ldb + width <= pa) return false;
+    if (lda != ldb) return true;             // (rows that interleave at two distances are refused too)
+    if (n == 1) return true;                 // the spans overlap
+    const int64_t d = ((pb - pa) % lda + lda) % lda;
+    return d < width || d + width > lda;
+}
+
+}  // namespace
+
+extern "C" int mlora_token_logprobs(const mlora_logits* x, const mlora_token_stats* out, void* stream) {
+    LogitsView v;
+    int rc = view_check(x, &v);
+    if (rc) return rc;
+    if (!out) return kv_fail(MLORA_E_ARG, "NULL results");
+    if (out->logprobs && !x->targets && x->n_rows > 0) return kv_fail(MLORA_E_ARG, "log-probabilities without targets");
+    mlora_token_stats o = *out;
+    if (v.top == 0) o.top_ids = nullptr, o.top_logprobs = nullptr;
+    if (!o.top_ids && !o.top_logprobs) v.top = 0;
+    if (v.n_rows == 0 || !(o.logprobs || o.entropy || o.lse || v.top)) return MLORA_OK;
+    int sms = 0;
+    if ((rc = sm_count(&sms))) return rc;
+    const cudaError_t e = launch_token_logprobs(v, o, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "log-probabilities launch: %s", cudaGetErrorString(e));
+    return MLORA_OK;
+}
+
+extern "C" int mlora_token_logprobs_backward(const mlora_logits* x, const mlora_token_grads* g, void* dlogits,
+                                             int64_t out_stride, void* stream) {
+    GradView w;
+    const int rc = view_check(x, &w.v);
+    if (rc) return rc;
+    if (!g) return kv_fail(MLORA_E_ARG, "NULL gradients");
+    const int64_t n = x->n_rows, es = x->dtype == MLORA_BF16 ? 2 : 4;
+    if (out_stride < x->vocab || out_stride > INT64_MAX / 4 / (n + 1) / es)
+        return kv_fail(MLORA_E_ARG, "output rows %lld elements apart", (long long)out_stride);
+    if (n == 0) return MLORA_OK;
+    if (!dlogits || reinterpret_cast<uintptr_t>(dlogits) % es)
+        return kv_fail(MLORA_E_ARG, "dlogits is NULL or not aligned to its elements");
+    if (!g->lse) return kv_fail(MLORA_E_ARG, "NULL lse");
+    if (g->d_entropy && !g->entropy) return kv_fail(MLORA_E_ARG, "d_entropy without the entropy");
+    if (g->d_logprobs && !x->targets) return kv_fail(MLORA_E_ARG, "d_logprobs without targets");
+    if (g->d_top && x->top > 0 && !g->top_ids) return kv_fail(MLORA_E_ARG, "d_top without the ids");
+    if (!(dlogits == x->logits && out_stride == x->stride) &&
+        rows_overlap(x->logits, x->stride * es, dlogits, out_stride * es, n, x->vocab * es))
+        return kv_fail(MLORA_E_ARG, "dlogits overlaps the logits and is not the logits themselves");
+    w.g = *g;
+    if (x->top == 0) w.g.d_top = nullptr;
+    w.out = dlogits;
+    w.ldo = out_stride;
+    // ids of a block: a whole number of rounds of 4 x 32 bytes a thread
+    w.segment = 4 * 32 / (int)es * BT;
+    const dim3 grid((unsigned)n, (unsigned)((x->vocab + w.segment - 1) / w.segment));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (x->dtype == MLORA_BF16) token_grad_kernel<bf16><<<grid, BT, 0, s>>>(w);
+    else token_grad_kernel<float><<<grid, BT, 0, s>>>(w);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "gradient launch: %s", cudaGetErrorString(e));
+    return MLORA_OK;
+}

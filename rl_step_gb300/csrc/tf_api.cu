@@ -5,7 +5,7 @@
 // (tf_kernels.cu), attention (attention_tc.cu), every projection on the
 // tcgen05 GEMM engine (gemm_tc.cu), rollouts over the paged caches (kv_cache.cu,
 // kv_attention.cu), and the LM head with its loss epilogue
-// (gemm_tc.cu, kernels_misc.cu).  The host validates, builds descriptors and
+// (gemm_tc.cu, kernels_misc.cu) or its logits' statistics (logits.cu).  The host validates, builds descriptors and
 // queues work.
 #include <stdarg.h>
 #include <stdio.h>
@@ -20,6 +20,7 @@
 #include "../../include/mlora_kv.h"
 #include "clip.cuh"
 #include "internal.h"
+#include "logits.cuh"
 #include "rollout.cuh"
 
 using namespace mlk;
@@ -414,7 +415,8 @@ extern "C" int mlora_tf_create(const mlora_tf_config* cfg, const mlora_tf_init* 
         TA(h->mt, (size_t)MP * h->part_ld);
         TA(h->zt, MP); TA(h->lse, MP); TA(h->gvec, MP); TA(h->tgt_pad, MP);
         h->nc_tiles = h->max_tiles < 128 ? h->max_tiles : 128;
-        TA(h->dz[0], (size_t)h->nc_tiles * TILE_M * h->Vpad);   // the kept-logits mode adds its buffers
+        // the kept-logits mode adds its buffers; row statistics hold a tile of fp32 logits here
+        TA(h->dz[0], (size_t)(h->nc_tiles > 2 ? h->nc_tiles : 2) * TILE_M * h->Vpad);
         TA(h->val_row, MP);
         TA(h->status, 1);
         TA(h->tile_counter, 1);
@@ -780,8 +782,48 @@ int cached_sample(mlora_tf_t* h, const TfCached& c, cudaStream_t s) {
     return MLORA_OK;
 }
 
+// What mlora_tf_forward_stats asks for.
+struct TfStats {
+    float scale;
+    int top;
+    mlora_token_stats out;
+};
+
+// The rows' statistics from h->xf: a chunk of rows' logits in fp32 where the
+// backward keeps its dz, which is zero between calls (its padding columns are an
+// operand of dz Wout) and is left so.
+int row_stats(mlora_tf_t* h, const TfStats& st, int mt_upper, cudaStream_t s) {
+    const int V = h->V, d = h->d;
+    float* z = reinterpret_cast<float*>(h->dz[0]);
+    const int chunk = h->nc_tiles >= 4 ? h->nc_tiles / 4 * 2 : 1;
+    for (int c0 = 0; c0 < mt_upper; c0 += chunk) {
+        const int cnt = mt_upper - c0 < chunk ? mt_upper - c0 : chunk;
+        GemmParams p = tf_dense(h, mt_upper, V, d);
+        p.mt_base = c0; p.mt_count = cnt;
+        p.A = opnd(h->xf, h->max_pad, d, d, 0);
+        p.B = opnd(h->Wout, V, d, d, 0);
+        p.ep.kind = EPI_LMFWD; p.ep.part = h->part; p.ep.zt = h->zt; p.ep.tgt = h->tgt_pad;
+        p.ep.part_ld = h->part_ld; p.ep.V = V; p.ep.Vpad = h->Vpad;
+        p.ep.mt = h->mt; p.ep.lm_bn = 256;
+        p.ep.out0 = z; p.ep.ld0 = h->Vpad; p.ep.out_row_shift = -(int64_t)c0 * TILE_M;
+        const int rc = tf_gemm(h, p, s, MLORA_TF_PROF_LM_FWD);
+        if (rc) return rc;
+        TfProf ps(h, s, MLORA_TF_PROF_LOSS);
+        LogitsView v{};
+        v.x = z; v.ld = h->Vpad; v.n_rows = (int64_t)cnt * TILE_M;
+        v.targets = h->tgt_pad + c0 * TILE_M;
+        v.out_row = h->rb.perm_pad + c0 * TILE_M;
+        v.row_tiles = h->rb.meta; v.row0 = (int64_t)c0 * TILE_M;
+        v.scale = st.scale; v.V = V; v.dtype = MLORA_FP32; v.top = st.top;
+        TF_CUDA(launch_token_logprobs(v, st.out, h->num_sms, s));
+        ++h->launches;
+    }
+    TF_CUDA(cudaMemsetAsync(z, 0, sizeof(float) * (size_t)(mt_upper < chunk ? mt_upper : chunk) * TILE_M * h->Vpad, s));
+    return MLORA_OK;
+}
+
 int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* logprobs_out, double* loss_out,
-            bool backward, cudaStream_t s, const TfCached* kc = nullptr) {
+            bool backward, cudaStream_t s, const TfCached* kc = nullptr, const TfStats* st = nullptr) {
     const int64_t N = b->n_tokens;
     const int n_ad = h->n_ad, L = h->L, d = h->d, f = h->f, V = h->V;
     const int64_t MP = h->max_pad;
@@ -875,6 +917,7 @@ int tf_step(mlora_tf_t* h, const mlora_tf_batch* b, const LossArgs& la, float* l
     if (kc && !kc->uniforms && !logprobs_out) return MLORA_OK;     // the caches are filled
     if ((rc = tf_norm_fwd(h, cur, h->gfinal, h->xf, h->rstdf, mp, s))) return rc;
     if (kc && kc->uniforms) return cached_sample(h, *kc, s);
+    if (st) return row_stats(h, *st, mt_upper, s);
 
     // LM head (Tinker API Implementation on TPUs, section 10.3-10.4): per-tile
     // log-sum-exp partials and the target logit over all rows; the backward
@@ -1070,6 +1113,32 @@ extern "C" int mlora_tf_forward(mlora_tf_t* h, const mlora_tf_batch* b, float* l
     if (!logprobs_out && b->n_tokens > 0) return tfail(MLORA_E_ARG, "NULL logprobs_out");
     LossArgs la{-1, nullptr, nullptr, nullptr, 0.f, nullptr};
     return tf_dispatch(h, b, la, logprobs_out, nullptr, false, stream);
+}
+
+extern "C" int mlora_tf_forward_stats(mlora_tf_t* h, const mlora_tf_batch* b, float scale, int32_t top,
+                                      const mlora_token_stats* out, void* stream) {
+    if (!h || !b || !out) return tfail(MLORA_E_ARG, "NULL handle, batch or results");
+    mlora_tf_batch bb = *b;
+    if (!bb.targets && !out->logprobs) bb.targets = bb.tokens;   // log-probabilities that nobody reads
+    int rc = tf_check_batch(h, &bb);
+    if (rc) return rc;
+    if ((rc = logits_check(scale, top, h->V))) return rc;
+    TfStats st{scale, top, *out};
+    if (top == 0) st.out.top_ids = nullptr, st.out.top_logprobs = nullptr;
+    if (!st.out.top_ids && !st.out.top_logprobs) st.top = 0;
+    const int64_t n = b->n_tokens;
+    // 0xff: NaN and -1, what stays where a token is flagged
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (n > 0) {
+        for (float* p : {st.out.logprobs, st.out.entropy, st.out.lse})
+            if (p) TF_CUDA(cudaMemsetAsync(p, 0xff, sizeof(float) * n, s));
+        if (st.out.top_ids) TF_CUDA(cudaMemsetAsync(st.out.top_ids, 0xff, sizeof(int32_t) * n * top, s));
+        if (st.out.top_logprobs) TF_CUDA(cudaMemsetAsync(st.out.top_logprobs, 0xff, sizeof(float) * n * top, s));
+    }
+    const LossArgs la{-1, nullptr, nullptr, nullptr, 0.f, nullptr};
+    if ((rc = tf_step(h, &bb, la, nullptr, nullptr, false, s, nullptr, &st))) return rc;
+    TF_CUDA(cudaGetLastError());
+    return MLORA_OK;
 }
 
 namespace {
