@@ -1,6 +1,6 @@
 /*
  * mlora_kv.h -- C ABI of libmlora.so: a paged key/value cache held in 8 bits,
- * the operators on it, and rollouts of the transformer-block model
+ * the operators on it, page tables made on the GPU, and rollouts of the transformer-block model
  * (mlora_tf.h) that call them.  The pages describe rollouts as a service
  * beside training (OpenTinker, "Multi-LoRA rollout") and fix no cache format;
  * everything below is this library's own.
@@ -145,6 +145,67 @@ typedef struct {
     float scale;           /* finite                                  */
 } mlora_kv_attn;
 int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const mlora_kv_attn* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Page tables on the GPU.  A pool says which pages are free, so that sequences
+ * grow and shrink by lengths that only the device knows (accepted drafted tokens,
+ * finished sequences), with no table made on the host.  One pool serves the caches
+ * of all layers, as they share their page ids.
+ *
+ * A row of the page table is a sequence's home: it owns the pages that it took.
+ * A page in a row that another row owns (a shared prefix, put there by the caller)
+ * is read as any other and never given back by this one.
+ *
+ * The free list is a stack, free_pages[0 .. *n_free).  A new pool of n pages has
+ * their ids there in any order, *n_free = n and owner[i] = -1.  What the device
+ * finds wrong never traps: it raises bits of *status, bit 0 for what is out of
+ * range, bit 2 where pages were too few.  Calls on one pool are serialised by the
+ * caller (one stream, or events).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int32_t* free_pages;   /* DEVICE [n_pages]                                             */
+    int32_t* n_free;       /* DEVICE [1]                                                   */
+    int32_t* owner;        /* DEVICE [n_pages]: the page table row that owns it, -1: none  */
+    int32_t* status;       /* DEVICE int32 (may be NULL)                                   */
+    int32_t n_pages;       /* >= 1                                                         */
+} mlora_kv_pool;
+
+/* Grow sequence s by n_new[s] >= 0 tokens: kv_len[s] += n_new[s], and the pages
+ * that positions kv_len[s] .. kv_len[s] + n_new[s] - 1 need beyond the first
+ * ceil(kv_len[s] / 64) come from the list's top, in the order of the sequences and
+ * of their pages, into page_table and owner.  Then, as the calls above take them:
+ *   row_off [n_seqs + 1]: the sequences' new rows, one sequence behind the other
+ *   positions, seqs, slots [n_rows] (any may be NULL): each new row's position, its
+ *     sequence, and its place page * 64 + position % 64 in a pool of pages; -1 for
+ *     the rows behind the last.
+ * A sequence is left as it is, with no rows, if its numbers are out of range
+ * (negative, or together more than max_pages * 64 or 2^31 - 1), if the new rows of the
+ * sequences up to it exceed n_rows (both bit 0), or if their pages exceed the free
+ * ones (bit 2).  Those sums count every sequence in range, so one that is too large
+ * refuses those behind it that need pages too.  Errors: E_ARG, E_CUDA. */
+typedef struct {
+    int32_t* page_table;       /* DEVICE [n_seqs x max_pages], updated       */
+    int32_t* kv_len;           /* DEVICE [n_seqs], updated                   */
+    const int32_t* n_new;      /* DEVICE [n_seqs]                            */
+    int32_t* row_off;          /* DEVICE [n_seqs + 1], written               */
+    int32_t* positions;        /* DEVICE, written                            */
+    int32_t* seqs;             /* DEVICE, written                            */
+    int64_t* slots;            /* DEVICE, written                            */
+    int64_t n_rows;            /* 0 .. 2^31 - 1                              */
+    int32_t n_seqs;            /* >= 0                                       */
+    int32_t max_pages;         /* >= 1                                       */
+} mlora_kv_growth;
+int mlora_kv_reserve(const mlora_kv_pool* p, const mlora_kv_growth* q, void* stream);
+
+/* Cut sequence s back to its first keep[s] tokens (keep NULL: to none): kv_len[s] =
+ * min(kv_len[s], keep[s]), the page table entries behind ceil(keep[s] / 64) become
+ * -1, and of those pages the ones that row s owns go back to the pool, last sequence
+ * and last page first: the call undoes a mlora_kv_reserve exactly, and a growth by
+ * as much takes the same pages again.  A sequence whose kv_len or keep is out of
+ * range stays as it is, a page id out of range is dropped (bit 0).  Errors: E_ARG,
+ * E_CUDA. */
+int mlora_kv_release(const mlora_kv_pool* p, int32_t* page_table, int32_t* kv_len, const int32_t* keep,
+                     int32_t n_seqs, int32_t max_pages, void* stream);
 
 /* ------------------------------------------------------------------------
  * Rollouts of the transformer-block model (OpenTinker, "Multi-LoRA rollout":

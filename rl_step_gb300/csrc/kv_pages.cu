@@ -1,0 +1,268 @@
+// Page tables of the paged cache built on the GPU (include/mlora_kv.h): sequences
+// grow by new tokens, whose pages come from a pool's free list, and are cut back,
+// which gives pages to it.
+//
+// What bounds it: latency.  A call moves kilobytes; the floor is a launch and a
+// chain of a few dependent reads.  So one block does a call's prefix sums and moves
+// its pages, and writes the rows' positions, sequences and slots as well where they
+// are few; more rows go to a second launch over all SMs.
+//
+// The free list is a stack.  Growing takes pages from its top in the order of the
+// sequences and of their pages; cutting back walks both the other way round, so
+// that it undoes a growth exactly, and a page's place does not depend on timing.
+#include "kv_common.cuh"
+
+namespace mlk {
+
+namespace {
+
+constexpr int ST_NO_PAGES = 4;
+constexpr int PT = 1024;                     // most threads, and sequences of a round
+
+struct PoolView {
+    int* free_pages;
+    int* n_free;
+    int* owner;
+    int* status;
+    int n_pages;
+};
+struct GrowView {
+    int* table;
+    int* kv_len;
+    const int* n_new;
+    int* row_off;
+    int* positions;
+    int* seqs;
+    int64_t* slots;
+    int64_t n_rows;
+    int64_t max_len;                         // what a table's row and kv_len hold
+    int n_seqs, max_pages;
+};
+
+__device__ __forceinline__ int pages_of(int64_t len) { return (int)((len + KV_PAGE - 1) / KV_PAGE); }
+
+struct Two {
+    int64_t a, b;
+};
+// inclusive prefix sums over the block; *total: of all threads
+__device__ __forceinline__ Two block_scan(Two v, Two* total) {
+    __shared__ Two part[PT / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o);
+        if (lane >= o) v.a += a, v.b += b;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    // every warp adds up the warps' sums
+    Two w = lane < warps ? part[lane] : Two{0, 0};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, w.a, o), b = __shfl_up_sync(0xffffffffu, w.b, o);
+        if (lane >= o) w.a += a, w.b += b;
+    }
+    total->a = __shfl_sync(0xffffffffu, w.a, 31);
+    total->b = __shfl_sync(0xffffffffu, w.b, 31);
+    const int64_t a = __shfl_sync(0xffffffffu, w.a, (warp + 31) & 31), b = __shfl_sync(0xffffffffu, w.b, (warp + 31) & 31);
+    if (warp > 0) v.a += a, v.b += b;
+    return v;
+}
+
+// the last of first[0 .. n) that is not above x; first[0] <= x
+template <typename I>
+__device__ __forceinline__ int find(const I* first, int n, int64_t x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Row r's position, sequence and slot from the lengths and tables as they are after the growth.
+__device__ __forceinline__ void write_row(const PoolView& p, const GrowView& g, int64_t r, int64_t total) {
+    int pos = -1, s = -1;
+    int64_t slot = -1;
+    if (r < total) {
+        s = find(g.row_off, g.n_seqs, r);
+        pos = g.kv_len[s] - (g.row_off[s + 1] - (int)r);
+        const int id = g.table[(int64_t)s * g.max_pages + pos / KV_PAGE];
+        if (id >= 0 && id < p.n_pages) slot = (int64_t)id * KV_PAGE + pos % KV_PAGE;
+        else raise_status(p.status, ST_RANGE);
+    }
+    if (g.positions) g.positions[r] = pos;
+    if (g.seqs) g.seqs[r] = s;
+    if (g.slots) g.slots[r] = slot;
+}
+
+__global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ PoolView p, const __grid_constant__ GrowView g,
+                                                     int rows_here) {
+    __shared__ int64_t s_first[PT];           // new pages before a sequence's own, of this round
+    __shared__ int s_have[PT];
+    const int tid = threadIdx.x, nt = blockDim.x;
+    int avail = *p.n_free;
+    const bool pool_ok = avail >= 0 && avail <= p.n_pages;
+    if (!pool_ok) {
+        if (tid == 0) raise_status(p.status, ST_RANGE);
+        avail = 0;
+    }
+    Two want{0, 0}, got{0, 0};                // pages and rows so far: asked for, and served
+    for (int base = 0; base < g.n_seqs; base += nt) {
+        const int s = base + tid;
+        const bool here = s < g.n_seqs;
+        const int len = here ? g.kv_len[s] : 0, add = here ? g.n_new[s] : 0;
+        const bool ok = here && len >= 0 && add >= 0 && (int64_t)len + add <= g.max_len;
+        const int have = ok ? pages_of(len) : 0;
+        const Two mine{ok ? pages_of((int64_t)len + add) - have : 0, ok ? add : 0};
+        Two all;
+        const Two upto = block_scan(mine, &all);
+        // A sequence is served if the pages and rows asked for up to it are there; what needs none always is.
+        const bool pages_ok = mine.a == 0 || want.a + upto.a <= avail, rows_ok = mine.b == 0 || want.b + upto.b <= g.n_rows;
+        const bool served = ok && pages_ok && rows_ok;
+        if (here && !served) raise_status(p.status, !ok || !rows_ok ? ST_RANGE : ST_NO_PAGES);
+        const Two take{served ? mine.a : 0, served ? mine.b : 0};
+        Two taken;
+        const Two before = block_scan(take, &taken);
+        if (here) {
+            g.row_off[s] = (int)(got.b + before.b - take.b);
+            if (served && add) g.kv_len[s] = len + add;
+        }
+        s_first[tid] = before.a - take.a;
+        s_have[tid] = have;
+        __syncthreads();
+        for (int64_t j = tid; j < taken.a; j += nt) {
+            // the last sequence that begins at or before page j: those behind it that take none begin later
+            const int q = find(s_first, nt, j);
+            const int id = p.free_pages[avail - 1 - (got.a + j)];
+            const bool good = id >= 0 && id < p.n_pages;
+            if (good) p.owner[id] = base + q;
+            else raise_status(p.status, ST_RANGE);
+            g.table[(int64_t)(base + q) * g.max_pages + s_have[q] + (j - s_first[q])] = good ? id : -1;
+        }
+        want.a += all.a, want.b += all.b;
+        got.a += taken.a, got.b += taken.b;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        g.row_off[g.n_seqs] = (int)got.b;
+        if (pool_ok) *p.n_free = (int)(avail - got.a);
+    }
+    if (!rows_here) return;
+    __syncthreads();
+    for (int64_t r = tid; r < g.n_rows; r += nt) write_row(p, g, r, got.b);
+}
+
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ PoolView p,
+                                                     const __grid_constant__ GrowView g) {
+    const int64_t total = g.row_off[g.n_seqs], step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < g.n_rows; r += step) write_row(p, g, r, total);
+}
+
+// Sequences and their pages from the last to the first; a page goes to the list if
+// the row of the table owns it.
+__global__ void __launch_bounds__(PT) release_kernel(const __grid_constant__ PoolView p, int* table, int* kv_len,
+                                                     const int* __restrict__ keep, int n_seqs, int max_pages) {
+    __shared__ int64_t s_first[PT];
+    __shared__ int s_end[PT];
+    const int tid = threadIdx.x, nt = blockDim.x;
+    int64_t top = *p.n_free;
+    if (top < 0 || top > p.n_pages) {
+        if (tid == 0) raise_status(p.status, ST_RANGE);
+        return;                               // (the whole block: all read the same number)
+    }
+    for (int base = 0; base < n_seqs; base += nt) {
+        const int s = n_seqs - 1 - (base + tid);
+        const bool here = s >= 0;
+        const int len = here ? kv_len[s] : 0, left = here && keep ? keep[s] : 0;
+        const bool ok = here && len >= 0 && len <= (int64_t)max_pages * KV_PAGE && left >= 0;
+        if (here && !ok) raise_status(p.status, ST_RANGE);
+        const bool cut = ok && left < len;
+        const Two mine{cut ? pages_of(len) - pages_of(left) : 0, 0};
+        Two all;
+        const Two upto = block_scan(mine, &all);
+        if (cut) kv_len[s] = left;
+        s_first[tid] = upto.a - mine.a;
+        s_end[tid] = pages_of(len);
+        __syncthreads();
+        for (int64_t j0 = 0; j0 < all.a; j0 += nt) {
+            const int64_t j = j0 + tid;
+            int id = -1;
+            bool mine_too = false;
+            if (j < all.a) {
+                const int q = find(s_first, nt, j), seq = n_seqs - 1 - (base + q);
+                int* at = table + (int64_t)seq * max_pages + s_end[q] - 1 - (j - s_first[q]);
+                id = *at;
+                *at = -1;
+                if (id < 0 || id >= p.n_pages) raise_status(p.status, ST_RANGE);
+                else mine_too = atomicCAS(p.owner + id, seq, -1) == seq;
+            }
+            Two n;
+            const Two place = block_scan(Two{mine_too, 0}, &n);
+            if (mine_too) {
+                const int64_t to = top + place.a - 1;
+                if (to < p.n_pages) p.free_pages[to] = id;
+                else raise_status(p.status, ST_RANGE);
+            }
+            top = top + n.a < p.n_pages ? top + n.a : p.n_pages;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) *p.n_free = (int)top;
+}
+
+int pool_check(const mlora_kv_pool* p, const int32_t* table, const int32_t* kv_len, int n_seqs, int max_pages, PoolView* v) {
+    if (!p) return kv_fail(MLORA_E_ARG, "NULL pool");
+    if (p->n_pages < 1) return kv_fail(MLORA_E_ARG, "a pool of %d pages", p->n_pages);
+    if (!p->free_pages || !p->n_free || !p->owner) return kv_fail(MLORA_E_ARG, "NULL pool arrays");
+    if (n_seqs < 0 || n_seqs > INT32_MAX - 2 * PT) return kv_fail(MLORA_E_ARG, "%d sequences", n_seqs);
+    if (max_pages < 1) return kv_fail(MLORA_E_ARG, "page tables of %d pages", max_pages);
+    if (n_seqs > 0 && (!table || !kv_len)) return kv_fail(MLORA_E_ARG, "NULL page table or lengths");
+    *v = PoolView{p->free_pages, p->n_free, p->owner, p->status, p->n_pages};
+    return MLORA_OK;
+}
+
+// threads of the one block
+int block_for(int64_t n) { return n <= 256 ? 256 : PT; }
+
+}  // namespace
+
+}  // namespace mlk
+
+using namespace mlk;
+
+extern "C" int mlora_kv_reserve(const mlora_kv_pool* p, const mlora_kv_growth* q, void* stream) {
+    if (!q) return kv_fail(MLORA_E_ARG, "NULL growth");
+    PoolView v;
+    const int rc = pool_check(p, q->page_table, q->kv_len, q->n_seqs, q->max_pages, &v);
+    if (rc) return rc;
+    if (q->n_rows < 0 || q->n_rows > INT32_MAX) return kv_fail(MLORA_E_ARG, "%lld rows", (long long)q->n_rows);
+    if (!q->row_off || (q->n_seqs > 0 && !q->n_new)) return kv_fail(MLORA_E_ARG, "NULL numbers of new rows or row offsets");
+    const GrowView g{q->page_table, q->kv_len, q->n_new, q->row_off, q->positions, q->seqs, q->slots, q->n_rows,
+                     q->max_pages < INT32_MAX / KV_PAGE ? (int64_t)q->max_pages * KV_PAGE : INT32_MAX, q->n_seqs, q->max_pages};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool rows = q->n_rows > 0 && (q->positions || q->seqs || q->slots);
+    const bool apart = rows && q->n_rows > 2 * PT;
+    reserve_kernel<<<1, block_for(q->n_seqs > q->n_rows ? q->n_seqs : apart ? 0 : q->n_rows), 0, s>>>(v, g, rows && !apart);
+    if (apart) {
+        const int64_t blocks = (q->n_rows + 255) / 256;
+        rows_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(v, g);
+    }
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "reserve launch: %s", cudaGetErrorString(e));
+    return MLORA_OK;
+}
+
+extern "C" int mlora_kv_release(const mlora_kv_pool* p, int32_t* page_table, int32_t* kv_len, const int32_t* keep,
+                                int32_t n_seqs, int32_t max_pages, void* stream) {
+    PoolView v;
+    const int rc = pool_check(p, page_table, kv_len, n_seqs, max_pages, &v);
+    if (rc) return rc;
+    if (n_seqs == 0) return MLORA_OK;
+    release_kernel<<<1, block_for(n_seqs), 0, reinterpret_cast<cudaStream_t>(stream)>>>(v, page_table, kv_len, keep, n_seqs,
+                                                                                      max_pages);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "release launch: %s", cudaGetErrorString(e));
+    return MLORA_OK;
+}

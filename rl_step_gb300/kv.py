@@ -9,6 +9,13 @@ library's CUDA kernels; PyTorch provides device memory and streams.
     k, v = kv_read(cache, page_table, kv_len, n_rows)                       # back as fp32 or bf16
     kv_check_status(cache)                                                  # 0, or -2 (E_RANGE)
 
+Page tables kept on the GPU, one pool for all layers' caches:
+
+    pool = PagePool.empty(n_pages)
+    rows = kv_reserve(pool, page_table, kv_len, n_new, n_rows)              # lengths grow; rows.row_off, .positions, ...
+    kv_release(pool, page_table, kv_len, keep)                              # cut back (keep None: to nothing)
+    kv_pool_check_status(pool)                                              # 0, -2 (E_RANGE) or -4 (too few pages)
+
 Rollouts of the transformer model over one cache per layer:
 
     tf_forward_cached(h, caches, prompt, None, adapter_ids, page_table, kv_len, max_len, row_off, max_rows)
@@ -23,6 +30,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from collections import namedtuple
 from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_void_p
 
 import torch
@@ -31,7 +39,8 @@ from . import _check, load_library
 from .transformer import _TfBatch
 
 __all__ = ["PAGE", "KvCache", "kv_workspace", "kv_append", "kv_read", "kv_attention", "kv_check_status",
-           "tf_forward_cached", "tf_sample_cached"]
+           "PagePool", "ReservedRows", "kv_reserve", "kv_release", "kv_pool_check_status", "tf_forward_cached",
+           "tf_sample_cached"]
 
 PAGE = 64
 WORKSPACE_BYTES = 32 << 20
@@ -53,6 +62,17 @@ class _KvAttn(ctypes.Structure):
                 ("dtype", c_int32), ("n_heads", c_int32), ("scale", c_float)]
 
 
+class _KvPool(ctypes.Structure):
+    _fields_ = [("free_pages", c_void_p), ("n_free", c_void_p), ("owner", c_void_p), ("status", c_void_p),
+                ("n_pages", c_int32)]
+
+
+class _KvGrowth(ctypes.Structure):
+    _fields_ = [("page_table", c_void_p), ("kv_len", c_void_p), ("n_new", c_void_p), ("row_off", c_void_p),
+                ("positions", c_void_p), ("seqs", c_void_p), ("slots", c_void_p), ("n_rows", c_int64),
+                ("n_seqs", c_int32), ("max_pages", c_int32)]
+
+
 class _TfContext(ctypes.Structure):
     _fields_ = [("caches", POINTER(_KvCache)), ("seqs", _KvSeqs), ("workspace", c_void_p),
                 ("workspace_bytes", c_int64), ("max_len", c_int64)]
@@ -63,6 +83,8 @@ _SIGNATURES = {
                                   c_int64, c_void_p]),
     "mlora_kv_read": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), c_int32, c_void_p, c_void_p, c_void_p]),
     "mlora_kv_attention": (c_int32, [POINTER(_KvCache), POINTER(_KvSeqs), POINTER(_KvAttn), c_void_p]),
+    "mlora_kv_reserve": (c_int32, [POINTER(_KvPool), POINTER(_KvGrowth), c_void_p]),
+    "mlora_kv_release": (c_int32, [POINTER(_KvPool), c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p]),
     "mlora_tf_forward_cached": (c_int32, [c_void_p, POINTER(_TfBatch), POINTER(_TfContext), c_void_p, c_void_p]),
     "mlora_tf_sample_cached": (c_int32, [c_void_p, POINTER(_TfBatch), POINTER(_TfContext), c_void_p, c_void_p,
                                          c_void_p, c_void_p]),
@@ -234,6 +256,78 @@ def kv_attention(cache: KvCache, page_table, kv_len, q, max_len: int, row_off=No
                 1.0 / math.sqrt(hd) if scale is None else scale)
     _check(_lib().mlora_kv_attention(cache._ref, byref(s), byref(a), _on(cache.index, stream)))
     return out, lse
+
+
+class PagePool:
+    """Which pages of the caches are free: int32 CUDA tensors free [n_pages] (a stack
+    of n_free[0] ids), n_free [1] and owner [n_pages], which the pool keeps alive.
+    The caches of all layers share one pool.  Calls on a pool have to follow one
+    another (one stream, or events between them)."""
+
+    def __init__(self, free, n_free, owner):
+        n = free.numel()
+        for t, shape in ((free, (n,)), (n_free, (1,)), (owner, (n,))):
+            if t.dtype is not _INT32 or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda or \
+                    t.device != free.device:
+                raise ValueError("a pool's tensors must be contiguous int32 CUDA tensors of a value a page, and one")
+        self.free, self.n_free, self.owner = free, n_free, owner
+        self.status = torch.zeros(1, dtype=torch.int32, device=free.device)
+        self.n_pages, self.device, self.index = n, free.device, free.get_device()
+        self._c = _KvPool(free.data_ptr(), n_free.data_ptr(), owner.data_ptr(), self.status.data_ptr(), n)
+        self._ref = byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, device="cuda") -> "PagePool":
+        """A pool whose pages are all free; the first ones are taken first."""
+        return cls(torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.full((1,), n_pages, dtype=torch.int32, device=device),
+                   torch.full((n_pages,), -1, dtype=torch.int32, device=device))
+
+
+ReservedRows = namedtuple("ReservedRows", ["row_off", "positions", "seqs", "slots"])
+
+
+def kv_reserve(pool: PagePool, page_table, kv_len, n_new, n_rows: int, stream=None) -> ReservedRows:
+    """Grow the sequences by n_new int32 [n_seqs] tokens: kv_len and page_table are
+    updated in place.  Returns int32 row_off [n_seqs + 1], positions and seqs
+    [n_rows] and int64 slots [n_rows] of the new rows (-1 behind the last); n_rows:
+    an upper bound of their number that the caller knows on the host."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seqs, max_pages]")
+    n, width = page_table.shape
+    i = pool.index
+    ids = (_ids("page_table", page_table, (n, width), i), _ids("kv_len", kv_len, (n,), i), _ids("n_new", n_new, (n,), i))
+    handle = _on(i, stream)
+    # one block for what comes out, the 8-byte slots first
+    m = max(int(n_rows), 0)
+    buf = _empty((4 * m + n + 1,), _INT32, pool.device, stream)
+    at = buf.data_ptr()
+    q = _KvGrowth(*ids, at + 16 * m, at + 8 * m, at + 12 * m, at, n_rows, n, width)
+    _check(_lib().mlora_kv_reserve(pool._ref, byref(q), handle))
+    return ReservedRows(buf[4 * m:], buf[2 * m:3 * m], buf[3 * m:4 * m], buf[:2 * m].view(torch.int64))
+
+
+def kv_release(pool: PagePool, page_table, kv_len, keep=None, stream=None) -> None:
+    """Cut the sequences back to keep int32 [n_seqs] tokens (None: to none): kv_len
+    and page_table are updated in place, the pages go back to the pool."""
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seqs, max_pages]")
+    n, width = page_table.shape
+    i = pool.index
+    _check(_lib().mlora_kv_release(pool._ref, _ids("page_table", page_table, (n, width), i),
+                                   _ids("kv_len", kv_len, (n,), i),
+                                   None if keep is None else _ids("keep", keep, (n,), i), n, width, _on(i, stream)))
+
+
+def kv_pool_check_status(pool: PagePool, stream=None) -> int:
+    """Synchronise, return and clear the pool's status: 0, -2 (E_RANGE) or -4 (pages
+    were too few), read and cleared in the order of `stream` (None: the current one)."""
+    stream = stream or torch.cuda.current_stream(pool.index)
+    with torch.cuda.stream(stream):
+        bad = int(pool.status.item())
+        if bad:
+            pool.status.zero_()
+    return -2 if bad & 1 else -4 if bad & 4 else 0
 
 
 def _context(h, caches, tokens, page_table, kv_len, max_len, row_off, max_rows, workspace, stream):
