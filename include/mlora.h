@@ -443,6 +443,44 @@ int64_t mlora_clip_grads_workspace(const mlora_grad_set* g);
 int mlora_clip_grads(const mlora_grad_set* g, float max_norm, float* norms_out, void* workspace,
                      int64_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Updates made orthogonal by Newton-Schulz products, as optimizers that bring all
+ * singular values of a matrix's update near 1 take it between the gradient (or its
+ * momentum) and the step (the pages name Adam alone; this definition is the
+ * library's).  For each matrix M, with x over its shorter side:
+ *     x = M / (|M| + eps),   |M| the Frobenius norm
+ *     steps times:  x <- a x + (b A + c A A) x,   A = x x^T
+ *     out = x, as M lies
+ * Sums are fp32, factors of products enter with 2^-21 of themselves.  Small
+ * singular values are multiplied by up to a^steps, and so are the rounding errors in
+ * their directions: with s the smallest singular value over |M| and five steps of the
+ * usual (3.4445, -4.7750, 2.0315), out is off by about 2^-20 + 2^-24 / s of its norm.
+ * A matrix of zeros stays zero.  One with an infinity or NaN becomes NaN throughout.
+ * Magnitudes whose squares leave fp32's range are taken relative to the largest.
+ * Results repeat bit for bit and do not depend on the other matrices of the set.
+ *   src, dst: HOST arrays of DEVICE pointers to contiguous row-major matrices of
+ *     `dtype`, aligned to their elements; dst NULL: in place.  A matrix and its
+ *     output are equal or do not overlap, and no output overlaps another matrix or
+ *     output of the set.  rows, cols: HOST; the shorter of the two is at most
+ *     MLORA_MAX_RANK; 0 is nothing to do.
+ * Queued on `stream`; no allocation on the device and no synchronisation, so the call
+ * can be captured into a CUDA graph.  Errors: E_ARG, E_CUDA, E_NOMEM (host memory). */
+#define MLORA_ORTHO_MAX_STEPS 12
+typedef struct {
+    const void* const* src;
+    void* const* dst;
+    const int64_t* rows;
+    const int64_t* cols;
+    int32_t n_matrices;
+    int32_t dtype;
+} mlora_matrix_set;
+typedef struct {
+    float a, b, c;
+    float eps;                 /* > 0                          */
+    int32_t steps;             /* 1 .. MLORA_ORTHO_MAX_STEPS   */
+} mlora_newton_schulz;
+int mlora_orthogonalize(const mlora_matrix_set* m, const mlora_newton_schulz* p, void* stream);
+
 /* Synchronise `stream`, then return and clear the device status word:
  * MLORA_OK, MLORA_E_RANGE or MLORA_E_TIMEOUT. */
 int mlora_check_status(mlora_t* h, void* stream);

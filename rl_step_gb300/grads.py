@@ -1,8 +1,11 @@
-"""Python binding of mlora_clip_grads (include/mlora.h): the gradient norm of
-each group of tensors, and clipping.  Argument marshalling only.
+"""Python binding of mlora_clip_grads and mlora_orthogonalize (include/mlora.h):
+the gradient norm of each group of tensors, and clipping; updates made orthogonal.
+Argument marshalling only.
 
     gs = GradSet(grads, groups)           # groups: an adapter id per tensor (None: one group)
     norms = clip_grads(gs, 1.0)           # in place; float32 [n_groups], device
+    ms = MatrixSet(updates, out=outs)     # LoRA factors' gradients or momenta, 2-D
+    orthogonalize(ms, steps=5)            # Newton-Schulz products
 """
 from __future__ import annotations
 
@@ -15,7 +18,7 @@ import torch
 from . import _check, load_library
 from .kv import _empty, _on
 
-__all__ = ["GradSet", "clip_grads"]
+__all__ = ["GradSet", "clip_grads", "MatrixSet", "orthogonalize"]
 
 
 class _GradSet(ctypes.Structure):
@@ -23,7 +26,17 @@ class _GradSet(ctypes.Structure):
                 ("groups", POINTER(c_int32)), ("n_tensors", c_int32), ("n_groups", c_int32), ("dtype", c_int32)]
 
 
+class _MatrixSet(ctypes.Structure):
+    _fields_ = [("src", POINTER(c_void_p)), ("dst", POINTER(c_void_p)), ("rows", POINTER(c_int64)),
+                ("cols", POINTER(c_int64)), ("n_matrices", c_int32), ("dtype", c_int32)]
+
+
+class _NewtonSchulz(ctypes.Structure):
+    _fields_ = [("a", c_float), ("b", c_float), ("c", c_float), ("eps", c_float), ("steps", c_int32)]
+
+
 _SIGNATURES = {
+    "mlora_orthogonalize": (c_int32, [POINTER(_MatrixSet), POINTER(_NewtonSchulz), c_void_p]),
     "mlora_clip_grads_workspace": (c_int64, [POINTER(_GradSet)]),
     "mlora_clip_grads": (c_int32, [POINTER(_GradSet), c_float, c_void_p, c_void_p, c_int64, c_void_p]),
 }
@@ -126,3 +139,45 @@ def clip_grads(gs: GradSet, max_norm: float, norms_out=None, stream=None):
     _check(_lib().mlora_clip_grads(gs._ref, max_norm, norms_out.data_ptr(), workspace.data_ptr(), gs._bytes,
                                    handle))
     return norms_out
+
+
+class MatrixSet:
+    """The matrices of repeated orthogonalize calls: contiguous 2-D CUDA tensors of
+    one dtype (float32 or bf16) whose shorter side is at most 64, and optional outputs
+    (None: in place).  Keeps the tensors alive; keep it where the same tensors are
+    taken step after step, as a GradSet."""
+
+    def __init__(self, mats: Sequence, out: Optional[Sequence] = None):
+        self.mats, self.out = list(mats), None if out is None else list(out)
+        n = len(self.mats)
+        if n == 0:
+            raise ValueError("no matrices")
+        dtype, self.device = self.mats[0].dtype, self.mats[0].device
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"dtype {dtype}: bfloat16 or float32 is needed")
+        if any(m.dim() != 2 for m in self.mats):
+            raise ValueError("matrices have two dimensions")
+        if self.out is not None and [tuple(o.shape) for o in self.out] != [tuple(m.shape) for m in self.mats]:
+            raise ValueError("out must have the matrices' shapes")
+        for t in self.mats + (self.out or []):
+            if t.dtype != dtype or t.device != self.device or not t.is_cuda or not t.is_contiguous():
+                raise ValueError("matrices must be contiguous CUDA tensors of one dtype on one device")
+        ptrs = [t.data_ptr() for t in self.mats]
+        outs = None if self.out is None else [t.data_ptr() for t in self.out]
+        _no_overlap(ptrs, outs or ptrs, [t.numel() for t in self.mats], self.mats[0].element_size())
+        shapes = [t.shape for t in self.mats]
+        self._arrays = ((c_void_p * n)(*ptrs), None if outs is None else (c_void_p * n)(*outs),
+                        (c_int64 * n)(*[s[0] for s in shapes]), (c_int64 * n)(*[s[1] for s in shapes]))
+        self._c = _MatrixSet(*self._arrays, n, 0 if dtype == torch.bfloat16 else 1)
+        self._ref = byref(self._c)
+        self.index = self.mats[0].get_device()
+
+
+def orthogonalize(ms: MatrixSet, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  stream=None):
+    """x <- m / (|m| + eps), then `steps` times x <- a x + (b A + c A A) x with A = x x^T
+    over the shorter side, for each matrix; returns the outputs (the matrices
+    themselves where the set has none).  Autograd sees nothing of it."""
+    a, b, c = coefficients
+    _check(_lib().mlora_orthogonalize(ms._ref, byref(_NewtonSchulz(a, b, c, eps, steps)), _on(ms.index, stream)))
+    return ms.mats if ms.out is None else ms.out
