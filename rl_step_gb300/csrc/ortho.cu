@@ -16,14 +16,15 @@
 // the long side: the second and third pass find it in L2, and no launch or
 // workspace is between them.  Sums meet in a fixed order: results repeat.
 //
-// The products run on mma.sync with tf32 operands, each fp32 factor as two of them
-// (x = hi + lo, hi of 11 bits; three products, at most 2^-20 of the terms off), straight
-// from registers: the same fragment of X serves as both operands of X X^T, and the
-// output fragment of P X serves as both of the next.  The tensor cores cut their sums off
-// (towards 0), so few products are chained, the small parts first, and their results
-// are added in fp32 (rounded to nearest): chained over the whole length a 64 x 700
-// matrix was off by 8e-6 of its norm where plain fp32 products are by 1e-6.  r is 4 to 64: a 128-row tcgen05
-// tile would hold 2 to 8 matrices and form their cross products for nothing.
+// The products run on mma.sync with fp16 operands and fp32 sums: each factor, scaled
+// by a power of two so that nothing leaves fp16 at either end, as two of them (x = hi +
+// lo, 2^-22 of itself; three products, the fourth is left out; an X that was bf16 needs
+// no lo).  Fragments of X come from a warp's own tiles in shared memory, filled ahead
+// with cp.async; the same fragment is both operands of X X^T, and the output fragment
+// of P X becomes both of the next without leaving its thread.  The tensor cores cut
+// their sums off (towards 0), so few products are chained, the small parts first, and
+// their results are added in fp32.  r is 4 to 64: a 128-row tcgen05 tile would hold 2 to
+// 8 matrices and form their cross products for nothing.
 #include <algorithm>
 #include <cfloat>
 #include <cooperative_groups.h>
@@ -61,13 +62,32 @@ struct OrthoTab {
 };
 
 // the nearest value of 11 bits (away from 0 between two); x is far below fp32's largest
+// the nearest value of 11 bits (away from 0 between two); x is far below fp32's largest
 __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
 
+// d += a b, 16 x 8 x 8 with tf32 operands
 __device__ __forceinline__ void mma8(float (&d)[4], const float (&a)[4], float b0, float b1) {
     asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
                    "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+// d += a b, 16 x 8 x 16 with pairs of fp16
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_of(float x, float y) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+    return h;
+}
+// x and y as fp16 and what that leaves
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = half2_of(x, y);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = half2_of(x - f.x, y - f.y);
 }
 
 // Four elements side by side as floats.
@@ -80,12 +100,33 @@ __device__ __forceinline__ void load4(const bf16* p, float (&v)[4]) {
     v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
     v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
 }
+// Two.
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 load2(const bf16* p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// 4 elements to shared memory, or zeros
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                 "n"(BYTES), "r"(there ? BYTES : 0)
+                 : "memory");
+}
+
+constexpr int STAGES = 2;                    // tiles of a warp
+constexpr int TC = 32;                       // columns of a tile
 
 // X of an entry: X(i, k) = M[i][k], or M[k][i] where M is tall; 0 outside.
 // Row slots: the fragments' row 8 j + g is row i = 8 j + g of X, or (R / 8) g + j where
 // M is tall, so that a thread's rows lie side by side there.
+// A tile holds the columns k0 .. k0 + 31 as M has them, [R][32] or tall [32][R], in
+// pieces of four elements that are moved inside their row so that the threads' reads
+// meet few banks twice.
 template <typename T, int R>
 struct Matrix {
+    static constexpr int TILE = R * TC;      // elements
     const T* src;
     T* dst;
     int n, r;
@@ -93,38 +134,72 @@ struct Matrix {
     float f;                                 // a power of two that X is taken with
     __device__ __forceinline__ explicit Matrix(const OrthoEntry& e)
         : src(static_cast<const T*>(e.src)), dst(static_cast<T*>(e.dst)), n(e.n), r(e.r), tall(e.tall), vec(e.vec), f(1.f) {}
-    __device__ __forceinline__ float at(int i, int k) const {
-        if (i >= r || k >= n) return 0.f;
-        return to_f(src[tall ? (int64_t)k * r + i : (int64_t)i * n + k]) * f;
-    }
-    // X(i, k .. k + 3)
-    __device__ __forceinline__ void along_k(int i, int k, float (&v)[4]) const {
-        if (vec && i < r && k + 4 <= n) {
-            load4(src + (int64_t)i * n + k, v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = at(i, k + e);
-        }
-    }
-    // X(i .. i + 3, k)
-    __device__ __forceinline__ void along_i(int i, int k, float (&v)[4]) const {
-        if (vec && i + 4 <= r && k < n) {
-            load4(src + (int64_t)k * r + i, v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = at(i + e, k);
-        }
-    }
     __device__ __forceinline__ int row_of(int slot) const { return tall ? slot % 8 * (R / 8) + slot / 8 : slot; }
-    // the row of X at place t (0 .. 3) or t + 4 of the k-step s of a product P X
-    __device__ __forceinline__ int k_row(int s, int t, int second) const {
-        return tall ? s / 2 * 16 + 4 * t + s % 2 * 2 + second : 8 * s + t + 4 * second;
+    // the row of X at place q (0 .. 3: 2 t, 2 t + 1, 2 t + 8, 2 t + 9) of the 16 rows s of a product P X
+    __device__ __forceinline__ int k_row(int s, int t, int q) const {
+        return 16 * s + (tall ? 4 * t + q : 2 * t + q % 2 + q / 2 * 8);
+    }
+    // where (row, piece) of a tile lies
+    static __device__ __forceinline__ int wide_at(int row, int piece) {
+        return row * TC + 4 * (piece ^ (2 * (row >> 1 & 3) ^ 4 * (row & 1)));
+    }
+    static __device__ __forceinline__ int tall_at(int row, int piece) {
+        return row * R + 4 * (piece ^ ((2 * (row >> 2 & 3) ^ 4 * (row & 1)) & (R / 4 - 1)));
+    }
+    // the tile from column k0 on, for a warp
+    __device__ __forceinline__ void fetch(T* tile, int k0, int lane) const {
+        if (vec) {
+#pragma unroll
+            for (int q = 0; q < R / 4; ++q) {
+                const int at = lane + 32 * q;
+                if (tall) {
+                    const int k = at / (R / 4), p = at % (R / 4);
+                    const bool in = k0 + k < n && 4 * p < r;
+                    copy_async<4 * sizeof(T)>(tile + tall_at(k, p), in ? src + (int64_t)(k0 + k) * r + 4 * p : src, in);
+                } else {
+                    const int i = at / 8, p = at % 8;
+                    const bool in = i < r && k0 + 4 * p < n;
+                    copy_async<4 * sizeof(T)>(tile + wide_at(i, p), in ? src + (int64_t)i * n + k0 + 4 * p : src, in);
+                }
+            }
+        } else {
+            for (int at = lane; at < TILE; at += 32) {
+                if (tall) {
+                    const int k = at / R, i = at % R;
+                    tile[tall_at(k, i / 4) + i % 4] = k0 + k < n && i < r ? src[(int64_t)(k0 + k) * r + i] : from_f<T>(0.f);
+                } else {
+                    const int i = at / TC, k = at % TC;
+                    tile[wide_at(i, k / 4) + k % 4] = i < r && k0 + k < n ? src[(int64_t)i * n + k0 + k] : from_f<T>(0.f);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
 };
+
+// A warp's tiles of its block's columns, one after the other: each(tile, k0).
+template <typename T, int R, typename F>
+__device__ __forceinline__ void over_tiles(const Matrix<T, R>& x, T* ring, int first, int end, F&& each) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    T* mine = ring + warp * STAGES * Matrix<T, R>::TILE;
+    int k0 = first + TC * warp, ahead = k0;
+    constexpr int STEP = TC * OW;
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i, ahead += STEP)
+        if (ahead < end) x.fetch(mine + i * Matrix<T, R>::TILE, ahead, lane);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int stage = 0; k0 < end; k0 += STEP, ahead += STEP) {
+        // the next tile into the place of the last one, which the whole warp has read
+        __syncwarp();
+        const int next = stage == 0 ? STAGES - 1 : stage - 1;
+        if (ahead < end) x.fetch(mine + next * Matrix<T, R>::TILE, ahead, lane);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        __syncwarp();
+        each(mine + stage * Matrix<T, R>::TILE, k0);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+}
 
 // Tiles of a symmetric product: block row m (16 rows) and 8 columns j, j >= 2 m.
 template <int R>
@@ -138,45 +213,38 @@ struct Gram {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[t][e] = 0.f;
     }
-    // += x x^T over 8 columns; x[j][0 / 1]: row slot 8 j + g, place t / t + 4.  EXACT: x has no low part.
+    // += x x^T over 16 columns; [j][0 / 1]: row slot 8 j + g, columns 2 t, 2 t + 1 / 2 t + 8, 2 t + 9.
+    // EXACT: x has no low part.
     template <bool EXACT>
-    __device__ __forceinline__ void add(const float (&x)[J][2]) {
-        float hi[J][2], lo[J][2];
+    __device__ __forceinline__ void add(const uint32_t (&hi)[J][2], const uint32_t (&lo)[J][2]) {
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                hi[j][e] = EXACT ? x[j][e] : tf32_hi(x[j][e]);
-                lo[j][e] = x[j][e] - hi[j][e];
-            }
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            const float ah[4] = {hi[2 * m][0], hi[2 * m + 1][0], hi[2 * m][1], hi[2 * m + 1][1]};
-            const float al[4] = {lo[2 * m][0], lo[2 * m + 1][0], lo[2 * m][1], lo[2 * m + 1][1]};
+        for (int m = 0; m < M; ++m)
 #pragma unroll
             for (int j = 2 * m; j < J; ++j) {
                 float d[4] = {0.f, 0.f, 0.f, 0.f};
                 if (!EXACT) {
-                    mma8(d, al, hi[j][0], hi[j][1]);
-                    mma8(d, ah, lo[j][0], lo[j][1]);
+                    mma16(d, lo[2 * m][0], lo[2 * m + 1][0], lo[2 * m][1], lo[2 * m + 1][1], hi[j][0], hi[j][1]);
+                    mma16(d, hi[2 * m][0], hi[2 * m + 1][0], hi[2 * m][1], hi[2 * m + 1][1], lo[j][0], lo[j][1]);
                 }
-                mma8(d, ah, hi[j][0], hi[j][1]);
+                mma16(d, hi[2 * m][0], hi[2 * m + 1][0], hi[2 * m][1], hi[2 * m + 1][1], hi[j][0], hi[j][1]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[tile(m, j)][e] += d[e];
             }
-        }
     }
 };
 
-// Shared memory of a block: the products, P and A as plain r x r matrices of pitch R + 4, and P's fragments.
-template <int R>
+// Shared memory of a block: r x r matrices of pitch R + 4, P's fragments, and the tiles,
+// whose place the sums of the warps take between the passes.
+template <typename T, int R>
 struct OrthoShared {
     static constexpr int LD = R + 4;
-    float part[4][R * LD];                   // the warps' sums; [0]: the block's
     float A[R * LD], Q[R * LD], B[R * LD], P[R * LD];
-    // P's fragments [m][s][lane][4], high and low parts
-    float4 ph[R / 16][R / 8][32], pl[R / 16][R / 8][32];
-    float red[OW];
+    uint4 ph[R / 16][R / 16][32], pl[R / 16][R / 16][32];   // [m][s][lane]
+    alignas(16) float red[OW];
+    union alignas(16) {
+        T ring[OW * STAGES * R * TC];
+        float part[OW / 2][R * LD];          // [0]: the block's
+    };
 };
 
 // C = x A B + y D + z I for R x R matrices in shared memory (D may be null); C is none of them.
@@ -213,12 +281,12 @@ __device__ __forceinline__ void small_product(float* C, const float* A, const fl
     __syncthreads();
 }
 
-// The blocks' sums of a product, in X's row order, in sh.A of every block of the cluster.
+// The blocks' sums of a product, in X's row order and times `scale`, in sh.A of every
+// block of the cluster.
 template <typename T, int R>
-__device__ __forceinline__ void gather(const Gram<R>& acc, const Matrix<T, R>& x, OrthoShared<R>& sh) {
+__device__ __forceinline__ void gather(Gram<R>& s, const Matrix<T, R>& x, float scale, OrthoShared<T, R>& sh) {
     constexpr int LD = R + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    Gram<R> s = acc;
     auto each = [&](float* p, bool load) {
 #pragma unroll
         for (int m = 0; m < R / 16; ++m)
@@ -231,6 +299,7 @@ __device__ __forceinline__ void gather(const Gram<R>& acc, const Matrix<T, R>& x
                     if (load) v += q; else q = v;
                 }
     };
+    __syncthreads();                         // (the tiles have been read)
     // half of the warps hand theirs to the other half
 #pragma unroll
     for (int half = OW / 2; half >= 1; half /= 2) {
@@ -244,163 +313,194 @@ __device__ __forceinline__ void gather(const Gram<R>& acc, const Matrix<T, R>& x
     cl.sync();
     const int blocks = (int)cl.num_blocks();
     for (int i = threadIdx.x; i < R * R; i += OT) {
-        int a = i / R, b = i % R;
+        const int a = i / R, b = i % R;
         // (the tiles below the diagonal's block row are not there)
         const int at = a / 16 <= b / 16 ? a * LD + b : b * LD + a;
         float v = 0.f;
         for (int k = 0; k < blocks; ++k) v += cl.map_shared_rank(&sh, k)->part[0][at];
-        sh.A[x.row_of(a) * LD + x.row_of(b)] = v;
+        sh.A[x.row_of(a) * LD + x.row_of(b)] = v * scale;
     }
     cl.sync();
 }
 
-// P as fragments for P X
-template <typename T, int R>
-__device__ __forceinline__ void fragments(const Matrix<T, R>& x, OrthoShared<R>& sh) {
-    constexpr int LD = R + 4;
-    for (int i = threadIdx.x; i < R / 16 * (R / 8) * 32; i += OT) {
-        const int lane = i % 32, s = i / 32 % (R / 8), m = i / 32 / (R / 8), g = lane >> 2, t = lane & 3;
-        float v[4], hi[4];
+// the largest of the block's values, none of them negative
+__device__ __forceinline__ float block_max(float m, float* red) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = sh.P[x.row_of(16 * m + g + e % 2 * 8) * LD + x.k_row(s, t, e / 2)];
-            hi[e] = tf32_hi(v[e]);
-        }
-        sh.ph[m][s][lane] = make_float4(hi[0], hi[1], hi[2], hi[3]);
-        sh.pl[m][s][lane] = make_float4(v[0] - hi[0], v[1] - hi[1], v[2] - hi[2], v[3] - hi[3]);
-    }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < OW; ++w) m = fmaxf(m, red[w]);
+    return m;
+}
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < OW; ++w) v += red[w];
+    return v;
+}
+// 2^e with e such that 2^e m lies in [2^(to - 1), 2^to); m is positive and finite, the
+// power is held to 2^+-126
+__device__ __forceinline__ float scale_to(float m, int to) {
+    int e;
+    frexpf(m, &e);
+    return ldexpf(1.f, max(-126, min(126, to - e)));
 }
 
-// A warp's columns [k0, k0 + 32) of P X: d[m][c][e], row slot 16 m + g + 8 (e / 2) and column
-// k0 + 4 (2 t + e % 2) + c (M wide) or k0 + 8 c + 2 t + e % 2 (tall).
+// sh.P as fragments for P X, times the power of two that is returned
 template <typename T, int R>
-__device__ __forceinline__ void times_p(const Matrix<T, R>& x, const OrthoShared<R>& sh, int k0, float (&d)[R / 16][4][4]) {
+__device__ __forceinline__ float fragments(const Matrix<T, R>& x, OrthoShared<T, R>& sh) {
+    constexpr int LD = R + 4;
+    float m = 0.f;
+    for (int i = threadIdx.x; i < R * R; i += OT) m = fmaxf(m, fabsf(sh.P[i / R * LD + i % R]));
+    m = block_max(m, sh.red);
+    const float scale = m > 0.f && m <= FLT_MAX ? scale_to(m, 14) : 1.f;
+    for (int i = threadIdx.x; i < R / 16 * (R / 16) * 32; i += OT) {
+        const int lane = i % 32, s = i / 32 % (R / 16), mm = i / 32 / (R / 16), g = lane >> 2, t = lane & 3;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {        // rows g, g + 8, g, g + 8; places 0, 1 and then 2, 3
+            const float* p = sh.P + x.row_of(16 * mm + g + e % 2 * 8) * LD;
+            split(p[x.k_row(s, t, e / 2 * 2)] * scale, p[x.k_row(s, t, e / 2 * 2 + 1)] * scale, hi[e], lo[e]);
+        }
+        sh.ph[mm][s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        sh.pl[mm][s][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    __syncthreads();
+    return scale;
+}
+
+// Columns 16 h .. 16 h + 15 of a tile of P X: d[m][c][e], row slot 16 m + g + 8 (e / 2), column
+// 16 h + 4 t + 2 (e % 2) + c (M wide) or 16 h + 8 c + 2 t + e % 2 (tall).
+template <typename T, int R>
+__device__ __forceinline__ void times_p(const Matrix<T, R>& x, const OrthoShared<T, R>& sh, const T* tile, int h,
+                                        float (&d)[R / 16][2][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    constexpr bool EXACT = sizeof(T) == 2;   // (times a power of two)
+    constexpr bool EXACT = sizeof(T) == 2;   // eight bits fit fp16
+    constexpr int S = R / 16;
+    uint32_t hi[S][2][2], lo[S][2][2];
 #pragma unroll
-    for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[m][c][e] = 0.f;
-#pragma unroll
-    for (int s2 = 0; s2 < R / 16; ++s2) {
-        // 16 rows of X: b[c][s][place]
-        float b[4][2][2];
+    for (int s = 0; s < S; ++s) {
+        float v[2][4];                       // [c][place]
         if (x.tall) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[4];
-                x.along_i(16 * s2 + 4 * t, k0 + 8 * c + g, v);
-                b[c][0][0] = v[0]; b[c][0][1] = v[1]; b[c][1][0] = v[2]; b[c][1][1] = v[3];
-            }
+            for (int c = 0; c < 2; ++c) load4(tile + Matrix<T, R>::tall_at(16 * h + 8 * c + g, 4 * s + t), v[c]);
         } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float v[4];
-                x.along_k(16 * s2 + 8 * (q / 2) + 4 * (q % 2) + t, k0 + 4 * g, v);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) b[c][q / 2][q % 2] = v[c];
+                const float2 w = load2(tile + Matrix<T, R>::wide_at(16 * s + 2 * t + q % 2 + q / 2 * 8, 4 * h + g / 2) + 2 * (g % 2));
+                v[0][q] = w.x;
+                v[1][q] = w.y;
             }
         }
-        float hi[2][4][2], lo[2][4][2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    hi[s][c][e] = EXACT ? b[c][s][e] : tf32_hi(b[c][s][e]);
-                    lo[s][c][e] = b[c][s][e] - hi[s][c][e];
-                }
-#pragma unroll
-        for (int m = 0; m < R / 16; ++m) {
-            float z[4][4] = {};
-            float ah[2][4];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const float4 h4 = sh.ph[m][2 * s2 + s][lane], l4 = sh.pl[m][2 * s2 + s][lane];
-                const float al[4] = {l4.x, l4.y, l4.z, l4.w};
-                ah[s][0] = h4.x; ah[s][1] = h4.y; ah[s][2] = h4.z; ah[s][3] = h4.w;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mma8(z[c], al, hi[s][c][0], hi[s][c][1]);
-                    if (!EXACT) mma8(z[c], ah[s], lo[s][c][0], lo[s][c][1]);
-                }
+            for (int e = 0; e < 2; ++e) {
+                if (EXACT) hi[s][c][e] = half2_of(v[c][2 * e] * x.f, v[c][2 * e + 1] * x.f);
+                else split(v[c][2 * e] * x.f, v[c][2 * e + 1] * x.f, hi[s][c][e], lo[s][c][e]);
             }
+    }
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+    for (int m = 0; m < R / 16; ++m) {
+        uint4 a[S];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mma8(z[c], ah[s], hi[s][c][0], hi[s][c][1]);
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int e = 0; e < 4; ++e) d[m][c][e] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[m][c][e] += z[c][e];
+        for (int s = 0; s < S; ++s) {
+            const uint4 l = sh.pl[m][s][lane];
+            a[s] = sh.ph[m][s][lane];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mma16(d[m][c], l.x, l.y, l.z, l.w, hi[s][c][0], hi[s][c][1]);
+                if (!EXACT) mma16(d[m][c], a[s].x, a[s].y, a[s].z, a[s].w, lo[s][c][0], lo[s][c][1]);
+            }
         }
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) mma16(d[m][c], a[s].x, a[s].y, a[s].z, a[s].w, hi[s][c][0], hi[s][c][1]);
     }
 }
 
 // The sums of X X^T over the block's columns.
 template <typename T, int R>
-__device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, int first, int end, Gram<R>& acc) {
+__device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, T* ring, int first, int end, Gram<R>& acc) {
     constexpr int J = R / 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr bool EXACT = sizeof(T) == 2;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     acc.clear();
-    for (int k0 = first + 32 * warp; k0 < end; k0 += 32 * OW) {
+    over_tiles<T, R>(x, ring, first, end, [&](const T* tile, int) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {        // 16 columns: two products of 8
-            float u[2][J][2];
+        for (int h = 0; h < 2; ++h) {
+            uint32_t hi[J][2], lo[J][2];
+            auto put = [&](int j, int e, float a, float b) {
+                if (EXACT) hi[j][e] = half2_of(a * x.f, b * x.f);
+                else split(a * x.f, b * x.f, hi[j][e], lo[j][e]);
+            };
             if (x.tall) {
+                // columns 16 h + 4 t + q, rows J g ..
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int e = 0; e < 2; ++e) {
+                    const int k = 16 * h + 4 * t + 2 * e;
+                    if constexpr (J >= 4) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int k = k0 + 16 * h + 8 * s + t + 4 * e;
-                        if constexpr (J % 4 == 0) {
+                        for (int j = 0; j < J; j += 4) {
+                            float a[4], b[4];
+                            load4(tile + Matrix<T, R>::tall_at(k, (J * g + j) / 4), a);
+                            load4(tile + Matrix<T, R>::tall_at(k + 1, (J * g + j) / 4), b);
 #pragma unroll
-                            for (int j = 0; j < J; j += 4) {
-                                float v[4];
-                                x.along_i(J * g + j, k, v);
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) u[s][j + q][e] = v[q];
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < J; ++j) u[s][j][e] = x.at(J * g + j, k);
+                            for (int q = 0; q < 4; ++q) put(j + q, e, a[q], b[q]);
                         }
+                    } else {
+                        const float2 a = load2(tile + Matrix<T, R>::tall_at(k, g / 2) + 2 * (g % 2));
+                        const float2 b = load2(tile + Matrix<T, R>::tall_at(k + 1, g / 2) + 2 * (g % 2));
+                        put(0, e, a.x, b.x);
+                        put(1, e, a.y, b.y);
                     }
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     float v[4];
-                    x.along_k(8 * j + g, k0 + 16 * h + 4 * t, v);
-                    u[0][j][0] = v[0]; u[0][j][1] = v[1]; u[1][j][0] = v[2]; u[1][j][1] = v[3];
+                    load4(tile + Matrix<T, R>::wide_at(8 * j + g, 4 * h + t), v);
+                    put(j, 0, v[0], v[1]);
+                    put(j, 1, v[2], v[3]);
                 }
             }
-            acc.template add<sizeof(T) == 2>(u[0]);
-            acc.template add<sizeof(T) == 2>(u[1]);
+            acc.template add<EXACT>(hi, lo);
         }
-    }
+    });
 }
 
-// The same of P X.
+// The same of P X times `scale`.
 template <typename T, int R>
-__device__ __forceinline__ void gram_of_px(const Matrix<T, R>& x, const OrthoShared<R>& sh, int first, int end, Gram<R>& acc) {
+__device__ __forceinline__ void gram_of_px(const Matrix<T, R>& x, OrthoShared<T, R>& sh, float scale, int first, int end,
+                                           Gram<R>& acc) {
     constexpr int J = R / 8;
-    const int warp = threadIdx.x >> 5;
     acc.clear();
-    for (int k0 = first + 32 * warp; k0 < end; k0 += 32 * OW) {
-        float d[R / 16][4][4];
-        times_p<T, R>(x, sh, k0, d);
+    over_tiles<T, R>(x, sh.ring, first, end, [&](const T* tile, int) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float u[J][2];
+        for (int h = 0; h < 2; ++h) {
+            float d[R / 16][2][4];
+            times_p<T, R>(x, sh, tile, h, d);
+            uint32_t hi[J][2], lo[J][2];
 #pragma unroll
-            for (int j = 0; j < J; ++j) u[j][0] = d[j / 2][c][j % 2 * 2], u[j][1] = d[j / 2][c][j % 2 * 2 + 1];
-            acc.template add<false>(u);
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    split(d[j / 2][c][j % 2 * 2] * scale, d[j / 2][c][j % 2 * 2 + 1] * scale, hi[j][c], lo[j][c]);
+            acc.template add<false>(hi, lo);
         }
-    }
+    });
 }
 
 __device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
@@ -410,79 +510,77 @@ __device__ __forceinline__ void store4(bf16* p, float a, float b, float c, float
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-// dst = P X
+// dst = P X times `scale`
 template <typename T, int R>
-__device__ __forceinline__ void write_px(const Matrix<T, R>& x, const OrthoShared<R>& sh, int first, int end) {
+__device__ __forceinline__ void write_px(const Matrix<T, R>& x, OrthoShared<T, R>& sh, float scale, int first, int end) {
     constexpr int J = R / 8;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    for (int k0 = first + 32 * warp; k0 < end; k0 += 32 * OW) {
-        float d[R / 16][4][4];
-        times_p<T, R>(x, sh, k0, d);
-        if (x.tall) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    over_tiles<T, R>(x, sh.ring, first, end, [&](const T* tile, int k0) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+        for (int h = 0; h < 2; ++h) {
+            float d[R / 16][2][4];
+            times_p<T, R>(x, sh, tile, h, d);
+            if (x.tall) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int k = k0 + 8 * c + 2 * t + e;
-                    if (k >= x.n) continue;
-                    T* out = x.dst + (int64_t)k * x.r;
-                    auto v = [&](int j) { return d[j / 2][c][j % 2 * 2 + e]; };
-                    if constexpr (J % 4 == 0) {
-#pragma unroll
-                        for (int j = 0; j < J; j += 4) {
-                            const int i = J * g + j;
-                            if (x.vec && i + 4 <= x.r) {
-                                store4(out + i, v(j), v(j + 1), v(j + 2), v(j + 3));
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (i + q < x.r) out[i + q] = from_f<T>(v(j + q));
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-                            if (J * g + j < x.r) out[J * g + j] = from_f<T>(v(j));
-                    }
-                }
-        } else {
-#pragma unroll
-            for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int i = 16 * m + 8 * h + g;
-                    if (i >= x.r) continue;
-                    T* out = x.dst + (int64_t)i * x.n;
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int k = k0 + 8 * t + 4 * e;
-                        auto v = [&](int c) { return d[m][c][2 * h + e]; };
+                        const int k = k0 + 16 * h + 8 * c + 2 * t + e;
+                        if (k >= x.n) continue;
+                        T* out = x.dst + (int64_t)k * x.r;
+                        auto v = [&](int j) { return d[j / 2][c][j % 2 * 2 + e] * scale; };
+                        if constexpr (J % 4 == 0) {
+#pragma unroll
+                            for (int j = 0; j < J; j += 4) {
+                                const int i = J * g + j;
+                                if (x.vec && i + 4 <= x.r) {
+                                    store4(out + i, v(j), v(j + 1), v(j + 2), v(j + 3));
+                                } else {
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        if (i + q < x.r) out[i + q] = from_f<T>(v(j + q));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < J; ++j)
+                                if (J * g + j < x.r) out[J * g + j] = from_f<T>(v(j));
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int m = 0; m < R / 16; ++m)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int i = 16 * m + 8 * q + g, k = k0 + 16 * h + 4 * t;
+                        if (i >= x.r) continue;
+                        T* out = x.dst + (int64_t)i * x.n + k;
+                        const float v[4] = {d[m][0][2 * q] * scale, d[m][1][2 * q] * scale, d[m][0][2 * q + 1] * scale,
+                                            d[m][1][2 * q + 1] * scale};
                         if (x.vec && k + 4 <= x.n) {
-                            store4(out + k, v(0), v(1), v(2), v(3));
+                            store4(out, v[0], v[1], v[2], v[3]);
                         } else {
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
-                                if (k + c < x.n) out[k + c] = from_f<T>(v(c));
+                                if (k + c < x.n) out[c] = from_f<T>(v[c]);
                         }
                     }
-                }
+            }
         }
-    }
+    });
 }
 
-// `steps` steps on sh.A and sh.P: P <- Q P with Q = a I + b A + c A^2, A <- Q A Q (they commute).
-template <int R>
-__device__ __forceinline__ void small_steps(OrthoShared<R>& sh, const OrthoCoeffs& co, int steps) {
+// `steps` steps on sh.A and sh.P: P <- Q P with Q = a I + b A + c A^2, A <- Q A Q (they
+// commute); the last A where it is wanted.
+template <typename T, int R>
+__device__ __forceinline__ void small_steps(OrthoShared<T, R>& sh, const OrthoCoeffs& co, int steps, bool last_a) {
     constexpr int LD = R + 4;
-    auto copy = [&](float* to, const float* from) {
-        for (int i = threadIdx.x; i < R * LD; i += OT) to[i] = from[i];
-        __syncthreads();
-    };
     for (int k = 0; k < steps; ++k) {
         small_product<R>(sh.Q, sh.A, sh.A, co.c, sh.A, co.b, co.a);
         small_product<R>(sh.B, sh.Q, sh.P, 1.f, nullptr, 0.f, 0.f);
-        copy(sh.P, sh.B);
-        if (k + 1 < steps) {
+        for (int i = threadIdx.x; i < R * LD; i += OT) sh.P[i] = sh.B[i];
+        __syncthreads();
+        if (k + 1 < steps || last_a) {
             small_product<R>(sh.B, sh.Q, sh.A, 1.f, nullptr, 0.f, 0.f);
             small_product<R>(sh.A, sh.B, sh.Q, 1.f, nullptr, 0.f, 0.f);
         }
@@ -490,63 +588,79 @@ __device__ __forceinline__ void small_steps(OrthoShared<R>& sh, const OrthoCoeff
 }
 
 template <typename T, int R, int N>
-__global__ void __launch_bounds__(OT) ortho_kernel(const __grid_constant__ OrthoTab<N> tab) {
+__global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid_constant__ OrthoTab<N> tab) {
     constexpr int LD = R + 4;
     extern __shared__ __align__(16) unsigned char smem[];
-    OrthoShared<R>& sh = *reinterpret_cast<OrthoShared<R>*>(smem);
+    OrthoShared<T, R>& sh = *reinterpret_cast<OrthoShared<T, R>*>(smem);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), blocks = (int)cl.num_blocks(), tid = threadIdx.x;
     Matrix<T, R> x(tab.e[blockIdx.x / blocks]);
-    // the block's columns, in stretches of 32
-    const int all = (x.n + 31) / 32, per = (all + blocks - 1) / blocks;
-    const int first = min(rank * per, all) * 32, end = min(rank * per + per, all) * 32;
+    // the block's columns, in whole tiles
+    const int all = (x.n + TC - 1) / TC, per = (all + blocks - 1) / blocks;
+    const int first = min(rank * per, all) * TC, end = min(rank * per + per, all) * TC;
+    const int64_t size = (int64_t)x.n * x.r;
     Gram<R> acc;
-    gram_of_x<T, R>(x, first, end, acc);
-    gather<T, R>(acc, x, sh);
     auto trace = [&]() {
         float s = 0.f;
         for (int i = 0; i < x.r; ++i) s += sh.A[i * LD + i];
         return s;
     };
-    float sq = trace();
-    if (!(sq > 1e-25f && sq < 1e30f)) {
-        // squares beyond fp32, or none: X relative to its largest magnitude
+    // The first scale from 1,024 elements: their root mean square becomes 2^5 or so, which leaves 2^10 for
+    // larger ones.  Where that does not do, the sums are no numbers, and the largest magnitude says.
+    float sq = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float v = to_f(x.src[(q * OT + tid) * size / (4 * OT)]);
+        sq = fmaf(v, v, sq);
+    }
+    sq = block_sum(sq, sh.red) / (4 * OT);
+    bool sure = sq > 1e-30f && sq < 1e30f;
+    if (sure) {
+        x.f = scale_to(sqrtf(sq), 5);
+        gram_of_x<T, R>(x, sh.ring, first, end, acc);
+        gather<T, R>(acc, x, 1.f, sh);
+        sq = trace();
+        sure = sq > 0.f && sq <= FLT_MAX;
+    }
+    if (!sure) {
         float m = 0.f;
         bool bad = false;
-        for (int64_t i = tid + (int64_t)rank * OT; i < (int64_t)x.n * x.r; i += (int64_t)OT * blocks) {
+        for (int64_t i = tid + (int64_t)rank * OT; i < size; i += (int64_t)OT * blocks) {
             const float v = fabsf(to_f(x.src[i]));
             bad |= !(v <= FLT_MAX);
             m = fmaxf(m, v);
         }
-        if (bad) m = INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((tid & 31) == 0) sh.red[tid >> 5] = m;
+        block_max(bad ? INFINITY : m, sh.red);
         cl.sync();
+        m = 0.f;
         for (int b = 0; b < blocks; ++b)
             for (int w = 0; w < OW; ++w) m = fmaxf(m, cl.map_shared_rank(&sh, b)->red[w]);
         cl.sync();
         if (m > FLT_MAX) {
             // an infinity or NaN
-            for (int64_t i = tid + (int64_t)rank * OT; i < (int64_t)x.n * x.r; i += (int64_t)OT * blocks)
+            for (int64_t i = tid + (int64_t)rank * OT; i < size; i += (int64_t)OT * blocks)
                 x.dst[i] = from_f<T>(__int_as_float(0x7fc00000));
             return;
         }
+        sq = 0.f;
         if (m > 0.f) {
-            int e;
-            frexpf(m, &e);
-            // X becomes at most 2; a factor that fp32 holds
-            x.f = ldexpf(1.f, min(1 - e, 126));
-            gram_of_x<T, R>(x, first, end, acc);
-            gather<T, R>(acc, x, sh);
+            x.f = scale_to(m, 15);
+            gram_of_x<T, R>(x, sh.ring, first, end, acc);
+            gather<T, R>(acc, x, 1.f, sh);
             sq = trace();
+        } else {
+            for (int i = tid; i < R * LD; i += OT) sh.A[i] = 0.f;
         }
     }
-    // X_0 = inv (f M); its products.  A matrix of zeros stays zero whatever eps.
-    const float inv = sq == 0.f ? 0.f : 1.f / (sqrtf(sq) + tab.co.eps * x.f);
+    // From here on |f M| is below 2^15, and so is every element.  X_0 = inv (f M); a matrix of zeros stays zero.
+    float f = sq > 0.f ? x.f * scale_to(sqrtf(sq), 15) : x.f;
+    if (!(f >= 0x1p-126f && f <= 0x1p126f)) f = x.f;         // (at the ends of fp32 the largest element's scale stays)
+    const float again = f / x.f;
+    const float inv = sq > 0.f ? 1.f / (sqrtf(sq) * again + tab.co.eps * f) : 0.f, to_a = inv * again;
+    x.f = f;
     __syncthreads();                         // (all have their trace)
     for (int i = tid; i < R * LD; i += OT) {
-        sh.A[i] = sh.A[i] * inv * inv;
+        sh.A[i] = sh.A[i] * to_a * to_a;
         sh.P[i] = i % LD == i / LD ? inv : 0.f;
     }
     __syncthreads();
@@ -554,14 +668,18 @@ __global__ void __launch_bounds__(OT) ortho_kernel(const __grid_constant__ Ortho
     int left = tab.co.steps, phases = (left + STEPS_A_PHASE - 1) / STEPS_A_PHASE;
     while (true) {
         const int now = left / phases;
-        small_steps<R>(sh, tab.co, now);
+        small_steps<T, R>(sh, tab.co, now, phases > 1);
         left -= now;
-        fragments<T, R>(x, sh);
-        if (--phases == 0) break;
-        gram_of_px<T, R>(x, sh, first, end, acc);
-        gather<T, R>(acc, x, sh);
+        const float p = 1.f / fragments<T, R>(x, sh);
+        if (--phases == 0) {
+            write_px<T, R>(x, sh, p, first, end);
+            return;
+        }
+        // |X_k| from the A that the steps have left, so that its elements fit fp16 too
+        const float now_sq = trace(), u = now_sq > 0.f && now_sq <= FLT_MAX ? scale_to(sqrtf(now_sq), 14) : 1.f;
+        gram_of_px<T, R>(x, sh, p * u, first, end, acc);
+        gather<T, R>(acc, x, 1.f / (u * u), sh);
     }
-    write_px<T, R>(x, sh, first, end);
 }
 
 template <typename T, int R, int N>
@@ -570,12 +688,12 @@ cudaError_t launch_n(const OrthoEntry* e, int n, const OrthoCoeffs& co, int bloc
     tab.co = co;
     std::copy(e, e + n, tab.e);
     auto* kern = ortho_kernel<T, R, N>;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(OrthoShared<R>));
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(OrthoShared<T, R>));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(n * blocks));
     cfg.blockDim = dim3(OT);
-    cfg.dynamicSmemBytes = sizeof(OrthoShared<R>);
+    cfg.dynamicSmemBytes = sizeof(OrthoShared<T, R>);
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -588,10 +706,14 @@ cudaError_t launch_n(const OrthoEntry* e, int n, const OrthoCoeffs& co, int bloc
 
 constexpr int TAB_SMALL = 64, TAB_LARGE = 1300;      // 1.6 KB and 31 KB of kernel parameters
 
+// Blocks of a matrix's cluster: 512 columns each, two tiles a warp, or more.
+int blocks_for(int n) { return n >= 4096 ? 8 : n >= 2048 ? 4 : n >= 1024 ? 2 : 1; }
+int tile_for(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+
 template <typename T, int R>
-cudaError_t launch_r(const OrthoEntry* e, int n, const OrthoCoeffs& co, cudaStream_t s) {
+cudaError_t launch_r(const OrthoEntry* e, int n, const OrthoCoeffs& co, int blocks, cudaStream_t s) {
     for (; n > 0; e += TAB_LARGE, n -= TAB_LARGE) {
-        const int k = n < TAB_LARGE ? n : TAB_LARGE, blocks = 4;
+        const int k = n < TAB_LARGE ? n : TAB_LARGE;
         const cudaError_t err = k <= TAB_SMALL ? launch_n<T, R, TAB_SMALL>(e, k, co, blocks, s)
                                                : launch_n<T, R, TAB_LARGE>(e, k, co, blocks, s);
         if (err != cudaSuccess) return err;
@@ -601,18 +723,20 @@ cudaError_t launch_r(const OrthoEntry* e, int n, const OrthoCoeffs& co, cudaStre
 
 template <typename T>
 cudaError_t launch_t(std::vector<OrthoEntry>& e, const OrthoCoeffs& co, cudaStream_t s) {
-    // by the tiles' size, the longest first: short ones fill the end
-    auto tile = [](const OrthoEntry& x) { return x.r <= 16 ? 16 : x.r <= 32 ? 32 : 64; };
-    std::stable_sort(e.begin(), e.end(), [&](const OrthoEntry& a, const OrthoEntry& b) {
-        return tile(a) != tile(b) ? tile(a) > tile(b) : a.n > b.n;
+    // a launch for each size of tile and cluster, the longest first
+    auto same = [](const OrthoEntry& a, const OrthoEntry& b) {
+        return tile_for(a.r) == tile_for(b.r) && blocks_for(a.n) == blocks_for(b.n);
+    };
+    std::stable_sort(e.begin(), e.end(), [](const OrthoEntry& a, const OrthoEntry& b) {
+        return tile_for(a.r) != tile_for(b.r) ? tile_for(a.r) > tile_for(b.r) : a.n > b.n;
     });
     for (size_t i = 0; i < e.size();) {
         size_t j = i;
-        while (j < e.size() && tile(e[j]) == tile(e[i])) ++j;
-        const int n = (int)(j - i);
-        const cudaError_t err = tile(e[i]) == 16   ? launch_r<T, 16>(&e[i], n, co, s)
-                                : tile(e[i]) == 32 ? launch_r<T, 32>(&e[i], n, co, s)
-                                                   : launch_r<T, 64>(&e[i], n, co, s);
+        while (j < e.size() && same(e[i], e[j])) ++j;
+        const int n = (int)(j - i), tile = tile_for(e[i].r), blocks = blocks_for(e[i].n);
+        const cudaError_t err = tile == 16   ? launch_r<T, 16>(&e[i], n, co, blocks, s)
+                                : tile == 32 ? launch_r<T, 32>(&e[i], n, co, blocks, s)
+                                             : launch_r<T, 64>(&e[i], n, co, blocks, s);
         if (err != cudaSuccess) return err;
         i = j;
     }

@@ -31,6 +31,7 @@ from __future__ import annotations
 import ctypes
 import math
 from collections import namedtuple
+from contextlib import nullcontext
 from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_void_p
 
 import torch
@@ -130,6 +131,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+_HERE = nullcontext()
+
+
+def _stream_memory(stream):
+    """_empty's rule for several tensors: inside it they come from the pool of `stream` (None: the current one)."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 class KvCache:
@@ -298,13 +307,15 @@ def kv_reserve(pool: PagePool, page_table, kv_len, n_new, n_rows: int, stream=No
     i = pool.index
     ids = (_ids("page_table", page_table, (n, width), i), _ids("kv_len", kv_len, (n,), i), _ids("n_new", n_new, (n,), i))
     handle = _on(i, stream)
-    # one block for what comes out, the 8-byte slots first
-    m = max(int(n_rows), 0)
-    buf = _empty((4 * m + n + 1,), _INT32, pool.device, stream)
-    at = buf.data_ptr()
-    q = _KvGrowth(*ids, at + 16 * m, at + 8 * m, at + 12 * m, at, n_rows, n, width)
+    dev, m = pool.device, max(n_rows, 0)
+    with _stream_memory(stream):
+        row_off = torch.empty(n + 1, dtype=_INT32, device=dev)
+        positions = torch.empty(m, dtype=_INT32, device=dev)
+        seqs = torch.empty(m, dtype=_INT32, device=dev)
+        slots = torch.empty(m, dtype=torch.int64, device=dev)
+    q = _KvGrowth(*ids, row_off.data_ptr(), positions.data_ptr(), seqs.data_ptr(), slots.data_ptr(), n_rows, n, width)
     _check(_lib().mlora_kv_reserve(pool._ref, byref(q), handle))
-    return ReservedRows(buf[4 * m:], buf[2 * m:3 * m], buf[3 * m:4 * m], buf[:2 * m].view(torch.int64))
+    return ReservedRows(row_off, positions, seqs, slots)
 
 
 def kv_release(pool: PagePool, page_table, kv_len, keep=None, stream=None) -> None:

@@ -18,7 +18,7 @@ from ctypes import POINTER, byref, c_float, c_int32, c_int64, c_void_p
 import torch
 
 from . import _check, load_library
-from .kv import _dtype, _empty, _ids, _on
+from .kv import _dtype, _empty, _ids, _on, _stream_memory
 from .transformer import _TfBatch
 
 __all__ = ["TokenStats", "token_logprobs", "token_logprobs_backward", "tf_forward_stats"]
@@ -101,16 +101,14 @@ def token_logprobs(logits, targets=None, top: int = 0, scale: float = 1.0, statu
     c = _rows(logits, targets, scale, top, status)
     n, dev = logits.shape[0], logits.device
     handle = _on(logits.get_device(), stream)
-    # one block for the results of a row
-    per = 2 + (targets is not None) + 2 * max(top, 0)
-    buf = _empty((per * n,), torch.float32, dev, stream)
-    entropy, lse = buf[:n], buf[n:2 * n]
-    lp = buf[2 * n:3 * n] if targets is not None else None
-    at = (per - 2 * max(top, 0)) * n
-    ids = tops = None
-    if top > 0:
-        tops = buf[at:at + top * n].view(n, top)
-        ids = buf[at + top * n:].view(torch.int32).view(n, top)
+    with _stream_memory(stream):
+        lp = None if targets is None else torch.empty(n, dtype=torch.float32, device=dev)
+        entropy = torch.empty(n, dtype=torch.float32, device=dev)
+        lse = torch.empty(n, dtype=torch.float32, device=dev)
+        ids = tops = None
+        if top > 0:
+            ids = torch.empty((n, top), dtype=torch.int32, device=dev)
+            tops = torch.empty((n, top), dtype=torch.float32, device=dev)
     out = _TokenStats(None if lp is None else lp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
                       None if ids is None else ids.data_ptr(), None if tops is None else tops.data_ptr())
     _check(_lib().mlora_token_logprobs(byref(c), byref(out), handle))
