@@ -115,7 +115,6 @@ __device__ __forceinline__ void copy_async(void* to, const void* from, bool ther
                  : "memory");
 }
 
-constexpr int STAGES = 2;                    // tiles of a warp
 constexpr int TC = 32;                       // columns of a tile
 
 // X of an entry: X(i, k) = M[i][k], or M[k][i] where M is tall; 0 outside.
@@ -177,27 +176,38 @@ struct Matrix {
     }
 };
 
-// A warp's tiles of its block's columns, one after the other: each(tile, k0).
+// A warp's tiles of its block's columns, one after the other.  The first one is fetched
+// by begin_tiles, long before it is needed; then each(tile, k0) has its tile while the
+// next one is on its way.
+template <typename T, int R>
+struct OrthoShared;
+constexpr int STEP = TC * OW;                // columns from a warp's tile to its next one
+template <typename T, int R>
+__device__ __forceinline__ void begin_tiles(const Matrix<T, R>& x, OrthoShared<T, R>& sh, int first, int end) {
+    const int warp = threadIdx.x >> 5, k0 = first + TC * warp;
+    __syncwarp();
+    if (k0 < end) x.fetch(sh.ring0[warp], k0, threadIdx.x & 31);
+}
 template <typename T, int R, typename F>
-__device__ __forceinline__ void over_tiles(const Matrix<T, R>& x, T* ring, int first, int end, F&& each) {
+__device__ __forceinline__ void over_tiles(const Matrix<T, R>& x, OrthoShared<T, R>& sh, int first, int end, F&& each) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    T* mine = ring + warp * STAGES * Matrix<T, R>::TILE;
-    int k0 = first + TC * warp, ahead = k0;
-    constexpr int STEP = TC * OW;
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i, ahead += STEP)
-        if (ahead < end) x.fetch(mine + i * Matrix<T, R>::TILE, ahead, lane);
-        else asm volatile("cp.async.commit_group;" ::: "memory");
-    for (int stage = 0; k0 < end; k0 += STEP, ahead += STEP) {
-        // the next tile into the place of the last one, which the whole warp has read
+    T* here = sh.ring0[warp];
+    T* other = sh.ring1[warp];
+#pragma unroll 1
+    for (int k0 = first + TC * warp; k0 < end; k0 += STEP) {
+        // (the whole warp has read the tile whose place the next one takes)
+        if (k0 + STEP < end) {
+            x.fetch(other, k0 + STEP, lane);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
         __syncwarp();
-        const int next = stage == 0 ? STAGES - 1 : stage - 1;
-        if (ahead < end) x.fetch(mine + next * Matrix<T, R>::TILE, ahead, lane);
-        else asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        each(here, k0);
         __syncwarp();
-        each(mine + stage * Matrix<T, R>::TILE, k0);
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        T* const swap = here;
+        here = other;
+        other = swap;
     }
 }
 
@@ -233,92 +243,116 @@ struct Gram {
     }
 };
 
-// Shared memory of a block: r x r matrices of pitch R + 4, P's fragments, and the tiles,
-// whose place the sums of the warps take between the passes.
+// Shared memory of a block: r x r matrices of pitch R + 8 (a thread reads two values
+// side by side, eight rows at once), P's fragments, the warps' tiles, and in the second
+// tiles' place the sums of the warps between the passes.
 template <typename T, int R>
 struct OrthoShared {
-    static constexpr int LD = R + 4;
-    float A[R * LD], Q[R * LD], B[R * LD], P[R * LD];
+    static constexpr int LD = R + 8, SLOTS = R == 64 ? OW / 2 : OW;
+    float A[R * LD], Q[R * LD], W[R * LD], P[R * LD];
     uint4 ph[R / 16][R / 16][32], pl[R / 16][R / 16][32];   // [m][s][lane]
     alignas(16) float red[OW];
-    union alignas(16) {
-        T ring[OW * STAGES * R * TC];
-        float part[OW / 2][R * LD];          // [0]: the block's
+    alignas(16) T ring0[OW][R * TC];
+    union {
+        alignas(16) T ring1[OW][R * TC];
+        float part[SLOTS][R * LD];           // [0]: the block's
     };
 };
 
-// C = x A B + y D + z I for R x R matrices in shared memory (D may be null); C is none of them.
-template <int R>
-__device__ __forceinline__ void small_product(float* C, const float* A, const float* B, float x, const float* D, float y,
-                                              float z) {
-    constexpr int LD = R + 4, TILES = R / 16 * (R / 8);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    for (int tile = warp; tile < TILES; tile += OW) {
-        const int m = tile / (R / 8) * 16, n = tile % (R / 8) * 8;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+// 16 x 8 of A B at (m, n) for R x R matrices in shared memory; ROWS: B is symmetric, its rows are read.
+template <int R, bool ROWS>
+__device__ __forceinline__ void small_tile(const float* A, const float* B, int m, int n, float (&sum)[4]) {
+    constexpr int LD = R + 8;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int k = 0; k < R; k += 8) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            const float a[4] = {A[(m + g) * LD + k + t], A[(m + g + 8) * LD + k + t], A[(m + g) * LD + k + t + 4],
-                                A[(m + g + 8) * LD + k + t + 4]};
-            const float b[2] = {B[(k + t) * LD + n + g], B[(k + t + 4) * LD + n + g]};
-            float ah[4], al[4];
+    for (int e = 0; e < 4; ++e) sum[e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ah[e] = tf32_hi(a[e]), al[e] = a[e] - ah[e];
-            const float bh[2] = {tf32_hi(b[0]), tf32_hi(b[1])};
-            mma8(d, al, bh[0], bh[1]);
-            mma8(d, ah, b[0] - bh[0], b[1] - bh[1]);
-            mma8(d, ah, bh[0], bh[1]);
+    for (int k = 0; k < R; k += 8) {
+        // the places t and t + 4 of the eight are 2 t and 2 t + 1 of both factors
+        const float2 u = *reinterpret_cast<const float2*>(A + (m + g) * LD + k + 2 * t);
+        const float2 v = *reinterpret_cast<const float2*>(A + (m + g + 8) * LD + k + 2 * t);
+        const float2 b = ROWS ? *reinterpret_cast<const float2*>(B + (n + g) * LD + k + 2 * t)
+                              : make_float2(B[(k + 2 * t) * LD + n + g], B[(k + 2 * t + 1) * LD + n + g]);
+        const float a[4] = {u.x, v.x, u.y, v.y};
+        float ah[4], al[4], d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] += d[e];
-        }
+        for (int e = 0; e < 4; ++e) ah[e] = tf32_hi(a[e]), al[e] = a[e] - ah[e];
+        const float b0 = tf32_hi(b.x), b1 = tf32_hi(b.y);
+        mma8(d, al, b0, b1);
+        mma8(d, ah, b.x - b0, b.y - b1);
+        mma8(d, ah, b0, b1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = m + g + e / 2 * 8, j = n + 2 * t + e % 2;
-            C[i * LD + j] = x * sum[e] + (D ? y * D[i * LD + j] : 0.f) + (i == j ? z : 0.f);
-        }
+        for (int e = 0; e < 4; ++e) sum[e] += d[e];
     }
-    __syncthreads();
+}
+
+// Every tile of an R x R product, shared among the warps: each(m, n).
+template <int R, typename F>
+__device__ __forceinline__ void small_tiles(F&& each) {
+#pragma unroll 1
+    for (int tile = threadIdx.x >> 5; tile < R / 16 * (R / 8); tile += OW) each(tile / (R / 8) * 16, tile % (R / 8) * 8);
+}
+template <int R, typename F>
+__device__ __forceinline__ void small_store(float* C, int m, int n, F&& value) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = m + g + 8 * h, j = n + 2 * t;
+        *reinterpret_cast<float2*>(C + i * (R + 8) + j) = make_float2(value(i, j, 2 * h), value(i, j + 1, 2 * h + 1));
+    }
 }
 
 // The blocks' sums of a product, in X's row order and times `scale`, in sh.A of every
 // block of the cluster.
 template <typename T, int R>
 __device__ __forceinline__ void gather(Gram<R>& s, const Matrix<T, R>& x, float scale, OrthoShared<T, R>& sh) {
-    constexpr int LD = R + 4;
+    constexpr int LD = R + 8, SLOTS = OrthoShared<T, R>::SLOTS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    auto each = [&](float* p, bool load) {
-#pragma unroll
-        for (int m = 0; m < R / 16; ++m)
-#pragma unroll
-            for (int j = 2 * m; j < R / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float& v = s.v[Gram<R>::tile(m, j)][e];
-                    float& q = p[(16 * m + g + e / 2 * 8) * LD + 8 * j + 2 * t + e % 2];
-                    if (load) v += q; else q = v;
-                }
-    };
     __syncthreads();                         // (the tiles have been read)
-    // half of the warps hand theirs to the other half
 #pragma unroll
-    for (int half = OW / 2; half >= 1; half /= 2) {
-        if (warp >= half && warp < 2 * half) each(sh.part[warp - half], false);
-        __syncthreads();
-        if (warp < half) each(sh.part[warp], true);
+    for (int turn = 0; turn < OW / SLOTS; ++turn) {
+        // (64 rows: room for half of the warps, the others add to theirs)
+        if (warp / SLOTS == turn) {
+            float* p = sh.part[warp % SLOTS];
+#pragma unroll
+            for (int m = 0; m < R / 16; ++m)
+#pragma unroll
+                for (int j = 2 * m; j < R / 8; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float* v = s.v[Gram<R>::tile(m, j)];
+                        float2& q = *reinterpret_cast<float2*>(p + (16 * m + g + h * 8) * LD + 8 * j + 2 * t);
+                        if (turn) q = make_float2(q.x + v[2 * h], q.y + v[2 * h + 1]);
+                        else q = make_float2(v[2 * h], v[2 * h + 1]);
+                    }
+        }
         __syncthreads();
     }
-    if (warp == 0) each(sh.part[0], false);
     cg::cluster_group cl = cg::this_cluster();
-    cl.sync();
     const int blocks = (int)cl.num_blocks();
+    // (the tiles below the diagonal's block row are not there)
+    auto place = [](int a, int b) { return a / 16 <= b / 16 ? a * LD + b : b * LD + a; };
+    auto of_block = [&](int at) {
+        float v = sh.part[0][at];
+#pragma unroll
+        for (int w = 1; w < SLOTS; ++w) v += sh.part[w][at];
+        return v;
+    };
+    if (blocks == 1) {
+        for (int i = threadIdx.x; i < R * R; i += OT)
+            sh.A[x.row_of(i / R) * LD + x.row_of(i % R)] = of_block(place(i / R, i % R)) * scale;
+        __syncthreads();
+        return;
+    }
+    // each element's sum over the block's warps by one thread, into the first place, which others do not read
+    for (int i = threadIdx.x; i < R * R; i += OT)
+        if (i / R / 16 <= i % R / 16) sh.part[0][i / R * LD + i % R] = of_block(i / R * LD + i % R);
+    cl.sync();
     for (int i = threadIdx.x; i < R * R; i += OT) {
-        const int a = i / R, b = i % R;
-        // (the tiles below the diagonal's block row are not there)
-        const int at = a / 16 <= b / 16 ? a * LD + b : b * LD + a;
+        const int at = place(i / R, i % R);
         float v = 0.f;
         for (int k = 0; k < blocks; ++k) v += cl.map_shared_rank(&sh, k)->part[0][at];
-        sh.A[x.row_of(a) * LD + x.row_of(b)] = v * scale;
+        sh.A[x.row_of(i / R) * LD + x.row_of(i % R)] = v * scale;
     }
     cl.sync();
 }
@@ -356,7 +390,7 @@ __device__ __forceinline__ float scale_to(float m, int to) {
 // sh.P as fragments for P X, times the power of two that is returned
 template <typename T, int R>
 __device__ __forceinline__ float fragments(const Matrix<T, R>& x, OrthoShared<T, R>& sh) {
-    constexpr int LD = R + 4;
+    constexpr int LD = R + 8;
     float m = 0.f;
     for (int i = threadIdx.x; i < R * R; i += OT) m = fmaxf(m, fabsf(sh.P[i / R * LD + i % R]));
     m = block_max(m, sh.red);
@@ -433,12 +467,12 @@ __device__ __forceinline__ void times_p(const Matrix<T, R>& x, const OrthoShared
 
 // The sums of X X^T over the block's columns.
 template <typename T, int R>
-__device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, T* ring, int first, int end, Gram<R>& acc) {
+__device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, OrthoShared<T, R>& sh, int first, int end, Gram<R>& acc) {
     constexpr int J = R / 8;
     constexpr bool EXACT = sizeof(T) == 2;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     acc.clear();
-    over_tiles<T, R>(x, ring, first, end, [&](const T* tile, int) {
+    over_tiles<T, R>(x, sh, first, end, [&](const T* tile, int) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t hi[J][2], lo[J][2];
@@ -487,7 +521,7 @@ __device__ __forceinline__ void gram_of_px(const Matrix<T, R>& x, OrthoShared<T,
                                            Gram<R>& acc) {
     constexpr int J = R / 8;
     acc.clear();
-    over_tiles<T, R>(x, sh.ring, first, end, [&](const T* tile, int) {
+    over_tiles<T, R>(x, sh, first, end, [&](const T* tile, int) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float d[R / 16][2][4];
@@ -515,7 +549,7 @@ template <typename T, int R>
 __device__ __forceinline__ void write_px(const Matrix<T, R>& x, OrthoShared<T, R>& sh, float scale, int first, int end) {
     constexpr int J = R / 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    over_tiles<T, R>(x, sh.ring, first, end, [&](const T* tile, int k0) {
+    over_tiles<T, R>(x, sh, first, end, [&](const T* tile, int k0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float d[R / 16][2][4];
@@ -570,26 +604,58 @@ __device__ __forceinline__ void write_px(const Matrix<T, R>& x, OrthoShared<T, R
     });
 }
 
-// `steps` steps on sh.A and sh.P: P <- Q P with Q = a I + b A + c A^2, A <- Q A Q (they
-// commute); the last A where it is wanted.
+// `steps` steps on sh.A and sh.P: P <- Q P with Q = a I + b A + c A^2, and A <- Q A Q
+// between them.  All are polynomials in A, which commute and are symmetric but for
+// roundings.  Two of the products take a factor by rows for that; A^2 and Q P by columns:
+// a transposed P or A there let the roundings grow (a spread of singular values of 100
+// was off by 1e-5 of the result's norm instead of 2e-6).
 template <typename T, int R>
-__device__ __forceinline__ void small_steps(OrthoShared<T, R>& sh, const OrthoCoeffs& co, int steps, bool last_a) {
-    constexpr int LD = R + 4;
+__device__ __forceinline__ void small_steps(OrthoShared<T, R>& sh, const OrthoCoeffs& co, int steps) {
+    constexpr int LD = R + 8, TILES = R / 16 * (R / 8), MINE = (TILES + OW - 1) / OW;
+    const int warp = threadIdx.x >> 5;
+#pragma unroll 1
     for (int k = 0; k < steps; ++k) {
-        small_product<R>(sh.Q, sh.A, sh.A, co.c, sh.A, co.b, co.a);
-        small_product<R>(sh.B, sh.Q, sh.P, 1.f, nullptr, 0.f, 0.f);
-        for (int i = threadIdx.x; i < R * LD; i += OT) sh.P[i] = sh.B[i];
+        small_tiles<R>([&](int m, int n) {
+            float d[4];
+            small_tile<R, false>(sh.A, sh.A, m, n, d);
+            small_store<R>(sh.Q, m, n, [&](int i, int j, int e) {
+                return fmaf(co.c, d[e], co.b * sh.A[i * LD + j]) + (i == j ? co.a : 0.f);
+            });
+        });
         __syncthreads();
-        if (k + 1 < steps || last_a) {
-            small_product<R>(sh.B, sh.Q, sh.A, 1.f, nullptr, 0.f, 0.f);
-            small_product<R>(sh.A, sh.B, sh.Q, 1.f, nullptr, 0.f, 0.f);
+        float p[MINE][4];
+#pragma unroll
+        for (int q = 0; q < MINE; ++q) {
+            const int tile = warp + q * OW;
+            if (tile < TILES) small_tile<R, false>(sh.Q, sh.P, tile / (R / 8) * 16, tile % (R / 8) * 8, p[q]);
         }
+        if (k + 1 < steps) {
+            small_tiles<R>([&](int m, int n) {
+                float d[4];
+                small_tile<R, true>(sh.Q, sh.A, m, n, d);
+                small_store<R>(sh.W, m, n, [&](int, int, int e) { return d[e]; });
+            });
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < MINE; ++q) {
+            const int tile = warp + q * OW;
+            if (tile < TILES) small_store<R>(sh.P, tile / (R / 8) * 16, tile % (R / 8) * 8, [&](int, int, int e) { return p[q][e]; });
+        }
+        if (k + 1 < steps) {
+            small_tiles<R>([&](int m, int n) {
+                float d[4];
+                small_tile<R, true>(sh.W, sh.Q, m, n, d);
+                small_store<R>(sh.A, m, n, [&](int, int, int e) { return d[e]; });
+            });
+        }
+        __syncthreads();
     }
 }
 
 template <typename T, int R, int N>
 __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid_constant__ OrthoTab<N> tab) {
-    constexpr int LD = R + 4;
+    constexpr int LD = R + 8;
     extern __shared__ __align__(16) unsigned char smem[];
     OrthoShared<T, R>& sh = *reinterpret_cast<OrthoShared<T, R>*>(smem);
     cg::cluster_group cl = cg::this_cluster();
@@ -607,6 +673,7 @@ __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid
     };
     // The first scale from 1,024 elements: their root mean square becomes 2^5 or so, which leaves 2^10 for
     // larger ones.  Where that does not do, the sums are no numbers, and the largest magnitude says.
+    begin_tiles<T, R>(x, sh, first, end);
     float sq = 0.f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -617,7 +684,8 @@ __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid
     bool sure = sq > 1e-30f && sq < 1e30f;
     if (sure) {
         x.f = scale_to(sqrtf(sq), 5);
-        gram_of_x<T, R>(x, sh.ring, first, end, acc);
+        gram_of_x<T, R>(x, sh, first, end, acc);
+        begin_tiles<T, R>(x, sh, first, end);
         gather<T, R>(acc, x, 1.f, sh);
         sq = trace();
         sure = sq > 0.f && sq <= FLT_MAX;
@@ -638,6 +706,7 @@ __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid
         cl.sync();
         if (m > FLT_MAX) {
             // an infinity or NaN
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
             for (int64_t i = tid + (int64_t)rank * OT; i < size; i += (int64_t)OT * blocks)
                 x.dst[i] = from_f<T>(__int_as_float(0x7fc00000));
             return;
@@ -645,7 +714,8 @@ __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid
         sq = 0.f;
         if (m > 0.f) {
             x.f = scale_to(m, 15);
-            gram_of_x<T, R>(x, sh.ring, first, end, acc);
+            gram_of_x<T, R>(x, sh, first, end, acc);
+            begin_tiles<T, R>(x, sh, first, end);
             gather<T, R>(acc, x, 1.f, sh);
             sq = trace();
         } else {
@@ -668,17 +738,18 @@ __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid
     int left = tab.co.steps, phases = (left + STEPS_A_PHASE - 1) / STEPS_A_PHASE;
     while (true) {
         const int now = left / phases;
-        small_steps<T, R>(sh, tab.co, now, phases > 1);
+        small_steps<T, R>(sh, tab.co, now);
         left -= now;
         const float p = 1.f / fragments<T, R>(x, sh);
         if (--phases == 0) {
             write_px<T, R>(x, sh, p, first, end);
             return;
         }
-        // |X_k| from the A that the steps have left, so that its elements fit fp16 too
-        const float now_sq = trace(), u = now_sq > 0.f && now_sq <= FLT_MAX ? scale_to(sqrtf(now_sq), 14) : 1.f;
-        gram_of_px<T, R>(x, sh, p * u, first, end, acc);
-        gather<T, R>(acc, x, 1.f / (u * u), sh);
+        // P's elements are below 2^14 and M's columns below 2^15 long, so the product's below 2^32
+        constexpr float u = 0x1p-17f;
+        gram_of_px<T, R>(x, sh, u, first, end, acc);
+        begin_tiles<T, R>(x, sh, first, end);
+        gather<T, R>(acc, x, (p / u) * (p / u), sh);
     }
 }
 
@@ -706,9 +777,15 @@ cudaError_t launch_n(const OrthoEntry* e, int n, const OrthoCoeffs& co, int bloc
 
 constexpr int TAB_SMALL = 64, TAB_LARGE = 1300;      // 1.6 KB and 31 KB of kernel parameters
 
-// Blocks of a matrix's cluster: 512 columns each, two tiles a warp, or more.
-int blocks_for(int n) { return n >= 4096 ? 8 : n >= 2048 ? 4 : n >= 1024 ? 2 : 1; }
 int tile_for(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+
+// Blocks of a cluster for n matrices, the longest of `longest` columns: as few as fill the SMs
+// twice over, and no more than have 512 columns each, two tiles a warp.
+int blocks_for(int n, int longest, int num_sms) {
+    int blocks = 1;
+    while (blocks < 8 && (int64_t)n * blocks < 4 * num_sms && longest / blocks >= 1024) blocks *= 2;
+    return blocks;
+}
 
 template <typename T, int R>
 cudaError_t launch_r(const OrthoEntry* e, int n, const OrthoCoeffs& co, int blocks, cudaStream_t s) {
@@ -722,18 +799,15 @@ cudaError_t launch_r(const OrthoEntry* e, int n, const OrthoCoeffs& co, int bloc
 }
 
 template <typename T>
-cudaError_t launch_t(std::vector<OrthoEntry>& e, const OrthoCoeffs& co, cudaStream_t s) {
-    // a launch for each size of tile and cluster, the longest first
-    auto same = [](const OrthoEntry& a, const OrthoEntry& b) {
-        return tile_for(a.r) == tile_for(b.r) && blocks_for(a.n) == blocks_for(b.n);
-    };
+cudaError_t launch_t(std::vector<OrthoEntry>& e, const OrthoCoeffs& co, int num_sms, cudaStream_t s) {
+    // a launch for each size of tile, the longest first: short ones fill the end
     std::stable_sort(e.begin(), e.end(), [](const OrthoEntry& a, const OrthoEntry& b) {
         return tile_for(a.r) != tile_for(b.r) ? tile_for(a.r) > tile_for(b.r) : a.n > b.n;
     });
     for (size_t i = 0; i < e.size();) {
         size_t j = i;
-        while (j < e.size() && same(e[i], e[j])) ++j;
-        const int n = (int)(j - i), tile = tile_for(e[i].r), blocks = blocks_for(e[i].n);
+        while (j < e.size() && tile_for(e[j].r) == tile_for(e[i].r)) ++j;
+        const int n = (int)(j - i), tile = tile_for(e[i].r), blocks = blocks_for(n, e[i].n, num_sms);
         const cudaError_t err = tile == 16   ? launch_r<T, 16>(&e[i], n, co, blocks, s)
                                 : tile == 32 ? launch_r<T, 32>(&e[i], n, co, blocks, s)
                                              : launch_r<T, 64>(&e[i], n, co, blocks, s);
@@ -789,7 +863,11 @@ extern "C" int mlora_orthogonalize(const mlora_matrix_set* m, const mlora_newton
     }
     const OrthoCoeffs co{p->a, p->b, p->c, p->eps, p->steps};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t err = m->dtype == MLORA_BF16 ? launch_t<bf16>(e, co, s) : launch_t<float>(e, co, s);
+    if (e.empty()) return MLORA_OK;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess) err = m->dtype == MLORA_BF16 ? launch_t<bf16>(e, co, sms, s) : launch_t<float>(e, co, sms, s);
     if (err != cudaSuccess) return kv_fail(MLORA_E_CUDA, "orthogonalising: %s", cudaGetErrorString(err));
     return MLORA_OK;
 } catch (const std::bad_alloc&) {
