@@ -42,6 +42,7 @@ namespace {
 constexpr int OT = 256;                      // threads of a block
 constexpr int OW = OT / 32;
 constexpr int STEPS_A_PHASE = 3;
+constexpr int MAX_BLOCKS = 8;                // of a cluster
 
 struct OrthoEntry {
     const void* src;
@@ -67,14 +68,14 @@ __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__fl
 
 // d += a b, 16 x 8 x 8 with tf32 operands
 __device__ __forceinline__ void mma8(float (&d)[4], const float (&a)[4], float b0, float b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
                    "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 // d += a b, 16 x 8 x 16 with pairs of fp16
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -83,11 +84,12 @@ __device__ __forceinline__ uint32_t half2_of(float x, float y) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
     return h;
 }
-// x and y as fp16 and what that leaves
-__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
-    hi = half2_of(x, y);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    lo = half2_of(x - f.x, y - f.y);
+// x and y times f (a power of two) as fp16, and what that leaves
+__device__ __forceinline__ void split(float x, float y, float f, uint32_t& hi, uint32_t& lo) {
+    const float2 v = make_float2(x, y), ff = make_float2(f, f), p = mul2(v, ff);
+    hi = half2_of(p.x, p.y);
+    const float2 h = __half22float2(__hneg2(*reinterpret_cast<const __half2*>(&hi))), q = fma2(v, ff, h);
+    lo = half2_of(q.x, q.y);
 }
 
 // Four elements side by side as floats.
@@ -110,9 +112,12 @@ __device__ __forceinline__ float2 load2(const bf16* p) {
 // 4 elements to shared memory, or zeros
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* to, const void* from, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
-                 "n"(BYTES), "r"(there ? BYTES : 0)
-                 : "memory");
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if (BYTES == 16)                         // (past the first cache, which takes no smaller pieces so)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(there ? BYTES : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(BYTES), "r"(there ? BYTES : 0)
+                     : "memory");
 }
 
 constexpr int TC = 32;                       // columns of a tile
@@ -230,15 +235,28 @@ struct Gram {
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int j = 2 * m; j < J; ++j) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j0 = 2 * m; j0 < J; j0 += 2) {
+                // two tiles at a time: a product waits for the one before it in its chain
+                float d[2][4] = {};
                 if (!EXACT) {
-                    mma16(d, lo[2 * m][0], lo[2 * m + 1][0], lo[2 * m][1], lo[2 * m + 1][1], hi[j][0], hi[j][1]);
-                    mma16(d, hi[2 * m][0], hi[2 * m + 1][0], hi[2 * m][1], hi[2 * m + 1][1], lo[j][0], lo[j][1]);
-                }
-                mma16(d, hi[2 * m][0], hi[2 * m + 1][0], hi[2 * m][1], hi[2 * m + 1][1], hi[j][0], hi[j][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[tile(m, j)][e] += d[e];
+                    for (int j = 0; j < 2; ++j)
+                        mma16(d[j], lo[2 * m][0], lo[2 * m + 1][0], lo[2 * m][1], lo[2 * m + 1][1], hi[j0 + j][0], hi[j0 + j][1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        mma16(d[j], hi[2 * m][0], hi[2 * m + 1][0], hi[2 * m][1], hi[2 * m + 1][1], lo[j0 + j][0], lo[j0 + j][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mma16(d[j], hi[2 * m][0], hi[2 * m + 1][0], hi[2 * m][1], hi[2 * m + 1][1], hi[j0 + j][0], hi[j0 + j][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        float* a = &v[tile(m, j0 + j)][e];
+                        const float2 sum = add2(make_float2(a[0], a[1]), make_float2(d[j][e], d[j][e + 1]));
+                        a[0] = sum.x;
+                        a[1] = sum.y;
+                    }
+                }
             }
     }
 };
@@ -348,11 +366,22 @@ __device__ __forceinline__ void gather(Gram<R>& s, const Matrix<T, R>& x, float 
     for (int i = threadIdx.x; i < R * R; i += OT)
         if (i / R / 16 <= i % R / 16) sh.part[0][i / R * LD + i % R] = of_block(i / R * LD + i % R);
     cl.sync();
+    const float* from[MAX_BLOCKS];
+#pragma unroll
+    for (int k = 0; k < MAX_BLOCKS; ++k) from[k] = cl.map_shared_rank(&sh, k < blocks ? k : 0)->part[0];
+#pragma unroll 4
     for (int i = threadIdx.x; i < R * R; i += OT) {
-        const int at = place(i / R, i % R);
-        float v = 0.f;
-        for (int k = 0; k < blocks; ++k) v += cl.map_shared_rank(&sh, k)->part[0][at];
-        sh.A[x.row_of(i / R) * LD + x.row_of(i % R)] = v * scale;
+        const int a = i / R, b = i % R;
+        if (a / 16 > b / 16) continue;
+        // all blocks' loads at once
+        float v[MAX_BLOCKS], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < MAX_BLOCKS; ++k) v[k] = k < blocks ? from[k][a * LD + b] : 0.f;
+#pragma unroll
+        for (int k = 0; k < MAX_BLOCKS; ++k) sum += v[k];
+        sum *= scale;
+        sh.A[x.row_of(a) * LD + x.row_of(b)] = sum;
+        if (a / 16 < b / 16) sh.A[x.row_of(b) * LD + x.row_of(a)] = sum;
     }
     cl.sync();
 }
@@ -401,7 +430,7 @@ __device__ __forceinline__ float fragments(const Matrix<T, R>& x, OrthoShared<T,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {        // rows g, g + 8, g, g + 8; places 0, 1 and then 2, 3
             const float* p = sh.P + x.row_of(16 * mm + g + e % 2 * 8) * LD;
-            split(p[x.k_row(s, t, e / 2 * 2)] * scale, p[x.k_row(s, t, e / 2 * 2 + 1)] * scale, hi[e], lo[e]);
+            split(p[x.k_row(s, t, e / 2 * 2)], p[x.k_row(s, t, e / 2 * 2 + 1)], scale, hi[e], lo[e]);
         }
         sh.ph[mm][s][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         sh.pl[mm][s][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -438,7 +467,7 @@ __device__ __forceinline__ void times_p(const Matrix<T, R>& x, const OrthoShared
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if (EXACT) hi[s][c][e] = half2_of(v[c][2 * e] * x.f, v[c][2 * e + 1] * x.f);
-                else split(v[c][2 * e] * x.f, v[c][2 * e + 1] * x.f, hi[s][c][e], lo[s][c][e]);
+                else split(v[c][2 * e], v[c][2 * e + 1], x.f, hi[s][c][e], lo[s][c][e]);
             }
     }
 #pragma unroll
@@ -453,9 +482,10 @@ __device__ __forceinline__ void times_p(const Matrix<T, R>& x, const OrthoShared
             const uint4 l = sh.pl[m][s][lane];
             a[s] = sh.ph[m][s][lane];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                mma16(d[m][c], l.x, l.y, l.z, l.w, hi[s][c][0], hi[s][c][1]);
-                if (!EXACT) mma16(d[m][c], a[s].x, a[s].y, a[s].z, a[s].w, lo[s][c][0], lo[s][c][1]);
+            for (int c = 0; c < 2; ++c) mma16(d[m][c], l.x, l.y, l.z, l.w, hi[s][c][0], hi[s][c][1]);
+            if (!EXACT) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) mma16(d[m][c], a[s].x, a[s].y, a[s].z, a[s].w, lo[s][c][0], lo[s][c][1]);
             }
         }
 #pragma unroll
@@ -473,12 +503,12 @@ __device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, OrthoShared<T, 
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     acc.clear();
     over_tiles<T, R>(x, sh, first, end, [&](const T* tile, int) {
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             uint32_t hi[J][2], lo[J][2];
             auto put = [&](int j, int e, float a, float b) {
                 if (EXACT) hi[j][e] = half2_of(a * x.f, b * x.f);
-                else split(a * x.f, b * x.f, hi[j][e], lo[j][e]);
+                else split(a, b, x.f, hi[j][e], lo[j][e]);
             };
             if (x.tall) {
                 // columns 16 h + 4 t + q, rows J g ..
@@ -522,7 +552,7 @@ __device__ __forceinline__ void gram_of_px(const Matrix<T, R>& x, OrthoShared<T,
     constexpr int J = R / 8;
     acc.clear();
     over_tiles<T, R>(x, sh, first, end, [&](const T* tile, int) {
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             float d[R / 16][2][4];
             times_p<T, R>(x, sh, tile, h, d);
@@ -531,7 +561,7 @@ __device__ __forceinline__ void gram_of_px(const Matrix<T, R>& x, OrthoShared<T,
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    split(d[j / 2][c][j % 2 * 2] * scale, d[j / 2][c][j % 2 * 2 + 1] * scale, hi[j][c], lo[j][c]);
+                    split(d[j / 2][c][j % 2 * 2], d[j / 2][c][j % 2 * 2 + 1], scale, hi[j][c], lo[j][c]);
             acc.template add<false>(hi, lo);
         }
     });
@@ -550,7 +580,7 @@ __device__ __forceinline__ void write_px(const Matrix<T, R>& x, OrthoShared<T, R
     constexpr int J = R / 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     over_tiles<T, R>(x, sh, first, end, [&](const T* tile, int k0) {
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             float d[R / 16][2][4];
             times_p<T, R>(x, sh, tile, h, d);
@@ -783,7 +813,7 @@ int tile_for(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
 // twice over, and no more than have 512 columns each, two tiles a warp.
 int blocks_for(int n, int longest, int num_sms) {
     int blocks = 1;
-    while (blocks < 8 && (int64_t)n * blocks < 4 * num_sms && longest / blocks >= 1024) blocks *= 2;
+    while (blocks < MAX_BLOCKS && (int64_t)n * blocks < 4 * num_sms && longest / blocks >= 1024) blocks *= 2;
     return blocks;
 }
 
