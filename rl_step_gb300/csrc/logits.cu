@@ -362,16 +362,23 @@ __global__ void __launch_bounds__(BT, 4) token_logprobs_kernel(const __grid_cons
     const int k = v.top;
 
     // the quick pass
-    constexpr int UN = sizeof(T) == 2 ? 4 : 2;      // groups in flight: 128 bytes a thread
+    constexpr int UN = sizeof(T) == 2 ? 2 : 1;      // groups in work, and as many on their way: 64 bytes each a thread
     Part p{-FLT_MAX, 0.f, 0.f};
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
     u64 best = 0;
     const float2 cc = make_float2(c, c);
+    Group<T> next[UN];
+    auto fetch = [&](int g0) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (g0 + u * NT < r.groups) next[u].load(r.first + (int64_t)(g0 + u * NT) * G);
+    };
+    fetch(tid);
     for (int g0 = tid; g0 < r.groups; g0 += UN * NT) {
         Group<T> q[UN];
 #pragma unroll
-        for (int u = 0; u < UN; ++u)
-            if (g0 + u * NT < r.groups) q[u].load(r.first + (int64_t)(g0 + u * NT) * G);
+        for (int u = 0; u < UN; ++u) q[u] = next[u];
+        fetch(g0 + UN * NT);
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             const int g = g0 + u * NT;
@@ -486,143 +493,172 @@ struct GradView {
     mlora_token_grads g;
     void* out;
     int64_t ldo;
-    int segment;                            // ids of a block
 };
 
 // dx = p (k0 + k1 a) + what the row's own ids add, a = log2 p.
 struct RowGrad {
     float c, lse2, k0, k1;
 };
-__device__ __forceinline__ float grad_of(float x, const RowGrad& r) {
-    const float a = max_nan(fmaf(x, r.c, -r.lse2), -200.f);
-    return ex2(a) * fmaf(r.k1, a, r.k0);
+__device__ __forceinline__ float2 grad2(float2 x, const RowGrad& r) {
+    float2 a = fma2(x, make_float2(r.c, r.c), make_float2(-r.lse2, -r.lse2));
+    a.x = max_nan(a.x, -200.f);
+    a.y = max_nan(a.y, -200.f);
+    return mul2(make_float2(ex2(a.x), ex2(a.y)), fma2(make_float2(r.k1, r.k1), a, make_float2(r.k0, r.k0)));
 }
 
-// A block takes `segment` ids of one row; bound by reading and writing them.  The
-// ids that get more than the softmax's part (the target and the alternatives) are
-// read before the block writes anything, as dlogits may be the logits, and written
-// last, each by one thread with all that it gets.
+// What a warp knows of its row: lane l the l-th alternative's id and gradient, every
+// lane the target's.
+struct RowIds {
+    int id, y;
+    float d, dy;
+    // which of them lie in [a, b); bit 32: the target
+    __device__ __forceinline__ u64 within(int a, int b) const {
+        const u64 m = __ballot_sync(0xffffffffu, id >= a && id < b);
+        return y >= a && y < b ? m | (u64)1 << 32 : m;
+    }
+    // f(id, gradient) for each id of the mask, in one order
+    template <typename F>
+    __device__ __forceinline__ void each(u64 mask, F&& f) const {
+        if (mask >> 32) f(y, dy);
+        for (uint32_t m = (uint32_t)mask; m; m &= m - 1) {
+            const int l = __ffs(m) - 1;
+            f(__shfl_sync(0xffffffffu, id, l), __shfl_sync(0xffffffffu, d, l));
+        }
+    }
+};
+
+// The ids [a, b) of a row one by one (ends, and rows that do not lie alike in memory).
 template <typename T>
-__global__ void __launch_bounds__(BT) token_grad_kernel(const __grid_constant__ GradView w) {
+__device__ __forceinline__ void grad_one_by_one(const T* x, T* out, int a, int b, const RowGrad& r, const RowIds& ids,
+                                                bool zero, int lane) {
+    for (int i0 = a; i0 < b; i0 += 32) {
+        const int i = i0 + lane;
+        const u64 hit = zero ? 0 : ids.within(i0, min(i0 + 32, b));
+        float d = 0.f;
+        if (i < b && !zero) d = grad2(make_float2(to_f(x[i]), 0.f), r).x;
+        ids.each(hit, [&](int id, float add) { d += id == i ? add : 0.f; });
+        if (i < b) out[i] = from_f<T>(d);
+    }
+}
+
+// A warp works alone: it finds what its row's gradients come to, then takes windows of
+// 2 x 32 x 32 bytes of the row, the next one on its way while one is formed.  The
+// target's and the alternatives' own gradients are added where a window holds them,
+// before the one rounding; as each id is read and written by one thread, dlogits may be
+// the logits.  WARPS: of a row (1: rows so short that a block takes eight).
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(BT, 3) token_grad_kernel(const __grid_constant__ GradView w) {
     const LogitsView& v = w.v;
-    const int64_t row = blockIdx.x;
-    const int V = v.V, k = w.g.d_top ? v.top : 0, tid = threadIdx.x;
-    const int a = blockIdx.y * w.segment, b = min(V - a, w.segment) + a;
+    constexpr int ROWS = BT / 32 / WARPS, PER = 32 / (int)sizeof(T);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + warp / WARPS;
+    if (row >= v.n_rows) return;
+    const int V = v.V, k = w.g.d_top ? v.top : 0;
+    const int first = blockIdx.y * WARPS + warp % WARPS, step = gridDim.y * WARPS;     // this warp's windows
     const T* x = static_cast<const T*>(v.x) + row * v.ld;
     T* out = static_cast<T*>(w.out) + row * w.ldo;
-    __shared__ int s_id[MAX_TOP + 1];
-    __shared__ float s_d[MAX_TOP + 1];
-    __shared__ RowGrad s_r;
-    __shared__ int s_zero;
-    if (tid <= k) {
-        int id;
-        float d = 0.f;
-        if (tid == 0) {
-            id = v.targets && w.g.d_logprobs ? v.targets[row] : -1;
-        } else {
-            id = w.g.top_ids[row * v.top + tid - 1];
-        }
-        if (id < -1 || id >= V) {
-            if (blockIdx.y == 0) raise_status(v.status, ST_RANGE);
-            id = -1;
-        }
-        if (id >= 0) d = tid == 0 ? w.g.d_logprobs[row] : w.g.d_top[row * v.top + tid - 1];
-        s_id[tid] = id;
-        s_d[tid] = d;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        const float de = w.g.d_entropy ? w.g.d_entropy[row] : 0.f, dl = w.g.d_lse ? w.g.d_lse[row] : 0.f;
-        const float lse = w.g.lse[row];
-        float sum = 0.f;
-        bool zero = de == 0.f && dl == 0.f;
-        for (int i = 0; i <= k; ++i) {
-            sum += s_d[i];
-            zero = zero && s_d[i] == 0.f;
-        }
-        RowGrad r;
-        r.c = v.scale * LOG2E;
-        r.lse2 = lse * LOG2E;
-        r.k0 = v.scale * (dl - sum);
-        r.k1 = 0.f;
-        if (de != 0.f) {
-            r.k0 = fmaf(-v.scale * de, w.g.entropy[row], r.k0);
-            r.k1 = -v.scale * de * LN2;
-        }
-        s_r = r;
-        s_zero = zero || lse == -INFINITY;
-    }
-    __syncthreads();
-    const RowGrad r = s_r;
-    const bool zero = s_zero;
-    // the ids with more, first
-    float own = 0.f;
-    int own_id = -1;
-    if (!zero && tid <= k && s_id[tid] >= a && s_id[tid] < b) {
-        const int id = s_id[tid];
-        bool first = true;
-        for (int i = 0; i < tid; ++i) first = first && s_id[i] != id;
-        if (first) {
-            float d = 0.f;
-            for (int i = tid; i <= k; ++i) d += s_id[i] == id ? s_d[i] : 0.f;
-            own_id = id;
-            own = fmaf(v.scale, d, grad_of(to_f(x[id]), r));
-        }
-    }
-    __syncthreads();
-    constexpr int PER = 32 / (int)sizeof(T);
-    const uintptr_t px = reinterpret_cast<uintptr_t>(x + a) & 31, po = reinterpret_cast<uintptr_t>(out + a) & 31;
-    int lead = b - a, vecs = 0;             // ids before the first whole 32 bytes, and 32 bytes
-    if (px == po) {
-        lead = min((int)((32 - px) % 32 / sizeof(T)), b - a);
-        vecs = (b - a - lead) / PER;
-    }
-    const T* xv = x + a + lead;
-    T* ov = out + a + lead;
-    const float2 cc = make_float2(r.c, r.c), ll = make_float2(-r.lse2, -r.lse2), k0 = make_float2(r.k0, r.k0),
-                 k1 = make_float2(r.k1, r.k1);
-    auto pair = [&](float2 q) {
-        float2 e = fma2(q, cc, ll);
-        e.x = max_nan(e.x, -200.f);
-        e.y = max_nan(e.y, -200.f);
-        return mul2(make_float2(ex2(e.x), ex2(e.y)), fma2(k1, e, k0));
-    };
-    constexpr int UN = 4;
-    for (int i0 = tid; i0 < vecs; i0 += UN * BT) {
-        uint32_t q[UN][8];
-        if (!zero) {
+
+    // every load that the row's factors need at once
+    RowIds ids;
+    ids.id = lane < k ? w.g.top_ids[row * v.top + lane] : -1;
+    ids.y = v.targets && w.g.d_logprobs ? v.targets[row] : -1;
+    ids.d = lane < k ? w.g.d_top[row * v.top + lane] : 0.f;
+    ids.dy = w.g.d_logprobs ? w.g.d_logprobs[row] : 0.f;
+    const float de = w.g.d_entropy ? w.g.d_entropy[row] : 0.f, dl = w.g.d_lse ? w.g.d_lse[row] : 0.f;
+    const float lse = w.g.lse[row], entropy = w.g.d_entropy ? w.g.entropy[row] : 0.f;
+    const bool bad = ids.id < -1 || ids.id >= V || ids.y < -1 || ids.y >= V;
+    if (bad && first == 0) raise_status(v.status, ST_RANGE);
+    if (ids.id < 0 || ids.id >= V) ids.id = -1, ids.d = 0.f;
+    if (ids.y < 0 || ids.y >= V) ids.y = -1, ids.dy = 0.f;
+    const bool zero = __all_sync(0xffffffffu, ids.d == 0.f && ids.dy == 0.f && de == 0.f && dl == 0.f) || lse == -INFINITY;
+    float sum = ids.d;
 #pragma unroll
-            for (int u = 0; u < UN; ++u)
-                if (i0 + u * BT < vecs) load32(xv + (int64_t)(i0 + u * BT) * PER, q[u]);
-        }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    RowGrad r;
+    r.c = v.scale * LOG2E;
+    r.lse2 = lse * LOG2E;
+    r.k0 = v.scale * (dl - (sum + ids.dy));
+    r.k1 = 0.f;
+    if (de != 0.f) {
+        r.k0 = fmaf(-v.scale * de, entropy, r.k0);
+        r.k1 = -v.scale * de * LN2;
+    }
+    ids.d *= v.scale;
+    ids.dy *= v.scale;
+
+    const uintptr_t px = reinterpret_cast<uintptr_t>(x) & 31, po = reinterpret_cast<uintptr_t>(out) & 31;
+    if (px != po) {
+        constexpr int SPAN = 256;
+        for (int64_t a = (int64_t)first * SPAN; a < V; a += (int64_t)step * SPAN)
+            grad_one_by_one(x, out, (int)a, (int)min(a + SPAN, (int64_t)V), r, ids, zero, lane);
+        return;
+    }
+    const int lead = min((int)((32 - px) % 32 / sizeof(T)), V), vecs = (V - lead) / PER, tail = lead + vecs * PER;
+    if (first == 0) grad_one_by_one(x, out, 0, lead, r, ids, zero, lane);
+    if (first == step - 1) grad_one_by_one(x, out, tail, V, r, ids, zero, lane);
+    const T* xv = x + lead;
+    T* ov = out + lead;
+    constexpr int UN = 2, WIN = UN * 32;                     // vectors of a window
+    uint32_t q[UN][8], next[UN][8];
+    auto fetch = [&](int v0, uint32_t (&to)[UN][8]) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (v0 + 32 * u + lane < vecs && !zero) load32(xv + (int64_t)(v0 + 32 * u + lane) * PER, to[u]);
+    };
+    fetch(first * WIN, next);
+    for (int v0 = first * WIN; v0 < vecs; v0 += step * WIN) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[u][j] = zero ? 0 : next[u][j];
+        fetch(v0 + step * WIN, next);
+        const int id0 = lead + v0 * PER;
+        const u64 hit = zero ? 0 : ids.within(id0, id0 + WIN * PER);
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            if (i0 + u * BT >= vecs) break;
-            if (zero) {
+            float2 d[PER / 2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) q[u][j] = 0;
-            } else if (sizeof(T) == 2) {
+            for (int j = 0; j < PER / 2; ++j) {
+                const float2 xx = sizeof(T) == 2 ? bf16_pair(q[u][j % 8])
+                                                 : make_float2(__uint_as_float(q[u][2 * j % 8]), __uint_as_float(q[u][(2 * j + 1) % 8]));
+                d[j] = grad2(xx, r);
+            }
+            if (hit) {
+                const int mine = id0 + (32 * u + lane) * PER;
+                ids.each(hit, [&](int id, float add) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 d = pair(bf16_pair(q[u][j]));
-                    q[u][j] = pack_bf16x2(d.x, d.y);
-                }
-            } else {
+                    for (int j = 0; j < PER / 2; ++j) {
+                        d[j].x += id == mine + 2 * j ? add : 0.f;
+                        d[j].y += id == mine + 2 * j + 1 ? add : 0.f;
+                    }
+                });
+            }
+            if (!zero) {
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float2 d = pair(make_float2(__uint_as_float(q[u][j]), __uint_as_float(q[u][j + 1])));
-                    q[u][j] = __float_as_uint(d.x);
-                    q[u][j + 1] = __float_as_uint(d.y);
+                for (int j = 0; j < PER / 2; ++j) {
+                    if (sizeof(T) == 2) {
+                        q[u][j % 8] = pack_bf16x2(d[j].x, d[j].y);
+                    } else {
+                        q[u][2 * j % 8] = __float_as_uint(d[j].x);
+                        q[u][(2 * j + 1) % 8] = __float_as_uint(d[j].y);
+                    }
                 }
             }
-            store32(ov + (int64_t)(i0 + u * BT) * PER, q[u]);
+            if (v0 + 32 * u + lane < vecs) store32(ov + (int64_t)(v0 + 32 * u + lane) * PER, q[u]);
         }
     }
-    const int done = lead + vecs * PER;
-    for (int i = tid; i < lead; i += BT) out[a + i] = zero ? from_f<T>(0.f) : from_f<T>(grad_of(to_f(x[a + i]), r));
-    for (int i = a + done + tid; i < b; i += BT) out[i] = zero ? from_f<T>(0.f) : from_f<T>(grad_of(to_f(x[i]), r));
-    __syncthreads();
-    if (own_id >= 0) out[own_id] = from_f<T>(own);
+}
+
+template <typename T>
+void launch_grad(const GradView& w, int num_sms, cudaStream_t s) {
+    const int64_t n = w.v.n_rows;
+    if (w.v.V <= WARP_V) {
+        token_grad_kernel<T, 1><<<(unsigned)((n + 7) / 8), BT, 0, s>>>(w);
+        return;
+    }
+    // as many blocks a row as fill the SMs, and as have a window for each warp
+    const int64_t most = w.v.V * (int64_t)sizeof(T) / (8 * 2048) + 1, want = (3 * 2 * (int64_t)num_sms + n - 1) / n;
+    token_grad_kernel<T, 8><<<dim3((unsigned)n, (unsigned)(want < most ? want : most)), BT, 0, s>>>(w);
 }
 
 // ----------------------------------------------------------------------------
@@ -753,7 +789,7 @@ extern "C" int mlora_token_logprobs(const mlora_logits* x, const mlora_token_sta
 extern "C" int mlora_token_logprobs_backward(const mlora_logits* x, const mlora_token_grads* g, void* dlogits,
                                              int64_t out_stride, void* stream) {
     GradView w;
-    const int rc = view_check(x, &w.v);
+    int rc = view_check(x, &w.v);
     if (rc) return rc;
     if (!g) return kv_fail(MLORA_E_ARG, "NULL gradients");
     const int64_t n = x->n_rows, es = x->dtype == MLORA_BF16 ? 2 : 4;
@@ -773,12 +809,11 @@ extern "C" int mlora_token_logprobs_backward(const mlora_logits* x, const mlora_
     if (x->top == 0) w.g.d_top = nullptr;
     w.out = dlogits;
     w.ldo = out_stride;
-    // ids of a block: a whole number of rounds of 4 x 32 bytes a thread
-    w.segment = 4 * 32 / (int)es * BT;
-    const dim3 grid((unsigned)n, (unsigned)((x->vocab + w.segment - 1) / w.segment));
+    int sms = 0;
+    if ((rc = sm_count(&sms))) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (x->dtype == MLORA_BF16) token_grad_kernel<bf16><<<grid, BT, 0, s>>>(w);
-    else token_grad_kernel<float><<<grid, BT, 0, s>>>(w);
+    if (x->dtype == MLORA_BF16) launch_grad<bf16>(w, sms, s);
+    else launch_grad<float>(w, sms, s);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "gradient launch: %s", cudaGetErrorString(e));
     return MLORA_OK;
