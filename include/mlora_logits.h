@@ -20,8 +20,9 @@
  * all results and ids -1.
  * Sums and statistics are fp32: lse and the logprobs are off by about 2^-21 plus
  * 2^-22 of themselves, the entropy by 2^-21 plus 2^-21 of itself.  scale * x has to
- * lie within fp32's range.  Results repeat bit for bit, and a row's do not depend on
- * the other rows' values.
+ * lie within fp32's range.  Results repeat bit for bit; a row's do not depend on the other
+ * rows' values, but their number and the vocabulary decide how many threads share a row,
+ * and so the order of its sums.
  *
  * Conventions are those of mlora.h.  No call allocates or synchronises, so all
  * can be captured into a CUDA graph.

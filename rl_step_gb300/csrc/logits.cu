@@ -4,8 +4,8 @@
 // What bounds both: bytes.  The forward reads each logit once, the gradient
 // reads and writes each once.
 //
-// Forward.  A team of threads (a warp for small vocabularies, a block, or a cluster
-// of blocks where the rows are few) takes a row.  In base 2, with c = scale log2 e,
+// Forward.  A team of threads (a warp to a block by the vocabulary, a cluster of blocks
+// where the rows are few) takes a row.  In base 2, with c = scale log2 e,
 // each thread keeps the maximum m of its x c and
 //     s = sum 2^(x c - m),   t = sum 2^(x c - m) (x c - m),
 // corrected when m rises, a group of 16 logits at a time; joined over the team
@@ -17,6 +17,7 @@
 // alternatives, as a group is 16 ids in a row; they are found from 64-bit keys
 // (value, complement of the id), whose order is the order of the results, and only
 // their 32 or 64 bytes are read again.
+#include <algorithm>
 #include <cfloat>
 #include <cooperative_groups.h>
 
@@ -32,7 +33,8 @@ namespace {
 constexpr int G = 16;                         // logits of a group
 constexpr int BT = 256;                       // threads of a block
 constexpr int MAX_TOP = MLORA_LOGITS_MAX_TOP;
-constexpr int LIST = 576;                     // entries of a team's list: MAX_TOP groups of 16 and at most 30 logits beside them
+constexpr int LIST = 96;                      // groups that a team lists
+constexpr int FOUND = MAX_TOP * G + 32;       // and logits: MAX_TOP groups of 16 and at most 30 beside them
 constexpr float LOWEST = -1e30f;              // below it a logit counts as -infinity in the quick pass
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -127,18 +129,24 @@ __device__ __forceinline__ Part join(const Part& a, const Part& b) {
 
 // What a team shares.
 struct TeamShared {
-    u64 list[LIST];
+    u64 list[LIST], found[FOUND];
     u64 pick[MAX_TOP];
     Part part[BT / 32];
-    Part all;
     u64 tau;
-    int n;
+    int n, n_found;
+};
+// What the blocks of a cluster hand to its first one.
+constexpr int MAX_BLOCKS = 8;
+struct ClusterShared {
+    u64 pick[MAX_BLOCKS * MAX_TOP];
+    Part part[MAX_BLOCKS];
 };
 
 template <int NT>
 __device__ __forceinline__ void team_sync() {
     if (NT == 32) __syncwarp();
-    else __syncthreads();
+    else if (NT == BT) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"((int)(threadIdx.x / NT) + 1), "n"(NT) : "memory");
 }
 
 // over the team; every thread returns it, in one fixed order
@@ -154,9 +162,9 @@ __device__ __forceinline__ Part team_join(Part p, TeamShared& sh, int tid) {
         p = tid & o ? join(q, p) : join(p, q);
     }
     if (NT == 32) return p;
-    __syncthreads();
+    team_sync<NT>();
     if ((tid & 31) == 0) sh.part[tid >> 5] = p;
-    __syncthreads();
+    team_sync<NT>();
     p = sh.part[0];
 #pragma unroll
     for (int w = 1; w < NT / 32; ++w) p = join(p, sh.part[w]);
@@ -204,36 +212,35 @@ __device__ __forceinline__ void rank_keys(const u64* list, int n, int k, u64* ou
 }
 
 // The share's k largest logits in sh.pick as (value, id) keys in falling order, 0
-// where there are none.  gmax: the groups' keys; mine: the largest (key, group) of
-// this thread's.
+// where there are none.  gmax: the groups' largest values; best, at: the largest of this
+// thread's and its group (-1: none).
 template <typename T, int NT>
-__device__ void top_of_share(const Share<T>& r, const uint32_t* gmax, u64 mine, int k, TeamShared& sh, int tid) {
-    constexpr int QUAD = NT == 32 ? 1 : NT / 64;       // threads of a first-round key: 32 or 64 keys, at least k
-    if (tid == 0) { sh.tau = 1; sh.n = 0; }
-    if (QUAD > 1) {
+__device__ void top_of_share(const Share<T>& r, const T* gmax, float best, int at, int k, TeamShared& sh, int tid) {
+    constexpr int QUAD = NT == 32 ? 1 : NT / 64, KEYS = NT / QUAD; // threads of a first-round key; 32 or 64 keys, at least k
+    u64 mine = at >= 0 ? key64(key_of(best), at) : 0;
+    if (tid == 0) { sh.tau = 1; sh.n = sh.n_found = 0; }
+    for (int i = tid; i < k; i += NT) sh.pick[i] = 0;
 #pragma unroll
-        for (int o = 1; o < QUAD; o <<= 1) {
-            const u64 q = __shfl_xor_sync(0xffffffffu, mine, o);
-            mine = q > mine ? q : mine;
-        }
+    for (int o = 1; o < QUAD; o <<= 1) {
+        const u64 q = __shfl_xor_sync(0xffffffffu, mine, o);
+        mine = q > mine ? q : mine;
     }
     if (tid % QUAD == 0) sh.list[tid / QUAD] = mine;
     team_sync<NT>();
-    // the k-th largest of these keys: at least k groups are not below it
-    if (tid < NT / QUAD) {
-        const u64 key = sh.list[tid];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < NT / QUAD; ++j) rank += sh.list[j] > key;
-        if (rank == k - 1 && key) sh.tau = key;
-    }
+    // the k-th largest of these keys: at least k groups are not below it.  A quad counts for its key together.
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < KEYS / QUAD; ++j) rank += sh.list[j * QUAD + tid % QUAD] > mine;
+#pragma unroll
+    for (int o = 1; o < QUAD; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (rank == k - 1 && mine && tid % QUAD == 0) sh.tau = mine;
     team_sync<NT>();
     u64 tau = sh.tau;
     for (int g = tid; g < r.groups; g += NT) {
-        const u64 key = key64(gmax[g], g);
+        const u64 key = key64(key_of(to_f(gmax[g])), g);
         if (key >= tau) {
-            const int at = atomicAdd(&sh.n, 1);
-            if (at < LIST) sh.list[at] = key;
+            const int to = atomicAdd(&sh.n, 1);
+            if (to < LIST) sh.list[to] = key;
         }
     }
     team_sync<NT>();
@@ -246,7 +253,7 @@ __device__ void top_of_share(const Share<T>& r, const uint32_t* gmax, u64 mine, 
             if (tid == 0) sh.n = 0;
             team_sync<NT>();
             int c = 0;
-            for (int g = tid; g < r.groups; g += NT) c += key64(gmax[g], g) >= want;
+            for (int g = tid; g < r.groups; g += NT) c += key64(key_of(to_f(gmax[g])), g) >= want;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
             if ((tid & 31) == 0) atomicAdd(&sh.n, c);
@@ -257,39 +264,42 @@ __device__ void top_of_share(const Share<T>& r, const uint32_t* gmax, u64 mine, 
         if (tid == 0) sh.n = 0;
         team_sync<NT>();
         for (int g = tid; g < r.groups; g += NT) {
-            const u64 key = key64(gmax[g], g);
+            const u64 key = key64(key_of(to_f(gmax[g])), g);
             if (key >= tau) sh.list[atomicAdd(&sh.n, 1)] = key;
         }
         team_sync<NT>();
     }
-    // the k largest groups
-    const int ng = sh.n, kg = ng < k ? ng : k;
-    rank_keys<NT>(sh.list, ng, k, sh.pick, tid);
-    team_sync<NT>();
-    const uint32_t low = kg == k ? (uint32_t)(sh.pick[k - 1] >> 32) : 0;
-    if (tid == 0) sh.n = 0;
-    team_sync<NT>();
-    // their logits that are not below the last one's largest, and the edges
-    for (int i = tid; i < kg * G + r.edges; i += NT) {
-        const int id = i < kg * G ? r.id0 + (int)id_of(sh.pick[i / G]) * G + i % G : r.edge_id(i - kg * G);
+    int ng = sh.n;
+    if (ng > MAX_TOP) {
+        // more than their logits have room for: the k largest alone
+        rank_keys<NT>(sh.list, ng, k, sh.pick, tid);
+        team_sync<NT>();
+        ng = k;
+        tau = sh.pick[k - 1];
+        u64 mine_too = 0;
+        if (NT == 32 || tid < 32) mine_too = tid < k ? sh.pick[tid] : 0;
+        team_sync<NT>();
+        if (tid < k) { sh.list[tid] = mine_too; sh.pick[tid] = 0; }
+        team_sync<NT>();
+    }
+    // their logits that are not below that group's largest, and the edges'
+    const uint32_t low = (uint32_t)(tau >> 32);
+#pragma unroll 4
+    for (int i = tid; i < ng * G + r.edges; i += NT) {
+        const int id = i < ng * G ? r.id0 + (int)id_of(sh.list[i / G]) * G + i % G : r.edge_id(i - ng * G);
         const float x = to_f(r.row[id]);
         const uint32_t key = key_of(x);
-        if (x > -INFINITY && key >= low) {
-            sh.list[atomicAdd(&sh.n, 1)] = key64(key, id);
-        }
+        if (x > -INFINITY && key >= low) sh.found[atomicAdd(&sh.n_found, 1)] = key64(key, id);
     }
     team_sync<NT>();
-    const int n = sh.n;
-    for (int i = tid; i < k; i += NT) sh.pick[i] = 0;
-    team_sync<NT>();
-    rank_keys<NT>(sh.list, n, k, sh.pick, tid);
+    rank_keys<NT>(sh.found, sh.n_found, k, sh.pick, tid);
     team_sync<NT>();
 }
 
 // A row that the quick pass cannot take: NaN, an infinite maximum, or one so large
 // that a product with c is off by a power of two.  *kind: 1 NaN or +infinity, 2 no
 // finite logit; *top: the maximum.
-template <typename T, int NT, bool CLUSTER>
+template <typename T, int NT>
 __device__ __noinline__ Part careful(const Share<T>& r, float c, TeamShared& sh, int tid, int* kind, float* top) {
     float m = -INFINITY;
     auto each = [&](auto&& f) {
@@ -306,15 +316,6 @@ __device__ __noinline__ Part careful(const Share<T>& r, float c, TeamShared& sh,
 #pragma unroll
     for (int w = 1; w < NT / 32; ++w) m = max_nan(m, sh.part[w].m);
     team_sync<NT>();
-    if (CLUSTER) {
-        cg::cluster_group cl = cg::this_cluster();
-        if (tid == 0) sh.all.m = m;
-        cl.sync();
-        float all = -INFINITY;
-        for (unsigned b = 0; b < cl.num_blocks(); ++b) all = max_nan(all, cl.map_shared_rank(&sh, b)->all.m);
-        cl.sync();
-        m = all;
-    }
     *kind = !(m <= FLT_MAX) ? 1 : m == -INFINITY ? 2 : 0;
     *top = m;
     Part p{0.f, 0.f, 0.f};                   // relative to the maximum, whose product with c may leave fp32
@@ -328,44 +329,54 @@ __device__ __noinline__ Part careful(const Share<T>& r, float c, TeamShared& sh,
     return team_join<NT>(p, sh, tid);
 }
 
-// Rows of at most this many logits go to a warp each.  1,000 logits: see launch.
-constexpr int WARP_V = 4096;
+
+template <typename T> constexpr int blocks_an_sm() { return sizeof(T) == 2 ? 4 : 3; }      // their registers
 
 template <typename T, int NT, bool CLUSTER>
-__global__ void __launch_bounds__(BT, 4) token_logprobs_kernel(const __grid_constant__ LogitsView v,
-                                                               const __grid_constant__ mlora_token_stats out, int gcap) {
-    extern __shared__ uint32_t gmax_all[];
+__global__ void __launch_bounds__(BT, blocks_an_sm<T>())
+token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constant__ mlora_token_stats out, int gcap) {
+    extern __shared__ __align__(16) unsigned char gmax_all[];
     __shared__ TeamShared shared[BT / NT];
+    __shared__ ClusterShared got;            // (the first block's is used)
     const int tid = threadIdx.x % NT, team = threadIdx.x / NT;
     TeamShared& sh = shared[team];
-    uint32_t* gmax = gmax_all + team * gcap;
+    T* gmax = reinterpret_cast<T*>(gmax_all) + team * gcap;
     int rank = 0, blocks = 1;
     if (CLUSTER) {
         rank = (int)cg::this_cluster().block_rank();
         blocks = (int)cg::this_cluster().num_blocks();
+        // the first block's memory may be written once it runs: waited for before that
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     }
-    const int64_t row = CLUSTER ? blockIdx.x / blocks : (int64_t)blockIdx.x * (BT / NT) + team;
-    if (row >= v.n_rows) return;             // a whole team (a cluster's row exists)
-    int64_t o = row;
-    int y = v.targets ? v.targets[row] : -1;
-    if (v.out_row) {
-        if (row + v.row0 >= (int64_t)v.row_tiles[0] * TILE_M) return;
-        o = v.out_row[row];
-        if (o < 0 || y < 0) return;
-    } else if (y < -1 || y >= v.V) {
-        if (rank == 0 && tid == 0) raise_status(v.status, ST_RANGE);
-        y = -1;
-    }
+    const int k = v.top;
     const float c = v.scale * LOG2E;
+    const int64_t row = CLUSTER ? blockIdx.x / blocks : (int64_t)blockIdx.x * (BT / NT) + team;
+    int64_t o = row;
+    int y = -1;
+    bool leave = row >= v.n_rows;            // a whole team, a whole cluster
+    if (!leave) {
+        y = v.targets ? v.targets[row] : -1;
+        if (v.out_row) {
+            leave = row + v.row0 >= (int64_t)v.row_tiles[0] * TILE_M || y < 0 || v.out_row[row] < 0;
+            if (!leave) o = v.out_row[row];
+        } else if (y < -1 || y >= v.V) {
+            if (rank == 0 && tid == 0) raise_status(v.status, ST_RANGE);
+            y = -1;
+        }
+    }
+    if (leave) {
+        if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        return;
+    }
     const T* x = static_cast<const T*>(v.x) + row * v.ld;
     const Share<T> r = share_of(x, v.V, rank, blocks);
-    const int k = v.top;
 
     // the quick pass
-    constexpr int UN = sizeof(T) == 2 ? 2 : 1;      // groups in work, and as many on their way: 64 bytes each a thread
+    constexpr int UN = 2;                    // groups in work, and as many on their way
     Part p{-FLT_MAX, 0.f, 0.f};
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
-    u64 best = 0;
+    float best = -INFINITY;
+    int at = -1;
     const float2 cc = make_float2(c, c);
     Group<T> next[UN];
     auto fetch = [&](int g0) {
@@ -385,10 +396,8 @@ __global__ void __launch_bounds__(BT, 4) token_logprobs_kernel(const __grid_cons
             if (g >= r.groups) break;
             const float gm = q[u].max();
             if (k) {
-                const uint32_t key = key_of(gm);
-                gmax[g] = key;
-                const u64 key2 = key64(key, g);
-                best = key2 > best ? key2 : best;
+                gmax[g] = from_f<T>(gm);     // (exact)
+                if (gm > best || at < 0) best = gm, at = g;
             }
             const float m = max_nan(p.m, max_nan(gm, LOWEST) * c);
             const float d = p.m - m, f = ex2(d);
@@ -419,24 +428,36 @@ __global__ void __launch_bounds__(BT, 4) token_logprobs_kernel(const __grid_cons
         p = join(p, Part{m, e, e * left});
     }
     p = team_join<NT>(p, sh, tid);
-    auto over_cluster = [&](Part q) {
-        if (!CLUSTER) return q;
+    // (in a row with NaN what is found is not used)
+    if (k) top_of_share<T, NT>(r, gmax, best, at, k, sh, tid);
+    if (CLUSTER) {
+        // the other blocks hand theirs to the first one and are done
         cg::cluster_group cl = cg::this_cluster();
-        if (tid == 0) sh.all = q;
-        cl.sync();
-        q = cl.map_shared_rank(&sh, 0)->all;
-        for (int b = 1; b < blocks; ++b) q = join(q, cl.map_shared_rank(&sh, b)->all);
-        cl.sync();
-        return q;
-    };
-    p = over_cluster(p);
+        ClusterShared& first = *cl.map_shared_rank(&got, 0);
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        for (int i = tid; i < k; i += NT) first.pick[rank * k + i] = sh.pick[i];
+        if (tid == 0) first.part[rank] = p;
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (rank) return;
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        p = got.part[0];
+        for (int b = 1; b < blocks; ++b) p = join(p, got.part[b]);
+        if (k) {
+            // places without one are all 0 and hold no rank of their own
+            if (tid == 0) sh.n_found = 0;
+            for (int i = tid; i < k; i += NT) sh.pick[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < blocks * k; i += NT)
+                if (got.pick[i]) sh.found[atomicAdd(&sh.n_found, 1)] = got.pick[i];
+            __syncthreads();
+            rank_keys<NT>(sh.found, sh.n_found, k, sh.pick, tid);
+            __syncthreads();
+        }
+    }
     int kind = 0;
     float top = 0.f;
     const bool large = !(fabsf(p.m) < 1e6f && p.s <= FLT_MAX);
-    if (large) {
-        p = careful<T, NT, CLUSTER>(r, c, sh, tid, &kind, &top);
-        if (!kind) p = over_cluster(p);
-    }
+    if (large) p = careful<T, NT>(share_of(x, v.V, 0, 1), c, sh, tid, &kind, &top);
     const float ls = log2f(p.s);
     auto logprob = [&](float xv) {
         if (large) return fmaf(xv - top, v.scale, -ls * LN2);
@@ -444,32 +465,6 @@ __global__ void __launch_bounds__(BT, 4) token_logprobs_kernel(const __grid_cons
         return (fmaf(xv, c, -p.m) - ls) * LN2;           // the product is taken from m before it is rounded, as in the sums
     };
     const float nan = __int_as_float(0x7fc00000);
-    if (k && !kind) {
-        top_of_share<T, NT>(r, gmax, best, k, sh, tid);
-        if (CLUSTER) {
-            cg::cluster_group cl = cg::this_cluster();
-            cl.sync();
-            if (rank == 0) {
-                for (int i = tid; i < blocks * k; i += NT) sh.list[i] = cl.map_shared_rank(&sh, i / k)->pick[i % k];
-            }
-            cl.sync();
-            if (rank == 0) {
-                // places without one are all 0 and hold no rank of their own
-                if (tid == 0) sh.n = 0;
-                u64 mine[(8 * MAX_TOP + NT - 1) / NT];
-                int n = 0;
-                for (int i = tid; i < blocks * k; i += NT) mine[n++] = sh.list[i];
-                __syncthreads();
-                for (int i = 0; i < n; ++i)
-                    if (mine[i]) sh.list[atomicAdd(&sh.n, 1)] = mine[i];
-                for (int i = tid; i < k; i += NT) sh.pick[i] = 0;
-                __syncthreads();
-                rank_keys<NT>(sh.list, sh.n, k, sh.pick, tid);
-                __syncthreads();
-            }
-        }
-    }
-    if (rank) return;
     for (int i = tid; i < k; i += NT) {
         const u64 key = kind ? 0 : sh.pick[i];
         if (out.top_ids) out.top_ids[o * k + i] = key ? (int)id_of(key) : -1;
@@ -649,10 +644,12 @@ __global__ void __launch_bounds__(BT, 3) token_grad_kernel(const __grid_constant
     }
 }
 
+constexpr int SHORT_V = 4096;                // rows of at most this many logits go to a warp each
+
 template <typename T>
 void launch_grad(const GradView& w, int num_sms, cudaStream_t s) {
     const int64_t n = w.v.n_rows;
-    if (w.v.V <= WARP_V) {
+    if (w.v.V <= SHORT_V) {
         token_grad_kernel<T, 1><<<(unsigned)((n + 7) / 8), BT, 0, s>>>(w);
         return;
     }
@@ -664,14 +661,14 @@ void launch_grad(const GradView& w, int num_sms, cudaStream_t s) {
 // ----------------------------------------------------------------------------
 // launches
 // ----------------------------------------------------------------------------
-constexpr int MAX_GROUPS = MLORA_LOGITS_MAX_VOCAB / G / 8;
+constexpr int MAX_GROUPS = MLORA_LOGITS_MAX_VOCAB / G / MAX_BLOCKS;
 
 template <typename T, int NT, bool CLUSTER>
 cudaError_t launch_rows(const LogitsView& v, const mlora_token_stats& out, int blocks, cudaStream_t s) {
     const int groups = v.V / G, gcap = v.top ? (groups + blocks - 1) / blocks : 0;
-    const size_t smem = sizeof(uint32_t) * gcap * (BT / NT);
+    const size_t smem = sizeof(T) * gcap * (BT / NT);
     auto* kern = token_logprobs_kernel<T, NT, CLUSTER>;
-    if (smem > 32 * 1024) {
+    if (smem > 2 * 1024) {
         // one size for all calls: threads that launch at once do not lower each other's
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_GROUPS * 4);
         if (e != cudaSuccess) return e;
@@ -691,14 +688,30 @@ cudaError_t launch_rows(const LogitsView& v, const mlora_token_stats& out, int b
     return cudaLaunchKernelEx(&cfg, kern, v, out, gcap);
 }
 
+// Rows of at most this many logits go to a warp each, to two warps, and to four while the
+// groups of a block's teams leave room for four blocks an SM.  8,192 bf16 rows with 20
+// alternatives, in us with teams of 32, 64, 128 and 256 threads: 4,000 logits 35, 39, 51, 80;
+// 16,000 84, 72, 80, 109; 32,000 142, 116, 117, 141; 151,936 -, 528, 416, 426 (4,096 fp32
+// rows: -, -, 428, 383): what a row takes besides its logits is most of it for short ones.
+constexpr int WARP_V = 8192, PAIR_V = 24576, QUAD_BYTES = 40 << 10;
+
 template <typename T>
 cudaError_t launch_t(const LogitsView& v, const mlora_token_stats& out, int num_sms, cudaStream_t s) {
-    if (v.V <= WARP_V) return launch_rows<T, 32, false>(v, out, 1, s);
-    // blocks of a cluster: four blocks an SM, shares of 4,096 logits at least, and groups that fit shared memory
+    // few rows: a cluster of blocks each, no more than give each SM two, with shares of 4,096 logits at least,
+    // and groups that fit shared memory (256 fp32 rows of 151,936: 35 us with a block each, 49 with two)
     int blocks = 1;
-    while (blocks < 8 && v.n_rows * blocks < 4 * (int64_t)num_sms && v.V / blocks >= 2 * WARP_V) blocks *= 2;
-    while (blocks < 8 && v.top && v.V / G / blocks > 12000) blocks *= 2;
-    return blocks == 1 ? launch_rows<T, BT, false>(v, out, 1, s) : launch_rows<T, BT, true>(v, out, blocks, s);
+    while (blocks < MAX_BLOCKS && v.n_rows * blocks <= (int64_t)num_sms && v.V / blocks >= 8192) blocks *= 2;
+    while (blocks < MAX_BLOCKS && v.top && v.V / G / blocks > 12000) blocks *= 2;
+    if (blocks > 1) return launch_rows<T, BT, true>(v, out, blocks, s);
+    int team = v.V <= WARP_V ? 32 : v.V <= PAIR_V ? 64 : 2 * (v.V / G) * (int)sizeof(T) <= QUAD_BYTES ? 128 : BT;
+    // too few teams for two blocks an SM: larger ones, of four groups a thread at least
+    while (team < BT && v.n_rows * team < 2 * BT * (int64_t)num_sms && v.V >= 4 * G * 2 * team) team *= 2;
+    switch (team) {
+    case 32: return launch_rows<T, 32, false>(v, out, 1, s);
+    case 64: return launch_rows<T, 64, false>(v, out, 1, s);
+    case 128: return launch_rows<T, 128, false>(v, out, 1, s);
+    default: return launch_rows<T, BT, false>(v, out, 1, s);
+    }
 }
 
 }  // namespace
