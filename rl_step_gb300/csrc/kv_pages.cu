@@ -10,6 +10,8 @@
 // The free list is a stack.  Growing takes pages from its top in the order of the
 // sequences and of their pages; cutting back walks both the other way round, so
 // that it undoes a growth exactly, and a page's place does not depend on timing.
+#include <algorithm>
+
 #include "kv_common.cuh"
 
 namespace mlk {
@@ -17,7 +19,8 @@ namespace mlk {
 namespace {
 
 constexpr int ST_NO_PAGES = 4;
-constexpr int PT = 1024;                     // most threads, and sequences of a round
+constexpr int PT = 1024;                     // most threads
+constexpr int SEQS = 4;                      // sequences of a thread in a round
 
 struct PoolView {
     int* free_pages;
@@ -70,6 +73,19 @@ __device__ __forceinline__ Two block_scan(Two v, Two* total) {
     return v;
 }
 
+// how many threads before this one have `have`; *total: of the block
+__device__ __forceinline__ int block_rank(bool have, int* total) {
+    __shared__ int part[PT / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t m = __ballot_sync(0xffffffffu, have);
+    __syncthreads();
+    if (lane == 0) part[warp] = __popc(m);
+    __syncthreads();
+    const int w = lane < warps ? part[lane] : 0;
+    *total = __reduce_add_sync(0xffffffffu, w);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + __popc(m & ((1u << lane) - 1));
+}
+
 // the last of first[0 .. n) that is not above x; first[0] <= x
 template <typename I>
 __device__ __forceinline__ int find(const I* first, int n, int64_t x) {
@@ -99,8 +115,8 @@ __device__ __forceinline__ void write_row(const PoolView& p, const GrowView& g, 
 
 __global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ PoolView p, const __grid_constant__ GrowView g,
                                                      int rows_here) {
-    __shared__ int64_t s_first[PT];           // new pages before a sequence's own, of this round
-    __shared__ int s_have[PT];
+    __shared__ int64_t s_first[PT * SEQS];    // new pages before a sequence's own, of this round
+    __shared__ int s_have[PT * SEQS];
     const int tid = threadIdx.x, nt = blockDim.x;
     int avail = *p.n_free;
     const bool pool_ok = avail >= 0 && avail <= p.n_pages;
@@ -109,32 +125,53 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ Poo
         avail = 0;
     }
     Two want{0, 0}, got{0, 0};                // pages and rows so far: asked for, and served
-    for (int base = 0; base < g.n_seqs; base += nt) {
-        const int s = base + tid;
-        const bool here = s < g.n_seqs;
-        const int len = here ? g.kv_len[s] : 0, add = here ? g.n_new[s] : 0;
-        const bool ok = here && len >= 0 && add >= 0 && (int64_t)len + add <= g.max_len;
-        const int have = ok ? pages_of(len) : 0;
-        const Two mine{ok ? pages_of((int64_t)len + add) - have : 0, ok ? add : 0};
-        Two all;
-        const Two upto = block_scan(mine, &all);
-        // A sequence is served if the pages and rows asked for up to it are there; what needs none always is.
-        const bool pages_ok = mine.a == 0 || want.a + upto.a <= avail, rows_ok = mine.b == 0 || want.b + upto.b <= g.n_rows;
-        const bool served = ok && pages_ok && rows_ok;
-        if (here && !served) raise_status(p.status, !ok || !rows_ok ? ST_RANGE : ST_NO_PAGES);
-        const Two take{served ? mine.a : 0, served ? mine.b : 0};
-        Two taken;
-        const Two before = block_scan(take, &taken);
-        if (here) {
-            g.row_off[s] = (int)(got.b + before.b - take.b);
-            if (served && add) g.kv_len[s] = len + add;
+    for (int base = 0; base < g.n_seqs; base += nt * SEQS) {
+        const int s0 = base + tid * SEQS;
+        int len[SEQS], add[SEQS], have[SEQS];
+        bool ok[SEQS], served[SEQS];
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) {
+            len[i] = s0 + i < g.n_seqs ? g.kv_len[s0 + i] : 0;
+            add[i] = s0 + i < g.n_seqs ? g.n_new[s0 + i] : 0;
         }
-        s_first[tid] = before.a - take.a;
-        s_have[tid] = have;
+        Two mine[SEQS], sum{0, 0};
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) {
+            ok[i] = len[i] >= 0 && add[i] >= 0 && (int64_t)len[i] + add[i] <= g.max_len;
+            have[i] = ok[i] ? pages_of(len[i]) : 0;
+            mine[i] = Two{ok[i] ? pages_of((int64_t)len[i] + add[i]) - have[i] : 0, ok[i] ? add[i] : 0};
+            sum.a += mine[i].a, sum.b += mine[i].b;
+        }
+        Two all;
+        Two upto = block_scan(sum, &all);
+        upto.a += want.a - sum.a, upto.b += want.b - sum.b;
+        Two take{0, 0};
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) {
+            // A sequence is served if the pages and rows asked for up to it are there; what needs none always is.
+            upto.a += mine[i].a, upto.b += mine[i].b;
+            const bool pages_ok = mine[i].a == 0 || upto.a <= avail, rows_ok = mine[i].b == 0 || upto.b <= g.n_rows;
+            served[i] = ok[i] && pages_ok && rows_ok;
+            if (!served[i]) raise_status(p.status, !ok[i] || !rows_ok ? ST_RANGE : ST_NO_PAGES);
+            else take.a += mine[i].a, take.b += mine[i].b;
+        }
+        Two taken;
+        Two before = block_scan(take, &taken);
+        before.a -= take.a, before.b -= take.b;
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) {
+            s_first[tid * SEQS + i] = before.a;
+            s_have[tid * SEQS + i] = have[i];
+            if (s0 + i < g.n_seqs) {
+                g.row_off[s0 + i] = (int)(got.b + before.b);
+                if (served[i] && add[i]) g.kv_len[s0 + i] = len[i] + add[i];
+            }
+            if (served[i]) before.a += mine[i].a, before.b += mine[i].b;
+        }
         __syncthreads();
         for (int64_t j = tid; j < taken.a; j += nt) {
             // the last sequence that begins at or before page j: those behind it that take none begin later
-            const int q = find(s_first, nt, j);
+            const int q = find(s_first, nt * SEQS, j);
             const int id = p.free_pages[avail - 1 - (got.a + j)];
             const bool good = id >= 0 && id < p.n_pages;
             if (good) p.owner[id] = base + q;
@@ -164,48 +201,60 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ PoolV
 // the row of the table owns it.
 __global__ void __launch_bounds__(PT) release_kernel(const __grid_constant__ PoolView p, int* table, int* kv_len,
                                                      const int* __restrict__ keep, int n_seqs, int max_pages) {
-    __shared__ int64_t s_first[PT];
-    __shared__ int s_end[PT];
+    __shared__ int64_t s_first[PT * SEQS];
+    __shared__ int s_end[PT * SEQS];
     const int tid = threadIdx.x, nt = blockDim.x;
     int64_t top = *p.n_free;
     if (top < 0 || top > p.n_pages) {
         if (tid == 0) raise_status(p.status, ST_RANGE);
         return;                               // (the whole block: all read the same number)
     }
-    for (int base = 0; base < n_seqs; base += nt) {
-        const int s = n_seqs - 1 - (base + tid);
-        const bool here = s >= 0;
-        const int len = here ? kv_len[s] : 0, left = here && keep ? keep[s] : 0;
-        const bool ok = here && len >= 0 && len <= (int64_t)max_pages * KV_PAGE && left >= 0;
-        if (here && !ok) raise_status(p.status, ST_RANGE);
-        const bool cut = ok && left < len;
-        const Two mine{cut ? pages_of(len) - pages_of(left) : 0, 0};
+    for (int base = 0; base < n_seqs; base += nt * SEQS) {
+        const int s0 = n_seqs - 1 - (base + tid * SEQS);                // and downwards
+        int len[SEQS], left[SEQS];
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) {
+            len[i] = s0 - i >= 0 ? kv_len[s0 - i] : 0;
+            left[i] = s0 - i >= 0 && keep ? keep[s0 - i] : 0;
+        }
+        int64_t count[SEQS], sum = 0;
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) {
+            const bool ok = len[i] >= 0 && len[i] <= (int64_t)max_pages * KV_PAGE && left[i] >= 0;
+            if (!ok) raise_status(p.status, ST_RANGE);
+            const bool cut = ok && left[i] < len[i];
+            count[i] = cut ? pages_of(len[i]) - pages_of(left[i]) : 0;
+            sum += count[i];
+            if (cut) kv_len[s0 - i] = left[i];
+        }
         Two all;
-        const Two upto = block_scan(mine, &all);
-        if (cut) kv_len[s] = left;
-        s_first[tid] = upto.a - mine.a;
-        s_end[tid] = pages_of(len);
+        int64_t at = block_scan(Two{sum, 0}, &all).a - sum;
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) {
+            s_first[tid * SEQS + i] = at;
+            s_end[tid * SEQS + i] = pages_of(len[i]);
+            at += count[i];
+        }
         __syncthreads();
         for (int64_t j0 = 0; j0 < all.a; j0 += nt) {
             const int64_t j = j0 + tid;
             int id = -1;
             bool mine_too = false;
             if (j < all.a) {
-                const int q = find(s_first, nt, j), seq = n_seqs - 1 - (base + q);
-                int* at = table + (int64_t)seq * max_pages + s_end[q] - 1 - (j - s_first[q]);
-                id = *at;
-                *at = -1;
+                const int q = find(s_first, nt * SEQS, j), seq = n_seqs - 1 - (base + q);
+                int* entry = table + (int64_t)seq * max_pages + s_end[q] - 1 - (j - s_first[q]);
+                id = *entry;
+                *entry = -1;
                 if (id < 0 || id >= p.n_pages) raise_status(p.status, ST_RANGE);
                 else mine_too = atomicCAS(p.owner + id, seq, -1) == seq;
             }
-            Two n;
-            const Two place = block_scan(Two{mine_too, 0}, &n);
+            int n = 0;
+            const int64_t to = top + block_rank(mine_too, &n);
             if (mine_too) {
-                const int64_t to = top + place.a - 1;
                 if (to < p.n_pages) p.free_pages[to] = id;
                 else raise_status(p.status, ST_RANGE);
             }
-            top = top + n.a < p.n_pages ? top + n.a : p.n_pages;
+            top = top + n < p.n_pages ? top + n : p.n_pages;
         }
         __syncthreads();
     }
@@ -216,7 +265,7 @@ int pool_check(const mlora_kv_pool* p, const int32_t* table, const int32_t* kv_l
     if (!p) return kv_fail(MLORA_E_ARG, "NULL pool");
     if (p->n_pages < 1) return kv_fail(MLORA_E_ARG, "a pool of %d pages", p->n_pages);
     if (!p->free_pages || !p->n_free || !p->owner) return kv_fail(MLORA_E_ARG, "NULL pool arrays");
-    if (n_seqs < 0 || n_seqs > INT32_MAX - 2 * PT) return kv_fail(MLORA_E_ARG, "%d sequences", n_seqs);
+    if (n_seqs < 0 || n_seqs > INT32_MAX - 2 * PT * SEQS) return kv_fail(MLORA_E_ARG, "%d sequences", n_seqs);
     if (max_pages < 1) return kv_fail(MLORA_E_ARG, "page tables of %d pages", max_pages);
     if (n_seqs > 0 && (!table || !kv_len)) return kv_fail(MLORA_E_ARG, "NULL page table or lengths");
     *v = PoolView{p->free_pages, p->n_free, p->owner, p->status, p->n_pages};
@@ -224,7 +273,7 @@ int pool_check(const mlora_kv_pool* p, const int32_t* table, const int32_t* kv_l
 }
 
 // threads of the one block
-int block_for(int64_t n) { return n <= 256 ? 256 : PT; }
+int block_for(int64_t n) { return n <= 256 ? 256 : n <= 512 ? 512 : PT; }
 
 }  // namespace
 
@@ -244,7 +293,7 @@ extern "C" int mlora_kv_reserve(const mlora_kv_pool* p, const mlora_kv_growth* q
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool rows = q->n_rows > 0 && (q->positions || q->seqs || q->slots);
     const bool apart = rows && q->n_rows > 2 * PT;
-    reserve_kernel<<<1, block_for(q->n_seqs > q->n_rows ? q->n_seqs : apart ? 0 : q->n_rows), 0, s>>>(v, g, rows && !apart);
+    reserve_kernel<<<1, block_for(std::max((q->n_seqs + SEQS - 1) / SEQS, (int)(rows && !apart ? q->n_rows : 0))), 0, s>>>(v, g, rows && !apart);
     if (apart) {
         const int64_t blocks = (q->n_rows + 255) / 256;
         rows_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(v, g);
@@ -260,7 +309,7 @@ extern "C" int mlora_kv_release(const mlora_kv_pool* p, int32_t* page_table, int
     const int rc = pool_check(p, page_table, kv_len, n_seqs, max_pages, &v);
     if (rc) return rc;
     if (n_seqs == 0) return MLORA_OK;
-    release_kernel<<<1, block_for(n_seqs), 0, reinterpret_cast<cudaStream_t>(stream)>>>(v, page_table, kv_len, keep, n_seqs,
+    release_kernel<<<1, block_for((n_seqs + SEQS - 1) / SEQS), 0, reinterpret_cast<cudaStream_t>(stream)>>>(v, page_table, kv_len, keep, n_seqs,
                                                                                       max_pages);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return kv_fail(MLORA_E_CUDA, "release launch: %s", cudaGetErrorString(e));

@@ -211,88 +211,146 @@ __device__ __forceinline__ void rank_keys(const u64* list, int n, int k, u64* ou
     }
 }
 
+// Appends the keys of the threads that have one, a warp's side by side; all threads of a warp come here.
+__device__ __forceinline__ void append(u64* list, int* n, int room, bool have, u64 key) {
+    const uint32_t m = __ballot_sync(0xffffffffu, have);
+    if (m == 0) return;
+    int at = 0;
+    if ((threadIdx.x & 31) == 0) at = atomicAdd(n, __popc(m));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << (threadIdx.x & 31)) - 1));
+    if (have && at < room) list[at] = key;
+}
+
+// For one warp: the k largest of list's n keys into out, in falling order, one after
+// the other: each lane knows the largest of its own that is left.
+__device__ __noinline__ void pick_one_by_one(const u64* list, int n, int k, u64* out, int lane) {
+    u64 mine = 0;
+    for (int i = lane; i < n; i += 32) mine = list[i] > mine ? list[i] : mine;
+    for (int r = 0; r < k; ++r) {
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(mine >> 32));
+        if (hi == 0) break;                  // none left (no key's upper half is 0)
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0);
+        const u64 best = (u64)hi << 32 | lo;
+        if (mine == best) {
+            out[r] = best;
+            mine = 0;
+            for (int i = lane; i < n; i += 32) {
+                const u64 key = list[i];
+                mine = key < best && key > mine ? key : mine;
+            }
+        }
+        __syncwarp();
+    }
+}
+
 // The share's k largest logits in sh.pick as (value, id) keys in falling order, 0
 // where there are none.  gmax: the groups' largest values; best, at: the largest of this
-// thread's and its group (-1: none).
+// thread's and its group (-1: none); a thread of a warp's team has two, of its even and its odd groups.
 template <typename T, int NT>
-__device__ void top_of_share(const Share<T>& r, const T* gmax, float best, int at, int k, TeamShared& sh, int tid) {
-    constexpr int QUAD = NT == 32 ? 1 : NT / 64, KEYS = NT / QUAD; // threads of a first-round key; 32 or 64 keys, at least k
-    u64 mine = at >= 0 ? key64(key_of(best), at) : 0;
-    if (tid == 0) { sh.tau = 1; sh.n = sh.n_found = 0; }
+__device__ void top_of_share(const Share<T>& r, const T* gmax, const float (&best)[2], const int (&at)[2], int k,
+                             TeamShared& sh, int tid) {
     for (int i = tid; i < k; i += NT) sh.pick[i] = 0;
+    u64 tau = 0;
+    int ng = r.groups;
+    const bool all = NT == 32 && ng <= MAX_TOP;          // (few groups: all of them)
+    if (tid == 0) sh.n_found = 0;
+    if (!all) {
+        // 64 first-round keys: two a thread of a warp, or one of NT / 64 threads
+        constexpr int MINE = NT == 32 ? 2 : 1, QUAD = NT == 32 ? 1 : NT / 64, KEYS = 64;
+        u64 mine[2];
 #pragma unroll
-    for (int o = 1; o < QUAD; o <<= 1) {
-        const u64 q = __shfl_xor_sync(0xffffffffu, mine, o);
-        mine = q > mine ? q : mine;
-    }
-    if (tid % QUAD == 0) sh.list[tid / QUAD] = mine;
-    team_sync<NT>();
-    // the k-th largest of these keys: at least k groups are not below it.  A quad counts for its key together.
-    int rank = 0;
+        for (int u = 0; u < MINE; ++u) mine[u] = at[u] >= 0 ? key64(key_of(best[u]), at[u]) : 0;
+        if (tid == 0) { sh.tau = 1; sh.n = 0; }
 #pragma unroll
-    for (int j = 0; j < KEYS / QUAD; ++j) rank += sh.list[j * QUAD + tid % QUAD] > mine;
-#pragma unroll
-    for (int o = 1; o < QUAD; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    if (rank == k - 1 && mine && tid % QUAD == 0) sh.tau = mine;
-    team_sync<NT>();
-    u64 tau = sh.tau;
-    for (int g = tid; g < r.groups; g += NT) {
-        const u64 key = key64(key_of(to_f(gmax[g])), g);
-        if (key >= tau) {
-            const int to = atomicAdd(&sh.n, 1);
-            if (to < LIST) sh.list[to] = key;
+        for (int o = 1; o < QUAD; o <<= 1) {
+            const u64 q = __shfl_xor_sync(0xffffffffu, mine[0], o);
+            mine[0] = q > mine[0] ? q : mine[0];
         }
-    }
-    team_sync<NT>();
-    if (sh.n > LIST) {
-        // few threads hold many of the largest groups: the k-th largest key bit by bit
-        tau = 0;
-        for (int bit = 63; bit >= 0; --bit) {
-            const u64 want = tau | (u64)1 << bit;
+        if (tid % QUAD == 0) {
+            sh.list[tid / QUAD] = mine[0];
+            if (MINE == 2) sh.list[32 + tid] = mine[1];
+        }
+        team_sync<NT>();
+        // the k-th largest of these keys: at least k groups are not below it.  A quad counts for its key together.
+        int rank[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < KEYS / QUAD; ++j) {
+            const u64 other = sh.list[j * QUAD + tid % QUAD];
+            rank[0] += other > mine[0];
+            if (MINE == 2) rank[1] += other > mine[1];
+        }
+#pragma unroll
+        for (int o = 1; o < QUAD; o <<= 1) rank[0] += __shfl_xor_sync(0xffffffffu, rank[0], o);
+#pragma unroll
+        for (int u = 0; u < MINE; ++u)
+            if (rank[u] == k - 1 && mine[u] && tid % QUAD == 0) sh.tau = mine[u];
+        team_sync<NT>();
+        tau = sh.tau;
+        for (int g0 = 0; g0 < r.groups; g0 += NT) {
+            const int g = g0 + tid;
+            const u64 key = g < r.groups ? key64(key_of(to_f(gmax[g])), g) : 0;
+            append(sh.list, &sh.n, LIST, g < r.groups && key >= tau, key);
+        }
+        team_sync<NT>();
+        if (sh.n > LIST) {
+            // few threads hold many of the largest groups: the k-th largest key bit by bit
+            tau = 0;
+            for (int bit = 63; bit >= 0; --bit) {
+                const u64 want = tau | (u64)1 << bit;
+                team_sync<NT>();
+                if (tid == 0) sh.n = 0;
+                team_sync<NT>();
+                int c = 0;
+                for (int g = tid; g < r.groups; g += NT) c += key64(key_of(to_f(gmax[g])), g) >= want;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+                if ((tid & 31) == 0) atomicAdd(&sh.n, c);
+                team_sync<NT>();
+                if (sh.n >= k) tau = want;
+            }
             team_sync<NT>();
             if (tid == 0) sh.n = 0;
             team_sync<NT>();
-            int c = 0;
-            for (int g = tid; g < r.groups; g += NT) c += key64(key_of(to_f(gmax[g])), g) >= want;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-            if ((tid & 31) == 0) atomicAdd(&sh.n, c);
+            for (int g = tid; g < r.groups; g += NT) {
+                const u64 key = key64(key_of(to_f(gmax[g])), g);
+                if (key >= tau) sh.list[atomicAdd(&sh.n, 1)] = key;      // (k of them)
+            }
             team_sync<NT>();
-            if (sh.n >= k) tau = want;
         }
-        team_sync<NT>();
-        if (tid == 0) sh.n = 0;
-        team_sync<NT>();
-        for (int g = tid; g < r.groups; g += NT) {
-            const u64 key = key64(key_of(to_f(gmax[g])), g);
-            if (key >= tau) sh.list[atomicAdd(&sh.n, 1)] = key;
+        ng = sh.n;
+        if (ng > MAX_TOP) {
+            // more than their logits have room for: the k largest alone
+            rank_keys<NT>(sh.list, ng, k, sh.pick, tid);
+            team_sync<NT>();
+            ng = k;
+            tau = sh.pick[k - 1];
+            u64 mine_too = 0;
+            if (NT == 32 || tid < 32) mine_too = tid < k ? sh.pick[tid] : 0;
+            team_sync<NT>();
+            if (tid < k) { sh.list[tid] = mine_too; sh.pick[tid] = 0; }
+            team_sync<NT>();
         }
-        team_sync<NT>();
-    }
-    int ng = sh.n;
-    if (ng > MAX_TOP) {
-        // more than their logits have room for: the k largest alone
-        rank_keys<NT>(sh.list, ng, k, sh.pick, tid);
-        team_sync<NT>();
-        ng = k;
-        tau = sh.pick[k - 1];
-        u64 mine_too = 0;
-        if (NT == 32 || tid < 32) mine_too = tid < k ? sh.pick[tid] : 0;
-        team_sync<NT>();
-        if (tid < k) { sh.list[tid] = mine_too; sh.pick[tid] = 0; }
-        team_sync<NT>();
-    }
-    // their logits that are not below that group's largest, and the edges'
-    const uint32_t low = (uint32_t)(tau >> 32);
-#pragma unroll 4
-    for (int i = tid; i < ng * G + r.edges; i += NT) {
-        const int id = i < ng * G ? r.id0 + (int)id_of(sh.list[i / G]) * G + i % G : r.edge_id(i - ng * G);
-        const float x = to_f(r.row[id]);
-        const uint32_t key = key_of(x);
-        if (x > -INFINITY && key >= low) sh.found[atomicAdd(&sh.n_found, 1)] = key64(key, id);
     }
     team_sync<NT>();
-    rank_keys<NT>(sh.found, sh.n_found, k, sh.pick, tid);
+    // their logits that are not below that group's largest, and the edges'
+    const uint32_t low = (uint32_t)(tau >> 32);
+    const int total = ng * G + r.edges;
+#pragma unroll 4
+    for (int i0 = 0; i0 < total; i0 += NT) {
+        const int i = i0 + tid;
+        u64 key = 0;
+        if (i < total) {
+            const int id = i >= ng * G ? r.edge_id(i - ng * G) : r.id0 + (all ? i : (int)id_of(sh.list[i / G]) * G + i % G);
+            const float x = to_f(r.row[id]);
+            const uint32_t value = key_of(x);
+            if (x > -INFINITY && value >= low) key = key64(value, id);
+        }
+        append(sh.found, &sh.n_found, FOUND, key != 0, key);
+    }
+    team_sync<NT>();
+    // (a warp's time: n^2 / 32 comparisons, or k rounds of about 25 of them)
+    if (NT == 32 && sh.n_found * sh.n_found > 800 * k) pick_one_by_one(sh.found, sh.n_found, k, sh.pick, tid);
+    else rank_keys<NT>(sh.found, sh.n_found, k, sh.pick, tid);
     team_sync<NT>();
 }
 
@@ -375,8 +433,8 @@ token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constan
     constexpr int UN = 2;                    // groups in work, and as many on their way
     Part p{-FLT_MAX, 0.f, 0.f};
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
-    float best = -INFINITY;
-    int at = -1;
+    float best[2] = {-INFINITY, -INFINITY};
+    int at[2] = {-1, -1};
     const float2 cc = make_float2(c, c);
     Group<T> next[UN];
     auto fetch = [&](int g0) {
@@ -397,7 +455,8 @@ token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constan
             const float gm = q[u].max();
             if (k) {
                 gmax[g] = from_f<T>(gm);     // (exact)
-                if (gm > best || at < 0) best = gm, at = g;
+                const int w = NT == 32 ? u : 0;
+                if (gm > best[w] || at[w] < 0) best[w] = gm, at[w] = g;
             }
             const float m = max_nan(p.m, max_nan(gm, LOWEST) * c);
             const float d = p.m - m, f = ex2(d);
@@ -506,10 +565,14 @@ __device__ __forceinline__ float2 grad2(float2 x, const RowGrad& r) {
 struct RowIds {
     int id, y;
     float d, dy;
-    // which of them lie in [a, b); bit 32: the target
+    // which of them are such; bit 32: the target
+    template <typename F>
+    __device__ __forceinline__ u64 which(F&& such) const {
+        const u64 m = __ballot_sync(0xffffffffu, such(id));
+        return such(y) ? m | (u64)1 << 32 : m;
+    }
     __device__ __forceinline__ u64 within(int a, int b) const {
-        const u64 m = __ballot_sync(0xffffffffu, id >= a && id < b);
-        return y >= a && y < b ? m | (u64)1 << 32 : m;
+        return which([=](int i) { return i >= a && i < b; });
     }
     // f(id, gradient) for each id of the mask, in one order
     template <typename F>
@@ -522,7 +585,7 @@ struct RowIds {
     }
 };
 
-// The ids [a, b) of a row one by one (ends, and rows that do not lie alike in memory).
+// The ids [a, b) of a row one by one (rows that do not lie alike in memory).
 template <typename T>
 __device__ __forceinline__ void grad_one_by_one(const T* x, T* out, int a, int b, const RowGrad& r, const RowIds& ids,
                                                 bool zero, int lane) {
@@ -542,7 +605,7 @@ __device__ __forceinline__ void grad_one_by_one(const T* x, T* out, int a, int b
 // before the one rounding; as each id is read and written by one thread, dlogits may be
 // the logits.  WARPS: of a row (1: rows so short that a block takes eight).
 template <typename T, int WARPS>
-__global__ void __launch_bounds__(BT, 3) token_grad_kernel(const __grid_constant__ GradView w) {
+__global__ void __launch_bounds__(BT, WARPS == 1 ? 4 : 3) token_grad_kernel(const __grid_constant__ GradView w) {
     const LogitsView& v = w.v;
     constexpr int ROWS = BT / 32 / WARPS, PER = 32 / (int)sizeof(T);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -553,6 +616,23 @@ __global__ void __launch_bounds__(BT, 3) token_grad_kernel(const __grid_constant
     const T* x = static_cast<const T*>(v.x) + row * v.ld;
     T* out = static_cast<T*>(w.out) + row * w.ldo;
 
+    const uintptr_t px = reinterpret_cast<uintptr_t>(x) & 31, po = reinterpret_cast<uintptr_t>(out) & 31;
+    // 32 bytes at a time between two ends
+    const int lead = min((int)((32 - px) % 32 / sizeof(T)), V), vecs = (V - lead) / PER, tail = lead + vecs * PER;
+    const int edge = first > 0 ? V : lane < lead ? lane : tail + lane - lead;          // this lane's id of the ends
+    constexpr int UN = WARPS == 1 ? 1 : 2, WIN = UN * 32;    // vectors of a window
+    uint32_t q[UN][8], next[UN][8];
+    auto fetch = [&](int v0, bool wanted) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (v0 + 32 * u + lane < vecs && wanted) load32(x + lead + (int64_t)(v0 + 32 * u + lane) * PER, next[u]);
+    };
+    float at_edge = 0.f;
+    // short rows: all loads at once
+    if (WARPS == 1 && px == po) {
+        if (edge < V) at_edge = to_f(x[edge]);
+        fetch(0, true);
+    }
     // every load that the row's factors need at once
     RowIds ids;
     ids.id = lane < k ? w.g.top_ids[row * v.top + lane] : -1;
@@ -581,32 +661,29 @@ __global__ void __launch_bounds__(BT, 3) token_grad_kernel(const __grid_constant
     ids.d *= v.scale;
     ids.dy *= v.scale;
 
-    const uintptr_t px = reinterpret_cast<uintptr_t>(x) & 31, po = reinterpret_cast<uintptr_t>(out) & 31;
     if (px != po) {
         constexpr int SPAN = 256;
         for (int64_t a = (int64_t)first * SPAN; a < V; a += (int64_t)step * SPAN)
             grad_one_by_one(x, out, (int)a, (int)min(a + SPAN, (int64_t)V), r, ids, zero, lane);
         return;
     }
-    const int lead = min((int)((32 - px) % 32 / sizeof(T)), V), vecs = (V - lead) / PER, tail = lead + vecs * PER;
-    if (first == 0) grad_one_by_one(x, out, 0, lead, r, ids, zero, lane);
-    if (first == step - 1) grad_one_by_one(x, out, tail, V, r, ids, zero, lane);
-    const T* xv = x + lead;
+    if (WARPS > 1) {
+        if (edge < V && !zero) at_edge = to_f(x[edge]);
+        fetch(first * WIN, !zero);
+    }
+    if (first == 0) {
+        const u64 hit = zero ? 0 : ids.which([=](int i) { return i >= 0 && (i < lead || i >= tail); });
+        float d = zero ? 0.f : grad2(make_float2(at_edge, 0.f), r).x;
+        ids.each(hit, [&](int id, float add) { d += id == edge ? add : 0.f; });
+        if (edge < V) out[edge] = from_f<T>(d);
+    }
     T* ov = out + lead;
-    constexpr int UN = 2, WIN = UN * 32;                     // vectors of a window
-    uint32_t q[UN][8], next[UN][8];
-    auto fetch = [&](int v0, uint32_t (&to)[UN][8]) {
-#pragma unroll
-        for (int u = 0; u < UN; ++u)
-            if (v0 + 32 * u + lane < vecs && !zero) load32(xv + (int64_t)(v0 + 32 * u + lane) * PER, to[u]);
-    };
-    fetch(first * WIN, next);
     for (int v0 = first * WIN; v0 < vecs; v0 += step * WIN) {
 #pragma unroll
         for (int u = 0; u < UN; ++u)
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[u][j] = zero ? 0 : next[u][j];
-        fetch(v0 + step * WIN, next);
+        fetch(v0 + step * WIN, !zero);
         const int id0 = lead + v0 * PER;
         const u64 hit = zero ? 0 : ids.within(id0, id0 + WIN * PER);
 #pragma unroll
