@@ -23,6 +23,7 @@
 
 #include "kv_common.cuh"
 #include "logits.cuh"
+#include "packed.cuh"
 
 namespace cg = cooperative_groups;
 

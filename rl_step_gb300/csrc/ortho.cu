@@ -32,6 +32,7 @@
 #include <vector>
 
 #include "kv_common.cuh"
+#include "packed.cuh"
 
 namespace cg = cooperative_groups;
 
