@@ -398,17 +398,6 @@ __device__ __forceinline__ float block_max(float m, float* red) {
     for (int w = 0; w < OW; ++w) m = fmaxf(m, red[w]);
     return m;
 }
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int w = 0; w < OW; ++w) v += red[w];
-    return v;
-}
 // 2^e with e such that 2^e m lies in [2^(to - 1), 2^to); m is positive and finite, the
 // power is held to 2^+-126
 __device__ __forceinline__ float scale_to(float m, int to) {
@@ -496,20 +485,42 @@ __device__ __forceinline__ void times_p(const Matrix<T, R>& x, const OrthoShared
     }
 }
 
-// The sums of X X^T over the block's columns.
+// The sums of X X^T over the block's columns.  f: the scale, or 0: each warp's own, from the
+// root mean square of its first tile (2^5, which leaves 2^10 for larger elements); then the
+// sums are those of M itself.  Where that does not do, they are no numbers.
 template <typename T, int R>
-__device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, OrthoShared<T, R>& sh, int first, int end, Gram<R>& acc) {
+__device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, OrthoShared<T, R>& sh, float f, int first, int end,
+                                          Gram<R>& acc) {
     constexpr int J = R / 8;
     constexpr bool EXACT = sizeof(T) == 2;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     acc.clear();
+    const bool own = f == 0.f && first + TC * warp < end;
+    bool sure = true;
+    if (own) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        float sq = 0.f;
+#pragma unroll
+        for (int q = 0; q < R / 4; ++q) {
+            float v[4];
+            load4(sh.ring0[warp] + 4 * (lane + 32 * q), v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sq = fmaf(v[e], v[e], sq);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        sq *= 1.f / (R * TC);
+        sure = sq > 0x1p-60f && sq < 0x1p60f;
+        f = sure ? scale_to(sqrtf(sq), 5) : 1.f;
+    }
     over_tiles<T, R>(x, sh, first, end, [&](const T* tile, int) {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             uint32_t hi[J][2], lo[J][2];
             auto put = [&](int j, int e, float a, float b) {
-                if (EXACT) hi[j][e] = half2_of(a * x.f, b * x.f);
-                else split(a, b, x.f, hi[j][e], lo[j][e]);
+                if (EXACT) hi[j][e] = half2_of(a * f, b * f);
+                else split(a, b, f, hi[j][e], lo[j][e]);
             };
             if (x.tall) {
                 // columns 16 h + 4 t + q, rows J g ..
@@ -544,6 +555,13 @@ __device__ __forceinline__ void gram_of_x(const Matrix<T, R>& x, OrthoShared<T, 
             acc.template add<EXACT>(hi, lo);
         }
     });
+    if (own) {
+        const float back = sure ? 1.f / (f * f) : __int_as_float(0x7fc00000);
+#pragma unroll
+        for (int i = 0; i < Gram<R>::TILES; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc.v[i][e] *= back;
+    }
 }
 
 // The same of P X times `scale`.
@@ -702,26 +720,13 @@ __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid
         for (int i = 0; i < x.r; ++i) s += sh.A[i * LD + i];
         return s;
     };
-    // The first scale from 1,024 elements: their root mean square becomes 2^5 or so, which leaves 2^10 for
-    // larger ones.  Where that does not do, the sums are no numbers, and the largest magnitude says.
     begin_tiles<T, R>(x, sh, first, end);
-    float sq = 0.f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float v = to_f(x.src[(q * OT + tid) * size / (4 * OT)]);
-        sq = fmaf(v, v, sq);
-    }
-    sq = block_sum(sq, sh.red) / (4 * OT);
-    bool sure = sq > 1e-30f && sq < 1e30f;
-    if (sure) {
-        x.f = scale_to(sqrtf(sq), 5);
-        gram_of_x<T, R>(x, sh, first, end, acc);
-        begin_tiles<T, R>(x, sh, first, end);
-        gather<T, R>(acc, x, 1.f, sh);
-        sq = trace();
-        sure = sq > 0.f && sq <= FLT_MAX;
-    }
-    if (!sure) {
+    gram_of_x<T, R>(x, sh, 0.f, first, end, acc);
+    begin_tiles<T, R>(x, sh, first, end);
+    gather<T, R>(acc, x, 1.f, sh);
+    float sq = trace();
+    if (!(sq > 0.f && sq <= FLT_MAX)) {
+        // the largest magnitude says
         float m = 0.f;
         bool bad = false;
         for (int64_t i = tid + (int64_t)rank * OT; i < size; i += (int64_t)OT * blocks) {
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(OT, R == 64 ? 1 : 2) ortho_kernel(const __grid
         sq = 0.f;
         if (m > 0.f) {
             x.f = scale_to(m, 15);
-            gram_of_x<T, R>(x, sh, first, end, acc);
+            gram_of_x<T, R>(x, sh, x.f, first, end, acc);
             begin_tiles<T, R>(x, sh, first, end);
             gather<T, R>(acc, x, 1.f, sh);
             sq = trace();

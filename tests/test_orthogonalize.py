@@ -270,6 +270,30 @@ def test_zeros_and_values_that_are_no_numbers(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_parts_of_very_different_size(dtype):
+    """zeros, tiny and huge values in the first columns (a warp's first tile says how it scales), outliers behind them"""
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    g = torch.Generator(device="cuda").manual_seed(11)
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    mats = []
+    for first in (0.0, 1e-9, 1e6, 1e-25):
+        for shape in ((32, 900), (900, 32), (12, 300), (300, 60)):
+            m = torch.randn(*shape, generator=g, device="cuda")
+            wide = m if shape[0] < shape[1] else m.t()
+            wide[:, :256] *= first
+            mats.append(m.to(dt))
+    m = torch.randn(16, 5000, generator=g, device="cuda")
+    m[3, 4999] = 1e5
+    m[5, 40] = -3e4
+    mats += [m.to(dt), (m.t() * 1e-3).to(dt).contiguous()]
+    outs = gr.orthogonalize(gr.MatrixSet(mats, out=[torch.empty_like(m) for m in mats]))
+    for m, o in zip(mats, outs):
+        _check(m, o, 2.0 ** -10)
+
+
+@pytest.mark.gpu
 def test_more_matrices_than_a_launch_holds():
     torch = _torch()
     import rl_step_gb300.grads as gr
