@@ -293,15 +293,17 @@ __device__ __forceinline__ void small_tile(const float* A, const float* B, int m
         const float2 b = ROWS ? *reinterpret_cast<const float2*>(B + (n + g) * LD + k + 2 * t)
                               : make_float2(B[(k + 2 * t) * LD + n + g], B[(k + 2 * t + 1) * LD + n + g]);
         const float a[4] = {u.x, v.x, u.y, v.y};
-        float ah[4], al[4], d[4] = {0.f, 0.f, 0.f, 0.f};
+        float ah[4], al[4], c[4] = {}, d[4] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ah[e] = tf32_hi(a[e]), al[e] = a[e] - ah[e];
-        const float b0 = tf32_hi(b.x), b1 = tf32_hi(b.y);
-        mma8(d, al, b0, b1);
-        mma8(d, ah, b.x - b0, b.y - b1);
+        for (int e = 0; e < 4; ++e) ah[e] = tf32_hi(a[e]), al[e] = tf32_hi(a[e] - ah[e]);
+        const float b0 = tf32_hi(b.x), b1 = tf32_hi(b.y), l0 = tf32_hi(b.x - b0), l1 = tf32_hi(b.y - b1);
+        // all four products of the parts, in two short chains
+        mma8(c, al, l0, l1);
+        mma8(d, ah, l0, l1);
+        mma8(c, al, b0, b1);
         mma8(d, ah, b0, b1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] += d[e];
+        for (int e = 0; e < 4; ++e) sum[e] += d[e] + c[e];
     }
 }
 
