@@ -443,6 +443,34 @@ def test_gradient_of_rows_without_numbers():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("v", [100, 9000])
+def test_gradient_beside_the_logits(v, dtype):
+    """rows of one buffer that hold logits and their gradient side by side; many rows of short ones"""
+    torch = _torch()
+    import rl_step_gb300 as m
+    import rl_step_gb300.logits as lg
+    n = 1500 if v < 1000 else 20
+    g = torch.Generator(device="cuda").manual_seed(v)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    buf = torch.randn(n, 2 * v + 6, generator=g, device="cuda").to(dt)
+    x, d = buf[:, :v], buf[:, v + 3:2 * v + 3]
+    rest = buf.clone()
+    y = torch.randint(0, v, (n,), generator=g, device="cuda", dtype=torch.int32)
+    dl = torch.randn(n, generator=g, device="cuda")
+    r = lg.token_logprobs(x, y, top=2)
+    lg.token_logprobs_backward(x, r.lse, r.entropy, y, dl, dl, top_ids=r.top_ids, d_top=r.top_logprobs, out=d)
+    want = lg.token_logprobs_backward(x.contiguous(), r.lse, r.entropy, y, dl, dl, top_ids=r.top_ids, d_top=r.top_logprobs)
+    assert torch.equal(d, want)
+    assert torch.equal(x, rest[:, :v]) and torch.equal(buf[:, v:v + 3], rest[:, v:v + 3])
+    assert torch.equal(buf[:, 2 * v + 3:], rest[:, 2 * v + 3:])
+    rows = list(range(0, n, 137)) + [n - 1]
+    _check(x[rows], y[rows], 1.0, 2, lg.TokenStats(*[t[rows] for t in r]))
+    with pytest.raises(m.MLoRAError):                       # one row for all
+        lg.token_logprobs(x[:1].expand(4, v), y[:4])
+
+
+@pytest.mark.gpu
 def test_rows_beyond_two_gigabytes():
     """offsets beyond 31 bits: the last rows of 2.4 G logits"""
     torch = _torch()
