@@ -1,6 +1,7 @@
 // The kernel of updates made orthogonal by Newton-Schulz products (mlora_orthogonalize in
-// include/mlora.h), compiled for each element type by a file of its own.  It takes matrices whose shorter side is at most 64, as LoRA
-// factors' is.  With X [r x n] over the shorter side, X_0 = M / (|M| + eps):
+// include/mlora.h), compiled for each element type by a file of its own.  It takes
+// matrices whose shorter side is at most 64, as LoRA factors' is.  With X [r x n] over
+// the shorter side, X_0 = M / (|M| + eps):
 //     X <- a X + (b A + c A^2) X,   A = X X^T.
 //
 // Everything but the long side is r x r: the products with X stay polynomials in A,
@@ -12,9 +13,15 @@
 // each tile's products at once.  Five steps are two such phases (2 + 3 steps) and
 // three passes over M; its trace gives the norm in the first.
 //
-// A cluster of blocks takes a matrix and does all of it, its blocks each a part of
-// the long side: the second and third pass find it in L2, and no launch or
-// workspace is between them.  Sums meet in a fixed order: results repeat.
+// A block, or a cluster of them where the matrices are few, takes a matrix and does all
+// of it: no launch, workspace or wait for other matrices is between the passes, and two
+// blocks an SM work while the other is at its r x r steps.  Sums meet in a fixed order:
+// results repeat.  What bounds it: for many matrices the passes, 1.7, 3.8 and 2.7
+// thousand cycles for 16 warps' tiles of 32 x 32 without their fetches (the tensor
+// cores' share 1.4, 3.4 and 1.9) and 2.7, 4.3 and 3.4 with them (32 x 4,096, fp32), at 54 %
+// of the copy rate and the tensor cores at 41 %: M is read three times, from HBM where
+// 304 matrices exceed L2.  For few matrices the chain of dependent steps: of 17 us for
+// one of 32 x 256 the r x r steps take 6, the three passes 4, the sums between them 3.
 //
 // The products run on mma.sync with fp16 operands and fp32 sums: each factor, scaled
 // by a power of two so that nothing leaves fp16 at either end, as two of them (x = hi +
@@ -816,11 +823,14 @@ constexpr int TAB_SMALL = 64, TAB_LARGE = 1300;      // 1.6 KB and 31 KB of kern
 
 int tile_for(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
 
-// Blocks of a cluster for n matrices, the longest of `longest` columns: as few as fill the SMs
-// twice over, and no more than have 512 columns each, two tiles a warp.
+// Blocks of a cluster for n matrices, the longest of `longest` columns: as few as give each SM
+// its two, and no more than have 512 columns each, two tiles a warp.  (Two fp32 adapters of the
+// 8B widths, 112 matrices: 98 us with clusters of four, 129 of eight, 121 of two; 1,200 of 32 x
+// 4,096: 478 us with a block each, 598 with two: a block does the r x r steps of its matrix, so
+// more blocks do them more often.)
 int blocks_for(int n, int longest, int num_sms) {
     int blocks = 1;
-    while (blocks < MAX_BLOCKS && (int64_t)n * blocks < 4 * num_sms && longest / blocks >= 1024) blocks *= 2;
+    while (blocks < MAX_BLOCKS && (int64_t)n * blocks < 2 * num_sms && longest / blocks >= 1024) blocks *= 2;
     return blocks;
 }
 
