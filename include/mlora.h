@@ -451,7 +451,7 @@ int mlora_clip_grads(const mlora_grad_set* g, float max_norm, float* norms_out, 
  *     x = M / (|M| + eps),   |M| the Frobenius norm
  *     steps times:  x <- a x + (b A + c A A) x,   A = x x^T
  *     out = x, as M lies
- * Sums are fp32, factors of products enter with 2^-21 of themselves.  Small
+ * Sums are fp32, factors of products enter with 2^-22 of themselves.  Small
  * singular values are multiplied by up to a^steps, and so are the rounding errors in
  * their directions: with s the smallest singular value over |M| and five steps of the
  * usual (3.4445, -4.7750, 2.0315), out is off by about 2^-20 + 2^-24 / s of its norm.

@@ -83,6 +83,7 @@ typedef struct {
 /* dlogits = the gradient in x, rounded once to x's type:
  *     dx_j = scale ( [j = y] d_logprob + sum_k [j = id_k] d_top_k
  *                    + p_j (d_lse - d_logprob - sum_k d_top_k) - d_entropy p_j (log p_j + entropy) )
+ * p_j comes from the rounded lse and carries about 2^-22 (1 + |lse|) of itself.
  * A row whose incoming gradients are all 0, and a row without a distribution (lse =
  * -infinity), gets zeros whatever its logits; the row of an lse that is NaN otherwise NaN.
  * An id outside -1 .. vocab-1 raises bit 0 of *status and counts as -1; an id may

@@ -21,7 +21,7 @@
 // cores' share 1.4, 3.4 and 1.9) and 2.7, 4.3 and 3.4 with them (32 x 4,096, fp32), at 54 %
 // of the copy rate and the tensor cores at 41 %: M is read three times, from HBM where
 // 304 matrices exceed L2.  For few matrices the chain of dependent steps: of 17 us for
-// one of 32 x 256 the r x r steps take 6, the three passes 4, the sums between them 3.
+// one of 32 x 256 the r x r steps take 6, the three passes 4, the sums between them 2.
 //
 // The products run on mma.sync with fp16 operands and fp32 sums: each factor, scaled
 // by a power of two so that nothing leaves fp16 at either end, as two of them (x = hi +

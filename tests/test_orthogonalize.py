@@ -1,7 +1,7 @@
 """Updates made orthogonal (mlora_orthogonalize) against the definition in doubles.
 
-Tolerance.  A product's terms are off by at most 2^-20 of themselves (three tf32
-products of parts of 11 bits; the fourth is left out), so with |X|_F = 1 the first A is
+Tolerance.  A product's terms are off by at most 2^-20 of themselves (three
+products of fp16 parts of 11 bits; the fourth is left out), so with |X|_F = 1 the first A is
 off by E, |E|_F <= 2^-20.  A step's polynomial Q = a + b A + c A^2 is then off by
 (|b| + 2 |c| |A|) E <= 10 E, x Q(x^2) has a slope of at most 3.9 where singular values
 fall (0 .. 1.2), and A's own error grows by a^2 = 11.9 a step inside a phase of at most
