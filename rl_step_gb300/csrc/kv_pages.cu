@@ -22,7 +22,7 @@ namespace {
 
 constexpr int ST_NO_PAGES = 4;
 constexpr int PT = 1024;                     // most threads
-// Sequences of a thread in a round: SEQS = 1, or 4 where the block has no thread for each (4,043 sequences
+// Sequences of a thread in a pass: SEQS = 1, or 4 where the block has no thread for each (4,043 sequences
 // cut and grown: 20 us, 51 with one; 256: 9 us with one, 13 with four).
 
 struct PoolView {
@@ -119,7 +119,7 @@ __device__ __forceinline__ void write_row(const PoolView& p, const GrowView& g, 
 template <int SEQS>
 __global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ PoolView p, const __grid_constant__ GrowView g,
                                                      int rows_here) {
-    __shared__ int s_first[PT * SEQS];        // new pages before a sequence's own, of this round (at most the free ones)
+    __shared__ int s_first[PT * SEQS];        // new pages before a sequence's own, of this pass (at most the free ones)
     __shared__ int s_have[PT * SEQS];
     const int tid = threadIdx.x, nt = blockDim.x;
     int avail = *p.n_free;
