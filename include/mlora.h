@@ -455,7 +455,8 @@ int mlora_clip_grads(const mlora_grad_set* g, float max_norm, float* norms_out, 
  * singular values are multiplied by up to a^steps, and so are the rounding errors in
  * their directions: with s the smallest singular value over |M| and five steps of the
  * usual (3.4445, -4.7750, 2.0315), out is off by about 2^-20 + 2^-24 / s of its norm.
- * A matrix of zeros stays zero.  One with an infinity or NaN becomes NaN throughout.
+ * A matrix of zeros stays zero.  One with an infinity or NaN becomes NaN throughout, and
+ * so does one whose iteration leaves fp32's range (coefficients that diverge).
  * Magnitudes whose squares leave fp32's range are taken relative to the largest.
  * Results repeat bit for bit and do not depend on the other matrices of the set.
  *   src, dst: HOST arrays of DEVICE pointers to contiguous row-major matrices of

@@ -59,8 +59,8 @@ struct OrthoTab {
     OrthoEntry e[N];
 };
 
-// the nearest value of 11 bits (away from 0 between two); x is far below fp32's largest
-// the nearest value of 11 bits (away from 0 between two); x is far below fp32's largest
+// the nearest value of 11 bits (away from 0 between two), infinity near fp32's largest; a NaN may become 0 here: small_steps
+// sees it where it comes up
 __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
 
 // d += a b, 16 x 8 x 8 with tf32 operands
@@ -406,14 +406,15 @@ __device__ __forceinline__ float scale_to(float m, int to) {
     return ldexpf(1.f, max(-126, min(126, to - e)));
 }
 
-// sh.P as fragments for P X, times the power of two that is returned
+// sh.P as fragments for P X, times the power of two that is returned; NaN, all of them and the power, where a
+// thread is `bad` or P has left fp32: so are P X, the next A and the result then
 template <typename T, int R, bool TALL>
-__device__ __forceinline__ float fragments(const Matrix<T, R, TALL>& x, OrthoShared<T, R>& sh) {
+__device__ __forceinline__ float fragments(const Matrix<T, R, TALL>& x, OrthoShared<T, R>& sh, bool bad) {
     constexpr int LD = R + 8;
     float m = 0.f;
     for (int i = threadIdx.x; i < R * R; i += OT) m = fmaxf(m, fabsf(sh.P[i / R * LD + i % R]));
-    m = block_max(m, sh.red);
-    const float scale = m > 0.f && m <= FLT_MAX ? scale_to(m, 14) : 1.f;
+    m = block_max(bad ? INFINITY : m, sh.red);
+    const float scale = m > FLT_MAX ? __int_as_float(0x7fc00000) : m > 0.f ? scale_to(m, 14) : 1.f;
     for (int i = threadIdx.x; i < R / 16 * (R / 16) * 32; i += OT) {
         const int lane = i % 32, s = i / 32 % (R / 16), mm = i / 32 / (R / 16), g = lane >> 2, t = lane & 3;
         uint32_t hi[4], lo[4];
@@ -657,18 +658,25 @@ __device__ __forceinline__ void write_px(const Matrix<T, R, TALL>& x, OrthoShare
 // between them.  All are polynomials in A, which commute and are symmetric but for
 // roundings.  Two of the products take a factor by rows for that; A^2 and Q P by columns:
 // a transposed P or A there let the roundings grow (a spread of singular values of 100
-// was off by 1e-5 of the result's norm instead of 2e-6).
+// was off by 1e-5 of the result's norm instead of 2e-6).  Returns whether this thread has
+// stored a number that is not finite: an iteration that leaves fp32 is seen by one of them (Q takes A's numbers
+// with b as they are), although the factors' parts need not keep its NaN.
 template <typename T, int R>
-__device__ __forceinline__ void small_steps(OrthoShared<T, R>& sh, const OrthoCoeffs& co, int steps) {
+__device__ __forceinline__ bool small_steps(OrthoShared<T, R>& sh, const OrthoCoeffs& co, int steps) {
     constexpr int LD = R + 8, TILES = R / 16 * (R / 8), MINE = (TILES + OW - 1) / OW;
     const int warp = threadIdx.x >> 5;
+    float none = 0.f;                        // NaN from the first infinity or NaN on
+    auto seen = [&](float v) {
+        none = fmaf(v, 0.f, none);
+        return v;
+    };
 #pragma unroll 1
     for (int k = 0; k < steps; ++k) {
         small_tiles<R>([&](int m, int n) {
             float d[4];
             small_tile<R, false>(sh.A, sh.A, m, n, d);
             small_store<R>(sh.Q, m, n, [&](int i, int j, int e) {
-                return fmaf(co.c, d[e], co.b * sh.A[i * LD + j]) + (i == j ? co.a : 0.f);
+                return seen(fmaf(co.c, d[e], co.b * sh.A[i * LD + j]) + (i == j ? co.a : 0.f));
             });
         });
         __syncthreads();
@@ -682,24 +690,25 @@ __device__ __forceinline__ void small_steps(OrthoShared<T, R>& sh, const OrthoCo
             small_tiles<R>([&](int m, int n) {
                 float d[4];
                 small_tile<R, true>(sh.Q, sh.A, m, n, d);
-                small_store<R>(sh.W, m, n, [&](int, int, int e) { return d[e]; });
+                small_store<R>(sh.W, m, n, [&](int, int, int e) { return seen(d[e]); });
             });
         }
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < MINE; ++q) {
             const int tile = warp + q * OW;
-            if (tile < TILES) small_store<R>(sh.P, tile / (R / 8) * 16, tile % (R / 8) * 8, [&](int, int, int e) { return p[q][e]; });
+            if (tile < TILES) small_store<R>(sh.P, tile / (R / 8) * 16, tile % (R / 8) * 8, [&](int, int, int e) { return seen(p[q][e]); });
         }
         if (k + 1 < steps) {
             small_tiles<R>([&](int m, int n) {
                 float d[4];
                 small_tile<R, true>(sh.W, sh.Q, m, n, d);
-                small_store<R>(sh.A, m, n, [&](int, int, int e) { return d[e]; });
+                small_store<R>(sh.A, m, n, [&](int, int, int e) { return seen(d[e]); });
             });
         }
         __syncthreads();
     }
+    return !(none == 0.f);
 }
 
 // All of one matrix, or a block's part of it.
@@ -773,9 +782,9 @@ __device__ __forceinline__ void orthogonal(const OrthoEntry& entry, const OrthoC
     int left = co.steps, phases = (left + STEPS_A_PHASE - 1) / STEPS_A_PHASE;
     while (true) {
         const int now = left / phases;
-        small_steps<T, R>(sh, co, now);
+        const bool bad = small_steps<T, R>(sh, co, now);
         left -= now;
-        const float p = 1.f / fragments<T, R, TALL>(x, sh);
+        const float p = 1.f / fragments<T, R, TALL>(x, sh, bad);
         if (--phases == 0) {
             write_px<T, R, TALL>(x, sh, p, first, end);
             return;

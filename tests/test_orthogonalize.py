@@ -294,6 +294,27 @@ def test_parts_of_very_different_size(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("co,steps", [((5.0, 5.0, 5.0), 5), ((5.0, 5.0, 5.0), 6), ((5.0, 5.0, 5.0), 9), ((5.0, 5.0, 5.0), 12),
+                                      ((1e10, 0.0, 0.0), 12), ((1.0, -1e20, 0.0), 3), ((1.0, 1.0, 1e30), 2)])
+def test_an_iteration_that_diverges_gives_nan(co, steps, dtype):
+    """x grows to a few times 5 |x|^5 a step from |x| near 1: beyond fp32's range after five.  (1, -1e20, 0): 1e20, 1e80;
+    (1, 1, 1e30): its second A is beyond 1e60.  No number that an optimizer would take, whatever the shape"""
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(steps)
+    for shape in ((32, 600), (600, 13), (64, 900), (8, 8), (4096, 16), (32, 12288)):
+        m = torch.randn(*shape, generator=g, device="cuda").to(dt)
+        out, zero = (gr.orthogonalize(gr.MatrixSet([x], out=[torch.empty_like(x)]), steps, co)[0] for x in (m, torch.zeros_like(m)))
+        assert torch.isnan(out).all(), (shape, torch.isfinite(out).sum().item())
+        assert (zero == 0).all()
+        m_in_place = m.clone()
+        gr.orthogonalize(gr.MatrixSet([m_in_place]), steps, co)
+        assert torch.isnan(m_in_place).all()
+
+
+@pytest.mark.gpu
 def test_more_matrices_than_a_launch_holds():
     torch = _torch()
     import rl_step_gb300.grads as gr
