@@ -154,7 +154,11 @@ int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const ml
  *
  * A row of the page table is a sequence's home: it owns the pages that it took.
  * A page in a row that another row owns (a shared prefix, put there by the caller)
- * is read as any other and never given back by this one.
+ * is read as any other, never given back by this one, and never written: a sequence
+ * does not grow inside a page that is not its own, so a shared prefix ends with a page
+ * and its readers are cut back to whole pages of it.  When the owner gives the pages
+ * back, entries of other rows stay and name pages that others will take: cut
+ * those rows first.
  *
  * The free list is a stack, free_pages[0 .. *n_free).  A new pool of n pages has
  * their ids there in any order, *n_free = n and owner[i] = -1.  What the device
@@ -180,8 +184,8 @@ typedef struct {
  *     the rows behind the last.
  * A sequence is left as it is, with no rows, if its numbers are out of range
  * (negative, or together more than max_pages * 64 or 2^31 - 1), if the new rows of the
- * sequences up to it exceed n_rows (both bit 0), or if their pages exceed the free
- * ones (bit 2).  Those sums count every sequence in range, so one that is too large
+ * sequences up to it exceed n_rows, if its last page is part-filled and row s does not
+ * own it (all bit 0), or if their pages exceed the free ones (bit 2).  Those sums count every sequence in range, so one that is too large
  * refuses those behind it that need pages too.  Errors: E_ARG, E_CUDA. */
 typedef struct {
     int32_t* page_table;       /* DEVICE [n_seqs x max_pages], updated       */

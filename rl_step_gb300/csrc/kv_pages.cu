@@ -108,8 +108,7 @@ __device__ __forceinline__ void write_row(const PoolView& p, const GrowView& g, 
         s = find(g.row_off, g.n_seqs, r);
         pos = g.kv_len[s] - (g.row_off[s + 1] - (int)r);
         const int id = g.table[(int64_t)s * g.max_pages + pos / KV_PAGE];
-        if (id >= 0 && id < p.n_pages) slot = (int64_t)id * KV_PAGE + pos % KV_PAGE;
-        else raise_status(p.status, ST_RANGE);
+        if (id >= 0) slot = (int64_t)id * KV_PAGE + pos % KV_PAGE;      // (else the list had no page there: raised)
     }
     if (g.positions) g.positions[r] = pos;
     if (g.seqs) g.seqs[r] = s;
@@ -139,24 +138,32 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ Poo
             add[i] = s0 + i < g.n_seqs ? g.n_new[s0 + i] : 0;
         }
         Two mine[SEQS], sum{0, 0};
+        int last[SEQS];                       // the page that the first new row goes into,
+        bool inside[SEQS];                    // where that page has rows already
 #pragma unroll
         for (int i = 0; i < SEQS; ++i) {
             ok[i] = len[i] >= 0 && add[i] >= 0 && (int64_t)len[i] + add[i] <= g.max_len;
             have[i] = ok[i] ? pages_of(len[i]) : 0;
             mine[i] = Two{ok[i] ? pages_of((int64_t)len[i] + add[i]) - have[i] : 0, ok[i] ? add[i] : 0};
             sum.a += mine[i].a, sum.b += mine[i].b;
+            inside[i] = mine[i].b > 0 && len[i] % KV_PAGE > 0;
+            last[i] = inside[i] ? g.table[(int64_t)(s0 + i) * g.max_pages + len[i] / KV_PAGE] : -1;
         }
         Two all;
         Two upto = block_scan(sum, &all);
         upto.a += want.a - sum.a, upto.b += want.b - sum.b;
+#pragma unroll
+        for (int i = 0; i < SEQS; ++i) last[i] = last[i] >= 0 && last[i] < p.n_pages ? p.owner[last[i]] : -1;     // whose it is
         Two take{0, 0};
 #pragma unroll
         for (int i = 0; i < SEQS; ++i) {
             // A sequence is served if the pages and rows asked for up to it are there; what needs none always is.
             upto.a += mine[i].a, upto.b += mine[i].b;
             const bool pages_ok = mine[i].a == 0 || upto.a <= avail, rows_ok = mine[i].b == 0 || upto.b <= g.n_rows;
-            served[i] = ok[i] && pages_ok && rows_ok;
-            if (!served[i]) raise_status(p.status, !ok[i] || !rows_ok ? ST_RANGE : ST_NO_PAGES);
+            // rows inside a page that is another's, or nobody's, would overwrite what its owner has or gets there
+            const bool own = !inside[i] || last[i] == s0 + i;
+            served[i] = ok[i] && pages_ok && rows_ok && own;
+            if (!served[i]) raise_status(p.status, !ok[i] || !rows_ok || !own ? ST_RANGE : ST_NO_PAGES);
             else take.a += mine[i].a, take.b += mine[i].b;
         }
         Two taken;

@@ -300,7 +300,9 @@ def kv_reserve(pool: PagePool, page_table, kv_len, n_new, n_rows: int, stream=No
     """Grow the sequences by n_new int32 [n_seqs] tokens: kv_len and page_table are
     updated in place.  Returns int32 row_off [n_seqs + 1], positions and seqs
     [n_rows] and int64 slots [n_rows] of the new rows (-1 behind the last); n_rows:
-    an upper bound of their number that the caller knows on the host."""
+    an upper bound of their number that the caller knows on the host.  A sequence
+    whose part-filled last page is another's (a shared prefix) does not grow: E_RANGE
+    of kv_pool_check_status."""
     if page_table.dim() != 2:
         raise ValueError("page_table must be [n_seqs, max_pages]")
     n, width = page_table.shape

@@ -309,6 +309,60 @@ def test_shared_pages_stay_with_their_owner():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [4, 1500])
+def test_no_growth_inside_a_page_of_another_sequence(n):
+    """a row cut to a length inside a shared page, a prefix that ends inside one, and a page that its owner has given back:
+    no slot in them, the sequence is left as it is and those behind it are served"""
+    torch = _torch()
+    b = Both(20, n, 4, seed=8)
+    rest = [0] * (n - 4)
+    b.reserve([130, 0, 0, 40] + rest)
+    b.m.table[1, :2], b.m.len[1] = b.m.table[0, :2], 128
+    b.m.table[2, :3], b.m.len[2] = b.m.table[0, :3], 130
+    b.push()
+    assert b.release([130, 100, 130, 40] + rest) == 0
+    table, free = b.m.table.copy(), list(b.m.free)
+
+    def grow(new, lens, off, slots, status=-2):
+        r = b.kv.kv_reserve(b.pool, b.table, b.len, b.i32(new + rest), 64)
+        assert b.kv.kv_pool_check_status(b.pool) == status
+        assert b.len.tolist() == lens + rest and (b.table.cpu().numpy() == table).all()
+        assert r.row_off.tolist() == off + [off[-1]] * len(rest)
+        assert r.slots.tolist() == slots + [-1] * (64 - len(slots)) and b.pool.n_free.item() == len(free)
+
+    def at(s, pos):
+        return int(table[s, pos // PAGE]) * PAGE + pos % PAGE
+
+    grow([0, 5, 3, 0], [130, 100, 130, 40], [0, 0, 0, 0, 0], [])
+    grow([1, 5, 3, 2], [131, 100, 130, 42], [0, 1, 1, 1, 3], [at(0, 130), at(3, 40), at(3, 41)])
+    grow([0, 0, 0, 1], [131, 100, 130, 43], [0, 0, 0, 0, 1], [at(3, 42)], status=0)
+    # 30 tokens would need a page as well: it is not taken
+    grow([0, 30, 0, 1], [131, 100, 130, 44], [0, 0, 0, 0, 1], [at(3, 43)])
+    # the same without rows asked for
+    new, row_off = b.i32([0, 5, 3, 1] + rest), b.i32([0] * (n + 1))
+    q = b.kv._KvGrowth(b.table.data_ptr(), b.len.data_ptr(), new.data_ptr(), row_off.data_ptr(), None, None, None, 64, n, 4)
+    torch.cuda.synchronize()
+    assert b.kv._lib().mlora_kv_reserve(b.pool._ref, ctypes.byref(q), None) == 0
+    assert b.kv.kv_pool_check_status(b.pool) == -2 and b.len.tolist() == [131, 100, 130, 45] + rest
+    # an entry that is no page
+    bad = b.table.clone()
+    for entry in (-1, 20, 2 ** 31 - 1, -2 ** 31):
+        bad[3, 0] = entry
+        r = b.kv.kv_reserve(b.pool, bad, b.len, b.i32([0, 0, 0, 1] + rest), 1)
+        assert b.kv.kv_pool_check_status(b.pool) == -2 and b.len.tolist() == [131, 100, 130, 45] + rest
+        assert r.slots.tolist() == [-1]
+    # the owner gives its pages back: nobody's now, and soon another's
+    b.m.len[:4] = [131, 100, 130, 45]
+    assert b.release([0, 100, 130, 45] + rest) == 0
+    table, free = b.m.table.copy(), list(b.m.free)
+    grow([0, 5, 3, 0], [0, 100, 130, 45], [0, 0, 0, 0, 0], [])
+    # cut back to whole pages both grow in pages of their own
+    assert b.release([0, 64, 128, 45] + rest) == 0
+    assert b.reserve([0, 5, 70, 1] + rest) == 0
+    assert b.m.owner[b.m.table[1, 1]] == 1 and b.m.owner[b.m.table[2, 2]] == b.m.owner[b.m.table[2, 3]] == 2
+
+
+@pytest.mark.gpu
 def test_captured_growth_replays_and_other_stream():
     """a decode step's cut and growth as a graph: lengths and lists are read at replay"""
     torch = _torch()
