@@ -458,7 +458,10 @@ int mlora_clip_grads(const mlora_grad_set* g, float max_norm, float* norms_out, 
  * A matrix of zeros stays zero.  One with an infinity or NaN becomes NaN throughout, and
  * so does one whose iteration leaves fp32's range (coefficients that diverge).
  * Magnitudes whose squares leave fp32's range are taken relative to the largest.
- * Results repeat bit for bit and do not depend on the other matrices of the set.
+ * Results repeat bit for bit.  Values of other matrices do not enter a matrix's result, but the
+ * number of matrices of a set and the longest one's length decide over how many blocks each is
+ * spread, and so the order of its sums: alone and in a large set it can differ by its rounding
+ * errors above.
  *   src, dst: HOST arrays of DEVICE pointers to contiguous row-major matrices of
  *     `dtype`, aligned to their elements; dst NULL: in place.  A matrix and its
  *     output are equal or do not overlap, and no output overlaps another matrix or

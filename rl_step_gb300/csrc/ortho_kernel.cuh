@@ -836,7 +836,8 @@ int tile_for(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
 // its two, and no more than have 512 columns each, two tiles a warp.  (Two fp32 adapters of the
 // 8B widths, 112 matrices: 98 us with clusters of four, 129 of eight, 121 of two; 1,200 of 32 x
 // 4,096: 478 us with a block each, 598 with two: a block does the r x r steps of its matrix, so
-// more blocks do them more often.)
+// more blocks do them more often.)  The blocks decide the order of a matrix's sums, and so do the other matrices of
+// a call: one size for each shape would cost a large set two blocks' r x r steps or one adapter its second block.
 int blocks_for(int n, int longest, int num_sms) {
     int blocks = 1;
     while (blocks < MAX_BLOCKS && (int64_t)n * blocks < 2 * num_sms && longest / blocks >= 1024) blocks *= 2;

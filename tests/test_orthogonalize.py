@@ -315,6 +315,38 @@ def test_an_iteration_that_diverges_gives_nan(co, steps, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_one_matrix_alone_and_among_many(dtype):
+    """the number and lengths of a set's matrices say over how many blocks one is spread, and so the order of its sums: the
+    results differ by what each is off at most, 2^-20 + 2^-24 / s, and by two roundings to bf16 of values that far apart
+    (each half a step of 2^-7 at most); a set as it is repeats bit for bit"""
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(21)
+    mats = [m for m in torch.randn(400, 32, 4096, generator=g, device="cuda").to(dt)]
+    outs = [torch.empty_like(m) for m in mats]
+    ms = gr.MatrixSet(mats, out=outs)
+    gr.orthogonalize(ms)
+    first = [o.clone() for o in outs]
+    gr.orthogonalize(ms)
+    assert all(torch.equal(a, b) for a, b in zip(first, outs))
+    for i in (0, 7, 399):
+        alone = gr.orthogonalize(gr.MatrixSet([mats[i]], out=[torch.empty_like(mats[i])]))[0]
+        for o in (alone, outs[i]):
+            _check(mats[i], o, 2.0 ** -16)
+        s = torch.linalg.svdvals(mats[i].double())
+        bound = 2 * (2.0 ** -20 + 2.0 ** -24 * (s.norm() / s[-1]).item())
+        a, b = alone.double(), outs[i].double()
+        apart = (a - b).abs()
+        if dtype == "bf16":
+            # neighbours at most, where the values before the rounding lie on two sides of a middle
+            assert (apart <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + bound * b.norm()).all()
+        else:
+            assert (apart.norm() <= (bound + 2.0 ** -24) * b.norm()).item(), (apart.norm() / b.norm()).item()
+
+
+@pytest.mark.gpu
 def test_more_matrices_than_a_launch_holds():
     torch = _torch()
     import rl_step_gb300.grads as gr
