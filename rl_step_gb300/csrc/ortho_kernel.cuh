@@ -24,14 +24,18 @@
 // one of 32 x 256 the r x r steps take 6, the three passes 4, the sums between them 2.
 //
 // The products run on mma.sync with fp16 operands and fp32 sums: each factor, scaled
-// by a power of two so that nothing leaves fp16 at either end, as two of them (x = hi +
-// lo, 2^-22 of itself; three products, the fourth is left out; an X that was bf16 needs
-// no lo).  Fragments of X come from a warp's own tiles in shared memory, filled ahead
-// with cp.async; the same fragment is both operands of X X^T, and the output fragment
-// of P X becomes both of the next without leaving its thread.  The tensor cores cut
-// their sums off (towards 0), so few products are chained, the small parts first, and
-// their results are added in fp32.  r is 4 to 64: a 128-row tcgen05 tile would hold 2 to
-// 8 matrices and form their cross products for nothing.
+// by a power of two so that nothing exceeds fp16, as two of them (x = hi + lo, three
+// products, the fourth is left out; an X that was bf16 needs no lo).  That is 2^-22 of x, or
+// 2^-25 of the scaled 1 where lo is below fp16's normal range: 2^-30 of the root mean
+// square that a warp's first tile is scaled by in the first pass, 2^-39 of |M| in the others.
+// All 24 bits would take a third part and six products; what the two leave in the result is of the
+// size of the plain fp32 form's errors (one small fp32 adapter 1.48e-6 beside 1.35e-6, 32 of the
+// 8B widths 1.47e-6 beside 4.45e-6).  Fragments of X come from a warp's own tiles in
+// shared memory, filled ahead with cp.async; the same fragment is both operands of X X^T,
+// and the output fragment of P X becomes both of the next without leaving its thread.  The
+// tensor cores cut their sums off (towards 0), so few products are chained, the small
+// parts first, and their results are added in fp32.  r is 4 to 64: a 128-row tcgen05 tile
+// would hold 2 to 8 matrices and form their cross products for nothing.
 #pragma once
 
 #include <algorithm>

@@ -315,6 +315,22 @@ def test_an_iteration_that_diverges_gives_nan(co, steps, dtype):
 
 
 @pytest.mark.gpu
+def test_elements_far_below_the_others():
+    """one step of x <- x is M / |M|, element by element.  The norm is off by 2^-20 (its squares' factors), P and M by 2^-22
+    each, the product of their low parts 2^-22, the result 2^-24: 2^-19 with room for P's and the norm's own roundings; an
+    element whose low part is below fp16's normal range by 2^-25 of what |M|, in 2^14 .. 2^15, is scaled to: 2^-39"""
+    torch = _torch()
+    import rl_step_gb300.grads as gr
+    g = torch.Generator(device="cuda").manual_seed(6)
+    for shape in ((32, 2048), (2048, 32), (12, 300), (300, 60)):
+        m = torch.randn(*shape, generator=g, device="cuda")
+        m *= 10.0 ** torch.randint(-9, 1, shape, generator=g, device="cuda")
+        out = gr.orthogonalize(gr.MatrixSet([m], out=[torch.empty_like(m)]), 1, (1.0, 0.0, 0.0))[0].double()
+        want = m.double() / (m.double().norm() + float(np.float32(1e-7)))
+        assert ((out - want).abs() <= 2.0 ** -19 * want.abs() + 2.0 ** -39).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_one_matrix_alone_and_among_many(dtype):
     """the number and lengths of a set's matrices say over how many blocks one is spread, and so the order of its sums: the
