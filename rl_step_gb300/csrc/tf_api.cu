@@ -12,6 +12,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <string>
 #include <utility>
@@ -789,13 +790,18 @@ struct TfStats {
     mlora_token_stats out;
 };
 
-// The rows' statistics from h->xf: a chunk of rows' logits in fp32 where the
-// backward keeps its dz, which is zero between calls (its padding columns are an
-// operand of dz Wout) and is left so.
-int row_stats(mlora_tf_t* h, const TfStats& st, int mt_upper, cudaStream_t s) {
+// Test hook (not in the public headers): mlk_test_fail_stats_at(n) makes the n-th launch of row
+// statistics from then on fail, on the host and without touching the device.
+std::atomic<int64_t> g_fail_stats_at{0};
+
+cudaError_t launch_stats(const LogitsView& v, const mlora_token_stats& out, int num_sms, cudaStream_t s) {
+    if (g_fail_stats_at.load() > 0 && --g_fail_stats_at == 0) return cudaErrorLaunchOutOfResources;
+    return launch_token_logprobs(v, out, num_sms, s);
+}
+
+// The rows' statistics from h->xf, `chunk` row tiles' logits at a time in z.
+int stats_of_chunks(mlora_tf_t* h, const TfStats& st, int mt_upper, int chunk, float* z, cudaStream_t s) {
     const int V = h->V, d = h->d;
-    float* z = reinterpret_cast<float*>(h->dz[0]);
-    const int chunk = h->nc_tiles >= 4 ? h->nc_tiles / 4 * 2 : 1;
     for (int c0 = 0; c0 < mt_upper; c0 += chunk) {
         const int cnt = mt_upper - c0 < chunk ? mt_upper - c0 : chunk;
         GemmParams p = tf_dense(h, mt_upper, V, d);
@@ -815,10 +821,22 @@ int row_stats(mlora_tf_t* h, const TfStats& st, int mt_upper, cudaStream_t s) {
         v.out_row = h->rb.perm_pad + c0 * TILE_M;
         v.row_tiles = h->rb.meta; v.row0 = (int64_t)c0 * TILE_M;
         v.scale = st.scale; v.V = V; v.dtype = MLORA_FP32; v.top = st.top;
-        TF_CUDA(launch_token_logprobs(v, st.out, h->num_sms, s));
+        TF_CUDA(launch_stats(v, st.out, h->num_sms, s));
         ++h->launches;
     }
-    TF_CUDA(cudaMemsetAsync(z, 0, sizeof(float) * (size_t)(mt_upper < chunk ? mt_upper : chunk) * TILE_M * h->Vpad, s));
+    return MLORA_OK;
+}
+
+// The logits lie in fp32 where the backward keeps its dz.  That is zero between calls: the
+// recomputing form reads columns up to the next multiple of 64 and writes them up to that of
+// 32.  It is left so, also when a launch has failed on the way.
+int row_stats(mlora_tf_t* h, const TfStats& st, int mt_upper, cudaStream_t s) {
+    float* z = reinterpret_cast<float*>(h->dz[0]);
+    const int chunk = h->nc_tiles >= 4 ? h->nc_tiles / 4 * 2 : 1;
+    const int rc = stats_of_chunks(h, st, mt_upper, chunk, z, s);
+    const cudaError_t e = cudaMemsetAsync(z, 0, sizeof(float) * (size_t)(mt_upper < chunk ? mt_upper : chunk) * TILE_M * h->Vpad, s);
+    if (rc) return rc;
+    TF_CUDA(e);
     return MLORA_OK;
 }
 
@@ -1114,6 +1132,8 @@ extern "C" int mlora_tf_forward(mlora_tf_t* h, const mlora_tf_batch* b, float* l
     LossArgs la{-1, nullptr, nullptr, nullptr, 0.f, nullptr};
     return tf_dispatch(h, b, la, logprobs_out, nullptr, false, stream);
 }
+
+extern "C" void mlk_test_fail_stats_at(int64_t n) { g_fail_stats_at.store(n); }
 
 extern "C" int mlora_tf_forward_stats(mlora_tf_t* h, const mlora_tf_batch* b, float scale, int32_t top,
                                       const mlora_token_stats* out, void* stream) {

@@ -635,3 +635,38 @@ def test_stats_of_the_transformer_match_the_oracle():
     best = r.top_ids[:, 0].cpu().numpy()
     want = s.o.forward(toks, best, pos, ads)
     assert np.abs(r.top_logprobs[:, 0].cpu().numpy() - want).max() <= 2e-2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fails", [1, 2])
+def test_a_step_after_statistics_that_failed(fails):
+    """a launch of the statistics fails (by the library's hook, on the host): the error is returned, and the logits that are
+    in the backward's buffer by then are none of the next step's"""
+    torch = _torch()
+    import rl_step_gb300 as m
+    import rl_step_gb300.logits as lg
+    import rl_step_gb300.transformer as t
+    from test_rollout import Setup
+    hook = lg._lib().mlk_test_fail_stats_at
+    hook.restype, hook.argtypes = None, [ctypes.c_int64]
+    s = Setup(max_tokens=640, qk_std=0.05, vocab=990)    # 992 .. 1023: columns that the backward reads and does not write
+    rng = np.random.default_rng(5)
+    n = 600                                              # five tiles of rows, two at a time
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (i32(rng.integers(0, s.cfg.vocab, n)), i32(rng.integers(0, s.cfg.vocab, n)), i32(np.arange(n)), i32(np.zeros(n)))
+    dl = torch.randn(n, device="cuda")
+
+    def step():
+        out, _ = t.tf_forward_backward_custom(s.h, *args, dl)
+        g = t.tf_read_adapter(s.h, 0, 0, "q", "A", "grad").clone()
+        t.tf_optim_step(s.h, lr=0.0)
+        return out.clone(), g
+
+    first = step()
+    hook(fails)
+    with pytest.raises(m.MLoRAError):
+        lg.tf_forward_stats(s.h, *args, top=3)
+    again = step()
+    assert torch.equal(first[0], again[0]) and torch.isfinite(again[1]).all()
+    assert torch.allclose(first[1], again[1], rtol=1e-4, atol=1e-6 * first[1].abs().max().item())   # atomics' order
+    assert torch.isfinite(lg.tf_forward_stats(s.h, *args, top=3).entropy).all()                     # the hook is off again
