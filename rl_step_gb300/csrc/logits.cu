@@ -40,7 +40,8 @@ constexpr int BT = 256;                       // threads of a block
 constexpr int MAX_TOP = MLORA_LOGITS_MAX_TOP;
 constexpr int LIST = 96;                      // groups that a team lists
 constexpr int FOUND = MAX_TOP * G + 32;       // and logits: MAX_TOP groups of 16 and at most 30 beside them
-constexpr float LOWEST = -1e30f;              // below it a logit counts as -infinity in the quick pass
+constexpr float LOWEST = -1e30f;              // a logit below it counts as this one in the quick pass: its products are finite
+constexpr float FAR = 1e6f;                   // a maximum this far from 0, in base 2, is for the careful pass
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 typedef unsigned long long u64;
@@ -99,7 +100,7 @@ template <> struct Group<bf16> {
         const float2 f = bf16_pair(m);
         return max_nan(f.x, f.y);
     }
-    // pair i, not below LOWEST (its nearest bf16 value)
+    // pair i, not below LOWEST (the bf16 value above it)
     __device__ __forceinline__ float2 clamped(int i) const { return bf16_pair(max_nan2(w[i], 0xf149f149u)); }
 };
 template <> struct Group<float> {
@@ -119,17 +120,17 @@ template <> struct Group<float> {
     }
 };
 
-// m, s, t of some of a row's logits (above); m = -FLT_MAX where there are none
+// m, s, t of some of a row's logits (above).  m is at least -FAR, so that tokens that are not
+// allowed (-infinity or any number far below) have terms of 0 wherever they stand: as the maximum of the first ids
+// that a thread sees they would be what the terms are relative to, and the rounding of their product, 2^-24 of a
+// huge number, the exponent.
 struct Part {
     float m, s, t;
 };
 __device__ __forceinline__ Part join(const Part& a, const Part& b) {
     const float m = max_nan(a.m, b.m);
     const float da = a.m - m, db = b.m - m, fa = ex2(da), fb = ex2(db);
-    // no terms, and a distance that need not be finite
-    const float ta = a.s == 0.f ? 0.f : fmaf(a.s, da, a.t) * fa, tb = b.s == 0.f ? 0.f : fmaf(b.s, db, b.t) * fb;
-    // (fa, fb are 0 beyond 2^-126 of the other, and their t with them)
-    return Part{m, fmaf(a.s, fa, b.s * fb), (fa == 0.f ? 0.f : ta) + (fb == 0.f ? 0.f : tb)};
+    return Part{m, fmaf(a.s, fa, b.s * fb), fmaf(a.s, da, a.t) * fa + fmaf(b.s, db, b.t) * fb};
 }
 
 // What a team shares.
@@ -359,8 +360,8 @@ __device__ void top_of_share(const Share<T>& r, const T* gmax, const float (&bes
     team_sync<NT>();
 }
 
-// A row that the quick pass cannot take: NaN, an infinite maximum, or one so large
-// that a product with c is off by a power of two.  *kind: 1 NaN or +infinity, 2 no
+// A row that the quick pass cannot take: NaN, an infinite maximum, or one so far from 0
+// that what a product's rounding leaves is not small.  *kind: 1 NaN or +infinity, 2 no
 // finite logit; *top: the maximum.
 template <typename T, int NT>
 __device__ __noinline__ Part careful(const Share<T>& r, float c, TeamShared& sh, int tid, int* kind, float* top) {
@@ -436,7 +437,7 @@ token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constan
 
     // the quick pass
     constexpr int UN = 2;                    // groups in work, and as many on their way
-    Part p{-FLT_MAX, 0.f, 0.f};
+    Part p{-FAR, 0.f, 0.f};
     float2 s2 = make_float2(0.f, 0.f), t2 = s2;
     float best[2] = {-INFINITY, -INFINITY};
     int at[2] = {-1, -1};
@@ -463,7 +464,7 @@ token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constan
                 const int w = NT == 32 ? u : 0;
                 if (gm > best[w] || at[w] < 0) best[w] = gm, at[w] = g;
             }
-            const float m = max_nan(p.m, max_nan(gm, LOWEST) * c);
+            const float m = max_nan(p.m, gm * c);
             const float d = p.m - m, f = ex2(d);
             p.m = m;
             // the group's sums apart: 8 and V / (16 threads) additions in a row, not their product
@@ -476,10 +477,8 @@ token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constan
                 sg = add2(sg, e);
                 tg = fma2(e, a, tg);
             }
-            // (before the first group d may be -infinity, and s and t are 0)
-            const float ds = fmaxf(d, -1e30f);
             const float2 ff = make_float2(f, f);
-            t2 = fma2(fma2(s2, make_float2(ds, ds), t2), ff, tg);
+            t2 = fma2(fma2(s2, make_float2(d, d), t2), ff, tg);
             s2 = fma2(s2, ff, sg);
         }
     }
@@ -487,8 +486,8 @@ token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constan
     p.t = t2.x + t2.y;
     for (int i = tid; i < r.edges; i += NT) {
         const float xv = max_nan(to_f(x[r.edge_id(i)]), LOWEST);
-        // what the rounding of its product leaves: up to 2^-24 of it, as in every group
-        const float m = __fmul_rn(xv, c), left = fmaf(xv, c, -m), e = ex2(left);
+        // its term relative to it: what the rounding of its product leaves, up to 2^-24 of it, as in every group
+        const float m = max_nan(__fmul_rn(xv, c), -FAR), left = fmaf(xv, c, -m), e = ex2(left);
         p = join(p, Part{m, e, e * left});
     }
     p = team_join<NT>(p, sh, tid);
@@ -520,7 +519,7 @@ token_logprobs_kernel(const __grid_constant__ LogitsView v, const __grid_constan
     }
     int kind = 0;
     float top = 0.f;
-    const bool large = !(fabsf(p.m) < 1e6f && p.s <= FLT_MAX);
+    const bool large = !(fabsf(p.m) < FAR);
     if (large) p = careful<T, NT>(share_of(x, v.V, 0, 1), c, sh, tid, &kind, &top);
     const float ls = log2f(p.s);
     auto logprob = [&](float xv) {

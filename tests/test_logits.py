@@ -270,6 +270,35 @@ def test_rows_of_special_values(v, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("v,n,offset", [(40, 64, 1), (1000, 64, 0), (20000, 64, 5), (32003, 500, 3), (151936, 3, 0),
+                                        (151936, 3, 7), (151936, 320, 0)])
+def test_tokens_that_are_not_allowed_cost_nothing(v, n, offset, dtype):
+    """masks over a row's first ids, its two ends, all but a few tokens: with -infinity, the type's lowest value or any
+    large negative number the row is taken as with -1e5, whose terms are 0 in fp32 as well, and all results have the same
+    bits (a second pass over the row, which other values need, rounds its sums elsewhere)"""
+    torch = _torch()
+    import rl_step_gb300.logits as lg
+    _, x, y = _case(torch, n, v, dtype, seed=v, offset=offset)
+    _, a, _ = _case(torch, n, v, dtype, offset=offset)             # lies as x does
+    first, ends, most = (torch.zeros(v, dtype=torch.bool, device="cuda") for _ in range(3))
+    first[:max(v // 3, 33)] = True
+    ends[0] = ends[v - 1] = True
+    most[:v - 7] = most[v - 1] = True
+    y[:] = v - 2                                                   # allowed by all three
+    rows = list(range(0, n, 50))
+    for mask in (first, ends, most):
+        a.copy_(x).masked_fill_(mask, -1e5)
+        want = lg.token_logprobs(a, y, top=5, scale=0.9)
+        for low in (-1e9, -1e10, -1e20, -1.2e30, torch.finfo(x.dtype).min, -math.inf):
+            a.masked_fill_(mask, low)
+            r = lg.token_logprobs(a, y, top=5, scale=0.9)
+            for name, p, q in zip(r._fields, r, want):
+                assert torch.equal(p, q), (name, low, (p != q).sum().item())
+        _check(a[rows], y[rows], 0.9, 5, lg.TokenStats(*[t[rows] for t in r]))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("v", [4096, 151936])
 def test_alternatives_that_few_threads_hold(v):
     """the largest groups all in one thread's stride, in more than the list holds, and in runs"""
