@@ -130,7 +130,7 @@ struct Part {
 __device__ __forceinline__ Part join(const Part& a, const Part& b) {
     const float m = max_nan(a.m, b.m);
     const float da = a.m - m, db = b.m - m, fa = ex2(da), fb = ex2(db);
-    return Part{m, fmaf(a.s, fa, b.s * fb), fmaf(a.s, da, a.t) * fa + fmaf(b.s, db, b.t) * fb};
+    return Part{m, fmaf(a.s, fa, b.s * fb), __fmul_rn(fmaf(a.s, da, a.t), fa) + __fmul_rn(fmaf(b.s, db, b.t), fb)};
 }
 
 // What a team shares.
