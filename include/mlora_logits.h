@@ -88,7 +88,9 @@ typedef struct {
  * -infinity), gets zeros whatever its logits; the row of an lse that is NaN otherwise NaN.
  * An id outside -1 .. vocab-1 raises bit 0 of *status and counts as -1; an id may
  * occur more than once in a row.  dlogits: rows of vocab elements of x's dtype,
- * out_stride apart; it is x->logits (with its stride) or overlaps no row of it.
+ * out_stride apart; it is x->logits (with its stride) or none of its rows overlaps one of x.
+ * Rows that do not lie like the logits' (addresses equal modulo 32 bytes) are read and written
+ * an element at a time.
  * Errors: E_ARG, E_CUDA. */
 int mlora_token_logprobs_backward(const mlora_logits* x, const mlora_token_grads* g, void* dlogits,
                                   int64_t out_stride, void* stream);

@@ -852,14 +852,20 @@ int sm_count(int* n) {
     return MLORA_OK;
 }
 
-// Whether rows of `width` bytes, lda and ldb bytes apart, share a byte.
+// Whether n rows of `width` bytes, lda and ldb bytes apart (width at least), share a byte.
 bool rows_overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t n, int64_t width) {
     const char *pa = static_cast<const char*>(a), *pb = static_cast<const char*>(b);
     if (pa + (n - 1) * lda + width <= pb || pb + (n - 1) * ldb + width <= pa) return false;
-    if (lda != ldb) return true;             // (rows that interleave at two distances are refused too)
-    if (n == 1) return true;                 // the spans overlap
-    const int64_t d = ((pb - pa) % lda + lda) % lda;
-    return d < width || d + width > lda;
+    if (lda == ldb && n > 1) {
+        const int64_t d = ((pb - pa) % lda + lda) % lda;
+        return d < width || d + width > lda;
+    }
+    // b's rows between a's: each against the last of a's rows that begins at or before it, and the next one
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t at = pb + i * ldb - pa, k = at < 0 ? -1 : at / lda < n ? at / lda : n - 1;
+        if ((k >= 0 && at - k * lda < width) || (k + 1 < n && (k + 1) * lda - at < width)) return true;
+    }
+    return false;
 }
 
 }  // namespace
@@ -897,7 +903,7 @@ extern "C" int mlora_token_logprobs_backward(const mlora_logits* x, const mlora_
     if (g->d_entropy && !g->entropy) return kv_fail(MLORA_E_ARG, "d_entropy without the entropy");
     if (g->d_logprobs && !x->targets) return kv_fail(MLORA_E_ARG, "d_logprobs without targets");
     if (g->d_top && x->top > 0 && !g->top_ids) return kv_fail(MLORA_E_ARG, "d_top without the ids");
-    if (!(dlogits == x->logits && out_stride == x->stride) &&
+    if (!(dlogits == x->logits && (out_stride == x->stride || n == 1)) &&
         rows_overlap(x->logits, x->stride * es, dlogits, out_stride * es, n, x->vocab * es))
         return kv_fail(MLORA_E_ARG, "dlogits overlaps the logits and is not the logits themselves");
     w.g = *g;

@@ -120,7 +120,10 @@ def token_logprobs_backward(logits, lse, entropy=None, targets=None, d_logprobs=
     """The gradient in logits of a loss whose gradients in token_logprobs' results
     are d_logprobs, d_entropy, d_lse [n] and d_top [n, top] (None: none).  lse and
     entropy are the forward's, top_ids int32 [n, top] its alternatives or any ids
-    (-1: none).  out: like logits, may be logits itself (None: a new tensor)."""
+    (-1: none).  out: like logits, may be logits itself (None: a new contiguous
+    tensor).  Rows of out that do not lie like the logits' (addresses equal modulo 32
+    bytes) take several times as long: for logits that are a part of wider rows give an
+    out that is one too."""
     top = 0
     if d_top is not None:
         if top_ids is None or d_top.dim() != 2:

@@ -500,6 +500,42 @@ def test_gradient_beside_the_logits(v, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_between_the_logits_at_another_distance(dtype):
+    """rows that overlap no row of the logits although they lie between them, and one row in place with any distance"""
+    torch = _torch()
+    import rl_step_gb300.logits as lg
+    n, v = 5, 1000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    buf = torch.randn(6 * n * v, generator=g, device="cuda").to(dt)
+    x = torch.as_strided(buf, (n, v), (5000, 1))                     # [0, 1000), [5000, 6000), .. [20000, 21000)
+    d = torch.as_strided(buf, (n, v), (4300, 1), 1300)               # [1300, 2300), [5600 ..: one reaches into a row
+    y = torch.randint(0, v, (n,), generator=g, device="cuda", dtype=torch.int32)
+    dl = torch.randn(n, generator=g, device="cuda")
+    rest = buf.clone()
+    r = lg.token_logprobs(x, y)
+    import rl_step_gb300 as m
+    with pytest.raises(m.MLoRAError):
+        lg.token_logprobs_backward(x, r.lse, r.entropy, y, dl, dl, out=d)
+    assert torch.equal(buf, rest)
+    d = torch.as_strided(buf, (n, v), (5500, 1), 1700)               # 1700, 7200, 12700, 18200 and 23700 on
+    want = lg.token_logprobs_backward(x, r.lse, r.entropy, y, dl, dl)
+    lg.token_logprobs_backward(x, r.lse, r.entropy, y, dl, dl, out=d)
+    assert torch.equal(d, want)
+    d.copy_(torch.as_strided(rest, (n, v), (5500, 1), 1700))
+    assert torch.equal(buf, rest)
+    # one row: its distance to the next says nothing
+    es = x.element_size()
+    c = lg._Logits(x.data_ptr(), y.data_ptr(), None, 5000, 1, v, lg._dtype(dt), 1.0, 0)
+    q = lg._TokenGrads(r.lse.data_ptr(), r.entropy.data_ptr(), None, dl.data_ptr(), dl.data_ptr(), None, None)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lg._lib().mlora_token_logprobs_backward(ctypes.byref(c), ctypes.byref(q), x.data_ptr() + es, v, stream) == -1
+    assert lg._lib().mlora_token_logprobs_backward(ctypes.byref(c), ctypes.byref(q), x.data_ptr(), v, stream) == 0
+    assert torch.equal(x[0], want[0]) and torch.equal(buf[1000:], rest[1000:])
+
+
+@pytest.mark.gpu
 def test_rows_beyond_two_gigabytes():
     """offsets beyond 31 bits: the last rows of 2.4 G logits"""
     torch = _torch()
