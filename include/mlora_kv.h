@@ -156,9 +156,9 @@ int mlora_kv_attention(const mlora_kv_cache* c, const mlora_kv_seqs* q, const ml
  * A page in a row that another row owns (a shared prefix, put there by the caller)
  * is read as any other, never given back by this one, and never written: a sequence
  * does not grow inside a page that is not its own, so a shared prefix ends with a page
- * and its readers are cut back to whole pages of it.  When the owner gives the pages
- * back, entries of other rows stay and name pages that others will take: cut
- * those rows first.
+ * and its readers are cut back to whole pages of it.  When the owner gives a page
+ * back, or is cut back inside it and grows again, entries of other rows stay and name
+ * what others, or its new rows, are written to: cut those rows first.
  *
  * The free list is a stack, free_pages[0 .. *n_free).  A new pool of n pages has
  * their ids there in any order, *n_free = n and owner[i] = -1.  What the device
@@ -185,8 +185,11 @@ typedef struct {
  * A sequence is left as it is, with no rows, if its numbers are out of range
  * (negative, or together more than max_pages * 64 or 2^31 - 1), if the new rows of the
  * sequences up to it exceed n_rows, if its last page is part-filled and row s does not
- * own it (all bit 0), or if their pages exceed the free ones (bit 2).  Those sums count every sequence in range, so one that is too large
- * refuses those behind it that need pages too.  Errors: E_ARG, E_CUDA. */
+ * own it (all bit 0), or if their pages exceed the free ones (bit 2).  Those sums
+ * count every sequence in range, so one that is too large refuses those behind it that
+ * need pages too.  Give row_off to the calls above even where every sequence was to get
+ * one row: without it they take one row of each, the last old one of a sequence that was
+ * left as it is.  Errors: E_ARG, E_CUDA. */
 typedef struct {
     int32_t* page_table;       /* DEVICE [n_seqs x max_pages], updated       */
     int32_t* kv_len;           /* DEVICE [n_seqs], updated                   */

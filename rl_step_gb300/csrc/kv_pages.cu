@@ -6,7 +6,7 @@
 // chain of a few dependent reads.  So one block does a call's prefix sums and moves
 // its pages, and writes the rows' positions, sequences and slots as well where they
 // are few; more rows go to a second launch over all SMs.  256 sequences cut by up to three
-// tokens and grown by four: 9 us for both calls; 51 of up to 2,048 tokens given back and
+// tokens and grown by four: 10 us for both calls; 51 of up to 2,048 tokens given back and
 // as many grown: 18 us.
 //
 // The free list is a stack.  Growing takes pages from its top in the order of the
@@ -23,7 +23,7 @@ namespace {
 constexpr int ST_NO_PAGES = 4;
 constexpr int PT = 1024;                     // most threads
 // Sequences of a thread in a pass: SEQS = 1, or 4 where the block has no thread for each (4,043 sequences
-// cut and grown: 20 us, 51 with one; 256: 9 us with one, 13 with four).
+// cut and grown: 21 us, 51 with one; 256: 10 us with one, 13 with four).
 
 struct PoolView {
     int* free_pages;

@@ -18,9 +18,9 @@
 // blocks an SM work while the other is at its r x r steps.  Sums meet in a fixed order:
 // results repeat.  What bounds it: for many matrices the passes, 1.7, 3.8 and 2.7
 // thousand cycles for 16 warps' tiles of 32 x 32 without their fetches (the tensor
-// cores' share 1.4, 3.4 and 1.9) and 2.7, 4.3 and 3.4 with them (32 x 4,096, fp32), at 54 %
-// of the copy rate and the tensor cores at 41 %: M is read three times, from HBM where
-// 304 matrices exceed L2.  For few matrices the chain of dependent steps: of 17 us for
+// cores' share 1.4, 3.4 and 1.9) and 2.7, 4.3 and 3.4 with them (32 x 4,096, fp32), at 63 %
+// of the copy rate for eight adapters of the 8B widths and 75 % for 32, the tensor cores at 41 %:
+// M is read three times, 2.7 of them from HBM where 304 matrices exceed L2.  For few matrices the chain of dependent steps: of 17 us for
 // one of 32 x 256 the r x r steps take 6, the three passes 4, the sums between them 2.
 //
 // The products run on mma.sync with fp16 operands and fp32 sums: each factor, scaled
@@ -492,7 +492,9 @@ __device__ __forceinline__ void times_p(const Matrix<T, R, TALL>& x, const Ortho
 
 // The sums of X X^T over the block's columns.  f: the scale, or 0: each warp's own, from the
 // root mean square of its first tile (2^5, which leaves 2^10 for larger elements); then the
-// sums are those of M itself.  Where that does not do, they are no numbers.
+// sums are those of M itself.  Where that does not do, they are no numbers, and the caller takes the
+// scale from M's largest element: an elementwise read and this pass again.  A first tile of zeros is such a
+// case (1,200 matrices of 32 x 4,096 whose first 32 columns are 0: 680 us instead of 473, all zeros 596).
 template <typename T, int R, bool TALL>
 __device__ __forceinline__ void gram_of_x(const Matrix<T, R, TALL>& x, OrthoShared<T, R>& sh, float f, int first, int end,
                                           Gram<R>& acc) {
@@ -836,8 +838,9 @@ constexpr int TAB_SMALL = 64, TAB_LARGE = 1300;      // 1.6 KB and 31 KB of kern
 
 int tile_for(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
 
-// Blocks of a cluster for n matrices, the longest of `longest` columns: as few as give each SM
-// its two, and no more than have 512 columns each, two tiles a warp.  (Two fp32 adapters of the
+// Blocks of a cluster for n matrices, the longest of `longest` columns: the first power of two that
+// gives each SM at least two (for 56 matrices 448 blocks on 304 places), and no more than have
+// 512 columns each, two tiles a warp.  (Two fp32 adapters of the
 // 8B widths, 112 matrices: 98 us with clusters of four, 129 of eight, 121 of two; 1,200 of 32 x
 // 4,096: 478 us with a block each, 598 with two: a block does the r x r steps of its matrix, so
 // more blocks do them more often.)  The blocks decide the order of a matrix's sums, and so do the other matrices of
