@@ -735,3 +735,35 @@ def test_a_step_after_statistics_that_failed(fails):
     assert torch.equal(first[0], again[0]) and torch.isfinite(again[1]).all()
     assert torch.allclose(first[1], again[1], rtol=1e-4, atol=1e-6 * first[1].abs().max().item())   # atomics' order
     assert torch.isfinite(lg.tf_forward_stats(s.h, *args, top=3).entropy).all()                     # the hook is off again
+
+
+@pytest.mark.gpu
+def test_statistics_captured_replayed_and_on_another_stream():
+    """the batch is read at replay; the same bits as calls outside a graph"""
+    torch = _torch()
+    import rl_step_gb300.logits as lg
+    from test_rollout import Setup
+    s = Setup(max_tokens=640, qk_std=0.05)
+    rng = np.random.default_rng(6)
+    n = 500
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    pos, ads = i32(np.r_[np.arange(350), np.arange(150)]), i32(np.r_[np.zeros(350), np.ones(150)])
+    batches = [(i32(rng.integers(0, s.cfg.vocab, n)), i32(rng.integers(0, s.cfg.vocab, n)), pos, ads) for _ in range(2)]
+    want = [lg.tf_forward_stats(s.h, *b, top=6, scale=0.7) for b in batches]
+    held = tuple(t.clone() for t in batches[0])
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        r = lg.tf_forward_stats(s.h, *held, top=6, scale=0.7)
+    for k in (0, 1, 0):
+        for d, t in zip(held, batches[k]):
+            d.copy_(t)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(r, want[k]))
+    side.wait_stream(torch.cuda.current_stream())
+    r = lg.tf_forward_stats(s.h, *batches[1], top=6, scale=0.7, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(r, want[1]))
+    empty = lg.tf_forward_stats(s.h, *[t[:0] for t in batches[0]], top=6)
+    assert empty.lse.shape == (0,) and empty.top_ids.shape == (0, 6)
